@@ -12,6 +12,10 @@
  *   pa_merge_attn_states  merge two partial attention results
  *   pa_cascade_decode     decode for sequences sharing a prefix (cascade)
  *   pa_*_fp8              the cache write and decode with an FP8 (e4m3) pool
+ *   pa_*_fp8_block        the cache write and decode with an e4m3 pool that has
+ *                         one scale for each (plane, block, kv head)
+ *   pa_update_block_bounds, pa_select_blocks, pa_decode_sparse
+ *                         decode over the blocks that can score highest
  *   pa_stage_copy         move a step's data between pinned host memory and
  *                         the device on the SMs
  *
@@ -234,6 +238,132 @@ pa_status pa_decode_splitk_fp8(void *out, const void *q, const void *kv_cache,
                                float scale, float k_scale, float v_scale, pa_dtype dtype,
                                int max_seq_len, int partition_size, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/*
+ * FP8 KV cache with block scales.  The pool is uint8 [2, num_blocks,
+ * block_size, num_kv_heads, head_size] of e4m3 codes as for the pa_*_fp8
+ * calls, and kv_scales float32 [2, num_blocks, num_kv_heads] holds one scale
+ * for each plane, block and kv head: a code c stands for c * scale.  No scale
+ * is chosen beforehand.  The pages have no counterpart of these calls.
+ *
+ * pa_reshape_and_cache_fp8_block appends new tokens.  Request r's new tokens
+ * are the rows query_start_loc[r] .. query_start_loc[r+1] of key and value;
+ * they sit at its last positions, ending at seq_lens[r] (as in pa_prefill),
+ * and go to the blocks that its table names.  For every (plane, block, head)
+ * that receives tokens:
+ *   s_new = the smallest 2^e with max |x| <= 448 * 2^e over the finite new
+ *           values, e held to [-60, 60];
+ *   scale = s_new where the new tokens begin at the block's first row, else
+ *           max(s_new, the block's scale);
+ *   codes = e4m3(x / scale), nearest even; magnitudes above 448 * scale and
+ *           infinities saturate, NaN stays NaN.  Where the scale has grown, the
+ *           block's older rows become e4m3(code * old_scale / scale), which is
+ *           exact except for values that fall among e4m3's subnormals.
+ * Other rows and scales are left as they were.  Every scale is a power of two;
+ * kv_scales need not be initialised.  The blocks that receive tokens belong to
+ * one request each; no other call writes them at the same time.
+ *   key, value       rows as in pa_reshape_and_cache (strides in elements,
+ *                    multiples of 8), num_tokens of them.
+ *   block_tables     as in pa_prefill, row r at block_tables +
+ *                    r * block_table_stride.
+ *   max_query_len    an upper bound of every request's new tokens.
+ * A request whose metadata is out of range is skipped and flagged
+ * (PA_DEVERR_SEQ_LEN), a block outside the pool likewise (PA_DEVERR_BLOCK_ID).
+ *
+ * pa_decode_fp8_block is pa_decode over such a pool:  keys scale * e4m3(K),
+ * values scale * e4m3(V), q and out in `dtype`, fp32 softmax and sums; the
+ * scales must lie in [2^-64, 2^64].  lse is NULL or receives each row's
+ * natural log-sum-exp as pa_decode_splitk_lse's (float32 [num_seqs,
+ * num_heads]).  max_seq_len bounds every seq_len (a longer one is clamped and
+ * flagged).  The call splits the work by itself; its workspace holds
+ * pa_block_decode_workspace_size bytes, 256-byte aligned, whatever the number
+ * and length of the sequences, with the rules of pa_decode_splitk's.  head_size 64 or
+ * 128, any number of kv heads.
+ */
+pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, void *kv_cache,
+                                         float *kv_scales, const int32_t *block_tables,
+                                         int64_t block_table_stride, const int32_t *seq_lens,
+                                         const int32_t *query_start_loc, int num_reqs,
+                                         int num_tokens, int max_query_len, int num_kv_heads,
+                                         int head_size, int block_size, int num_blocks,
+                                         int max_blocks_per_seq, int64_t key_stride,
+                                         int64_t value_stride, pa_dtype src_dtype, void *stream);
+size_t pa_block_decode_workspace_size(int num_heads, int num_kv_heads, int head_size);
+pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *kv_cache,
+                              const float *kv_scales, const int32_t *block_tables,
+                              const int32_t *seq_lens, int num_seqs, int num_heads,
+                              int num_kv_heads, int head_size, int block_size, int num_blocks,
+                              int max_blocks_per_seq, float scale, pa_dtype dtype,
+                              int max_seq_len, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * Block-sparse decode: a step attends the blocks of its cache that can hold
+ * the highest scores.  Three calls, none of which the pages have: the bounds
+ * of each block's keys are refreshed after the cache write, the blocks of
+ * every (sequence, kv head) are selected for the step's queries, and the
+ * decode reads those alone.  kv_scales is NULL for a 16-bit pool of `dtype`,
+ * and the block scales above for an e4m3 pool.
+ *
+ * pa_update_block_bounds recomputes the bounds of every block that holds a
+ * new token (query_start_loc, seq_lens, tables and errors as in
+ * pa_reshape_and_cache_fp8_block; the tokens are already in the pool), over
+ * all rows of the block below seq_lens[r]:
+ *   bounds        int8 [num_blocks, num_kv_heads, 2, head_size], 16-byte
+ *                 aligned: ceil(max_t k[t][d] / s) then floor(min_t k[t][d] / s)
+ *   bounds_scale  float32 [num_blocks, num_kv_heads]: s, the smallest 2^e with
+ *                 max |k| <= 127 * 2^e, e held to [-60, 60] (codes beyond +-127
+ *                 saturate).  A block with a key that is not finite gets s =
+ *                 +inf and codes 0.
+ * A block may be shared by requests as long as they agree on the rows it holds.
+ *
+ * pa_select_blocks scores block j of sequence s for kv head h as
+ *   max over the group's queries of 2^e_q 2^e_j sum_d c_d (c_d > 0 ? U_d : L_d),
+ * with U and L its upper and lower bounds: an upper bound of the block's scores up to the rounding of the query's codes
+ * c = rint(q / 2^e_q) (e_q the smallest in [-60, 60] that keeps them within
+ * +-127; NaN counts as 0).  The sum is an integer, so a score is exact and the
+ * selection does not depend on the order of sums.  The first num_sink_blocks
+ * and the last num_recent_blocks of a sequence (together at most
+ * max_selected) are always chosen, then blocks with s = +inf, then the highest
+ * scores; equal ones from the lowest position.
+ *   block_lists   int32 [num_seqs, num_kv_heads, max_selected]: the chosen
+ *                 positions j (entries of the sequence's table) in ascending
+ *                 order, -1 behind the last
+ *   list_lens     int32 [num_seqs]: min(max_selected, the sequence's blocks)
+ *   workspace     pa_select_blocks_workspace_size bytes, 256-byte aligned,
+ *                 with the rules of pa_decode_splitk's
+ *
+ * pa_decode_sparse is pa_decode over the tokens of the listed blocks (those
+ * below seq_lens[s]).  Entries of a list may come in any order; one that
+ * appears twice counts twice, a negative one is skipped, one past the
+ * sequence's last block is skipped and flagged (PA_DEVERR_BLOCK_ID), and
+ * entries behind list_lens[s] (at most max_selected, or clamped and flagged)
+ * are not read.  A row that attends nothing is zero, its lse -inf.
+ * Workspace and lse as in pa_decode_fp8_block.
+ */
+pa_status pa_update_block_bounds(int8_t *bounds, float *bounds_scale, const void *kv_cache,
+                                 const float *kv_scales, const int32_t *block_tables,
+                                 int64_t block_table_stride, const int32_t *seq_lens,
+                                 const int32_t *query_start_loc, int num_reqs, int max_query_len,
+                                 int num_kv_heads, int head_size, int block_size, int num_blocks,
+                                 int max_blocks_per_seq, pa_dtype dtype, void *stream);
+size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int max_seq_len,
+                                       int block_size);
+pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void *q,
+                           const int8_t *bounds, const float *bounds_scale,
+                           const int32_t *block_tables, const int32_t *seq_lens, int num_seqs,
+                           int num_heads, int num_kv_heads, int head_size, int block_size,
+                           int num_blocks, int max_blocks_per_seq, int max_selected,
+                           int num_sink_blocks, int num_recent_blocks, pa_dtype dtype,
+                           int max_seq_len, void *workspace, size_t workspace_bytes,
+                           void *stream);
+pa_status pa_decode_sparse(void *out, float *lse, const void *q, const void *kv_cache,
+                           const float *kv_scales, const int32_t *block_tables,
+                           const int32_t *seq_lens, const int32_t *block_lists,
+                           const int32_t *list_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_size, int block_size, int num_blocks,
+                           int max_blocks_per_seq, int max_selected, float scale, pa_dtype dtype,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * pa_decode_splitk that also writes each row's log-sum-exp: lse[s][h] =

@@ -23,6 +23,9 @@ __all__ = [
     "pa_decode_splitk_lse", "pa_merge_attn_states", "pa_cascade_decode",
     "pa_cascade_decode_workspace_size", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
     "pa_decode_splitk_fp8", "pa_decode_splitk_fp8_workspace_size",
+    "pa_reshape_and_cache_fp8_block", "pa_decode_fp8_block", "pa_block_decode_workspace_size",
+    "pa_update_block_bounds", "pa_select_blocks", "pa_select_blocks_workspace_size",
+    "pa_decode_sparse",
     "pa_validate_block_mapping", "pa_status_string", "pa_version", "pa_profile_kernel_events",
     "DEVERR_BLOCK_ID",
     "DEVERR_SEQ_LEN", "DEVERR_SLOT", "DEVERR_TIMEOUT",
@@ -86,6 +89,25 @@ _lib.pa_decode_splitk_fp8_workspace_size.argtypes = [_I, _I, _I, _I, _I]
 _lib.pa_decode_splitk_fp8.restype = _I
 _lib.pa_decode_splitk_fp8.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F,
                                       _F, _I, _I, _I, _P, _SZ, _P]
+_lib.pa_reshape_and_cache_fp8_block.restype = _I
+_lib.pa_reshape_and_cache_fp8_block.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I,
+                                                _I, _I, _I, _I, _I64, _I64, _I, _P]
+_lib.pa_block_decode_workspace_size.restype = _SZ
+_lib.pa_block_decode_workspace_size.argtypes = [_I, _I, _I]
+_lib.pa_decode_fp8_block.restype = _I
+_lib.pa_decode_fp8_block.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
+                                     _I, _I, _P, _SZ, _P]
+_lib.pa_update_block_bounds.restype = _I
+_lib.pa_update_block_bounds.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I,
+                                        _I, _I, _P]
+_lib.pa_select_blocks_workspace_size.restype = _SZ
+_lib.pa_select_blocks_workspace_size.argtypes = [_I, _I, _I, _I]
+_lib.pa_select_blocks.restype = _I
+_lib.pa_select_blocks.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                                  _I, _I, _I, _P, _SZ, _P]
+_lib.pa_decode_sparse.restype = _I
+_lib.pa_decode_sparse.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                  _I, _F, _I, _P, _SZ, _P]
 _lib.pa_prefill.restype = _I
 _lib.pa_prefill.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                             _I, _F, _I, _I, _P]
@@ -472,6 +494,253 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
                                      _DTYPE[q.dtype], int(max_seq_len), int(partition_size),
                                      _dev(workspace, "workspace"), ws_bytes, _stream(stream)),
            "pa_decode_splitk_fp8")
+    return out
+
+
+# The block-scaled and block-sparse calls.  Their tensors must all lie on the
+# current device: a pointer of another one would reach this device's kernels.
+def _here(named) -> None:
+    dev = None
+    for name, t in named:
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            dev = torch.cuda.current_device() if _current_device is None else _current_device()
+            if d != dev:
+                raise ValueError(f"{name} must be on the current device, cuda:{dev}")
+
+
+def _block_pool(kv_cache, kv_scales, block_size: int):
+    """Dimensions of an e4m3 pool (with scales) or a 16-bit one (kv_scales None)."""
+    nb, hkv, d = _pool_dims(kv_cache, block_size)
+    if kv_scales is None:
+        if kv_cache.dtype not in _DTYPE:
+            raise ValueError("a pool without kv_scales must be float16 or bfloat16")
+    else:
+        if kv_cache.dtype != torch.uint8:
+            raise ValueError("a pool with kv_scales must be a uint8 tensor of e4m3 codes")
+        if kv_scales.dtype != torch.float32 or kv_scales.shape != (2, nb, hkv) or \
+                not kv_scales.is_contiguous():
+            raise ValueError("kv_scales must be contiguous float32 [2, num_blocks, num_kv_heads]")
+    return nb, hkv, d
+
+
+def _requests(block_tables, seq_lens, query_start_loc) -> int:
+    r = seq_lens.numel()
+    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [R]")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != r or block_tables.stride(1) != 1 or \
+            block_tables.stride(0) < block_tables.shape[1]:
+        raise ValueError("block_tables must be int32 [R, max_blocks] with contiguous rows")
+    if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != r + 1 or \
+            not query_start_loc.is_contiguous():
+        raise ValueError("query_start_loc must be contiguous int32 [R + 1]")
+    return r
+
+
+def _block_queries(q, d: int, hkv: int, block_tables, seq_lens):
+    if q.dim() != 3 or q.shape[2] != d or q.dtype not in _DTYPE or not q.is_contiguous():
+        raise ValueError("q must be contiguous fp16/bf16 [B, H, head_size]")
+    b, h, _ = q.shape
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != b or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [B, max_blocks_per_seq]")
+    if seq_lens.dtype != torch.int32 or seq_lens.numel() != b or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [B]")
+    return b, h
+
+
+def _workspace_arg(workspace):
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor,
+                                   kv_cache: torch.Tensor, kv_scales: torch.Tensor,
+                                   block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                   query_start_loc: torch.Tensor, block_size: int,
+                                   max_query_len: int, stream=None) -> None:
+    """Quantise each request's new tokens (rows query_start_loc[r]:
+    query_start_loc[r+1] of key and value [T, Hkv, D] fp16/bf16, its last
+    positions) to e4m3 with one power-of-two scale for each (plane, block, kv
+    head) and append them to the uint8 pool; ``kv_scales`` (float32 [2,
+    num_blocks, Hkv]) is updated with it."""
+    if kv_scales is None:
+        raise ValueError("kv_scales is required")
+    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
+    r = _requests(block_tables, seq_lens, query_start_loc)
+    tokens = key.shape[0]
+    for name, t in (("key", key), ("value", value)):
+        if t.dtype not in _DTYPE or t.dtype != key.dtype or t.dim() != 3 or \
+                t.shape != (tokens, hkv, d):
+            raise ValueError(f"{name} must be fp16/bf16 [T, num_kv_heads, head_size] like key")
+        if t.stride(2) != 1 or t.stride(1) != d:
+            raise ValueError(f"{name} must have contiguous rows")
+    if r == 0 or tokens == 0:
+        return
+    _here((("key", key), ("value", value), ("kv_cache", kv_cache), ("kv_scales", kv_scales),
+           ("block_tables", block_tables), ("seq_lens", seq_lens),
+           ("query_start_loc", query_start_loc)))
+    _check(_lib.pa_reshape_and_cache_fp8_block(
+        key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(),
+        block_tables.data_ptr(), block_tables.stride(0), seq_lens.data_ptr(),
+        query_start_loc.data_ptr(), r, tokens, int(max_query_len), hkv, d, block_size, nb,
+        block_tables.shape[1], key.stride(0) if tokens > 1 else hkv * d,
+        value.stride(0) if tokens > 1 else hkv * d, _DTYPE[key.dtype], _stream(stream)), "pa_reshape_and_cache_fp8_block")
+
+
+def pa_block_decode_workspace_size(num_heads: int, num_kv_heads: int, head_size: int) -> int:
+    """Workspace bytes of pa_decode_fp8_block and pa_decode_sparse."""
+    return int(_lib.pa_block_decode_workspace_size(num_heads, num_kv_heads, head_size))
+
+
+def _block_out(out, lse, q, b: int, h: int):
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous and match q")
+    if lse is None:
+        return None
+    return _lse_arg(lse, b, h)
+
+
+def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
+                        kv_scales: torch.Tensor, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, scale: float, block_size: int, max_seq_len: int,
+                        workspace: torch.Tensor, lse: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Paged decode attention over an e4m3 pool with block scales; writes and
+    returns ``out``, and the natural-log softmax denominators into ``lse``
+    (float32 [B, H]) if given.  ``workspace`` holds
+    pa_block_decode_workspace_size bytes."""
+    if kv_scales is None:
+        raise ValueError("kv_scales is required")
+    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
+    b, h = _block_queries(q, d, hkv, block_tables, seq_lens)
+    lp = _block_out(out, lse, q, b, h)
+    _here((("out", out), ("q", q), ("kv_cache", kv_cache), ("kv_scales", kv_scales),
+           ("block_tables", block_tables), ("seq_lens", seq_lens), ("workspace", workspace)) +
+          ((("lse", lse),) if lse is not None else ()))
+    wp, wb = _workspace_arg(workspace)
+    _check(_lib.pa_decode_fp8_block(
+        out.data_ptr(), lp, q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), b, h, hkv, d, block_size, nb,
+        block_tables.shape[1], float(scale), _DTYPE[q.dtype], int(max_seq_len), wp, wb,
+        _stream(stream)), "pa_decode_fp8_block")
+    return out
+
+
+def _bounds_args(bounds, bounds_scale, nb, hkv: int, d: int):
+    nb = bounds.shape[0] if nb is None else nb
+    if bounds.dtype != torch.int8 or bounds.shape != (nb, hkv, 2, d) or \
+            not bounds.is_contiguous():
+        raise ValueError("bounds must be contiguous int8 [num_blocks, num_kv_heads, 2, head_size]")
+    if bounds_scale.dtype != torch.float32 or bounds_scale.shape != (nb, hkv) or \
+            not bounds_scale.is_contiguous():
+        raise ValueError("bounds_scale must be contiguous float32 [num_blocks, num_kv_heads]")
+    return nb
+
+
+def pa_update_block_bounds(bounds: torch.Tensor, bounds_scale: torch.Tensor,
+                           kv_cache: torch.Tensor, block_tables: torch.Tensor,
+                           seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                           block_size: int, max_query_len: int,
+                           kv_scales: torch.Tensor | None = None, stream=None) -> None:
+    """Recompute the key bounds (int8 [num_blocks, Hkv, 2, D] with float32
+    [num_blocks, Hkv] scales) of every block that holds a new token of a
+    request; the tokens are already in the pool (16-bit, or e4m3 with
+    ``kv_scales``)."""
+    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
+    _bounds_args(bounds, bounds_scale, nb, hkv, d)
+    r = _requests(block_tables, seq_lens, query_start_loc)
+    if r == 0:
+        return
+    _here((("bounds", bounds), ("bounds_scale", bounds_scale), ("kv_cache", kv_cache),
+           ("block_tables", block_tables), ("seq_lens", seq_lens),
+           ("query_start_loc", query_start_loc)) +
+          ((("kv_scales", kv_scales),) if kv_scales is not None else ()))
+    _check(_lib.pa_update_block_bounds(
+        bounds.data_ptr(), bounds_scale.data_ptr(), kv_cache.data_ptr(),
+        None if kv_scales is None else kv_scales.data_ptr(), block_tables.data_ptr(),
+        block_tables.stride(0), seq_lens.data_ptr(), query_start_loc.data_ptr(), r,
+        int(max_query_len), hkv, d, block_size, nb, block_tables.shape[1],
+        0 if kv_scales is not None else _DTYPE[kv_cache.dtype], _stream(stream)),
+        "pa_update_block_bounds")
+
+
+def pa_select_blocks_workspace_size(num_seqs: int, num_kv_heads: int, max_seq_len: int,
+                                    block_size: int) -> int:
+    return int(_lib.pa_select_blocks_workspace_size(num_seqs, num_kv_heads, max_seq_len,
+                                                    block_size))
+
+
+def _lists_arg(block_lists, list_lens, b: int, hkv: int) -> int:
+    if block_lists.dtype != torch.int32 or block_lists.dim() != 3 or \
+            block_lists.shape[0] != b or block_lists.shape[1] != hkv or \
+            not block_lists.is_contiguous():
+        raise ValueError("block_lists must be contiguous int32 [B, num_kv_heads, max_selected]")
+    if list_lens.dtype != torch.int32 or list_lens.numel() != b or not list_lens.is_contiguous():
+        raise ValueError("list_lens must be contiguous int32 [B]")
+    return block_lists.shape[2]
+
+
+def pa_select_blocks(block_lists: torch.Tensor, list_lens: torch.Tensor, q: torch.Tensor,
+                     bounds: torch.Tensor, bounds_scale: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
+                     max_seq_len: int, workspace: torch.Tensor, num_sink_blocks: int = 0,
+                     num_recent_blocks: int = 1, stream=None):
+    """Choose, for every (sequence, kv head), the blocks whose keys can score
+    highest for the group's queries: ``block_lists`` (int32 [B, Hkv, K])
+    receives their positions in ascending order (-1 behind the last) and
+    ``list_lens`` (int32 [B]) their number; both are returned.  The first
+    ``num_sink_blocks`` and the last ``num_recent_blocks`` are always chosen."""
+    if bounds.dim() != 4:
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_size]")
+    hkv, d = bounds.shape[1], bounds.shape[3]
+    nb = _bounds_args(bounds, bounds_scale, None, hkv, d)
+    b, h = _block_queries(q, d, hkv, block_tables, seq_lens)
+    k = _lists_arg(block_lists, list_lens, b, hkv)
+    _here((("block_lists", block_lists), ("list_lens", list_lens), ("q", q), ("bounds", bounds),
+           ("bounds_scale", bounds_scale), ("block_tables", block_tables),
+           ("seq_lens", seq_lens), ("workspace", workspace)))
+    wp, wb = _workspace_arg(workspace)
+    _check(_lib.pa_select_blocks(
+        block_lists.data_ptr(), list_lens.data_ptr(), q.data_ptr(), bounds.data_ptr(),
+        bounds_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b, h, hkv, d,
+        block_size, nb, block_tables.shape[1], k, int(num_sink_blocks), int(num_recent_blocks),
+        _DTYPE[q.dtype], int(max_seq_len), wp, wb, _stream(stream)), "pa_select_blocks")
+    return block_lists, list_lens
+
+
+def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     block_lists: torch.Tensor, list_lens: torch.Tensor, scale: float,
+                     block_size: int, workspace: torch.Tensor,
+                     kv_scales: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Paged decode attention over the listed blocks of every (sequence, kv
+    head), of a 16-bit pool or of an e4m3 pool with ``kv_scales``; writes and
+    returns ``out`` (and ``lse``, float32 [B, H], if given).  ``workspace``
+    holds pa_block_decode_workspace_size bytes."""
+    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
+    b, h = _block_queries(q, d, hkv, block_tables, seq_lens)
+    if kv_scales is None and q.dtype != kv_cache.dtype:
+        raise ValueError("q and a 16-bit kv_cache must share their dtype")
+    lp = _block_out(out, lse, q, b, h)
+    k = _lists_arg(block_lists, list_lens, b, hkv)
+    _here((("out", out), ("q", q), ("kv_cache", kv_cache), ("block_tables", block_tables),
+           ("seq_lens", seq_lens), ("block_lists", block_lists), ("list_lens", list_lens),
+           ("workspace", workspace)) +
+          ((("kv_scales", kv_scales),) if kv_scales is not None else ()) +
+          ((("lse", lse),) if lse is not None else ()))
+    wp, wb = _workspace_arg(workspace)
+    _check(_lib.pa_decode_sparse(
+        out.data_ptr(), lp, q.data_ptr(), kv_cache.data_ptr(),
+        None if kv_scales is None else kv_scales.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), block_lists.data_ptr(), list_lens.data_ptr(), b, h, hkv, d,
+        block_size, nb, block_tables.shape[1], k, float(scale), _DTYPE[q.dtype], wp, wb,
+        _stream(stream)), "pa_decode_sparse")
     return out
 
 

@@ -25,7 +25,7 @@ namespace pa {
 // device address as a parameter.
 __device__ unsigned int g_device_errors = 0;
 
-static unsigned int *device_error_word(cudaError_t *err)
+unsigned int *device_error_word(cudaError_t *err)
 {
     static unsigned int *addr[64] = {nullptr};
     static std::mutex mu;
@@ -190,7 +190,7 @@ static bool make_q_rows_map(CUtensorMap *map, const void *q, int dtype, int num_
     return r == CUDA_SUCCESS;
 }
 
-static int sm_count(cudaError_t *err)
+int sm_count(cudaError_t *err)
 {
     static int count[64] = {0};
     int dev = 0;

@@ -1,0 +1,212 @@
+// pa_block_decode.cu -- C entries of the decode over an e4m3 pool with block
+// scales and over listed blocks; compiled once per type of q
+// (PA_INST_DTYPE: 0 fp16 with the entries, 1 bf16).
+#include <type_traits>
+
+#include "pa.h"
+#include "pa_block_decode.cuh"
+
+namespace pa {
+namespace block {
+
+cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+                                    cudaStream_t s);
+cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+                                     cudaStream_t s);
+
+template <typename T, bool E4M3, int D>
+static cudaError_t launch(const DecodeArgs &p, int ctas, cudaStream_t s)
+{
+    const cudaError_t e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas),
+                                                dim3(32 * kWarps), 0, s, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_after_previous(block_merge_kernel<T, E4M3, D>,
+                                 dim3(ctas, p.group << p.heads_log2), dim3(D), 0, s, p, ctas);
+}
+
+#if PA_INST_DTYPE == 1
+cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+                                     cudaStream_t s)
+{
+    if (head_size == 128)
+        return e4m3 ? launch<__nv_bfloat16, true, 128>(p, ctas, s) : launch<__nv_bfloat16, false, 128>(p, ctas, s);
+    return e4m3 ? launch<__nv_bfloat16, true, 64>(p, ctas, s) : launch<__nv_bfloat16, false, 64>(p, ctas, s);
+}
+#else
+cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+                                    cudaStream_t s)
+{
+    if (head_size == 128)
+        return e4m3 ? launch<__half, true, 128>(p, ctas, s) : launch<__half, false, 128>(p, ctas, s);
+    return e4m3 ? launch<__half, true, 64>(p, ctas, s) : launch<__half, false, 64>(p, ctas, s);
+}
+
+static bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+static size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// kv heads of a CTA: the largest of 8, 4, 2, 1 that divides them.
+static int heads_log2(int num_kv_heads)
+{
+    return num_kv_heads % 8 == 0 ? 3 : num_kv_heads % 4 == 0 ? 2 : num_kv_heads % 2 == 0 ? 1 : 0;
+}
+
+// Workspace: the cuts, then two partial states of each CTA.
+struct Layout {
+    size_t ml, o, total;
+};
+
+static Layout layout(int num_heads, int num_kv_heads, int head_size)
+{
+    const size_t rows = (size_t)kMaxCtas * 2 * (num_heads / num_kv_heads)
+                        << heads_log2(num_kv_heads);
+    Layout w;
+    w.ml = round_up(kMaxCtas * sizeof(int4));
+    w.o = w.ml + round_up(rows * 2 * sizeof(float));
+    w.total = w.o + round_up(rows * head_size * sizeof(float));
+    return w;
+}
+
+static pa_status decode(void *out, float *lse, const void *q, const void *kv_cache,
+                        const float *kv_scales, const int32_t *tables, const int32_t *seq_lens,
+                        const int32_t *lists, const int32_t *list_lens, int num_seqs,
+                        int num_heads, int num_kv_heads, int head_size, int block_size,
+                        int num_blocks, int max_blocks, int max_listed, float scale,
+                        pa_dtype dtype, int64_t len_cap, void *workspace, size_t workspace_bytes,
+                        void *stream)
+{
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        block_size <= 0 || num_blocks <= 0 || max_blocks <= 0 || !isfinite(scale) ||
+        num_heads % num_kv_heads != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!out || !q || !kv_cache || !tables || !seq_lens))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(q, 16) || !aligned(kv_cache, 16) ||
+        !aligned(kv_scales, 4) || !aligned(tables, 4) || !aligned(seq_lens, 4) ||
+        !aligned(lists, 4) || !aligned(list_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_heads / num_kv_heads;
+    if ((head_size != 64 && head_size != 128) || (block_size != 16 && block_size != 32) ||
+        (group != 1 && group != 2 && group != 4 && group != 8) ||
+        (dtype != PA_FP16 && dtype != PA_BF16))
+        return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_blocks * block_size >= (int64_t)INT32_MAX ||
+        (int64_t)max_blocks * block_size >= (int64_t)INT32_MAX || num_kv_heads > 65535 ||
+        num_seqs > 65535)
+        return PA_ERR_UNSUPPORTED;
+    // tiles are counted in 32 bits
+    const int64_t cap = len_cap < (int64_t)max_blocks * block_size
+                            ? len_cap
+                            : (int64_t)max_blocks * block_size;
+    const int hl = heads_log2(num_kv_heads);
+    const int64_t most = lists ? (int64_t)max_listed * (block_size / kTile) : cap / kTile + 1;
+    const int64_t tiles = most * num_seqs * (num_kv_heads >> hl);
+    if (tiles > INT32_MAX / 2)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return PA_OK;
+    const Layout w = layout(num_heads, num_kv_heads, head_size);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total)
+        return PA_ERR_WORKSPACE;
+    cudaError_t e;
+    DecodeArgs p = {};
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    const int sms = sm_count(&e);
+    if (!sms)
+        return PA_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    p.out = out;
+    p.lse = lse;
+    p.q = q;
+    p.pool = static_cast<const char *>(kv_cache);
+    p.scales = kv_scales;
+    p.tables = tables;
+    p.seq_lens = seq_lens;
+    p.lists = lists;
+    p.list_lens = list_lens;
+    p.cuts = reinterpret_cast<int4 *>(ws);
+    p.ws_ml = reinterpret_cast<float *>(ws + w.ml);
+    p.ws_o = reinterpret_cast<float *>(ws + w.o);
+    p.plane = (int64_t)num_blocks * block_size * num_kv_heads * head_size * (kv_scales ? 1 : 2);
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.heads_log2 = hl;
+    p.num_groups = num_kv_heads >> hl;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks;
+    p.block_log2 = block_size == 16 ? 4 : 5;
+    p.max_listed = max_listed;
+    p.len_cap = (int)cap;
+    p.qscale = scale * 1.4426950408889634f;
+    // At least kMinRun tiles a warp: no more CTAs than that can use.
+    int64_t ctas = tiles / (kMinRun * (kWarps >> hl)) + 1;
+    if (ctas > 2 * sms)
+        ctas = 2 * sms;
+    if (ctas > kMaxCtas)
+        ctas = kMaxCtas;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    e = dtype == PA_BF16
+            ? launch_block_decode_bf16(kv_scales != nullptr, head_size, p, (int)ctas, st)
+            : launch_block_decode_f16(kv_scales != nullptr, head_size, p, (int)ctas, st);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+#endif
+
+} // namespace block
+} // namespace pa
+
+#if PA_INST_DTYPE == 0
+using namespace pa;
+using namespace pa::block;
+
+extern "C" {
+
+size_t pa_block_decode_workspace_size(int num_heads, int num_kv_heads, int head_size)
+{
+    if (num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 || num_heads % num_kv_heads)
+        return 0;
+    return layout(num_heads, num_kv_heads, head_size).total;
+}
+
+pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *kv_cache,
+                              const float *kv_scales, const int32_t *block_tables,
+                              const int32_t *seq_lens, int num_seqs, int num_heads,
+                              int num_kv_heads, int head_size, int block_size, int num_blocks,
+                              int max_blocks_per_seq, float scale, pa_dtype dtype,
+                              int max_seq_len, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    if (max_seq_len < 0 || (num_seqs > 0 && !kv_scales))
+        return PA_ERR_INVALID_ARG;
+    return decode(out, lse, q, kv_cache, kv_scales, block_tables, seq_lens, nullptr, nullptr,
+                  num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                  max_blocks_per_seq, 0, scale, dtype, max_seq_len, workspace, workspace_bytes,
+                  stream);
+}
+
+pa_status pa_decode_sparse(void *out, float *lse, const void *q, const void *kv_cache,
+                           const float *kv_scales, const int32_t *block_tables,
+                           const int32_t *seq_lens, const int32_t *block_lists,
+                           const int32_t *list_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_size, int block_size, int num_blocks,
+                           int max_blocks_per_seq, int max_selected, float scale, pa_dtype dtype,
+                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (max_selected <= 0 || (num_seqs > 0 && (!block_lists || !list_lens)))
+        return PA_ERR_INVALID_ARG;
+    return decode(out, lse, q, kv_cache, kv_scales, block_tables, seq_lens, block_lists, list_lens,
+                  num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                  max_blocks_per_seq, max_selected, scale, dtype,
+                  (int64_t)max_blocks_per_seq * block_size, workspace, workspace_bytes, stream);
+}
+
+} // extern "C"
+#endif

@@ -1,0 +1,393 @@
+// pa_block_select.cu -- choosing the cache blocks a decode step attends: an
+// exact upper-bound score of every block for every (sequence, kv head), and
+// the blocks of the highest scores.
+#include <cuda_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "pa.h"
+#include "pa_block.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace block {
+
+// Order-preserving keys of scores; a block that is kept whatever its score
+// comes before all of them (a score of +inf is 0xFF800000).
+constexpr uint32_t kKeyKept = 0xFFFFFFFFu;
+
+__device__ __forceinline__ uint32_t key_of(float score)
+{
+    const uint32_t b = __float_as_uint(score);
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+struct SelectParams {
+    int32_t *lists;              // [B, Hkv, K]
+    int32_t *list_lens;          // [B]
+    const void *q;               // [B, H, D]
+    const int8_t *bounds;        // [NB, Hkv, 2, D]
+    const float *bounds_scale;   // [NB, Hkv]
+    const int32_t *tables, *seq_lens;
+    uint32_t *keys;              // [B, Hkv, stride]
+    unsigned int *err;
+    int num_heads, num_kv_heads, group, num_blocks, max_blocks, block_size, len_cap, most, sink,
+        recent, stride;
+};
+
+__device__ __forceinline__ int checked_len(const SelectParams &p, int s, bool report)
+{
+    const int len = p.seq_lens[s];
+    if (len >= 0 && len <= p.len_cap)
+        return len;
+    if (report)
+        atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
+    return len < 0 ? 0 : p.len_cap;
+}
+
+constexpr int kScoreWarps = 8;
+
+// Scores.  With U and L a block's upper and lower codes and c a query's codes,
+//   sum_d c_d (c_d > 0 ? U_d : L_d) = sum_d max(c_d, 0) U_d + min(c_d, 0) L_d,
+// one product of length 2 D in signed bytes, summed exactly in 32-bit
+// integers; times the two powers of two it is exact in fp32.  A warp scores 16
+// consecutive blocks of one (sequence, kv head) against the group's (at most
+// 8) queries with m16n8k32 products, the bounds loaded straight into the
+// operand's registers: contraction index k of a product is any permutation of
+// the channels as long as the queries use the same, so a lane takes 16-byte
+// pieces.  Bound by the read of the bounds, 2 D + 4 bytes a block and head.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p)
+{
+    constexpr int kPieces = 2 * D / 64;           // 16-byte pieces of a lane and row
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int head = blockIdx.x % p.num_kv_heads;
+    const int s = blockIdx.y;
+    const int len = checked_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
+    const int n = (len + p.block_size - 1) / p.block_size;
+    const int j0 = (blockIdx.x / p.num_kv_heads * kScoreWarps + (threadIdx.x >> 5)) * 16;
+    if (j0 >= n || n <= p.most)
+        return;
+    // Query codes: c = rint(q / 2^e), the largest magnitude within 127; NaN
+    // counts as zero.  Lane 4g + t holds query g's channels of its pieces.
+    uint32_t bq[kPieces][4];
+    float qs = 0.f;
+    {
+        float x[kPieces / 2][16];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < kPieces / 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const T *src = static_cast<const T *>(p.q) +
+                               ((int64_t)s * p.num_heads + head * p.group + min(g, p.group - 1)) * D +
+                               c * 64 + t * 16 + h * 8;
+                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = float2_of<T>((&v.x)[k]);
+                    x[c][h * 8 + 2 * k] = f.x;
+                    x[c][h * 8 + 2 * k + 1] = f.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+        qs = pow2_scale<127>(amax);
+        const float inv = pow2_inverse(qs);
+#pragma unroll
+        for (int c = 0; c < kPieces / 2; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t pos = 0, neg = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = x[c][4 * w + k];
+                    const float r = f == f ? fminf(fmaxf(rintf(f * inv), -127.f), 127.f) : 0.f;
+                    pos |= (uint32_t)((int)fmaxf(r, 0.f) & 255) << 8 * k;
+                    neg |= (uint32_t)((int)fminf(r, 0.f) & 255) << 8 * k;
+                }
+                bq[c][w] = pos;
+                bq[kPieces / 2 + c][w] = neg;
+            }
+    }
+    // Block ids of rows g and g + 8.
+    const int ja = j0 + g, jb = j0 + g + 8;
+    int pa = -1, pb = -1;
+    const int32_t *row = p.tables + (int64_t)s * p.max_blocks;
+    if (ja < n)
+        pa = row[ja];
+    if (jb < n)
+        pb = row[jb];
+    const bool bad_a = ja < n && (pa < 0 || pa >= p.num_blocks);
+    const bool bad_b = jb < n && (pb < 0 || pb >= p.num_blocks);
+    if ((bad_a || bad_b) && t == 0)
+        atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+    if (bad_a || pa < 0)
+        pa = -1;
+    if (bad_b || pb < 0)
+        pb = -1;
+    const int64_t ia = (int64_t)pa * p.num_kv_heads + head, ib = (int64_t)pb * p.num_kv_heads + head;
+    uint4 va[kPieces], vb[kPieces];
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+        va[c] = pa >= 0 ? load16(p.bounds + ia * 2 * D + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+        vb[c] = pb >= 0 ? load16(p.bounds + ib * 2 * D + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+    }
+    const float sa = pa >= 0 ? p.bounds_scale[ia] : 0.f;
+    const float sb = pb >= 0 ? p.bounds_scale[ib] : 0.f;
+    int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+        mma_16832_s8(acc, va[c].x, vb[c].x, va[c].y, vb[c].y, bq[c][0], bq[c][1]);
+        mma_16832_s8(acc, va[c].z, vb[c].z, va[c].w, vb[c].w, bq[c][2], bq[c][3]);
+    }
+    // Columns 2t and 2t + 1 are queries 2t and 2t + 1 of the group.
+    const float q0 = __shfl_sync(~0u, qs, 8 * t), q1 = __shfl_sync(~0u, qs, 8 * t + 4);
+    float best_a = -INFINITY, best_b = -INFINITY;
+    if (2 * t < p.group) {
+        best_a = (float)acc[0] * q0 * sa;
+        best_b = (float)acc[2] * q0 * sb;
+    }
+    if (2 * t + 1 < p.group) {
+        best_a = fmaxf(best_a, (float)acc[1] * q1 * sa);
+        best_b = fmaxf(best_b, (float)acc[3] * q1 * sb);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        best_a = fmaxf(best_a, __shfl_xor_sync(~0u, best_a, o));
+        best_b = fmaxf(best_b, __shfl_xor_sync(~0u, best_b, o));
+    }
+    uint32_t *keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
+    const float inf = INFINITY;
+    if (t == 0 && ja < n)
+        keys[ja] = ja < p.sink || ja >= n - p.recent ? kKeyKept : key_of(sa == inf ? inf : best_a);
+    if (t == 1 && jb < n)
+        keys[jb] = jb < p.sink || jb >= n - p.recent ? kKeyKept : key_of(sb == inf ? inf : best_b);
+}
+
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
+
+// Exclusive prefix of a pair of counts over the block's threads, and their
+// totals; the counts are packed as 16-bit halves of one word.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    if (lane == 31)
+        warp_sums[warp] = x;
+    __syncthreads();
+    uint32_t base = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kPickWarps; ++w) {
+        const uint32_t y = warp_sums[w];
+        base += w < warp ? y : 0;
+        total += y;
+    }
+    __syncthreads();
+    return base + x - v;
+}
+
+// The `most` largest keys of one (sequence, kv head), in ascending order of
+// the block's position; among equal keys the lowest positions.  A radix select
+// finds the smallest chosen key in four passes of 8 bits over the keys, and an
+// ordered scan writes the positions.
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p)
+{
+    __shared__ uint32_t hist[256], warp_sums[kPickWarps], found[2];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+    const int len = checked_len(p, s, false);
+    const int n = (len + p.block_size - 1) / p.block_size;
+    const int count = min(n, p.most);
+    int32_t *list = p.lists + ((int64_t)s * p.num_kv_heads + head) * p.most;
+    if (head == 0 && tid == 0)
+        p.list_lens[s] = count;
+    for (int i = count + tid; i < p.most; i += kPickThreads)
+        list[i] = -1;
+    if (n <= p.most) {
+        for (int i = tid; i < n; i += kPickThreads)
+            list[i] = i;
+        return;
+    }
+    const uint32_t *keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
+    uint32_t prefix = 0, need = p.most; // keys above the prefix's range are chosen
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kPickThreads)
+            hist[i] = 0;
+        __syncthreads();
+        const uint32_t above = shift == 24 ? 0 : ~0u << (shift + 8);
+        for (int i = tid; i < n; i += kPickThreads) {
+            const uint32_t k = keys[i];
+            if ((k & above) == prefix)
+                atomicAdd(&hist[k >> shift & 255], 1u);
+        }
+        __syncthreads();
+        if (tid < 32) { // digits from the top: lane l owns digits 255-8l .. 248-8l
+            uint32_t c[8], sum = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sum += c[k] = hist[255 - 8 * tid - k];
+            uint32_t x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(~0u, x, o);
+                if (tid >= o)
+                    x += y;
+            }
+            uint32_t before = x - sum;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (before < need && before + c[k] >= need) {
+                    found[0] = 255 - 8 * tid - k;
+                    found[1] = need - before;
+                }
+                before += c[k];
+            }
+        }
+        __syncthreads();
+        prefix |= found[0] << shift;
+        need = found[1];
+        __syncthreads();
+    }
+    // All keys above `prefix`, and the first `need` equal to it.
+    uint32_t above = 0, equal = 0;
+    for (int i0 = 0; i0 < n; i0 += kPickThreads) {
+        const int i = i0 + tid;
+        const uint32_t k = i < n ? keys[i] : 0;
+        const bool gt = i < n && k > prefix, eq = i < n && k == prefix;
+        uint32_t total;
+        const uint32_t x = block_scan((gt ? 1u : 0u) | (eq ? 1u << 16 : 0u), warp_sums, total);
+        const uint32_t a = above + (x & 0xFFFF), b = equal + (x >> 16);
+        if (gt || (eq && b < need))
+            list[a + min(b, need)] = i;
+        above += total & 0xFFFF;
+        equal += total >> 16;
+    }
+}
+
+static bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+static size_t key_stride(int max_seq_len, int block_size)
+{
+    return ((size_t)max_seq_len + block_size - 1) / block_size;
+}
+
+} // namespace block
+} // namespace pa
+
+using namespace pa;
+using namespace pa::block;
+
+extern "C" {
+
+size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int max_seq_len,
+                                       int block_size)
+{
+    if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || block_size <= 0)
+        return 0;
+    const size_t bytes = (size_t)num_seqs * num_kv_heads * key_stride(max_seq_len, block_size) * 4;
+    return (bytes + 256) / 256 * 256;
+}
+
+pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void *q,
+                           const int8_t *bounds, const float *bounds_scale,
+                           const int32_t *block_tables, const int32_t *seq_lens, int num_seqs,
+                           int num_heads, int num_kv_heads, int head_size, int block_size,
+                           int num_blocks, int max_blocks_per_seq, int max_selected,
+                           int num_sink_blocks, int num_recent_blocks, pa_dtype dtype,
+                           int max_seq_len, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_selected <= 0 ||
+        num_sink_blocks < 0 || num_recent_blocks < 0 || max_seq_len < 0 ||
+        (int64_t)num_sink_blocks + num_recent_blocks > max_selected ||
+        num_heads % num_kv_heads != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!block_lists || !list_lens || !q || !bounds || !bounds_scale ||
+                         !block_tables || !seq_lens))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(block_lists, 4) || !aligned(list_lens, 4) || !aligned(q, 16) ||
+        !aligned(bounds, 16) || !aligned(bounds_scale, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_heads / num_kv_heads;
+    if ((head_size != 64 && head_size != 128) || (block_size != 16 && block_size != 32) ||
+        (group != 1 && group != 2 && group != 4 && group != 8) ||
+        (dtype != PA_FP16 && dtype != PA_BF16))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_kv_heads > 65535 ||
+        (int64_t)num_blocks * block_size >= (int64_t)INT32_MAX ||
+        (int64_t)max_blocks_per_seq * block_size >= (int64_t)INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t len_cap = (int64_t)max_blocks_per_seq * block_size;
+    const int64_t cap = max_seq_len < len_cap ? max_seq_len : len_cap;
+    const int stride = (int)key_stride((int)cap, block_size);
+    const int64_t chunks = (stride + 16 * kScoreWarps - 1) / (16 * kScoreWarps);
+    if (chunks * num_kv_heads > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < pa_select_blocks_workspace_size(num_seqs, num_kv_heads, max_seq_len,
+                                                          block_size))
+        return PA_ERR_WORKSPACE;
+    cudaError_t e;
+    SelectParams p = {};
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.lists = block_lists;
+    p.list_lens = list_lens;
+    p.q = q;
+    p.bounds = bounds;
+    p.bounds_scale = bounds_scale;
+    p.tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.keys = static_cast<uint32_t *>(workspace);
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.block_size = block_size;
+    p.len_cap = (int)cap;
+    p.most = max_selected;
+    p.sink = num_sink_blocks;
+    p.recent = num_recent_blocks;
+    p.stride = stride;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (stride > max_selected) { // else every block of every sequence is chosen
+        const dim3 grid((unsigned)(chunks * num_kv_heads), num_seqs), threads(32 * kScoreWarps);
+        if (dtype == PA_BF16)
+            e = head_size == 128
+                    ? launch_after_previous(score_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, p)
+                    : launch_after_previous(score_kernel<__nv_bfloat16, 64>, grid, threads, 0, st, p);
+        else
+            e = head_size == 128
+                    ? launch_after_previous(score_kernel<__half, 128>, grid, threads, 0, st, p)
+                    : launch_after_previous(score_kernel<__half, 64>, grid, threads, 0, st, p);
+        if (e != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    e = launch_after_previous(pick_kernel, dim3(num_kv_heads, num_seqs), dim3(kPickThreads), 0, st,
+                              p);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+} // extern "C"

@@ -17,6 +17,11 @@
 
 namespace pa {
 
+// Device address of the current device's sticky error word, and its number of
+// SMs; NULL / 0 with *err set if the lookup fails (pa_api.cu).
+unsigned int *device_error_word(cudaError_t *err);
+int sm_count(cudaError_t *err);
+
 // Launch `kern` so that it may start while the previous kernel on the stream
 // is finishing (programmatic dependent launch); the kernel calls
 // griddep_wait() before it reads anything that kernel wrote.
