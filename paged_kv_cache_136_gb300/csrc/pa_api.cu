@@ -68,7 +68,7 @@ static inline void mark_after(cudaStream_t s)
         cudaEventRecord(t_mark_after, s);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn(cudaError_t *err)
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn(cudaError_t *err)
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;

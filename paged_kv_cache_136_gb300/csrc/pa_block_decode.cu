@@ -1,6 +1,9 @@
 // pa_block_decode.cu -- C entries of the decode over an e4m3 pool with block
 // scales and over listed blocks; compiled once per type of q
 // (PA_INST_DTYPE: 0 fp16 with the entries, 1 bf16).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "pa.h"
@@ -9,16 +12,30 @@
 namespace pa {
 namespace block {
 
-cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas,
                                     cudaStream_t s);
-cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas,
                                      cudaStream_t s);
 
 template <typename T, bool E4M3, int D>
-static cudaError_t launch(const DecodeArgs &p, int ctas, cudaStream_t s)
+static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
 {
-    const cudaError_t e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas),
-                                                dim3(32 * kWarps), 0, s, p);
+    constexpr int smem = decode_smem<E4M3, D>();
+    // once a device: a CTA of this kernel takes most of an SM's shared memory
+    static bool ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !ready[dev & 63]) {
+        e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        ready[dev & 63] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return e;
+    e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas), dim3(32 * kWarps), smem,
+                              s, map, p);
     if (e != cudaSuccess)
         return e;
     return launch_after_previous(block_merge_kernel<T, E4M3, D>,
@@ -26,20 +43,22 @@ static cudaError_t launch(const DecodeArgs &p, int ctas, cudaStream_t s)
 }
 
 #if PA_INST_DTYPE == 1
-cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas,
                                      cudaStream_t s)
 {
     if (head_size == 128)
-        return e4m3 ? launch<__nv_bfloat16, true, 128>(p, ctas, s) : launch<__nv_bfloat16, false, 128>(p, ctas, s);
-    return e4m3 ? launch<__nv_bfloat16, true, 64>(p, ctas, s) : launch<__nv_bfloat16, false, 64>(p, ctas, s);
+        return e4m3 ? launch<__nv_bfloat16, true, 128>(map, p, ctas, s) : launch<__nv_bfloat16, false, 128>(map, p, ctas, s);
+    return e4m3 ? launch<__nv_bfloat16, true, 64>(map, p, ctas, s) : launch<__nv_bfloat16, false, 64>(map, p, ctas, s);
 }
 #else
-cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const DecodeArgs &p, int ctas,
+cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas,
                                     cudaStream_t s)
 {
     if (head_size == 128)
-        return e4m3 ? launch<__half, true, 128>(p, ctas, s) : launch<__half, false, 128>(p, ctas, s);
-    return e4m3 ? launch<__half, true, 64>(p, ctas, s) : launch<__half, false, 64>(p, ctas, s);
+        return e4m3 ? launch<__half, true, 128>(map, p, ctas, s) : launch<__half, false, 128>(map, p, ctas, s);
+    return e4m3 ? launch<__half, true, 64>(map, p, ctas, s) : launch<__half, false, 64>(map, p, ctas, s);
 }
 
 static bool aligned(const void *p, uintptr_t a)
@@ -48,6 +67,43 @@ static bool aligned(const void *p, uintptr_t a)
 }
 
 static size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// The pool as TMA sees it: 128-byte columns (64-byte ones for e4m3 rows of 64),
+// token rows, columns of a head's row, heads, planes.  A box is both planes of
+// a 16-row tile of one head, swizzled.  Rows past the pool read as zeros.
+static bool make_map(CUtensorMap *map, const void *pool, bool e4m3, int dtype, int num_blocks,
+                     int block_size, int num_kv_heads, int head_size)
+{
+    cudaError_t err;
+    auto fn = encode_fn(&err);
+    if (!fn)
+        return false;
+    const cuuint64_t es = e4m3 ? 1 : 2, row = head_size * es, rows = (cuuint64_t)num_blocks * block_size;
+    const cuuint64_t wide = row > 128 ? 128 : row, all = row * num_kv_heads;
+    const CUtensorMapDataType type = e4m3               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle swizzle =
+        wide == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    CUresult r;
+    if (row > 128) {
+        const cuuint64_t dims[5] = {wide / es, rows, row / wide, (cuuint64_t)num_kv_heads, 2};
+        const cuuint64_t strides[4] = {all, wide, row, rows * all};
+        const cuuint32_t box[5] = {(cuuint32_t)(wide / es), kTile, (cuuint32_t)(row / wide), 1, 2};
+        r = fn(map, type, 5, const_cast<void *>(pool), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        const cuuint64_t dims[4] = {wide / es, rows, (cuuint64_t)num_kv_heads, 2};
+        const cuuint64_t strides[3] = {all, row, rows * all};
+        const cuuint32_t box[4] = {(cuuint32_t)(wide / es), kTile, 1, 2};
+        r = fn(map, type, 4, const_cast<void *>(pool), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return r == CUDA_SUCCESS;
+}
 
 // kv heads of a CTA: the largest of 8, 4, 2, 1 that divides them.
 static int heads_log2(int num_kv_heads)
@@ -124,7 +180,6 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.out = out;
     p.lse = lse;
     p.q = q;
-    p.pool = static_cast<const char *>(kv_cache);
     p.scales = kv_scales;
     p.tables = tables;
     p.seq_lens = seq_lens;
@@ -133,7 +188,6 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.cuts = reinterpret_cast<int4 *>(ws);
     p.ws_ml = reinterpret_cast<float *>(ws + w.ml);
     p.ws_o = reinterpret_cast<float *>(ws + w.o);
-    p.plane = (int64_t)num_blocks * block_size * num_kv_heads * head_size * (kv_scales ? 1 : 2);
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
@@ -148,14 +202,19 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.qscale = scale * 1.4426950408889634f;
     // At least kMinRun tiles a warp: no more CTAs than that can use.
     int64_t ctas = tiles / (kMinRun * (kWarps >> hl)) + 1;
-    if (ctas > 2 * sms)
-        ctas = 2 * sms;
+    const int per_sm = head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2;
+    if (ctas > per_sm * sms)
+        ctas = per_sm * sms;
     if (ctas > kMaxCtas)
         ctas = kMaxCtas;
+    alignas(64) CUtensorMap map;
+    if (!make_map(&map, kv_cache, kv_scales != nullptr, dtype, num_blocks, block_size,
+                  num_kv_heads, head_size))
+        return PA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     e = dtype == PA_BF16
-            ? launch_block_decode_bf16(kv_scales != nullptr, head_size, p, (int)ctas, st)
-            : launch_block_decode_f16(kv_scales != nullptr, head_size, p, (int)ctas, st);
+            ? launch_block_decode_bf16(kv_scales != nullptr, head_size, map, p, (int)ctas, st)
+            : launch_block_decode_f16(kv_scales != nullptr, head_size, map, p, (int)ctas, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 #endif

@@ -9,12 +9,16 @@
 // O^T += V^T P (D x 8) with m16n8k16 products, and keeps the running maximum
 // and normaliser of the softmax in fp32.
 //
-// The operands are loaded straight into the registers of the products.  The
+// A tile comes by one TMA copy (both planes of 16 rows) into the warp's own
+// ring, and from there straight into the registers of the products.  The
 // contraction index of a product is any permutation of the channels (S) or of
 // the tokens (O) as long as both operands use the same one, and the rows of
 // O^T are any permutation of the channels, so every lane takes 16-byte pieces:
-//   K  lane 4g + t: rows g and g + 8, bytes 16t + 64c of the row;
-//   V  lane 4g + t: rows 2t, 2t+1, 2t+8, 2t+9, bytes 16g (+ 128 c) of the row.
+//   K  lane 4g + t: rows token(g) and token(g) + 8, bytes 16t + 64c of the row;
+//   V  lane 4g + t: rows token(2t), token(2t+1) and those + 8, bytes 16g of
+//      each 128.
+// With token(k) = k for even k, (k + 4) mod 8 for odd k, the eight lanes that
+// read at once meet eight different 16-byte columns of the 128-byte swizzle.
 // e4m3 codes become halves (exactly) in registers.
 //
 // Work.  The (sequence, group of HG kv heads, 16-token tile) triples are laid
@@ -30,6 +34,7 @@
 // absolute precision.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -46,13 +51,12 @@ namespace block {
 constexpr int kWarps = 8;      // warps of a CTA
 constexpr int kMaxCtas = 304;  // CTAs of a launch, at most (workspace size)
 constexpr int kTile = 16;      // tokens a warp takes at a time
-constexpr int kMinRun = 8;     // tiles a warp takes at least before work is cut
+constexpr int kMinRun = 4;     // tiles a warp takes at least before work is cut
 
 struct DecodeArgs {
     void *out;                 // [B, H, D]
     float *lse;                // [B, H] or NULL
     const void *q;             // [B, H, D]
-    const char *pool;          // [2, NB, bs, Hkv, D]
     const float *scales;       // [2, NB, Hkv] (e4m3 pool)
     const int32_t *tables;     // [B, MB]
     const int32_t *seq_lens;   // [B]
@@ -62,7 +66,6 @@ struct DecodeArgs {
     int4 *cuts;                // [CTAs] {sequence, head group, CTAs sharing it, -}
     float *ws_o;               // [CTAs, 2, HG * G, D]
     float *ws_ml;              // [CTAs, 2, HG * G, 2]
-    int64_t plane;             // bytes of a plane
     int num_seqs, num_heads, num_kv_heads, group, heads_log2, num_groups, num_blocks, max_blocks,
         block_log2, max_listed, len_cap;
     float qscale;              // scale * log2 e
@@ -98,46 +101,37 @@ __device__ __forceinline__ int length_of(const DecodeArgs &p, int s, bool report
 }
 
 // Where a tile's 16 tokens are: the first pool row, or -1 for a block outside
-// the pool (read as zeros); how many of them count.
-struct Tile {
-    int64_t row;
-    int block, live;
-};
-
-// `listed`: entries of the sequence's lists.
-__device__ __forceinline__ Tile locate(const DecodeArgs &p, int s, int head, int tile, int len,
-                                       int listed)
+// the pool (read as zeros); how many of them count.  `listed`: entries of the
+// sequence's lists.
+__device__ __forceinline__ void locate(const DecodeArgs &p, int s, int head, int tile, int len,
+                                       int listed, int &row, int &live)
 {
     const int per = p.block_log2 - 4;
     int j = tile >> per;
     const int sub = tile & ((1 << per) - 1);
-    Tile r = {-1, -1, 0};
     const int blocks = (len + (1 << p.block_log2) - 1) >> p.block_log2;
+    row = -1;
+    live = 0;
     if (p.lists) {
-        const int i = j;
-        if (i >= listed)
-            return r;
-        j = p.lists[((int64_t)s * p.num_kv_heads + head) * p.max_listed + i];
+        if (j >= listed)
+            return;
+        j = __ldg(p.lists + ((int64_t)s * p.num_kv_heads + head) * p.max_listed + j);
         if (j < 0)
-            return r; // padding
+            return; // padding
         if (j >= blocks) {
             atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
-            return r;
+            return;
         }
     }
-    r.live = min(kTile, len - (j << p.block_log2) - sub * kTile);
-    if (j >= blocks || r.live <= 0) {
-        r.live = 0;
-        return r;
-    }
-    const int blk = p.tables[(int64_t)s * p.max_blocks + j];
+    live = j >= blocks ? 0 : max(0, min(kTile, len - (j << p.block_log2) - sub * kTile));
+    if (live == 0)
+        return;
+    const int blk = __ldg(p.tables + (int64_t)s * p.max_blocks + j);
     if (blk < 0 || blk >= p.num_blocks) {
         atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
-        return r;
+        return;
     }
-    r.block = blk;
-    r.row = ((int64_t)blk << p.block_log2) + sub * kTile;
-    return r;
+    row = (blk << p.block_log2) + sub * kTile;
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -147,9 +141,64 @@ constexpr float kLn2 = 0.6931471805599453f;
 // it; bf16 has fp32's range and needs none.
 template <typename M> constexpr float lift_of() { return std::is_same<M, __half>::value ? 15.f : 0.f; }
 
+// Tiles of up to 4 KB: two CTAs an SM, 12 KB of tiles in flight a warp.  Tiles
+// of 8 KB: one CTA, 24 KB a warp.
+template <bool E4M3, int D> constexpr int tile_bytes() { return 2 * kTile * D * (E4M3 ? 1 : 2); }
+template <bool E4M3, int D> constexpr int ctas_per_sm() { return tile_bytes<E4M3, D>() > 4096 ? 1 : 2; }
+template <bool E4M3, int D> constexpr int stages_of()
+{
+    return 24576 / ctas_per_sm<E4M3, D>() / tile_bytes<E4M3, D>();
+}
+
+// One tile of a warp's ring: whose it is, and its scales.
+struct Meta {
+    int live, seq, head, flags; // tokens that count; whose; kLast.. bits
+    float k_scale, v_scale;
+    uint64_t bar;               // completes when the tile has landed
+};
+constexpr int kLast = 1;   // the warp's last tile of its part of a (sequence, group)
+constexpr int kBegins = 2; // that part begins the (sequence, group)
+constexpr int kEnds = 4;   // ... and ends it
+
+// Shared memory of a CTA: the rings (aligned to 1024), their Metas, and half of
+// the states that a head's upper warps hand to its lower ones.
+template <bool E4M3, int D> constexpr int decode_smem()
+{
+    return 1024 + kWarps * stages_of<E4M3, D>() * (tile_bytes<E4M3, D>() + (int)sizeof(Meta)) +
+           kWarps / 2 * 4 * (D + 2) * 4;
+}
+
+__device__ __forceinline__ void tma_load_5d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                                 int c0, int c1, int c2, int c3, int c4,
+                                                 uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+        "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The running maximum starts here: finite, so that differences of maxima are
+// never NaN, and below no score but -inf.
+constexpr float kNone = -3.402823466e38f;
+
 // T: type of q and out (and of a 16-bit pool).  E4M3: pool of e4m3 codes.
+//
+// A warp fetches for itself, kStages tiles ahead: the lane that looked a tile
+// up issues its copy, so nothing is handed from warp to warp before a part's
+// end.
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeArgs p)
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
+    block_decode_kernel(const __grid_constant__ CUtensorMap pool_map, const DecodeArgs p)
 {
     using M = typename std::conditional<E4M3, __half, T>::type; // type of the products
     // P is split into a 16-bit high part and the rounded remainder where one
@@ -161,14 +210,28 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
     constexpr int kKPieces = kRow / 64;          // 16-byte pieces of a lane and row of K
     constexpr int kVWords = kRow / 32;           // words of a lane and row of V
     constexpr int kSteps = D / 16;               // products along D
-    __shared__ int first_seq, first_base, total_tiles, warp_sums[kWarps];
-    __shared__ float merge[kWarps][8][D + 2];
+    constexpr int kStages = stages_of<E4M3, D>();
+    constexpr int kTileBytes = tile_bytes<E4M3, D>();
+    extern __shared__ char smem_raw[];
+    __shared__ int first_seq, first_base, warp_sums[kWarps];
 
-    griddep_wait();
-    griddep_launch_dependents();
+    char *const smem = smem_raw + (-smem_addr(smem_raw) & 1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int heads = 1 << p.heads_log2;         // kv heads of the CTA
     const int hl = warp & (heads - 1), tw = warp >> p.heads_log2, tws = kWarps >> p.heads_log2;
+    char *const ring = smem + warp * kStages * kTileBytes;
+    Meta *const meta = reinterpret_cast<Meta *>(smem + kWarps * kStages * kTileBytes) +
+                       warp * kStages;
+    float *const handed = reinterpret_cast<float *>(smem + kWarps * kStages *
+                                                    (kTileBytes + (int)sizeof(Meta)));
+    if (lane < kStages)
+        mbar_init(&meta[lane].bar, 1);
+    fence_barrier_init();
+    if (tid == 0)
+        prefetch_tensormap(&pool_map);
+    __syncwarp();
+    griddep_wait();
+    griddep_launch_dependents();
 
     // ---- this CTA's run: [begin, end) of the line of tiles ----
     const int slice = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
@@ -213,25 +276,165 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
         first_base = base;
     }
     __syncthreads();
-    int s = first_seq, at = begin, seg = first_base;
-    int tiles = tiles_of(p, s, false);
-    int grp = (at - seg) / tiles;
-    seg += grp * tiles;
 
-    while (at < end) { // one (sequence, head group) after another
-        const int seg_end = seg + tiles, stop = min(end, seg_end);
-        const int head = (grp << p.heads_log2) + hl;
-        const int len = length_of(p, s, lane == 0 && warp == 0);
-        const int listed = p.lists ? min(p.list_lens[s], p.max_listed) : 0;
+    // ---- the walk that fetches: one part of a (sequence, group) after the
+    // other, in batches of 32 tiles whose places the lanes look up at once ----
+    int f_at = begin, f_seq = first_seq, f_tiles = tiles_of(p, f_seq, false);
+    int f_grp = (begin - first_base) / f_tiles, f_seg = first_base + f_grp * f_tiles;
+    int f_len = 0, f_listed = 0, f_next = 0, f_left = 0, f_flags = 0; // of the part
+    // the batch being fetched, and the one behind it
+    int b_row = 0, b_live = 0, b_n = 0, b_i = 0, b_seq = 0, b_head = 0, b_flags = 0, b_last = 0;
+    int n_row = 0, n_live = 0, n_n = 0, n_seq = 0, n_head = 0, n_flags = 0, n_last = 0;
+    float b_ks = 1.f, b_vs = 1.f, n_ks = 1.f, n_vs = 1.f;
 
-        // Query rows of the group, as the products take them; for e4m3 in
-        // halves, scaled by a power of two so that the largest is near 2^15
-        // (bf16 values keep their 8 bits over 29 binades below it).
-        uint32_t qf[kSteps][2];
-        float qmul0 = p.qscale, qmul1 = p.qscale;
-        {
+    auto look_up = [&]() { // fills the batch behind
+        n_n = 0;
+        if (f_left == 0) {
+            if (f_at >= end)
+                return;
+            const int seg_end = f_seg + f_tiles, stop = min(end, seg_end);
+            f_flags = (f_at == f_seg ? kBegins : 0) | (stop == seg_end ? kEnds : 0);
+            f_len = length_of(p, f_seq, lane == 0 && warp == 0);
+            f_listed = p.lists ? min(__ldg(p.list_lens + f_seq), p.max_listed) : 0;
+            f_next = f_at - f_seg + tw;
+            // a warp without a tile takes an empty one: all meet at the part's end
+            f_left = max(1, (stop - f_at - tw + tws - 1) / tws);
+            if (stop - f_at <= tw)
+                f_next = -1;
+            if (tid == 0 && f_flags == kBegins)
+                p.cuts[blockIdx.x] =
+                    make_int4(f_seq, f_grp, (seg_end - 1) / run - (int)blockIdx.x + 1, 0);
+            n_seq = f_seq;
+            n_head = (f_grp << p.heads_log2) + hl;
+            f_at = stop;
+        }
+        n_flags = f_flags;
+        n_n = min(32, f_left);
+        f_left -= n_n;
+        n_last = f_left == 0;
+        n_row = -1;
+        n_live = 0;
+        if (lane < n_n && f_next >= 0)
+            locate(p, n_seq, n_head, f_next + lane * tws, f_len, f_listed, n_row, n_live);
+        if constexpr (E4M3) {
+            n_ks = n_vs = 1.f;
+            if (n_row >= 0) {
+                const float *sc = p.scales + (int64_t)(n_row >> p.block_log2) * p.num_kv_heads +
+                                  n_head;
+                n_ks = __ldg(sc);
+                n_vs = __ldg(sc + (int64_t)p.num_blocks * p.num_kv_heads);
+            }
+        }
+        f_next += 32 * tws;
+        if (n_last) {
+            if (f_at == f_seg + f_tiles) {
+                f_seg = f_at;
+                if (++f_grp == p.num_groups) {
+                    f_grp = 0;
+                    if (++f_seq < p.num_seqs)
+                        f_tiles = tiles_of(p, f_seq, false);
+                }
+            }
+        }
+    };
+
+    const uint64_t policy = policy_evict_first();
+    bool lost = false;
+    auto fetch = [&](int stage) { // the next tile, or the end, into `stage`
+        if (b_i == b_n) {
+            b_row = n_row, b_live = n_live, b_n = n_n, b_seq = n_seq, b_head = n_head;
+            b_flags = n_flags, b_last = n_last, b_ks = n_ks, b_vs = n_vs;
+            b_i = 0;
+            if (b_n > 0)
+                look_up();
+        }
+        Meta &m = meta[stage];
+        if (b_i < b_n) {
+            if (lane == b_i) {
+                *reinterpret_cast<int4 *>(&m) =
+                    make_int4(b_live, b_seq, b_head,
+                              b_flags | (b_last && b_i + 1 == b_n ? kLast : 0));
+                if (lost) {
+                } else if (b_live) {
+                    // a row past the pool reads as zeros
+                    const int row = b_row < 0 ? p.num_blocks << p.block_log2 : b_row;
+                    mbar_arrive_expect_tx(&m.bar, kTileBytes);
+                    if constexpr (kRow == 256)
+                        tma_load_5d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row, 0,
+                                         b_head, 0, policy);
+                    else
+                        tma_load_4d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row,
+                                         b_head, 0, policy);
+                    if constexpr (E4M3)
+                        *reinterpret_cast<float2 *>(&m.k_scale) = make_float2(b_ks, b_vs);
+                } else {
+                    mbar_arrive(&m.bar);
+                }
+            }
+            ++b_i;
+        } else if (lane == 0) {
+            m.flags = -1;
+            if (!lost)
+                mbar_arrive(&m.bar);
+        }
+    };
+
+    look_up();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(i);
+
+    // lane constants: token(g), and where the lane's pieces lie in a tile
+    const int token = g & 1 ? (g + 4) & 7 : g;
+    const int tok0 = 2 * t, tok1 = (2 * t + 5) & 7;
+    const int k_at = kRow == 64 ? token * 64 + ((t ^ (token >> 1 & 3)) << 4)
+                                : token * 128 + ((t ^ token) << 4);
+    const int v_at0 = kRow == 64
+                          ? tok0 * 64 + ((g >> 1 ^ (tok0 >> 1 & 3)) << 4) + (g & 1) * 8
+                          : tok0 * 128 + ((g ^ tok0) << 4);
+    const int v_at1 = kRow == 64
+                          ? tok1 * 64 + ((g >> 1 ^ (tok1 >> 1 & 3)) << 4) + (g & 1) * 8
+                          : tok1 * 128 + ((g ^ tok1) << 4);
+    constexpr int kEight = 8 * (kRow == 64 ? 64 : 128); // eight rows further
+    constexpr int kHalf = 16 * 128;                     // the row's second 128 bytes
+    uint32_t qf[kSteps][2];
+    float qmul0 = 0.f, qmul1 = 0.f;
+    float o[kSteps][4];
+    float m0 = kNone, m1 = kNone, l0 = 0.f, l1 = 0.f;
+    bool fresh = true;
+    int stage = 0, drain = 0;
+    uint32_t parity = 0;
+    while (true) {
+        // A copy that does not arrive is reported; the warp then starts no
+        // more, waits (within the limit) for those in flight, and walks on
+        // without data, so that it still meets the others.
+        if (!lost || drain > 0) {
+            const bool here = __all_sync(~0u, mbar_wait(&meta[stage].bar, parity));
+            if (lost) {
+                --drain;
+            } else if (!here) {
+                lost = true;
+                drain = kStages - 1;
+                if (lane == 0)
+                    atomicOr(p.err, PA_DEVERR_TIMEOUT_);
+            }
+        }
+        __syncwarp();
+        const int4 info = *reinterpret_cast<const int4 *>(&meta[stage]);
+        const int live = lost ? 0 : info.x, s = info.y, head = info.z, flags = info.w;
+        if (flags < 0)
+            break;
+        // every lane has left the stage before this one: refill it
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+
+        if (fresh) { // a part begins
+            fresh = false;
+            // Query rows of the group, as the products take them; for e4m3 in
+            // halves, scaled by a power of two so that the largest is near 2^15
+            // (bf16 values keep their 8 bits over 29 binades below it).
             const T *q = static_cast<const T *>(p.q) +
                          ((int64_t)s * p.num_heads + head * p.group + min(g, p.group - 1)) * D;
+            qmul0 = qmul1 = p.qscale;
             uint2 raw[kSteps];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
@@ -267,85 +470,53 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
                 for (int i = 0; i < kSteps; ++i)
                     qf[i][0] = raw[i].x, qf[i][1] = raw[i].y;
             }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[i][k] = 0.f;
+            m0 = m1 = kNone;
+            l0 = l1 = 0.f;
         }
 
-        float o[kSteps][4];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[i][k] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-        for (int tile = at - seg + tw; tile < stop - seg; tile += tws) {
-            const Tile where = locate(p, s, head, tile, len, listed);
-            if (where.live == 0)
-                continue;
+        if (live) {
+            const char *const slot = ring + stage * kTileBytes;
             float ks = 1.f, vs = 1.f;
-            uint4 kr[2][kKPieces];
-            uint32_t vr[4][kVWords];
-#pragma unroll
-            for (int i = 0; i < kKPieces; ++i)
-                kr[0][i] = kr[1][i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < kVWords; ++k)
-                    vr[i][k] = 0;
-            if (where.block >= 0) {
-                const int64_t stride = (int64_t)p.num_kv_heads * kRow;
-                const char *src = p.pool + where.row * stride + head * kRow;
-#pragma unroll
-                for (int i = 0; i < kKPieces; ++i) {
-                    kr[0][i] = load16(src + g * stride + i * 64 + t * 16);
-                    kr[1][i] = load16(src + (g + 8) * stride + i * 64 + t * 16);
-                }
-                src += p.plane;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 2 * t + (i & 1) + (i >> 1) * 8;
-                    if constexpr (kRow == 64) {
-                        const uint2 v = load8(src + row * stride + g * 8);
-                        vr[i][0] = v.x, vr[i][1] = v.y;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < kVWords; k += 4) {
-                            const uint4 v = load16(src + row * stride + k * 32 + g * 16);
-                            vr[i][k] = v.x, vr[i][k + 1] = v.y, vr[i][k + 2] = v.z,
-                            vr[i][k + 3] = v.w;
-                        }
-                    }
-                    if (row >= where.live) // what lies there may be NaN
-#pragma unroll
-                        for (int k = 0; k < kVWords; ++k)
-                            vr[i][k] = 0;
-                }
-                if constexpr (E4M3) {
-                    const int64_t sc = (int64_t)where.block * p.num_kv_heads + head;
-                    ks = p.scales[sc];
-                    vs = p.scales[sc + (int64_t)p.num_blocks * p.num_kv_heads];
-                }
+            if constexpr (E4M3) {
+                const float2 sc = *reinterpret_cast<const float2 *>(&meta[stage].k_scale);
+                ks = sc.x;
+                vs = sc.y;
             }
-
-            // S^T: rows are tokens g and g + 8, columns queries 2t and 2t + 1
+            // S^T: rows are token(g) and token(g) + 8, columns queries 2t and 2t + 1
             float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                if constexpr (E4M3) {
-                    const uint32_t a = (&kr[0][i / 4].x)[i % 4], b = (&kr[1][i / 4].x)[i % 4];
-                    mma_16816<M>(c, half2_of_e4m3x2(a), half2_of_e4m3x2(b), half2_of_e4m3x2_hi(a),
-                                 half2_of_e4m3x2_hi(b), qf[i][0], qf[i][1]);
-                } else {
-                    const uint32_t *a = &kr[0][i / 2].x + i % 2 * 2, *b = &kr[1][i / 2].x + i % 2 * 2;
-                    mma_16816<M>(c, a[0], b[0], a[1], b[1], qf[i][0], qf[i][1]);
+            for (int j = 0; j < kKPieces; ++j) {
+                const char *const k = slot + (j >> 1) * kHalf + (k_at ^ (j & 1) * 64);
+                const uint4 ka = *reinterpret_cast<const uint4 *>(k);
+                const uint4 kb = *reinterpret_cast<const uint4 *>(k + kEight);
+#pragma unroll
+                for (int i = 0; i < (E4M3 ? 4 : 2); ++i) {
+                    if constexpr (E4M3) {
+                        const uint32_t a = (&ka.x)[i], b = (&kb.x)[i];
+                        mma_16816<M>(c, half2_of_e4m3x2(a), half2_of_e4m3x2(b),
+                                     half2_of_e4m3x2_hi(a), half2_of_e4m3x2_hi(b),
+                                     qf[4 * j + i][0], qf[4 * j + i][1]);
+                    } else {
+                        mma_16816<M>(c, (&ka.x)[2 * i], (&kb.x)[2 * i], (&ka.x)[2 * i + 1],
+                                     (&kb.x)[2 * i + 1], qf[2 * j + i][0], qf[2 * j + i][1]);
+                    }
                 }
             }
             const float f0 = E4M3 ? qmul0 * ks : qmul0, f1 = E4M3 ? qmul1 * ks : qmul1;
-            const bool live0 = g < where.live, live1 = g + 8 < where.live;
-            c[0] = live0 ? c[0] * f0 : -INFINITY;
-            c[1] = live0 ? c[1] * f1 : -INFINITY;
-            c[2] = live1 ? c[2] * f0 : -INFINITY;
-            c[3] = live1 ? c[3] * f1 : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                c[k] *= k & 1 ? f1 : f0;
+            if (live < kTile) {
+                if (token >= live)
+                    c[0] = c[1] = -INFINITY;
+                if (token + 8 >= live)
+                    c[2] = c[3] = -INFINITY;
+            }
 
             // running maximum of score + log2(value scale), over the 16 tokens
             float n0 = fmaxf(c[0], c[2]), n1 = fmaxf(c[1], c[3]);
@@ -355,15 +526,14 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
                 n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, off));
             }
             if constexpr (E4M3) {
-                const float lift = __log2f(vs);
+                const float lift = lg2(vs);
                 n0 += lift;
                 n1 += lift;
             }
             n0 = fmaxf(m0, n0);
             n1 = fmaxf(m1, n1);
-            float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
             if (__any_sync(~0u, n0 != m0 || n1 != m1)) {
-                const float a0 = ex2(m0 - r0), a1 = ex2(m1 - r1);
+                const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);
                 l0 *= a0;
                 l1 *= a1;
 #pragma unroll
@@ -376,8 +546,7 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
                 m0 = n0;
                 m1 = n1;
             }
-            r0 -= kLift;
-            r1 -= kLift;
+            const float r0 = m0 - kLift, r1 = m1 - kLift;
             c[0] = ex2(c[0] - r0);
             c[1] = ex2(c[1] - r1);
             c[2] = ex2(c[2] - r0);
@@ -400,6 +569,30 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
             }
 
             // O^T: rows are channels 2i and 2i + 1 of each lane's list
+            uint32_t vr[4][kVWords];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const char *const v =
+                    slot + kTileBytes / 2 + (i & 1 ? v_at1 : v_at0) + (i >> 1) * kEight;
+                if constexpr (kRow == 64) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(v);
+                    vr[i][0] = w.x, vr[i][1] = w.y;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kVWords; k += 4) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(v + (k >> 2) * kHalf);
+                        vr[i][k] = w.x, vr[i][k + 1] = w.y, vr[i][k + 2] = w.z, vr[i][k + 3] = w.w;
+                    }
+                }
+            }
+            if (live < kTile) { // what lies behind the last token may be NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((i & 1 ? tok1 : tok0) + (i >> 1) * 8 >= live)
+#pragma unroll
+                        for (int k = 0; k < kVWords; ++k)
+                            vr[i][k] = 0;
+            }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 uint32_t a0, a1, a2, a3;
@@ -422,109 +615,91 @@ __global__ void __launch_bounds__(32 * kWarps) block_decode_kernel(const DecodeA
                     mma_16816<M>(o[i], a0, a1, a2, a3, lo[0], lo[1]);
             }
         }
+        if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+        }
+
+        if (!(flags & kLast))
+            continue;
+        fresh = true;
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l0 += __shfl_xor_sync(~0u, l0, off);
             l1 += __shfl_xor_sync(~0u, l1, off);
         }
 
-        // Join the warps that shared the head's tiles.
-        if (tws > 1) {
-            __syncthreads();
-            float *const dst0 = merge[warp][2 * t], *const dst1 = merge[warp][2 * t + 1];
+        // Join the warps that shared the head's tiles: half of the warps at a
+        // time, and of their queries the even ones, then the odd ones.
+        for (int half = tws >> 1; half; half >>= 1) {
+            float *const box =
+                handed + ((((tw & (half - 1)) << p.heads_log2) + hl) * 4 + t) * (D + 2);
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                dst0[g * (D / 8) + 2 * i] = o[i][0];
-                dst1[g * (D / 8) + 2 * i] = o[i][1];
-                dst0[g * (D / 8) + 2 * i + 1] = o[i][2];
-                dst1[g * (D / 8) + 2 * i + 1] = o[i][3];
-            }
-            if (g == 0) {
-                dst0[D] = m0, dst0[D + 1] = l0;
-                dst1[D] = m1, dst1[D + 1] = l1;
-            }
-            __syncthreads();
-            if (tw == 0) {
-                float w0 = m0, w1 = m1;
-                for (int k = 1; k < tws; ++k) {
-                    w0 = fmaxf(w0, merge[hl + (k << p.heads_log2)][2 * t][D]);
-                    w1 = fmaxf(w1, merge[hl + (k << p.heads_log2)][2 * t + 1][D]);
+            for (int k = 0; k < 2; ++k) {
+                float &m = k ? m1 : m0, &l = k ? l1 : l0;
+                if (tw >= half && tw < 2 * half) {
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i)
+                        *reinterpret_cast<float2 *>(box + g * (D / 8) + 2 * i) =
+                            make_float2(o[i][k], o[i][k + 2]);
+                    if (g == 0)
+                        *reinterpret_cast<float2 *>(box + D) = make_float2(m, l);
                 }
-                const float r0 = w0 == -INFINITY ? 0.f : w0, r1 = w1 == -INFINITY ? 0.f : w1;
-                float a0 = ex2(m0 - r0), a1 = ex2(m1 - r1);
-                l0 *= a0;
-                l1 *= a1;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    o[i][0] *= a0, o[i][1] *= a1, o[i][2] *= a0, o[i][3] *= a1;
-                for (int k = 1; k < tws; ++k) {
-                    const float *src0 = merge[hl + (k << p.heads_log2)][2 * t];
-                    const float *src1 = merge[hl + (k << p.heads_log2)][2 * t + 1];
-                    a0 = ex2(src0[D] - r0);
-                    a1 = ex2(src1[D] - r1);
-                    l0 += a0 * src0[D + 1];
-                    l1 += a1 * src1[D + 1];
+                __syncthreads();
+                if (tw < half) {
+                    const float2 other = *reinterpret_cast<float2 *>(box + D);
+                    const float top = fmaxf(m, other.x);
+                    const float a = ex2(m - top), b = ex2(other.x - top);
+                    l = l * a + b * other.y;
+                    m = top;
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
-                        o[i][0] += a0 * src0[g * (D / 8) + 2 * i];
-                        o[i][1] += a1 * src1[g * (D / 8) + 2 * i];
-                        o[i][2] += a0 * src0[g * (D / 8) + 2 * i + 1];
-                        o[i][3] += a1 * src1[g * (D / 8) + 2 * i + 1];
+                        const float2 y = *reinterpret_cast<float2 *>(box + g * (D / 8) + 2 * i);
+                        o[i][k] = o[i][k] * a + b * y.x;
+                        o[i][k + 2] = o[i][k + 2] * a + b * y.y;
                     }
                 }
-                m0 = w0;
-                m1 = w1;
+                __syncthreads();
             }
         }
+        if (tw != 0)
+            continue;
 
         // A whole (sequence, group) is finished here; a cut one leaves its
         // state: slot 1 of the CTA that began it, slot 0 of the others.
-        const bool whole = at == seg && stop == seg_end;
-        const int slot = at == seg ? 1 : 0;
-        if (tid == 0 && at == seg && !whole)
-            p.cuts[blockIdx.x] = make_int4(s, grp, (seg_end - 1) / run - (int)blockIdx.x + 1, 0);
-        if (tw == 0) {
+        const bool whole = (flags & (kBegins | kEnds)) == (kBegins | kEnds);
+        const int slot = flags & kBegins ? 1 : 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int col = 2 * t + k;
-                if (col >= p.group)
-                    continue;
-                const float l = k ? l1 : l0, m = k ? m1 : m0;
-                if (whole) {
-                    const int64_t row = (int64_t)s * p.num_heads + head * p.group + col;
-                    const float inv = l != 0.f ? 1.f / l : 0.f;
-                    T *dst = static_cast<T *>(p.out) + row * D;
+        for (int k = 0; k < 2; ++k) {
+            const int col = 2 * t + k;
+            if (col >= p.group)
+                continue;
+            const float l = k ? l1 : l0, m = k ? m1 : m0;
+            if (whole) {
+                const int64_t row = (int64_t)s * p.num_heads + head * p.group + col;
+                const float inv = l != 0.f ? 1.f / l : 0.f;
+                T *dst = static_cast<T *>(p.out) + row * D;
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int d = E4M3 || D == 64 ? g * (D / 8) + 2 * i
-                                                      : (i / 4) * 64 + g * 8 + (i % 4) * 2;
-                        *reinterpret_cast<uint32_t *>(dst + d) =
-                            pair_of<T>(o[i][k] * inv, o[i][k + 2] * inv);
-                    }
-                    if (p.lse && g == 0)
-                        p.lse[row] = l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
-                } else {
-                    const int64_t row = ((int64_t)(2 * blockIdx.x + slot) << p.heads_log2) * p.group +
-                                        hl * p.group + col;
-                    float *dst = p.ws_o + row * D;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int d = E4M3 || D == 64 ? g * (D / 8) + 2 * i
-                                                      : (i / 4) * 64 + g * 8 + (i % 4) * 2;
-                        *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][k], o[i][k + 2]);
-                    }
-                    if (g == 0)
-                        *reinterpret_cast<float2 *>(p.ws_ml + row * 2) = make_float2(m, l);
+                for (int i = 0; i < kSteps; ++i) {
+                    const int d = E4M3 || D == 64 ? g * (D / 8) + 2 * i
+                                                  : (i / 4) * 64 + g * 8 + (i % 4) * 2;
+                    *reinterpret_cast<uint32_t *>(dst + d) =
+                        pair_of<T>(o[i][k] * inv, o[i][k + 2] * inv);
                 }
-            }
-        }
-        at = stop;
-        if (at == seg_end) {
-            seg = seg_end;
-            if (++grp == p.num_groups) {
-                grp = 0;
-                if (++s < p.num_seqs)
-                    tiles = tiles_of(p, s, false);
+                if (p.lse && g == 0)
+                    p.lse[row] = l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                const int64_t row = ((int64_t)(2 * blockIdx.x + slot) << p.heads_log2) * p.group +
+                                    hl * p.group + col;
+                float *dst = p.ws_o + row * D;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int d = E4M3 || D == 64 ? g * (D / 8) + 2 * i
+                                                  : (i / 4) * 64 + g * 8 + (i % 4) * 2;
+                    *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][k], o[i][k + 2]);
+                }
+                if (g == 0)
+                    *reinterpret_cast<float2 *>(p.ws_ml + row * 2) = make_float2(m, l);
             }
         }
     }
@@ -545,16 +720,15 @@ __global__ void __launch_bounds__(D) block_merge_kernel(const DecodeArgs p, int 
         if (cut.z < 2)
             continue;
         for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-            float top = -INFINITY;
+            float top = kNone;
             for (int i = 0; i < cut.z; ++i) {
                 const int64_t row = (int64_t)(2 * (c + i) + (i == 0)) * rows + r;
                 top = fmaxf(top, p.ws_ml[row * 2]);
             }
-            const float ref = top == -INFINITY ? 0.f : top;
             float acc = 0.f, l = 0.f;
             for (int i = 0; i < cut.z; ++i) {
                 const int64_t row = (int64_t)(2 * (c + i) + (i == 0)) * rows + r;
-                const float w = ex2(p.ws_ml[row * 2] - ref);
+                const float w = ex2(p.ws_ml[row * 2] - top);
                 l += w * p.ws_ml[row * 2 + 1];
                 acc += w * p.ws_o[row * D + threadIdx.x];
             }

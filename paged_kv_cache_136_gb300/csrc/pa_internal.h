@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -17,10 +18,12 @@
 
 namespace pa {
 
-// Device address of the current device's sticky error word, and its number of
-// SMs; NULL / 0 with *err set if the lookup fails (pa_api.cu).
+// Device address of the current device's sticky error word, its number of SMs,
+// and the driver's tensor-map encoder; NULL / 0 with *err set if the lookup
+// fails (pa_api.cu).
 unsigned int *device_error_word(cudaError_t *err);
 int sm_count(cudaError_t *err);
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn(cudaError_t *err);
 
 // Launch `kern` so that it may start while the previous kernel on the stream
 // is finishing (programmatic dependent launch); the kernel calls
