@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pa.h"
@@ -22,14 +23,15 @@ cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap
 template <typename T, bool E4M3, int D>
 static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
 {
-    constexpr int smem = decode_smem<E4M3, D>();
+    const int smem = decode_smem<E4M3, D>(1 << p.heads_log2 < kWarps);
     // once a device: a CTA of this kernel takes most of an SM's shared memory
     static bool ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !ready[dev & 63]) {
         e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 decode_smem<E4M3, D>(true));
         ready[dev & 63] = e == cudaSuccess;
     }
     if (e != cudaSuccess)
@@ -38,8 +40,12 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
                               s, map, p);
     if (e != cudaSuccess)
         return e;
-    return launch_after_previous(block_merge_kernel<T, E4M3, D>,
-                                 dim3(ctas, p.group << p.heads_log2), dim3(D), 0, s, p, ctas);
+    // Enough warps for two query rows each of the most cuts there can be, and
+    // at most four CTAs an SM.
+    const int rows = p.group << p.heads_log2;
+    const int merge = std::min((ctas * rows + 2 * kMergeWarps - 1) / (2 * kMergeWarps), 2 * kMaxCtas);
+    return launch_after_previous(block_merge_kernel<T, E4M3, D>, dim3(merge),
+                                 dim3(32 * kMergeWarps), 0, s, p, ctas);
 }
 
 #if PA_INST_DTYPE == 1

@@ -161,11 +161,12 @@ constexpr int kBegins = 2; // that part begins the (sequence, group)
 constexpr int kEnds = 4;   // ... and ends it
 
 // Shared memory of a CTA: the rings (aligned to 1024), their Metas, and half of
-// the states that a head's upper warps hand to its lower ones.
-template <bool E4M3, int D> constexpr int decode_smem()
+// the states that a head's upper warps hand to its lower ones
+// (none where every warp has a head of its own).
+template <bool E4M3, int D> constexpr int decode_smem(bool hand_over)
 {
     return 1024 + kWarps * stages_of<E4M3, D>() * (tile_bytes<E4M3, D>() + (int)sizeof(Meta)) +
-           kWarps / 2 * 4 * (D + 2) * 4;
+           (hand_over ? kWarps / 2 * 4 * (D + 2) * 4 : 0);
 }
 
 __device__ __forceinline__ void tma_load_5d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
@@ -706,37 +707,115 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 }
 
 // Merge of the (sequence, group)s that a cut divides: with M = max m_i,
-// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  One CTA of D threads a
-// (cut, row) pair in turn.
+// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Every CTA lists the cuts;
+// the (cut, query row) pairs then go round the warps, or round the CTAs, whose
+// warps split the states, where there are too few to fill the warps.  Lane i
+// weighs state i; a row of a state is one coalesced read.
+constexpr int kMergeWarps = 8;
+
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(D) block_merge_kernel(const DecodeArgs p, int ctas)
+__global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const DecodeArgs p, int ctas)
 {
     constexpr float kLift = lift_of<typename std::conditional<E4M3, __half, T>::type>();
+    constexpr int kCols = D / 32;                // columns of a lane
+    using Vec = typename std::conditional<kCols == 4, float4, float2>::type;
+    __shared__ uint16_t list[kMaxCtas];          // CTAs whose cut is to be merged
+    __shared__ int counts[kMergeWarps + 1];
+    __shared__ float part[kMergeWarps][D + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const int rows = p.group << p.heads_log2;
-    for (int c = blockIdx.x; c < ctas; c += gridDim.x) {
-        const int4 cut = p.cuts[c];
-        if (cut.z < 2)
-            continue;
-        for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-            float top = kNone;
-            for (int i = 0; i < cut.z; ++i) {
-                const int64_t row = (int64_t)(2 * (c + i) + (i == 0)) * rows + r;
-                top = fmaxf(top, p.ws_ml[row * 2]);
-            }
-            float acc = 0.f, l = 0.f;
-            for (int i = 0; i < cut.z; ++i) {
-                const int64_t row = (int64_t)(2 * (c + i) + (i == 0)) * rows + r;
-                const float w = ex2(p.ws_ml[row * 2] - top);
-                l += w * p.ws_ml[row * 2 + 1];
-                acc += w * p.ws_o[row * D + threadIdx.x];
-            }
-            const int64_t row = (int64_t)cut.x * p.num_heads + (int64_t)cut.y * rows + r;
-            static_cast<T *>(p.out)[row * D + threadIdx.x] = static_cast<T>(l != 0.f ? acc / l : 0.f);
-            if (p.lse && threadIdx.x == 0)
-                p.lse[row] = l != 0.f ? (top - kLift + log2f(l)) * kLn2 : -INFINITY;
+    int found = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32 * kMergeWarps) {
+        const int c = c0 + threadIdx.x;
+        const bool mine = c < ctas && p.cuts[c].z >= 2;
+        const unsigned some = __ballot_sync(~0u, mine);
+        if (lane == 0)
+            counts[warp] = __popc(some);
+        __syncthreads();
+        int at = found + __popc(some & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            at += w < warp ? counts[w] : 0;
+            found += counts[w];
         }
+        if (mine)
+            list[at] = (uint16_t)c;
+        __syncthreads();
+    }
+    const int rows = p.group << p.heads_log2, items = found * rows;
+    const bool wide = items * 2 <= (int)gridDim.x * kMergeWarps;
+    const int step = wide ? gridDim.x : gridDim.x * kMergeWarps;
+    for (int item = wide ? blockIdx.x : blockIdx.x * kMergeWarps + warp; item < items;
+         item += step) {
+        const int begun = list[item / rows];
+        const int4 cut = p.cuts[begun];          // sequence, head group, states
+        const int r = item % rows, first = wide ? warp : 0, each = wide ? kMergeWarps : 1;
+        // states first, first + each, ..., 32 at a time
+        float top = kNone, l = 0.f, acc[kCols];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+            acc[k] = 0.f;
+        for (int i0 = first; i0 < cut.z; i0 += 32 * each) {
+            const int i = i0 + lane * each, n = min(32, (cut.z - i0 + each - 1) / each);
+            float2 ml = make_float2(kNone, 0.f);
+            const int64_t row = (int64_t)(2 * (begun + i) + (i == 0)) * rows + r;
+            if (lane < n)
+                ml = *reinterpret_cast<const float2 *>(p.ws_ml + row * 2);
+            const float now = fmaxf(top, warp_max(ml.x));
+            const float weight = ex2(ml.x - now), old = ex2(top - now);
+            top = now;
+            l = l * old + weight * ml.y;         // summed over the lanes below
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                acc[k] *= old;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const int64_t src = __shfl_sync(~0u, row, j);
+                const float w = __shfl_sync(~0u, weight, j);
+                const Vec v = reinterpret_cast<const Vec *>(p.ws_o + src * D)[lane];
+                acc[0] += w * v.x;
+                acc[1] += w * v.y;
+                if constexpr (kCols == 4) {
+                    acc[2] += w * v.z;
+                    acc[3] += w * v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            l += __shfl_xor_sync(~0u, l, o);
+        if (wide) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                part[warp][lane * kCols + k] = acc[k];
+            if (lane == 0) {
+                part[warp][D] = top;
+                part[warp][D + 1] = l;
+            }
+            __syncthreads();
+            if (warp)
+                continue;
+            for (int w = 1; w < kMergeWarps; ++w) {
+                const float now = fmaxf(top, part[w][D]);
+                const float a = ex2(top - now), b = ex2(part[w][D] - now);
+                top = now;
+                l = l * a + b * part[w][D + 1];
+#pragma unroll
+                for (int k = 0; k < kCols; ++k)
+                    acc[k] = acc[k] * a + b * part[w][lane * kCols + k];
+            }
+        }
+        const int64_t row = (int64_t)cut.x * p.num_heads + (int64_t)cut.y * rows + r;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + row * D) +
+                        lane * (kCols / 2);
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2)
+            dst[k / 2] = pair_of<T>(acc[k] * inv, acc[k + 1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[row] = l != 0.f ? (top - kLift + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
