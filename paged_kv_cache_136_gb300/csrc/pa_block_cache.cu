@@ -6,6 +6,9 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "pa.h"
 #include "pa_block.cuh"
 #include "pa_internal.h"
@@ -22,106 +25,140 @@ struct WriteParams {
     const int32_t *query_start_loc; // [R + 1]
     unsigned int *err;
     int64_t table_stride, key_stride, value_stride;
-    int num_tokens, max_query_len, num_kv_heads, num_blocks, len_cap, units;
+    int num_tokens, max_query_len, num_kv_heads, num_blocks, len_cap, pieces;
 };
 
 constexpr int kWriteWarps = 8;
 
-// One warp quantises one (request's block, plane, kv head): it reads the new
-// tokens' values once, keeps them in registers while it forms their largest
-// magnitude, and writes the codes; the block's older codes are touched only
-// when the scale grows.  Grid: x = chunks of kWriteWarps (plane, head) units
-// of one block, y = block of the request, z = request.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) // unsigned 16-bit pairs
+{
+    return __vmaxu2(a, b);
+}
+
+// One warp quantises one block of a request for the kv heads of 32 consecutive
+// 16-byte (8-byte for blocks of 32) pieces of a token row: a lane holds the
+// same 8 (4) channels of every row of the block, so the new values are read
+// once, coalesced, and stay in registers while their largest magnitude is
+// formed.  The block's older codes are touched only when the scale grows.
+// Bound by HBM: 2 bytes read and 1 written a value.
+// Grid: x = chunks of kWriteWarps (block of the request, piece of the row,
+// plane) units, y = request.
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(32 * kWriteWarps) write_block_kernel(const WriteParams p)
 {
-    constexpr int kLanesPerRow = D / 8;           // 16-byte loads of 8 values
-    constexpr int kRowsAtOnce = 32 / kLanesPerRow;
-    constexpr int kLoads = BS / kRowsAtOnce;
+    constexpr int kWords = BS == 16 ? 4 : 2;      // 32-bit words of a lane and row
+    constexpr int kVals = 2 * kWords;             // values of a lane and row
+    constexpr int kLanes = D / kVals;             // lanes of a head
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int unit = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
-    if (unit >= p.units)
-        return;
-    const int r = blockIdx.z;
+    const int r = blockIdx.y;
+    const int plane = unit % 2, piece = unit / 2 % p.pieces, jj = unit / 2 / p.pieces;
     Request q;
     if (!read_request(q, r, p.seq_lens, p.query_start_loc, p.num_tokens, p.max_query_len,
-                      p.len_cap, unit == 0 && blockIdx.y == 0 && lane == 0, p.err))
+                      p.len_cap, unit == 0 && lane == 0, p.err))
         return;
     const int first = q.len - q.fresh;            // position of the first new token
-    const int j = first / BS + blockIdx.y;
-    if (j * BS >= q.len)
+    const int j = first / BS + jj;
+    if ((int64_t)j * BS >= q.len)
         return;
     const int blk = p.tables[r * p.table_stride + j];
     if (blk < 0 || blk >= p.num_blocks) {
-        if (unit == 0 && lane == 0)
+        if (piece == 0 && plane == 0 && lane == 0)
             atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
         return;
     }
-    const int plane = unit >= p.num_kv_heads, head = unit - plane * p.num_kv_heads;
     const int lo = max(0, first - j * BS), hi = min(BS, q.len - j * BS); // rows written
-    const T *src = static_cast<const T *>(plane ? p.value : p.key);
-    const int64_t stride = plane ? p.value_stride : p.key_stride;
-    const int sub = lane / kLanesPerRow, col = lane % kLanesPerRow * 8;
-    src += (q.row + (int64_t)j * BS - first) * stride + head * D + col;
+    const int64_t stride = plane ? p.value_stride : p.key_stride, wide = (int64_t)p.num_kv_heads * D;
+    const int col = (piece * 32 + lane) * kVals, head = col / D;
+    const bool in = col < wide;                   // the row may end inside the piece
+    const T *src = static_cast<const T *>(plane ? p.value : p.key) +
+                   (q.row + (int64_t)j * BS - first) * stride + col;
 
-    uint4 x[kLoads];
-    float amax = 0.f;
+    uint32_t x[BS][kWords];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int row = i * kRowsAtOnce + sub;
-        x[i] = row >= lo && row < hi ? load16(src + row * stride) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = float2_of<T>((&x[i].x)[k]);
-            amax = fmaxf(amax, isfinite(f.x) ? fabsf(f.x) : 0.f);
-            amax = fmaxf(amax, isfinite(f.y) ? fabsf(f.y) : 0.f);
+    for (int i = 0; i < BS; ++i) {
+        const bool read = in && i >= lo && i < hi;
+        if constexpr (kWords == 4) {
+            const uint4 v = read ? load16(src + i * stride) : make_uint4(0, 0, 0, 0);
+            x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        } else {
+            const uint2 v = read ? load8(src + i * stride) : make_uint2(0, 0);
+            x[i][0] = v.x, x[i][1] = v.y;
         }
-    amax = warp_max(amax);
-    float scale = pow2_scale<448>(amax);
-    const int64_t pool_row = ((int64_t)plane * p.num_blocks + blk) * BS;
-    float *const where = p.scales + ((int64_t)plane * p.num_blocks + blk) * p.num_kv_heads + head;
-    uint8_t *dst = p.pool + (pool_row * p.num_kv_heads + head) * D + col;
-    const int64_t step = (int64_t)p.num_kv_heads * D;
+    }
+    // Magnitudes of 16-bit floats order as their bits do; what is not finite
+    // is left out, in a second look that is rarely taken.
+    constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < BS; ++i)
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            top = max_halves(top, x[i][k] & 0x7FFF7FFFu);
+    if (__any_sync(~0u, (top & 0xFFFFu) >= kInf || top >> 16 >= kInf)) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < BS; ++i)
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                uint32_t m = x[i][k] & 0x7FFF7FFFu;
+                if ((m & 0xFFFFu) >= kInf)
+                    m &= 0xFFFF0000u;
+                if (m >> 16 >= kInf)
+                    m &= 0xFFFFu;
+                top = max_halves(top, m);
+            }
+    }
+    uint32_t most = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1)
+        most = max(most, __shfl_xor_sync(~0u, most, o));
+    float scale = pow2_scale<448>(float2_of<T>(most).x);
+
+    const int64_t at = (int64_t)plane * p.num_blocks + blk;
+    float *const where = p.scales + at * p.num_kv_heads + head;
+    uint8_t *dst = p.pool + at * BS * wide + col;
+    const unsigned writers = __ballot_sync(~0u, in);
+    if (!in)
+        return;
     if (lo > 0) {
         const float before = *where;
         scale = fmaxf(scale, before);
         if (scale > before) { // older codes move to the larger scale
             const float ratio = before / scale;
-            for (int row = sub; row < lo; row += kRowsAtOnce) {
-                uint2 c = *reinterpret_cast<uint2 *>(dst + row * step);
+            for (int row = 0; row < lo; ++row) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t &w = k ? c.y : c.x;
+                for (int k = 0; k < kVals / 4; ++k) {
+                    uint32_t *const at4 = reinterpret_cast<uint32_t *>(dst + row * wide) + k;
+                    const uint32_t w = *at4;
                     const float2 a = float2_of<__half>(half2_of_e4m3x2(w));
                     const float2 b = float2_of<__half>(half2_of_e4m3x2_hi(w));
-                    w = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
+                    *at4 = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
                 }
-                *reinterpret_cast<uint2 *>(dst + row * step) = c;
             }
         }
+        // every lane of the head has read the old scale before one writes it
+        __syncwarp(writers);
     }
-    __syncwarp();
-    if (lane == 0)
+    if (lane % kLanes == 0)
         *where = scale;
-    const float inv = 1.f / scale;
+    const float inv = pow2_inverse(scale);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int row = i * kRowsAtOnce + sub;
-        if (row < lo || row >= hi)
+    for (int i = 0; i < BS; ++i) {
+        if (i < lo || i >= hi)
             continue;
-        uint2 c;
+        uint32_t c[kVals / 4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 a = float2_of<T>((&x[i].x)[2 * k]);
-            const float2 b = float2_of<T>((&x[i].x)[2 * k + 1]);
-            (k ? c.y : c.x) = e4m3x2(a.x * inv, a.y * inv) | e4m3x2(b.x * inv, b.y * inv) << 16;
+        for (int k = 0; k < kVals / 4; ++k) {
+            const float2 a = float2_of<T>(x[i][2 * k]), b = float2_of<T>(x[i][2 * k + 1]);
+            c[k] = e4m3x2(a.x * inv, a.y * inv) | e4m3x2(b.x * inv, b.y * inv) << 16;
         }
-        *reinterpret_cast<uint2 *>(dst + row * step) = c;
+        if constexpr (kWords == 4)
+            *reinterpret_cast<uint2 *>(dst + i * wide) = make_uint2(c[0], c[1]);
+        else
+            *reinterpret_cast<uint32_t *>(dst + i * wide) = c[0];
     }
 }
 
@@ -133,114 +170,145 @@ struct BoundsParams {
     const int32_t *tables, *seq_lens, *query_start_loc;
     unsigned int *err;
     int64_t table_stride;
-    int max_query_len, num_kv_heads, num_blocks, len_cap;
+    int max_query_len, num_kv_heads, num_blocks, len_cap, pieces;
 };
 
 constexpr int kBoundsWarps = 8;
 
-// One warp forms the bounds of one (request's block, kv head): a lane holds
-// D / 32 channels and walks the block's rows that are in the cache.  The
-// kernel reads those keys once and writes 2 D + 4 bytes.  KIND: 0 fp16, 1
-// bf16, 2 e4m3 with scales.  Grid as the write's, without the planes.
-template <int KIND, int D, int BS>
+// Larger and smaller of two pairs; NaN wins.
+template <typename T> __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b);
+template <typename T> __device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t pair_max<__half>(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pair_min<__half>(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pair_max<__nv_bfloat16>(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pair_min<__nv_bfloat16>(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// One warp forms the bounds of one block of a request for the kv heads of 32
+// consecutive 16-byte (8-byte for blocks of 32) pieces of a key row: a lane
+// walks the same channels down the block's rows, so each key is read once,
+// coalesced, and only the largest magnitude goes across the head's lanes.
+// Bound by HBM: the keys, and 2 D + 4 bytes written a head.  T: type of a
+// 16-bit pool (e4m3 codes become halves).  Grid as the write's, without planes.
+template <typename T, bool E4M3, int D, int BS>
 __global__ void __launch_bounds__(32 * kBoundsWarps) block_bounds_kernel(const BoundsParams p)
 {
-    constexpr int kPer = D / 32;                  // channels of a lane: 2 or 4
-    constexpr int kBytes = kPer * (KIND == 2 ? 1 : 2);
+    constexpr int kWords = BS == 16 ? 4 : 2;      // 32-bit words of a lane and row
+    constexpr int kVals = kWords * (E4M3 ? 4 : 2);
+    constexpr int kPairs = kVals / 2;
+    constexpr int kLanes = D / kVals;             // lanes of a head
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int head = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
-    if (head >= p.num_kv_heads)
-        return;
-    const int r = blockIdx.z;
+    const int unit = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
+    const int r = blockIdx.y, piece = unit % p.pieces, jj = unit / p.pieces;
     Request q;
     if (!read_request(q, r, p.seq_lens, p.query_start_loc, INT32_MAX, p.max_query_len, p.len_cap,
-                      head == 0 && blockIdx.y == 0 && lane == 0, p.err))
+                      unit == 0 && lane == 0, p.err))
         return;
-    const int j = (q.len - q.fresh) / BS + blockIdx.y;
-    if (j * BS >= q.len)
+    const int j = (q.len - q.fresh) / BS + jj;
+    if ((int64_t)j * BS >= q.len)
         return;
     const int blk = p.tables[r * p.table_stride + j];
     if (blk < 0 || blk >= p.num_blocks) {
-        if (head == 0 && lane == 0)
+        if (piece == 0 && lane == 0)
             atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
         return;
     }
     const int rows = min(BS, q.len - j * BS);
-    const int64_t step = (int64_t)p.num_kv_heads * D * (KIND == 2 ? 1 : 2);
-    const char *src = static_cast<const char *>(p.pool) + (int64_t)blk * BS * step +
-                      (head * 32 + lane) * kBytes;
-    uint2 raw[BS];
+    const int wide = p.num_kv_heads * D, head = (piece * 32 + lane) * kVals / D;
+    const int col = min((piece * 32 + lane) * kVals, wide - kVals); // past the row: not written
+    const bool in = (piece * 32 + lane) * kVals < wide;
+    const int64_t step = (int64_t)wide * (E4M3 ? 1 : 2);
+    const char *src = static_cast<const char *>(p.pool) + blk * (BS * step) + col * (E4M3 ? 1 : 2);
+    uint32_t raw[BS][kWords];
 #pragma unroll
     for (int i = 0; i < BS; ++i) {
-        raw[i] = make_uint2(0, 0);
-        const int row = min(i, rows - 1); // a repeated row changes no bound
-        if constexpr (kBytes == 8)
-            raw[i] = *reinterpret_cast<const uint2 *>(src + row * step);
-        else if constexpr (kBytes == 4)
-            raw[i].x = *reinterpret_cast<const uint32_t *>(src + row * step);
-        else
-            raw[i].x = *reinterpret_cast<const uint16_t *>(src + row * step);
+        const char *const at = src + min(i, rows - 1) * step; // a repeated row changes no bound
+        if constexpr (kWords == 4) {
+            const uint4 v = load16(at);
+            raw[i][0] = v.x, raw[i][1] = v.y, raw[i][2] = v.z, raw[i][3] = v.w;
+        } else {
+            const uint2 v = load8(at);
+            raw[i][0] = v.x, raw[i][1] = v.y;
+        }
     }
-    float up[kPer], low[kPer];
-    bool odd = false; // a key that is not finite
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        up[k] = -INFINITY, low[k] = INFINITY;
+    float s = 1.f;
+    if constexpr (E4M3)
+        s = p.scales[(int64_t)blk * p.num_kv_heads + min(head, p.num_kv_heads - 1)];
+    uint32_t up[kPairs], low[kPairs];
 #pragma unroll
     for (int i = 0; i < BS; ++i)
 #pragma unroll
-        for (int k = 0; k < kPer; k += 2) {
-            float2 f;
-            if constexpr (KIND == 2)
-                f = float2_of<__half>(k ? half2_of_e4m3x2_hi(raw[i].x) : half2_of_e4m3x2(raw[i].x));
-            else if constexpr (KIND == 1)
-                f = float2_of<__nv_bfloat16>(k ? raw[i].y : raw[i].x);
+        for (int k = 0; k < kPairs; ++k) {
+            uint32_t v;
+            if constexpr (E4M3)
+                v = k % 2 ? half2_of_e4m3x2_hi(raw[i][k / 2]) : half2_of_e4m3x2(raw[i][k / 2]);
             else
-                f = float2_of<__half>(k ? raw[i].y : raw[i].x);
-            odd |= !isfinite(f.x) || !isfinite(f.y);
-            up[k] = fmaxf(up[k], f.x);
-            low[k] = fminf(low[k], f.x);
-            up[k + 1] = fmaxf(up[k + 1], f.y);
-            low[k + 1] = fminf(low[k + 1], f.y);
+                v = raw[i][k];
+            up[k] = i ? pair_max<T>(up[k], v) : v;
+            low[k] = i ? pair_min<T>(low[k], v) : v;
         }
-    if constexpr (KIND == 2) {
-        const float s = p.scales[(int64_t)blk * p.num_kv_heads + head];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            up[k] *= s;
-            low[k] *= s;
-            odd |= !isfinite(up[k]) || !isfinite(low[k]);
-        }
-    }
-    odd = __any_sync(~0u, odd);
+    bool odd = false; // a key that is not finite
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        amax = fmaxf(amax, fmaxf(fabsf(up[k]), fabsf(low[k])));
-    amax = warp_max(amax);
+    for (int k = 0; k < kPairs; ++k) {
+        const float2 u = float2_of<T>(up[k]), l = float2_of<T>(low[k]);
+        const float a = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(l.x), fabsf(l.y))) * s;
+        odd |= !isfinite(a) || u.x != u.x || u.y != u.y;
+        amax = fmaxf(amax, a);
+    }
+    amax = odd ? INFINITY : amax;
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    odd = amax == INFINITY;
     const float scale = pow2_scale<127>(odd ? 0.f : amax), inv = pow2_inverse(scale);
-    uint32_t cu = 0, cl = 0;
+    uint32_t cu[kVals / 4], cl[kVals / 4];
+#pragma unroll
+    for (int k = 0; k < kVals / 4; ++k)
+        cu[k] = cl[k] = 0;
     if (!odd) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) { // rounded outwards: still bounds
-            const int u = (int)fminf(fmaxf(ceilf(up[k] * inv), -127.f), 127.f);
-            const int l = (int)fminf(fmaxf(floorf(low[k] * inv), -127.f), 127.f);
-            cu |= (uint32_t)(u & 255) << 8 * k;
-            cl |= (uint32_t)(l & 255) << 8 * k;
+        for (int k = 0; k < kVals; ++k) { // rounded outwards: still bounds
+            const float2 u = float2_of<T>(up[k / 2]), l = float2_of<T>(low[k / 2]);
+            const float a = (k % 2 ? u.y : u.x) * s * inv;
+            const float b = (k % 2 ? l.y : l.x) * s * inv;
+            const int x = (int)fminf(fmaxf(ceilf(a), -127.f), 127.f);
+            const int y = (int)fminf(fmaxf(floorf(b), -127.f), 127.f);
+            cu[k / 4] |= (uint32_t)(x & 255) << 8 * (k % 4);
+            cl[k / 4] |= (uint32_t)(y & 255) << 8 * (k % 4);
         }
     }
+    if (!in)
+        return;
     const int64_t at = (int64_t)blk * p.num_kv_heads + head;
-    int8_t *dst = p.bounds + at * 2 * D + lane * kPer;
-    if constexpr (kPer == 4) {
-        *reinterpret_cast<uint32_t *>(dst) = cu;
-        *reinterpret_cast<uint32_t *>(dst + D) = cl;
-    } else {
-        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)cu;
-        *reinterpret_cast<uint16_t *>(dst + D) = (uint16_t)cl;
+    uint32_t *const dst = reinterpret_cast<uint32_t *>(p.bounds + at * 2 * D + col % D);
+#pragma unroll
+    for (int k = 0; k < kVals / 4; ++k) {
+        dst[k] = cu[k];
+        dst[k + D / 4] = cl[k];
     }
-    if (lane == 0)
+    if (lane % kLanes == 0)
         p.bounds_scale[at] = odd ? INFINITY : scale;
 }
 
@@ -270,15 +338,7 @@ static pa_status check_requests(const int32_t *tables, int64_t table_stride,
         (int64_t)num_blocks * block_size >= (int64_t)INT32_MAX ||
         (int64_t)max_blocks_per_seq * block_size >= (int64_t)INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    // blocks that one request's new tokens can reach: the grid's y extent
-    if ((max_query_len + (int64_t)block_size - 2) / block_size + 1 > 65535)
-        return PA_ERR_UNSUPPORTED;
     return PA_OK;
-}
-
-static int reached_blocks(int max_query_len, int block_size)
-{
-    return (max_query_len + block_size - 2) / block_size + 1;
 }
 
 template <typename T>
@@ -295,18 +355,26 @@ static cudaError_t launch_write(int head_size, int block_size, const WriteParams
                : launch_after_previous(write_block_kernel<T, 64, 32>, grid, threads, 0, s, p);
 }
 
-template <int KIND>
+template <typename T, bool E4M3>
 static cudaError_t launch_bounds(int head_size, int block_size, const BoundsParams &p, dim3 grid,
                                  cudaStream_t s)
 {
     const dim3 threads(32 * kBoundsWarps);
     if (head_size == 128)
         return block_size == 16
-                   ? launch_after_previous(block_bounds_kernel<KIND, 128, 16>, grid, threads, 0, s, p)
-                   : launch_after_previous(block_bounds_kernel<KIND, 128, 32>, grid, threads, 0, s, p);
+                   ? launch_after_previous(block_bounds_kernel<T, E4M3, 128, 16>, grid, threads, 0, s, p)
+                   : launch_after_previous(block_bounds_kernel<T, E4M3, 128, 32>, grid, threads, 0, s, p);
     return block_size == 16
-               ? launch_after_previous(block_bounds_kernel<KIND, 64, 16>, grid, threads, 0, s, p)
-               : launch_after_previous(block_bounds_kernel<KIND, 64, 32>, grid, threads, 0, s, p);
+               ? launch_after_previous(block_bounds_kernel<T, E4M3, 64, 16>, grid, threads, 0, s, p)
+               : launch_after_previous(block_bounds_kernel<T, E4M3, 64, 32>, grid, threads, 0, s, p);
+}
+
+// Grid x of `warps` warps a CTA: every (block that a request's new tokens can
+// reach, 32-lane piece of `bytes` bytes a row) times `planes`.
+static int64_t chunks(int max_query_len, int block_size, int64_t pieces, int planes, int warps)
+{
+    const int64_t reached = (max_query_len + (int64_t)block_size - 2) / block_size + 1;
+    return (reached * pieces * planes + warps - 1) / warps;
 }
 
 } // namespace block
@@ -362,9 +430,13 @@ pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, voi
     p.num_kv_heads = num_kv_heads;
     p.num_blocks = num_blocks;
     p.len_cap = max_blocks_per_seq * block_size;
-    p.units = 2 * num_kv_heads;
-    const dim3 grid((p.units + kWriteWarps - 1) / kWriteWarps,
-                    reached_blocks(max_query_len, block_size), num_reqs);
+    const int piece = 32 * (block_size == 16 ? 8 : 4); // values of a warp and row
+    p.pieces = (int)((row + piece - 1) / piece);
+    const int64_t gx = chunks(std::min(max_query_len, p.len_cap), block_size, p.pieces, 2,
+                              kWriteWarps);
+    if (gx > INT32_MAX / kWriteWarps)
+        return PA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)gx, num_reqs);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     e = src_dtype == PA_BF16 ? launch_write<__nv_bfloat16>(head_size, block_size, p, grid, s)
                              : launch_write<__half>(head_size, block_size, p, grid, s);
@@ -407,12 +479,18 @@ pa_status pa_update_block_bounds(int8_t *bounds, float *bounds_scale, const void
     p.num_kv_heads = num_kv_heads;
     p.num_blocks = num_blocks;
     p.len_cap = max_blocks_per_seq * block_size;
-    const dim3 grid((num_kv_heads + kBoundsWarps - 1) / kBoundsWarps,
-                    reached_blocks(max_query_len, block_size), num_reqs);
+    const int64_t row = (int64_t)num_kv_heads * head_size * (kv_scales ? 1 : 2);
+    const int piece = 32 * (block_size == 16 ? 16 : 8); // bytes of a warp and row
+    p.pieces = (int)((row + piece - 1) / piece);
+    const int64_t gx = chunks(std::min(max_query_len, p.len_cap), block_size, p.pieces, 1,
+                              kBoundsWarps);
+    if (gx > INT32_MAX / kBoundsWarps)
+        return PA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)gx, num_reqs);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    e = kv_scales            ? launch_bounds<2>(head_size, block_size, p, grid, s)
-        : dtype == PA_BF16   ? launch_bounds<1>(head_size, block_size, p, grid, s)
-                             : launch_bounds<0>(head_size, block_size, p, grid, s);
+    e = kv_scales          ? launch_bounds<__half, true>(head_size, block_size, p, grid, s)
+        : dtype == PA_BF16 ? launch_bounds<__nv_bfloat16, false>(head_size, block_size, p, grid, s)
+                           : launch_bounds<__half, false>(head_size, block_size, p, grid, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
