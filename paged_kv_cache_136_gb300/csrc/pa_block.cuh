@@ -149,7 +149,7 @@ __device__ __forceinline__ void mma_16832_s8(int (&c)[4], uint32_t a0, uint32_t 
 __device__ __forceinline__ uint4 load16(const void *p)
 {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -158,7 +158,7 @@ __device__ __forceinline__ uint4 load16(const void *p)
 __device__ __forceinline__ uint2 load8(const void *p)
 {
     uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+    asm("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
                  : "=r"(v.x), "=r"(v.y)
                  : "l"(p));
     return v;

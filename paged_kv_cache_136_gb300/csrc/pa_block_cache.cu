@@ -210,7 +210,7 @@ template <> __device__ __forceinline__ uint32_t pair_min<__nv_bfloat16>(uint32_t
 // Bound by HBM: the keys, and 2 D + 4 bytes written a head.  T: type of a
 // 16-bit pool (e4m3 codes become halves).  Grid as the write's, without planes.
 template <typename T, bool E4M3, int D, int BS>
-__global__ void __launch_bounds__(32 * kBoundsWarps) block_bounds_kernel(const BoundsParams p)
+__global__ void __launch_bounds__(32 * kBoundsWarps, 2) block_bounds_kernel(const BoundsParams p)
 {
     constexpr int kWords = BS == 16 ? 4 : 2;      // 32-bit words of a lane and row
     constexpr int kVals = kWords * (E4M3 ? 4 : 2);

@@ -169,11 +169,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
         keys[jb] = jb < p.sink || jb >= n - p.recent ? kKeyKept : key_of(sb == inf ? inf : best_b);
 }
 
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
-
-// Exclusive prefix of a pair of counts over the block's threads, and their
-// totals; the counts are packed as 16-bit halves of one word.
+// Exclusive prefix of a count over the block's threads, and the total.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -187,94 +184,167 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
     if (lane == 31)
         warp_sums[warp] = x;
     __syncthreads();
-    uint32_t base = 0;
-    total = 0;
+    uint32_t sum = lane < THREADS / 32 ? warp_sums[lane] : 0, up = sum;
 #pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) {
-        const uint32_t y = warp_sums[w];
-        base += w < warp ? y : 0;
-        total += y;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, up, o);
+        if (lane >= o)
+            up += y;
     }
+    total = __shfl_sync(~0u, up, 31);
+    const uint32_t base = __shfl_sync(~0u, up - sum, warp);
     __syncthreads();
     return base + x - v;
 }
 
+constexpr int kDigit = 11; // bits of a pass
+
 // The `most` largest keys of one (sequence, kv head), in ascending order of
 // the block's position; among equal keys the lowest positions.  A radix select
-// finds the smallest chosen key in four passes of 8 bits over the keys, and an
-// ordered scan writes the positions.
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p)
+// over the range that the keys take finds the smallest chosen key, 11 bits a
+// pass, and stops early when a digit's keys are all wanted; an ordered scan
+// writes the positions.  A thread holds PER consecutive keys in registers; a
+// longer row goes through in several rounds, read again (from L2) each pass.
+// Bound by latency: the passes' barriers.
+template <int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
 {
-    __shared__ uint32_t hist[256], warp_sums[kPickWarps], found[2];
+    __shared__ uint32_t hist[1 << kDigit], warp_sums[32], range[2][32], found[3];
     griddep_wait();
     griddep_launch_dependents();
     const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
     const int len = checked_len(p, s, false);
     const int n = (len + p.block_size - 1) / p.block_size;
     const int count = min(n, p.most);
     int32_t *list = p.lists + ((int64_t)s * p.num_kv_heads + head) * p.most;
     if (head == 0 && tid == 0)
         p.list_lens[s] = count;
-    for (int i = count + tid; i < p.most; i += kPickThreads)
+    for (int i = count + tid; i < p.most; i += THREADS)
         list[i] = -1;
     if (n <= p.most) {
-        for (int i = tid; i < n; i += kPickThreads)
+        for (int i = tid; i < n; i += THREADS)
             list[i] = i;
         return;
     }
     const uint32_t *keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
-    uint32_t prefix = 0, need = p.most; // keys above the prefix's range are chosen
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kPickThreads)
-            hist[i] = 0;
-        __syncthreads();
-        const uint32_t above = shift == 24 ? 0 : ~0u << (shift + 8);
-        for (int i = tid; i < n; i += kPickThreads) {
-            const uint32_t k = keys[i];
-            if ((k & above) == prefix)
-                atomicAdd(&hist[k >> shift & 255], 1u);
+    const int rounds = (n + THREADS * PER - 1) / (THREADS * PER);
+    uint32_t k[PER];
+    auto load = [&](int round) { // keys past the end are 0, below every score
+        const int i0 = (round * THREADS + tid) * PER;
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i0 + i < n)
+                v = *reinterpret_cast<const uint4 *>(keys + i0 + i);
+            k[i] = v.x;
+            k[i + 1] = i0 + i + 1 < n ? v.y : 0;
+            k[i + 2] = i0 + i + 2 < n ? v.z : 0;
+            k[i + 3] = i0 + i + 3 < n ? v.w : 0;
+        }
+    };
+    // how many are kept anyway, and the range of the others
+    uint32_t lo = ~0u, hi = 0, kept = 0;
+    for (int round = 0; round < rounds; ++round) {
+        load(round);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool scored = k[i] != 0 && k[i] != kKeyKept;
+            lo = scored ? min(lo, k[i]) : lo;
+            hi = scored ? max(hi, k[i]) : hi;
+            kept += k[i] == kKeyKept;
+        }
+    }
+    lo = __reduce_min_sync(~0u, lo);
+    hi = __reduce_max_sync(~0u, hi);
+    if (lane == 0) {
+        range[0][warp] = lo;
+        range[1][warp] = hi;
+    }
+    for (int i = tid; i < 1 << kDigit; i += THREADS)
+        hist[i] = 0;
+    uint32_t all;
+    block_scan<THREADS>(kept, warp_sums, all);
+    lo = __reduce_min_sync(~0u, lane < THREADS / 32 ? range[0][lane] : ~0u);
+    hi = __reduce_max_sync(~0u, lane < THREADS / 32 ? range[1][lane] : 0u);
+    uint32_t need = p.most - all;    // of the scored ones
+    const int bits = 32 - __clz(hi - lo);
+    // distance d = key - lo; `border` is the found digits of the smallest chosen
+    uint32_t border = 0, ties = need;
+    for (int top = bits; top > 0 && need > 0;) {
+        const int shift = max(top - kDigit, 0);
+        for (int round = 0; round < rounds; ++round) {
+            if (rounds > 1)
+                load(round);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t d = k[i] - lo;
+                if (k[i] != 0 && k[i] != kKeyKept && (top == 32 || (d ^ border) >> top == 0))
+                    atomicAdd(&hist[d >> shift & ((1 << kDigit) - 1)], 1u);
+            }
         }
         __syncthreads();
-        if (tid < 32) { // digits from the top: lane l owns digits 255-8l .. 248-8l
-            uint32_t c[8], sum = 0;
+        // digits from the largest down, kEach a thread
+        constexpr int kEach = (1 << kDigit) / THREADS;
+        uint32_t c[kEach], sum = 0, total;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                sum += c[k] = hist[255 - 8 * tid - k];
-            uint32_t x = sum;
+        for (int i = 0; i < kEach; ++i) {
+            uint32_t &bin = hist[(1 << kDigit) - 1 - tid * kEach - i];
+            sum += c[i] = bin;
+            bin = 0;
+        }
+        uint32_t before = block_scan<THREADS>(sum, warp_sums, total);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(~0u, x, o);
-                if (tid >= o)
-                    x += y;
+        for (int i = 0; i < kEach; ++i) {
+            if (before < need && before + c[i] >= need) {
+                found[0] = (1 << kDigit) - 1 - tid * kEach - i;
+                found[1] = need - before;
+                found[2] = c[i];
             }
-            uint32_t before = x - sum;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (before < need && before + c[k] >= need) {
-                    found[0] = 255 - 8 * tid - k;
-                    found[1] = need - before;
-                }
-                before += c[k];
-            }
+            before += c[i];
         }
         __syncthreads();
-        prefix |= found[0] << shift;
-        need = found[1];
+        border |= found[0] << shift;
+        ties = need = found[1];
+        top = shift;
+        if (found[2] == need) { // all that share the digits are chosen
+            ties = ~0u;
+            break;
+        }
         __syncthreads();
     }
-    // All keys above `prefix`, and the first `need` equal to it.
+    // Chosen: the kept, those above the border, the first `ties` on it (where
+    // the search stopped early, everything from the border up).
+    const bool some = p.most > all;
+    const uint32_t most_e = some ? ties : 0;
     uint32_t above = 0, equal = 0;
-    for (int i0 = 0; i0 < n; i0 += kPickThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < n ? keys[i] : 0;
-        const bool gt = i < n && k > prefix, eq = i < n && k == prefix;
-        uint32_t total;
-        const uint32_t x = block_scan((gt ? 1u : 0u) | (eq ? 1u << 16 : 0u), warp_sums, total);
-        const uint32_t a = above + (x & 0xFFFF), b = equal + (x >> 16);
-        if (gt || (eq && b < need))
-            list[a + min(b, need)] = i;
-        above += total & 0xFFFF;
-        equal += total >> 16;
+    for (int round = 0; round < rounds; ++round) {
+        if (rounds > 1)
+            load(round);
+        uint32_t a = 0, e = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t d = k[i] - lo;
+            const bool scored = k[i] != 0 && k[i] != kKeyKept;
+            a += k[i] == kKeyKept || (scored && some && d > border);
+            e += scored && d == border;
+        }
+        uint32_t total_a, total_e;
+        uint32_t at_a = above + block_scan<THREADS>(a, warp_sums, total_a);
+        uint32_t at_e = equal + block_scan<THREADS>(e, warp_sums, total_e);
+        above += total_a;
+        equal += total_e;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t d = k[i] - lo;
+            const bool scored = k[i] != 0 && k[i] != kKeyKept;
+            const bool gt = k[i] == kKeyKept || (scored && some && d > border);
+            const bool eq = scored && d == border;
+            if (gt || (eq && at_e < most_e))
+                list[at_a + min(at_e, most_e)] = (round * THREADS + tid) * PER + i;
+            at_a += gt;
+            at_e += eq;
+        }
     }
 }
 
@@ -283,9 +353,10 @@ static bool aligned(const void *p, uintptr_t a)
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// Keys of a row, a multiple of four.
 static size_t key_stride(int max_seq_len, int block_size)
 {
-    return ((size_t)max_seq_len + block_size - 1) / block_size;
+    return (((size_t)max_seq_len + block_size - 1) / block_size + 3) / 4 * 4;
 }
 
 } // namespace block
@@ -385,8 +456,11 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
         if (e != cudaSuccess)
             return PA_ERR_CUDA;
     }
-    e = launch_after_previous(pick_kernel, dim3(num_kv_heads, num_seqs), dim3(kPickThreads), 0, st,
-                              p);
+    // Rows that fit the registers of 512 threads of 8 keys; longer ones, 16384
+    // keys at a time.
+    const dim3 rows(num_kv_heads, num_seqs);
+    e = stride <= 4096 ? launch_after_previous(pick_kernel<512, 8>, rows, dim3(512), 0, st, p)
+                       : launch_after_previous(pick_kernel<1024, 16>, rows, dim3(1024), 0, st, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
