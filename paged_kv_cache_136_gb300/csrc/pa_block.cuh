@@ -133,16 +133,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
     return r;
 }
 
-// c += a * b of signed bytes in 32-bit integers: a 16 x 32, b 32 x 8; lane
-// 4g + t holds a of rows g, g + 8, bytes 4t..4t+3 and 16+4t..16+4t+3, and b of
-// column g, the same bytes.
-__device__ __forceinline__ void mma_16832_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1)
+// kv heads that a CTA of eight warps takes side by side: the largest of 8, 4,
+// 2, 1 that divides them.
+inline int heads_log2(int num_kv_heads)
 {
-    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    return num_kv_heads % 8 == 0 ? 3 : num_kv_heads % 4 == 0 ? 2 : num_kv_heads % 2 == 0 ? 1 : 0;
 }
 
 // 16- and 8-byte loads that do not stay in L1.

@@ -111,12 +111,6 @@ static bool make_map(CUtensorMap *map, const void *pool, bool e4m3, int dtype, i
     return r == CUDA_SUCCESS;
 }
 
-// kv heads of a CTA: the largest of 8, 4, 2, 1 that divides them.
-static int heads_log2(int num_kv_heads)
-{
-    return num_kv_heads % 8 == 0 ? 3 : num_kv_heads % 4 == 0 ? 2 : num_kv_heads % 2 == 0 ? 1 : 0;
-}
-
 // Workspace: the cuts, then two partial states of each CTA.
 struct Layout {
     size_t ml, o, total;

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "pa.h"
 #include "pa_block.cuh"
 #include "pa_internal.h"
@@ -33,7 +35,7 @@ struct SelectParams {
     uint32_t *keys;              // [B, Hkv, stride]
     unsigned int *err;
     int num_heads, num_kv_heads, group, num_blocks, max_blocks, block_size, len_cap, most, sink,
-        recent, stride;
+        recent, stride, heads_log2, chunk; // kv heads and 16-block tiles of a score CTA
 };
 
 __device__ __forceinline__ int checked_len(const SelectParams &p, int s, bool report)
@@ -50,31 +52,52 @@ constexpr int kScoreWarps = 8;
 
 // Scores.  With U and L a block's upper and lower codes and c a query's codes,
 //   sum_d c_d (c_d > 0 ? U_d : L_d) = sum_d max(c_d, 0) U_d + min(c_d, 0) L_d,
-// one product of length 2 D in signed bytes, summed exactly in 32-bit
-// integers; times the two powers of two it is exact in fp32.  A warp scores 16
-// consecutive blocks of one (sequence, kv head) against the group's (at most
-// 8) queries with m16n8k32 products, the bounds loaded straight into the
-// operand's registers: contraction index k of a product is any permutation of
-// the channels as long as the queries use the same, so a lane takes 16-byte
-// pieces.  Bound by the read of the bounds, 2 D + 4 bytes a block and head.
+// one product of length 2 D.  A warp scores 16 consecutive blocks of one
+// (sequence, kv head) at a time against the group's (at most 8) queries, the
+// bounds loaded straight into the operand's registers: the contraction index
+// of a product is any permutation of the channels as long as the queries use
+// the same, so a lane takes 16-byte pieces.
+//
+// The products are m16n8k16 in halves (a byte product of this shape is eight
+// times slower here: 65 against 8 cycles an SM quarter), and exact: a code b
+// goes in as the half with the bits b + 128, the subnormal (b + 128) 2^-24,
+// which takes one exclusive-or and two byte permutations for four codes.  The
+// sum of (b + 128) c is a whole number below 255 * 127 * 256 < 2^24 and stays
+// exact in the fp32 accumulator; 128 sum c is taken off at the end.  The two
+// scales are powers of two.  So a score has one value, whatever the order.
+//
+// Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's 8
+// warps are 8 kv heads (or fewer, times several tiles), so that the bounds of a
+// block, which lie together, are read at one time, and go through p.chunk tiles.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p)
+__global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(const SelectParams p)
 {
     constexpr int kPieces = 2 * D / 64;           // 16-byte pieces of a lane and row
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int head = blockIdx.x % p.num_kv_heads;
+    const int warp = threadIdx.x >> 5, groups = p.num_kv_heads >> p.heads_log2;
+    const int head = (blockIdx.x % groups << p.heads_log2) + (warp & ((1 << p.heads_log2) - 1));
+    const int step = 16 * (kScoreWarps >> p.heads_log2); // blocks the CTA takes at a time
     const int s = blockIdx.y;
     const int len = checked_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
     const int n = (len + p.block_size - 1) / p.block_size;
-    const int j0 = (blockIdx.x / p.num_kv_heads * kScoreWarps + (threadIdx.x >> 5)) * 16;
-    if (j0 >= n || n <= p.most)
+    const int first = blockIdx.x / groups * p.chunk * 16;
+    const int last = min(n, first + p.chunk * 16);
+    int j0 = first + (warp >> p.heads_log2) * 16;
+    if (j0 >= last || n <= p.most)
         return;
+    const int32_t *const row = p.tables + (int64_t)s * p.max_blocks;
+    int ids[2]; // blocks of rows g and g + 8
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        ids[r] = j0 + g + 8 * r < last ? row[j0 + g + 8 * r] : -1;
+
     // Query codes: c = rint(q / 2^e), the largest magnitude within 127; NaN
-    // counts as zero.  Lane 4g + t holds query g's channels of its pieces.
-    uint32_t bq[kPieces][4];
-    float qs = 0.f;
+    // counts as zero.  Lane 4g + t holds query g's channels of its pieces, the
+    // positive codes for the upper bounds, then the negative for the lower.
+    uint32_t bq[kPieces][4][2];
+    float qs, off;
     {
         float x[kPieces / 2][16];
         float amax = 0.f;
@@ -98,75 +121,74 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
         qs = pow2_scale<127>(amax);
         const float inv = pow2_inverse(qs);
+        float sum = 0.f;
 #pragma unroll
         for (int c = 0; c < kPieces / 2; ++c)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t pos = 0, neg = 0;
+            for (int k = 0; k < 16; k += 2) {
+                float r[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float f = x[c][4 * w + k];
-                    const float r = f == f ? fminf(fmaxf(rintf(f * inv), -127.f), 127.f) : 0.f;
-                    pos |= (uint32_t)((int)fmaxf(r, 0.f) & 255) << 8 * k;
-                    neg |= (uint32_t)((int)fminf(r, 0.f) & 255) << 8 * k;
+                for (int i = 0; i < 2; ++i) {
+                    const float f = x[c][k + i];
+                    r[i] = f == f ? fminf(fmaxf(rintf(f * inv), -127.f), 127.f) : 0.f;
+                    sum += r[i];
                 }
-                bq[c][w] = pos;
-                bq[kPieces / 2 + c][w] = neg;
+                bq[c][k / 4][k / 2 % 2] = pair_of<__half>(fmaxf(r[0], 0.f), fmaxf(r[1], 0.f));
+                bq[kPieces / 2 + c][k / 4][k / 2 % 2] =
+                    pair_of<__half>(fminf(r[0], 0.f), fminf(r[1], 0.f));
             }
-    }
-    // Block ids of rows g and g + 8.
-    const int ja = j0 + g, jb = j0 + g + 8;
-    int pa = -1, pb = -1;
-    const int32_t *row = p.tables + (int64_t)s * p.max_blocks;
-    if (ja < n)
-        pa = row[ja];
-    if (jb < n)
-        pb = row[jb];
-    const bool bad_a = ja < n && (pa < 0 || pa >= p.num_blocks);
-    const bool bad_b = jb < n && (pb < 0 || pb >= p.num_blocks);
-    if ((bad_a || bad_b) && t == 0)
-        atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
-    if (bad_a || pa < 0)
-        pa = -1;
-    if (bad_b || pb < 0)
-        pb = -1;
-    const int64_t ia = (int64_t)pa * p.num_kv_heads + head, ib = (int64_t)pb * p.num_kv_heads + head;
-    uint4 va[kPieces], vb[kPieces];
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-        va[c] = pa >= 0 ? load16(p.bounds + ia * 2 * D + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-        vb[c] = pb >= 0 ? load16(p.bounds + ib * 2 * D + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-    }
-    const float sa = pa >= 0 ? p.bounds_scale[ia] : 0.f;
-    const float sb = pb >= 0 ? p.bounds_scale[ib] : 0.f;
-    int acc[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-        mma_16832_s8(acc, va[c].x, vb[c].x, va[c].y, vb[c].y, bq[c][0], bq[c][1]);
-        mma_16832_s8(acc, va[c].z, vb[c].z, va[c].w, vb[c].w, bq[c][2], bq[c][3]);
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        off = 128.f * sum;
     }
     // Columns 2t and 2t + 1 are queries 2t and 2t + 1 of the group.
     const float q0 = __shfl_sync(~0u, qs, 8 * t), q1 = __shfl_sync(~0u, qs, 8 * t + 4);
-    float best_a = -INFINITY, best_b = -INFINITY;
-    if (2 * t < p.group) {
-        best_a = (float)acc[0] * q0 * sa;
-        best_b = (float)acc[2] * q0 * sb;
-    }
-    if (2 * t + 1 < p.group) {
-        best_a = fmaxf(best_a, (float)acc[1] * q1 * sa);
-        best_b = fmaxf(best_b, (float)acc[3] * q1 * sb);
-    }
+    const float off0 = __shfl_sync(~0u, off, 8 * t), off1 = __shfl_sync(~0u, off, 8 * t + 4);
+    uint32_t *const keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
+
+    for (; j0 < last; j0 += step) {
+        uint4 v[2][kPieces];
+        float bs[2];
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        best_a = fmaxf(best_a, __shfl_xor_sync(~0u, best_a, o));
-        best_b = fmaxf(best_b, __shfl_xor_sync(~0u, best_b, o));
+        for (int r = 0; r < 2; ++r) {
+            const int j = j0 + g + 8 * r;
+            const bool in = j < last && ids[r] >= 0 && ids[r] < p.num_blocks;
+            if (j < last && !in && t == 0)
+                atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+            const int64_t at = (int64_t)(in ? ids[r] : 0) * p.num_kv_heads + head;
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c)
+                v[r][c] = load16(p.bounds + at * 2 * D + c * 64 + t * 16);
+            bs[r] = in ? p.bounds_scale[at] : 0.f; // a block outside the pool scores 0
+            const int next = j + step;
+            ids[r] = next < last ? row[next] : -1;
+        }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t a = (&v[0][c].x)[w] ^ 0x80808080u, b = (&v[1][c].x)[w] ^ 0x80808080u;
+                mma_16816<__half>(acc, __byte_perm(a, 0, 0x4140), __byte_perm(b, 0, 0x4140),
+                                  __byte_perm(a, 0, 0x4342), __byte_perm(b, 0, 0x4342),
+                                  bq[c][w][0], bq[c][w][1]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int j = j0 + g + 8 * r;
+            float best = -INFINITY;
+            if (2 * t < p.group)
+                best = (acc[2 * r] * 16777216.f - off0) * q0 * bs[r];
+            if (2 * t + 1 < p.group)
+                best = fmaxf(best, (acc[2 * r + 1] * 16777216.f - off1) * q1 * bs[r]);
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
+            if (t == r && j < last)
+                keys[j] = j < p.sink || j >= n - p.recent
+                              ? kKeyKept
+                              : key_of(bs[r] == INFINITY ? INFINITY : best + 0.f);
+        }
     }
-    uint32_t *keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
-    const float inf = INFINITY;
-    if (t == 0 && ja < n)
-        keys[ja] = ja < p.sink || ja >= n - p.recent ? kKeyKept : key_of(sa == inf ? inf : best_a);
-    if (t == 1 && jb < n)
-        keys[jb] = jb < p.sink || jb >= n - p.recent ? kKeyKept : key_of(sb == inf ? inf : best_b);
 }
 
 // Exclusive prefix of a count over the block's threads, and the total.
@@ -409,8 +431,8 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     const int64_t len_cap = (int64_t)max_blocks_per_seq * block_size;
     const int64_t cap = max_seq_len < len_cap ? max_seq_len : len_cap;
     const int stride = (int)key_stride((int)cap, block_size);
-    const int64_t chunks = (stride + 16 * kScoreWarps - 1) / (16 * kScoreWarps);
-    if (chunks * num_kv_heads > INT32_MAX)
+    const int64_t row_tiles = (stride + 15) / 16;
+    if (row_tiles * num_kv_heads > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0)
         return PA_OK;
@@ -444,7 +466,19 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     p.stride = stride;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (stride > max_selected) { // else every block of every sequence is chosen
-        const dim3 grid((unsigned)(chunks * num_kv_heads), num_seqs), threads(32 * kScoreWarps);
+        // Tiles of a CTA: about three CTAs an SM in all, so that the queries'
+        // codes are formed few times, but no more than 16 tiles a warp.
+        const int sms = sm_count(&e);
+        if (!sms)
+            return PA_ERR_CUDA;
+        const int64_t all = row_tiles * num_kv_heads * num_seqs, slots = 3ll * sms * kScoreWarps;
+        const int64_t each = std::min<int64_t>((all + slots - 1) / slots, 16);
+        p.heads_log2 = heads_log2(num_kv_heads);
+        p.chunk = (int)each * (kScoreWarps >> p.heads_log2);
+        const dim3 grid((unsigned)((row_tiles + p.chunk - 1) / p.chunk *
+                                   (num_kv_heads >> p.heads_log2)),
+                        num_seqs);
+        const dim3 threads(32 * kScoreWarps);
         if (dtype == PA_BF16)
             e = head_size == 128
                     ? launch_after_previous(score_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, p)
