@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <stdlib.h>
 #include <algorithm>
 #include <type_traits>
 
@@ -40,10 +41,12 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
                               s, map, p);
     if (e != cudaSuccess)
         return e;
-    // Enough warps for two query rows each of the most cuts there can be, and
-    // at most four CTAs an SM.
+    if (p.whole)
+        return cudaSuccess;
+    // A warp for each query row of the most cuts there can be, as far as three
+    // CTAs an SM go.
     const int rows = p.group << p.heads_log2;
-    const int merge = std::min((ctas * rows + 2 * kMergeWarps - 1) / (2 * kMergeWarps), 2 * kMaxCtas);
+    const int merge = std::min((ctas * rows + kMergeWarps - 1) / kMergeWarps, 3 * kMaxCtas / 2);
     return launch_after_previous(block_merge_kernel<T, E4M3, D>, dim3(merge),
                                  dim3(32 * kMergeWarps), 0, s, p, ctas);
 }
@@ -158,8 +161,24 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     const int64_t cap = len_cap < (int64_t)max_blocks * block_size
                             ? len_cap
                             : (int64_t)max_blocks * block_size;
-    const int hl = heads_log2(num_kv_heads);
-    const int64_t most = lists ? (int64_t)max_listed * (block_size / kTile) : cap / kTile + 1;
+    int hl = heads_log2(num_kv_heads);
+    if (getenv("PA_HL") && atoi(getenv("PA_HL")) < hl) hl = atoi(getenv("PA_HL"));
+    const int64_t all = cap / kTile + 1;
+    const int64_t most = lists ? std::max<int64_t>(1, (int64_t)max_listed * (block_size / kTile)) : all;
+    // Short work is not cut: one CTA a (sequence, head group), of as many heads
+    // as leave a warp 8 tiles at most, if all of them fit the GPU at once.  (A
+    // cut and its merge cost about as much as those 8 tiles.)
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (!sms)
+        return PA_ERR_CUDA;
+    const int slots = std::min((head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2) * sms, kMaxCtas);
+    bool whole = false;
+    for (int h = hl; h >= 0 && !whole; --h)
+        if (most <= 8ll << (3 - h) && (int64_t)num_seqs * (num_kv_heads >> h) <= slots) {
+            whole = true;
+            hl = h;
+        }
     const int64_t tiles = most * num_seqs * (num_kv_heads >> hl);
     if (tiles > INT32_MAX / 2)
         return PA_ERR_UNSUPPORTED;
@@ -168,13 +187,9 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     const Layout w = layout(num_heads, num_kv_heads, head_size);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total)
         return PA_ERR_WORKSPACE;
-    cudaError_t e;
     DecodeArgs p = {};
     p.err = device_error_word(&e);
     if (!p.err)
-        return PA_ERR_CUDA;
-    const int sms = sm_count(&e);
-    if (!sms)
         return PA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     p.out = out;
@@ -200,13 +215,10 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.max_listed = max_listed;
     p.len_cap = (int)cap;
     p.qscale = scale * 1.4426950408889634f;
-    // At least kMinRun tiles a warp: no more CTAs than that can use.
-    int64_t ctas = tiles / (kMinRun * (kWarps >> hl)) + 1;
-    const int per_sm = head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2;
-    if (ctas > per_sm * sms)
-        ctas = per_sm * sms;
-    if (ctas > kMaxCtas)
-        ctas = kMaxCtas;
+    p.whole = whole;
+    // Else equal runs, of at least kMinRun tiles a warp.
+    const int64_t ctas = whole ? (int64_t)num_seqs * p.num_groups
+                               : std::min<int64_t>(tiles / (kMinRun * (kWarps >> hl)) + 1, slots);
     alignas(64) CUtensorMap map;
     if (!make_map(&map, kv_cache, kv_scales != nullptr, dtype, num_blocks, block_size,
                   num_kv_heads, head_size))

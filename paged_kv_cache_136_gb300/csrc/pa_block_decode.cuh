@@ -68,6 +68,7 @@ struct DecodeArgs {
     float *ws_ml;              // [CTAs, 2, HG * G, 2]
     int num_seqs, num_heads, num_kv_heads, group, heads_log2, num_groups, num_blocks, max_blocks,
         block_log2, max_listed, len_cap;
+    int whole;                 // a CTA is one (sequence, head group): nothing is cut
     float qscale;              // scale * log2 e
 };
 
@@ -169,6 +170,13 @@ template <bool E4M3, int D> constexpr int decode_smem(bool hand_over)
            (hand_over ? kWarps / 2 * 4 * (D + 2) * 4 : 0);
 }
 
+// Where a warp's walk over its CTA's run stands.
+struct Walk {
+    int at, seq, tiles, grp, seg; // run position; (sequence, group), its tiles and first one
+    int len, listed, next, left, flags; // of the part being walked: tokens, list entries, the
+                                        // warp's next tile and how many it has left
+};
+
 __device__ __forceinline__ void tma_load_5d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
                                                  int c0, int c1, int c2, int c3, int c4,
                                                  uint64_t policy)
@@ -214,7 +222,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
     constexpr int kStages = stages_of<E4M3, D>();
     constexpr int kTileBytes = tile_bytes<E4M3, D>();
     extern __shared__ char smem_raw[];
-    __shared__ int first_seq, first_base, warp_sums[kWarps];
+    __shared__ int3 first; // sequence that the run begins in, its first tile, its tiles
+    __shared__ int warp_sums[kWarps];
+    __shared__ Walk walks[kWarps];
 
     char *const smem = smem_raw + (-smem_addr(smem_raw) & 1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -235,137 +245,152 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
     griddep_launch_dependents();
 
     // ---- this CTA's run: [begin, end) of the line of tiles ----
-    const int slice = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
-    const int s_lo = min(tid * slice, p.num_seqs), s_hi = min(s_lo + slice, p.num_seqs);
-    int mine = 0;
-    for (int s = s_lo; s < s_hi; ++s)
-        mine += tiles_of(p, s, blockIdx.x == 0);
-    mine *= p.num_groups;
-    int x = mine;
+    int run = 0, begin = 0, end;
+    int f_seq, f_tiles, f_grp, f_seg; // sequence and group that it begins in
+    if (p.whole) {
+        f_seq = blockIdx.x / p.num_groups;
+        f_grp = blockIdx.x - f_seq * p.num_groups;
+        f_seg = 0;
+        end = f_tiles = tiles_of(p, f_seq, warp == 0);
+    } else {
+        const int slice = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
+        const int s_lo = min(tid * slice, p.num_seqs), s_hi = min(s_lo + slice, p.num_seqs);
+        int mine = 0;
+        for (int s = s_lo; s < s_hi; ++s)
+            mine += tiles_of(p, s, blockIdx.x == 0);
+        mine *= p.num_groups;
+        int x = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    if (lane == 31)
-        warp_sums[warp] = x;
-    __syncthreads();
-    int base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        base += w < warp ? warp_sums[w] : 0;
-        total += warp_sums[w];
-    }
-    base += x - mine;
-    const int run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinRun * tws);
-    const int begin = blockIdx.x * run, end = min(begin + run, total);
-    if (tid == 0)
-        p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (begin >= total)
-        return;
-    if (begin >= base && begin < base + mine) {
-        int s = s_lo;
-        while (true) {
-            const int n = tiles_of(p, s, false) * p.num_groups;
-            if (begin < base + n)
-                break;
-            base += n;
-            ++s;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o)
+                x += y;
         }
-        first_seq = s;
-        first_base = base;
+        if (lane == 31)
+            warp_sums[warp] = x;
+        __syncthreads();
+        int base = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            base += w < warp ? warp_sums[w] : 0;
+            total += warp_sums[w];
+        }
+        base += x - mine;
+        run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinRun * tws);
+        begin = blockIdx.x * run;
+        end = min(begin + run, total);
+        if (tid == 0)
+            p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (begin >= total)
+            return;
+        if (begin >= base && begin < base + mine) {
+            int s = s_lo, n = slice == 1 ? mine : tiles_of(p, s, false) * p.num_groups;
+            while (begin >= base + n) {
+                base += n;
+                n = tiles_of(p, ++s, false) * p.num_groups;
+            }
+            first = make_int3(s, base, n);
+        }
+        __syncthreads();
+        f_seq = first.x;
+        f_tiles = first.z / p.num_groups;
+        f_grp = (begin - first.y) / f_tiles;
+        f_seg = first.y + f_grp * f_tiles;
     }
-    __syncthreads();
 
     // ---- the walk that fetches: one part of a (sequence, group) after the
-    // other, in batches of 32 tiles whose places the lanes look up at once ----
-    int f_at = begin, f_seq = first_seq, f_tiles = tiles_of(p, f_seq, false);
-    int f_grp = (begin - first_base) / f_tiles, f_seg = first_base + f_grp * f_tiles;
-    int f_len = 0, f_listed = 0, f_next = 0, f_left = 0, f_flags = 0; // of the part
-    // the batch being fetched, and the one behind it
-    int b_row = 0, b_live = 0, b_n = 0, b_i = 0, b_seq = 0, b_head = 0, b_flags = 0, b_last = 0;
-    int n_row = 0, n_live = 0, n_n = 0, n_seq = 0, n_head = 0, n_flags = 0, n_last = 0;
+    // other, in batches of 32 tiles whose places the lanes look up at once.
+    // Its state is looked at once a batch and waits in shared memory. ----
+    Walk &walk = walks[warp];
+    if (lane == 0)
+        walk = Walk{begin, f_seq, f_tiles, f_grp, f_seg, 0, 0, 0, 0, 0};
+    __syncwarp();
+    // The batch being fetched, and the one behind it: a lane's tile (first pool
+    // row, scales, live | flags << 8 | batch's last tile ends the part << 12 |
+    // tiles of the batch << 16) and whose it is (sequence << 16 | head).
+    int b_row = 0, b_info = 0, b_whose = 0, b_i = 0, n_row = 0, n_info = 0, n_whose = 0;
     float b_ks = 1.f, b_vs = 1.f, n_ks = 1.f, n_vs = 1.f;
 
     auto look_up = [&]() { // fills the batch behind
-        n_n = 0;
-        if (f_left == 0) {
-            if (f_at >= end)
+        Walk w = walk;
+        n_info = 0;
+        if (w.left == 0) {
+            if (w.at >= end)
                 return;
-            const int seg_end = f_seg + f_tiles, stop = min(end, seg_end);
-            f_flags = (f_at == f_seg ? kBegins : 0) | (stop == seg_end ? kEnds : 0);
-            f_len = length_of(p, f_seq, lane == 0 && warp == 0);
-            f_listed = p.lists ? min(__ldg(p.list_lens + f_seq), p.max_listed) : 0;
-            f_next = f_at - f_seg + tw;
+            const int seg_end = w.seg + w.tiles, stop = min(end, seg_end);
+            w.flags = (w.at == w.seg ? kBegins : 0) | (stop == seg_end ? kEnds : 0);
+            w.len = length_of(p, w.seq, lane == 0 && warp == 0);
+            w.listed = p.lists ? min(__ldg(p.list_lens + w.seq), p.max_listed) : 0;
+            w.next = w.at - w.seg + tw;
             // a warp without a tile takes an empty one: all meet at the part's end
-            f_left = max(1, (stop - f_at - tw + tws - 1) / tws);
-            if (stop - f_at <= tw)
-                f_next = -1;
-            if (tid == 0 && f_flags == kBegins)
+            w.left = max(1, (stop - w.at - tw + tws - 1) / tws);
+            if (stop - w.at <= tw)
+                w.next = -1;
+            if (tid == 0 && w.flags == kBegins)
                 p.cuts[blockIdx.x] =
-                    make_int4(f_seq, f_grp, (seg_end - 1) / run - (int)blockIdx.x + 1, 0);
-            n_seq = f_seq;
-            n_head = (f_grp << p.heads_log2) + hl;
-            f_at = stop;
+                    make_int4(w.seq, w.grp, (seg_end - 1) / run - (int)blockIdx.x + 1, 0);
+            w.at = stop;
         }
-        n_flags = f_flags;
-        n_n = min(32, f_left);
-        f_left -= n_n;
-        n_last = f_left == 0;
+        const int head = (w.grp << p.heads_log2) + hl, n = min(32, w.left);
+        n_whose = w.seq << 16 | head;
+        w.left -= n;
+        int live = 0;
         n_row = -1;
-        n_live = 0;
-        if (lane < n_n && f_next >= 0)
-            locate(p, n_seq, n_head, f_next + lane * tws, f_len, f_listed, n_row, n_live);
+        if (lane < n && w.next >= 0)
+            locate(p, w.seq, head, w.next + lane * tws, w.len, w.listed, n_row, live);
+        n_info = live | w.flags << 8 | (w.left == 0 ? 1 << 12 : 0) | n << 16;
         if constexpr (E4M3) {
             n_ks = n_vs = 1.f;
             if (n_row >= 0) {
                 const float *sc = p.scales + (int64_t)(n_row >> p.block_log2) * p.num_kv_heads +
-                                  n_head;
+                                  head;
                 n_ks = __ldg(sc);
                 n_vs = __ldg(sc + (int64_t)p.num_blocks * p.num_kv_heads);
             }
         }
-        f_next += 32 * tws;
-        if (n_last) {
-            if (f_at == f_seg + f_tiles) {
-                f_seg = f_at;
-                if (++f_grp == p.num_groups) {
-                    f_grp = 0;
-                    if (++f_seq < p.num_seqs)
-                        f_tiles = tiles_of(p, f_seq, false);
-                }
+        w.next += 32 * tws;
+        if (w.left == 0 && w.at == w.seg + w.tiles) {
+            w.seg = w.at;
+            if (++w.grp == p.num_groups) {
+                w.grp = 0;
+                if (++w.seq < p.num_seqs)
+                    w.tiles = tiles_of(p, w.seq, false);
             }
         }
+        __syncwarp();
+        if (lane == 0)
+            walk = w;
+        __syncwarp();
     };
 
     const uint64_t policy = policy_evict_first();
     bool lost = false;
     auto fetch = [&](int stage) { // the next tile, or the end, into `stage`
-        if (b_i == b_n) {
-            b_row = n_row, b_live = n_live, b_n = n_n, b_seq = n_seq, b_head = n_head;
-            b_flags = n_flags, b_last = n_last, b_ks = n_ks, b_vs = n_vs;
+        if (b_i == b_info >> 16) {
+            b_row = n_row, b_info = n_info, b_whose = n_whose, b_ks = n_ks, b_vs = n_vs;
             b_i = 0;
-            if (b_n > 0)
+            if (b_info >> 16)
                 look_up();
         }
         Meta &m = meta[stage];
-        if (b_i < b_n) {
+        if (b_i < b_info >> 16) {
             if (lane == b_i) {
+                const int live = b_info & 255;
+                const bool ends = b_info >> 12 & 1 && b_i + 1 == b_info >> 16;
                 *reinterpret_cast<int4 *>(&m) =
-                    make_int4(b_live, b_seq, b_head,
-                              b_flags | (b_last && b_i + 1 == b_n ? kLast : 0));
+                    make_int4(live, b_whose >> 16 & 0xFFFF, b_whose & 0xFFFF,
+                              (b_info >> 8 & 15) | (ends ? kLast : 0));
                 if (lost) {
-                } else if (b_live) {
+                } else if (live) {
                     // a row past the pool reads as zeros
                     const int row = b_row < 0 ? p.num_blocks << p.block_log2 : b_row;
                     mbar_arrive_expect_tx(&m.bar, kTileBytes);
                     if constexpr (kRow == 256)
                         tma_load_5d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row, 0,
-                                         b_head, 0, policy);
+                                         b_whose & 0xFFFF, 0, policy);
                     else
                         tma_load_4d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row,
-                                         b_head, 0, policy);
+                                         b_whose & 0xFFFF, 0, policy);
                     if constexpr (E4M3)
                         *reinterpret_cast<float2 *>(&m.k_scale) = make_float2(b_ks, b_vs);
                 } else {
@@ -406,6 +431,22 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
     int stage = 0, drain = 0;
     uint32_t parity = 0;
     while (true) {
+        __syncwarp();
+        const int4 info = *reinterpret_cast<const int4 *>(&meta[stage]);
+        const int s = info.y, head = info.z, flags = info.w;
+        if (flags < 0)
+            break;
+        if (fresh) { // a part begins: ask for the query rows of the group
+            const T *q = static_cast<const T *>(p.q) +
+                         ((int64_t)s * p.num_heads + head * p.group + min(g, p.group - 1)) * D;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int d = E4M3 ? (i / 4) * 64 + t * 16 + (i % 4) * 4
+                                   : (i / 2) * 32 + t * 8 + (i % 2) * 4;
+                const uint2 v = *reinterpret_cast<const uint2 *>(q + d);
+                qf[i][0] = v.x, qf[i][1] = v.y;
+            }
+        }
         // A copy that does not arrive is reported; the warp then starts no
         // more, waits (within the limit) for those in flight, and walks on
         // without data, so that it still meets the others.
@@ -420,36 +461,26 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     atomicOr(p.err, PA_DEVERR_TIMEOUT_);
             }
         }
-        __syncwarp();
-        const int4 info = *reinterpret_cast<const int4 *>(&meta[stage]);
-        const int live = lost ? 0 : info.x, s = info.y, head = info.z, flags = info.w;
-        if (flags < 0)
-            break;
         // every lane has left the stage before this one: refill it
         fetch(stage == 0 ? kStages - 1 : stage - 1);
 
-        if (fresh) { // a part begins
+        const int live = lost ? 0 : info.x;
+
+        if (fresh) {
             fresh = false;
-            // Query rows of the group, as the products take them; for e4m3 in
-            // halves, scaled by a power of two so that the largest is near 2^15
-            // (bf16 values keep their 8 bits over 29 binades below it).
-            const T *q = static_cast<const T *>(p.q) +
-                         ((int64_t)s * p.num_heads + head * p.group + min(g, p.group - 1)) * D;
+            // The queries as the products take them; for e4m3 in halves, bf16
+            // ones scaled by a power of two so that the largest is near 2^15
+            // (they keep their 8 bits over 29 binades below it).
             qmul0 = qmul1 = p.qscale;
-            uint2 raw[kSteps];
+            if (g >= p.group)
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int d = E4M3 ? (i / 4) * 64 + t * 16 + (i % 4) * 4
-                                   : (i / 2) * 32 + t * 8 + (i % 2) * 4;
-                raw[i] = *reinterpret_cast<const uint2 *>(q + d);
-                if (g >= p.group)
-                    raw[i] = make_uint2(0, 0);
-            }
+                for (int i = 0; i < kSteps; ++i)
+                    qf[i][0] = qf[i][1] = 0;
             if constexpr (E4M3 && std::is_same<T, __nv_bfloat16>::value) {
                 float amax = 0.f;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const float2 a = float2_of<T>(raw[i].x), b = float2_of<T>(raw[i].y);
+                    const float2 a = float2_of<T>(qf[i][0]), b = float2_of<T>(qf[i][1]);
                     amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)),
                                              fmaxf(fabsf(b.x), fabsf(b.y))));
                 }
@@ -459,17 +490,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                 const float down = two_to(-e);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const float2 a = float2_of<T>(raw[i].x), b = float2_of<T>(raw[i].y);
+                    const float2 a = float2_of<T>(qf[i][0]), b = float2_of<T>(qf[i][1]);
                     qf[i][0] = pair_of<__half>(a.x * down, a.y * down);
                     qf[i][1] = pair_of<__half>(b.x * down, b.y * down);
                 }
                 const float up = two_to(e);
                 qmul0 *= __shfl_sync(~0u, up, 8 * t);
                 qmul1 *= __shfl_sync(~0u, up, 8 * t + 4);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    qf[i][0] = raw[i].x, qf[i][1] = raw[i].y;
             }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
@@ -709,82 +736,91 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 // Merge of the (sequence, group)s that a cut divides: with M = max m_i,
 // out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Every CTA lists the cuts;
 // the (cut, query row) pairs then go round the warps, or round the CTAs, whose
-// warps split the states, where there are too few to fill the warps.  Lane i
-// weighs state i; a row of a state is one coalesced read.
-constexpr int kMergeWarps = 8;
+// warps split the states, where there are too few to fill the warps.  Bound by
+// latency, so that what a row needs is asked for at once: four states' m, l
+// and o at a time.
+constexpr int kMergeWarps = 10; // a thread for each cut there can be
+static_assert(32 * kMergeWarps >= kMaxCtas, "one look at the cuts");
 
 template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const DecodeArgs p, int ctas)
 {
     constexpr float kLift = lift_of<typename std::conditional<E4M3, __half, T>::type>();
     constexpr int kCols = D / 32;                // columns of a lane
+    constexpr int kAtOnce = 4;
     using Vec = typename std::conditional<kCols == 4, float4, float2>::type;
-    __shared__ uint16_t list[kMaxCtas];          // CTAs whose cut is to be merged
-    __shared__ int counts[kMergeWarps + 1];
+    __shared__ int4 list[kMaxCtas];              // sequence, head group, states, first CTA
+    __shared__ int counts[kMergeWarps];
     __shared__ float part[kMergeWarps][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    int found = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32 * kMergeWarps) {
-        const int c = c0 + threadIdx.x;
-        const bool mine = c < ctas && p.cuts[c].z >= 2;
-        const unsigned some = __ballot_sync(~0u, mine);
-        if (lane == 0)
-            counts[warp] = __popc(some);
-        __syncthreads();
-        int at = found + __popc(some & ((1u << lane) - 1));
+    int4 seen = make_int4(0, 0, 0, 0);
+    if ((int)threadIdx.x < ctas)
+        seen = p.cuts[threadIdx.x];
+    seen.w = threadIdx.x;
+    const unsigned some = __ballot_sync(~0u, seen.z >= 2);
+    if (lane == 0)
+        counts[warp] = __popc(some);
+    __syncthreads();
+    int at = __popc(some & ((1u << lane) - 1)), found = 0;
 #pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
-            at += w < warp ? counts[w] : 0;
-            found += counts[w];
-        }
-        if (mine)
-            list[at] = (uint16_t)c;
-        __syncthreads();
+    for (int w = 0; w < kMergeWarps; ++w) {
+        at += w < warp ? counts[w] : 0;
+        found += counts[w];
     }
+    if (seen.z >= 2)
+        list[at] = seen;
+    __syncthreads();
     const int rows = p.group << p.heads_log2, items = found * rows;
     const bool wide = items * 2 <= (int)gridDim.x * kMergeWarps;
     const int step = wide ? gridDim.x : gridDim.x * kMergeWarps;
     for (int item = wide ? blockIdx.x : blockIdx.x * kMergeWarps + warp; item < items;
          item += step) {
-        const int begun = list[item / rows];
-        const int4 cut = p.cuts[begun];          // sequence, head group, states
-        const int r = item % rows, first = wide ? warp : 0, each = wide ? kMergeWarps : 1;
-        // states first, first + each, ..., 32 at a time
+        const int4 cut = list[item / rows];
+        const int r = item % rows, each = wide ? kMergeWarps : 1;
         float top = kNone, l = 0.f, acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
             acc[k] = 0.f;
-        for (int i0 = first; i0 < cut.z; i0 += 32 * each) {
-            const int i = i0 + lane * each, n = min(32, (cut.z - i0 + each - 1) / each);
-            float2 ml = make_float2(kNone, 0.f);
-            const int64_t row = (int64_t)(2 * (begun + i) + (i == 0)) * rows + r;
-            if (lane < n)
-                ml = *reinterpret_cast<const float2 *>(p.ws_ml + row * 2);
-            const float now = fmaxf(top, warp_max(ml.x));
-            const float weight = ex2(ml.x - now), old = ex2(top - now);
+        for (int i0 = wide ? warp : 0; i0 < cut.z; i0 += kAtOnce * each) {
+            float2 ml[kAtOnce];
+            Vec v[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int i = i0 + j * each;
+                // the state of the CTA that began the pair, or of one that went on
+                const int64_t row = (int64_t)(2 * (cut.w + i) + (i == 0)) * rows + r;
+                ml[j] = make_float2(kNone, 0.f);
+                if (i < cut.z) {
+                    ml[j] = *reinterpret_cast<const float2 *>(p.ws_ml + row * 2);
+                    v[j] = reinterpret_cast<const Vec *>(p.ws_o + row * D)[lane];
+                }
+            }
+            float now = top;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                now = fmaxf(now, ml[j].x);
+            const float old = ex2(top - now);
             top = now;
-            l = l * old + weight * ml.y;         // summed over the lanes below
+            l *= old;
 #pragma unroll
             for (int k = 0; k < kCols; ++k)
                 acc[k] *= old;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const int64_t src = __shfl_sync(~0u, row, j);
-                const float w = __shfl_sync(~0u, weight, j);
-                const Vec v = reinterpret_cast<const Vec *>(p.ws_o + src * D)[lane];
-                acc[0] += w * v.x;
-                acc[1] += w * v.y;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (i0 + j * each >= cut.z)
+                    continue;
+                const float w = ex2(ml[j].x - now);
+                l += w * ml[j].y;
+                acc[0] += w * v[j].x;
+                acc[1] += w * v[j].y;
                 if constexpr (kCols == 4) {
-                    acc[2] += w * v.z;
-                    acc[3] += w * v.w;
+                    acc[2] += w * v[j].z;
+                    acc[3] += w * v[j].w;
                 }
             }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            l += __shfl_xor_sync(~0u, l, o);
         if (wide) {
             __syncthreads();
 #pragma unroll
@@ -797,7 +833,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
             __syncthreads();
             if (warp)
                 continue;
-            for (int w = 1; w < kMergeWarps; ++w) {
+            for (int w = 1; w < min(kMergeWarps, cut.z); ++w) {
                 const float now = fmaxf(top, part[w][D]);
                 const float a = ex2(top - now), b = ex2(part[w][D] - now);
                 top = now;
