@@ -4,7 +4,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <stdlib.h>
 #include <algorithm>
 #include <type_traits>
 
@@ -162,7 +161,6 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
                             ? len_cap
                             : (int64_t)max_blocks * block_size;
     int hl = heads_log2(num_kv_heads);
-    if (getenv("PA_HL") && atoi(getenv("PA_HL")) < hl) hl = atoi(getenv("PA_HL"));
     const int64_t all = cap / kTile + 1;
     const int64_t most = lists ? std::max<int64_t>(1, (int64_t)max_listed * (block_size / kTile)) : all;
     // Short work is not cut: one CTA a (sequence, head group), of as many heads

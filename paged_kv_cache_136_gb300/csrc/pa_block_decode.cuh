@@ -735,10 +735,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 
 // Merge of the (sequence, group)s that a cut divides: with M = max m_i,
 // out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Every CTA lists the cuts;
-// the (cut, query row) pairs then go round the warps, or round the CTAs, whose
-// warps split the states, where there are too few to fill the warps.  Bound by
-// latency, so that what a row needs is asked for at once: four states' m, l
-// and o at a time.
+// the (cut, query row) pairs then go round the warps, or round pairs, halves
+// or wholes of a CTA's warps, which split the states, where there are many
+// states and too few rows to fill the warps.  Bound by latency, so that what a
+// row needs is asked for at once: four states' m, l and o at a time.
 constexpr int kMergeWarps = 10; // a thread for each cut there can be
 static_assert(32 * kMergeWarps >= kMaxCtas, "one look at the cuts");
 
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
     constexpr int kAtOnce = 4;
     using Vec = typename std::conditional<kCols == 4, float4, float2>::type;
     __shared__ int4 list[kMaxCtas];              // sequence, head group, states, first CTA
-    __shared__ int counts[kMergeWarps];
+    __shared__ int counts[kMergeWarps], most[kMergeWarps];
     __shared__ float part[kMergeWarps][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
@@ -760,30 +760,40 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
         seen = p.cuts[threadIdx.x];
     seen.w = threadIdx.x;
     const unsigned some = __ballot_sync(~0u, seen.z >= 2);
-    if (lane == 0)
+    const int longest = __reduce_max_sync(~0u, seen.z);
+    if (lane == 0) {
         counts[warp] = __popc(some);
+        most[warp] = longest;
+    }
     __syncthreads();
-    int at = __popc(some & ((1u << lane) - 1)), found = 0;
+    int at = __popc(some & ((1u << lane) - 1)), found = 0, states = 0;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
         at += w < warp ? counts[w] : 0;
         found += counts[w];
+        states = max(states, most[w]);
     }
     if (seen.z >= 2)
         list[at] = seen;
     __syncthreads();
     const int rows = p.group << p.heads_log2, items = found * rows;
-    const bool wide = items * 2 <= (int)gridDim.x * kMergeWarps;
-    const int step = wide ? gridDim.x : gridDim.x * kMergeWarps;
-    for (int item = wide ? blockIdx.x : blockIdx.x * kMergeWarps + warp; item < items;
-         item += step) {
-        const int4 cut = list[item / rows];
-        const int r = item % rows, each = wide ? kMergeWarps : 1;
+    // warps of a row: 1, 2, 5 or all 10, with at least kAtOnce states each
+    int each = 1;
+#pragma unroll
+    for (int e = 2; e <= 10; e = e == 2 ? 5 : e + 5)
+        if (states > kAtOnce * (e - 1) && items * e <= (int)gridDim.x * kMergeWarps)
+            each = e;
+    const int at_once = kMergeWarps / each, mine = warp / each, lead = mine * each;
+    for (int item0 = blockIdx.x * at_once; item0 < items; item0 += gridDim.x * at_once) {
+        const int item = item0 + mine;
+        const bool some_row = item < items;
+        const int4 cut = some_row ? list[item / rows] : make_int4(0, 0, 0, 0);
+        const int r = item % rows;
         float top = kNone, l = 0.f, acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
             acc[k] = 0.f;
-        for (int i0 = wide ? warp : 0; i0 < cut.z; i0 += kAtOnce * each) {
+        for (int i0 = warp - lead; i0 < cut.z; i0 += kAtOnce * each) {
             float2 ml[kAtOnce];
             Vec v[kAtOnce];
 #pragma unroll
@@ -821,7 +831,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
                 }
             }
         }
-        if (wide) {
+        if (each > 1) {
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kCols; ++k)
@@ -831,9 +841,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
                 part[warp][D + 1] = l;
             }
             __syncthreads();
-            if (warp)
+            if (warp != lead)
                 continue;
-            for (int w = 1; w < min(kMergeWarps, cut.z); ++w) {
+            for (int w = lead + 1; w < lead + min(each, cut.z); ++w) {
                 const float now = fmaxf(top, part[w][D]);
                 const float a = ex2(top - now), b = ex2(part[w][D] - now);
                 top = now;
@@ -843,6 +853,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
                     acc[k] = acc[k] * a + b * part[w][lane * kCols + k];
             }
         }
+        if (!some_row)
+            continue;
         const int64_t row = (int64_t)cut.x * p.num_heads + (int64_t)cut.y * rows + r;
         const float inv = l != 0.f ? 1.f / l : 0.f;
         uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + row * D) +
