@@ -157,20 +157,24 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
         num_seqs > 65535)
         return PA_ERR_UNSUPPORTED;
     // tiles are counted in 32 bits
-    const int64_t cap = len_cap < (int64_t)max_blocks * block_size
-                            ? len_cap
-                            : (int64_t)max_blocks * block_size;
-    int hl = heads_log2(num_kv_heads);
-    const int64_t all = cap / kTile + 1;
-    const int64_t most = lists ? std::max<int64_t>(1, (int64_t)max_listed * (block_size / kTile)) : all;
-    // Short work is not cut: one CTA a (sequence, head group), of as many heads
-    // as leave a warp 8 tiles at most, if all of them fit the GPU at once.  (A
-    // cut and its merge cost about as much as those 8 tiles.)
+    const int64_t cap = std::min<int64_t>(len_cap, (int64_t)max_blocks * block_size);
+    const int64_t most = lists ? (int64_t)max_listed * (block_size / kTile) : cap / kTile + 1;
+    if (most * num_seqs > INT32_MAX / 2 / num_kv_heads)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return PA_OK;
+    const Layout w = layout(num_heads, num_kv_heads, head_size);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total)
+        return PA_ERR_WORKSPACE;
     cudaError_t e;
     const int sms = sm_count(&e);
     if (!sms)
         return PA_ERR_CUDA;
+    // Short work is not cut: one CTA a (sequence, head group), of as many heads
+    // as leave a warp 8 tiles at most, if all of them fit the GPU at once.  (A
+    // cut and its merge cost about as much as those 8 tiles.)
     const int slots = std::min((head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2) * sms, kMaxCtas);
+    int hl = heads_log2(num_kv_heads);
     bool whole = false;
     for (int h = hl; h >= 0 && !whole; --h)
         if (most <= 8ll << (3 - h) && (int64_t)num_seqs * (num_kv_heads >> h) <= slots) {
@@ -178,13 +182,6 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
             hl = h;
         }
     const int64_t tiles = most * num_seqs * (num_kv_heads >> hl);
-    if (tiles > INT32_MAX / 2)
-        return PA_ERR_UNSUPPORTED;
-    if (num_seqs == 0)
-        return PA_OK;
-    const Layout w = layout(num_heads, num_kv_heads, head_size);
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total)
-        return PA_ERR_WORKSPACE;
     DecodeArgs p = {};
     p.err = device_error_word(&e);
     if (!p.err)

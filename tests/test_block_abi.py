@@ -170,13 +170,13 @@ def test_binding_wants_cuda_tensors(pa, name):
 def test_binding_wants_the_current_device(pa, monkeypatch):
     monkeypatch.setattr(pa, "_current_device", lambda: 0)
     here, there, host = (types.SimpleNamespace(get_device=lambda i=i: i) for i in (0, 1, -1))
-    pa._here((("a", here), ("b", here)))
+    pa._here("a b", here, here)
     with pytest.raises(ValueError, match="b must be a CUDA tensor"):
-        pa._here((("a", here), ("b", host)))
-    with pytest.raises(ValueError, match="a must be on the current device, cuda:0"):
-        pa._here((("a", there), ("b", here)))
+        pa._here("a b", here, host)
     with pytest.raises(ValueError, match="b must be on the current device, cuda:0"):
-        pa._here((("a", here), ("b", there)))
+        pa._here("a b", here, there)
+    with pytest.raises(ValueError, match="a must be on the current device, cuda:0"):
+        pa._here("a b", there, there)
 
 
 @pytest.mark.parametrize("field,value,names", [
@@ -219,7 +219,7 @@ def test_binding_checks_shapes(pa, field, value, names):
 
 def test_a_broadcast_key_is_refused(pa, monkeypatch):
     """A row stride of zero is no row stride: the C call refuses it."""
-    monkeypatch.setattr(pa, "_here", lambda named: None)
+    monkeypatch.setattr(pa, "_here", lambda *a: None)
     monkeypatch.setattr(pa, "_stream", lambda stream: 0)
     a = _args()
     a.key = torch.zeros(1, 2, 64, dtype=torch.float16).expand(3, 2, 64)
