@@ -69,8 +69,10 @@ constexpr int kScoreWarps = 8;
 // Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's 8
 // warps are 8 kv heads (or fewer, times several tiles), so that the bounds of a
 // block, which lie together, are read at one time, and go through p.chunk tiles.
+// A tile's bounds are asked for while the tile before it (or the queries) are
+// worked on.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(const SelectParams p)
+__global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const SelectParams p)
 {
     constexpr int kPieces = 2 * D / 64;           // 16-byte pieces of a lane and row
     griddep_wait();
@@ -88,10 +90,38 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(const Select
     if (j0 >= last || n <= p.most)
         return;
     const int32_t *const row = p.tables + (int64_t)s * p.max_blocks;
-    int ids[2]; // blocks of rows g and g + 8
+    // Rows g and g + 8 of a tile: blocks, then bounds and scales.
+    int ids[2];
+    uint4 v[2][kPieces];
+    float bs[2];
+    auto name = [&](int j) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            ids[r] = j + g + 8 * r < last ? row[j + g + 8 * r] : -1;
+    };
+    auto read = [&](int j) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool past = j + g + 8 * r >= last;
+            const bool in = !past && ids[r] >= 0 && ids[r] < p.num_blocks;
+            if (!past && !in && t == 0)
+                atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+            const int64_t at = (int64_t)(in ? ids[r] : 0) * p.num_kv_heads + head;
+            if (!past)
+#pragma unroll
+                for (int c = 0; c < kPieces; ++c)
+                    v[r][c] = load16(p.bounds + at * 2 * D + c * 64 + t * 16);
+            bs[r] = in ? p.bounds_scale[at] : 0.f; // a block outside the pool scores 0
+        }
+    };
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-        ids[r] = j0 + g + 8 * r < last ? row[j0 + g + 8 * r] : -1;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c)
+            v[r][c] = make_uint4(0, 0, 0, 0);
+    name(j0);
+    read(j0);
+    name(j0 + step);
 
     // Query codes: c = rint(q / 2^e), the largest magnitude within 127; NaN
     // counts as zero.  Lane 4g + t holds query g's channels of its pieces, the
@@ -147,46 +177,48 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(const Select
     uint32_t *const keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
 
     for (; j0 < last; j0 += step) {
-        uint4 v[2][kPieces];
-        float bs[2];
+        uint4 now[2][kPieces];
+        float scale[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int j = j0 + g + 8 * r;
-            const bool in = j < last && ids[r] >= 0 && ids[r] < p.num_blocks;
-            if (j < last && !in && t == 0)
-                atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
-            const int64_t at = (int64_t)(in ? ids[r] : 0) * p.num_kv_heads + head;
+            scale[r] = bs[r];
 #pragma unroll
             for (int c = 0; c < kPieces; ++c)
-                v[r][c] = load16(p.bounds + at * 2 * D + c * 64 + t * 16);
-            bs[r] = in ? p.bounds_scale[at] : 0.f; // a block outside the pool scores 0
-            const int next = j + step;
-            ids[r] = next < last ? row[next] : -1;
+                now[r][c] = v[r][c];
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j0 + step < last) {
+            read(j0 + step);
+            name(j0 + 2 * step);
+        }
+        // two chains of products
+        float acc[4] = {0.f, 0.f, 0.f, 0.f}, more[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kPieces; ++c)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t a = (&v[0][c].x)[w] ^ 0x80808080u, b = (&v[1][c].x)[w] ^ 0x80808080u;
-                mma_16816<__half>(acc, __byte_perm(a, 0, 0x4140), __byte_perm(b, 0, 0x4140),
-                                  __byte_perm(a, 0, 0x4342), __byte_perm(b, 0, 0x4342),
-                                  bq[c][w][0], bq[c][w][1]);
+                const uint32_t a = (&now[0][c].x)[w] ^ 0x80808080u;
+                const uint32_t b = (&now[1][c].x)[w] ^ 0x80808080u;
+                mma_16816<__half>(w % 2 ? more : acc, __byte_perm(a, 0, 0x4140),
+                                  __byte_perm(b, 0, 0x4140), __byte_perm(a, 0, 0x4342),
+                                  __byte_perm(b, 0, 0x4342), bq[c][w][0], bq[c][w][1]);
             }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            acc[k] += more[k]; // exact, as the sums are
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int j = j0 + g + 8 * r;
             float best = -INFINITY;
             if (2 * t < p.group)
-                best = (acc[2 * r] * 16777216.f - off0) * q0 * bs[r];
+                best = (acc[2 * r] * 16777216.f - off0) * q0 * scale[r];
             if (2 * t + 1 < p.group)
-                best = fmaxf(best, (acc[2 * r + 1] * 16777216.f - off1) * q1 * bs[r]);
+                best = fmaxf(best, (acc[2 * r + 1] * 16777216.f - off1) * q1 * scale[r]);
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
             if (t == r && j < last)
                 keys[j] = j < p.sink || j >= n - p.recent
                               ? kKeyKept
-                              : key_of(bs[r] == INFINITY ? INFINITY : best + 0.f);
+                              : key_of(scale[r] == INFINITY ? INFINITY : best + 0.f);
         }
     }
 }
@@ -466,12 +498,12 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     p.stride = stride;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (stride > max_selected) { // else every block of every sequence is chosen
-        // Tiles of a CTA: about three CTAs an SM in all, so that the queries'
+        // Tiles of a CTA: about two CTAs an SM in all, so that the queries'
         // codes are formed few times, but no more than 16 tiles a warp.
         const int sms = sm_count(&e);
         if (!sms)
             return PA_ERR_CUDA;
-        const int64_t all = row_tiles * num_kv_heads * num_seqs, slots = 3ll * sms * kScoreWarps;
+        const int64_t all = row_tiles * num_kv_heads * num_seqs, slots = 2ll * sms * kScoreWarps;
         const int64_t each = std::min<int64_t>((all + slots - 1) / slots, 16);
         p.heads_log2 = heads_log2(num_kv_heads);
         p.chunk = (int)each * (kScoreWarps >> p.heads_log2);
