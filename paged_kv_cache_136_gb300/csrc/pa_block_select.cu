@@ -251,19 +251,24 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
     return base + x - v;
 }
 
-constexpr int kDigit = 11; // bits of a pass
+constexpr int kDigit = 8;        // bits of a pass
+constexpr int kCandidates = 256; // keys that are ranked against each other
 
 // The `most` largest keys of one (sequence, kv head), in ascending order of
-// the block's position; among equal keys the lowest positions.  A radix select
-// over the range that the keys take finds the smallest chosen key, 11 bits a
-// pass, and stops early when a digit's keys are all wanted; an ordered scan
-// writes the positions.  A thread holds PER consecutive keys in registers; a
-// longer row goes through in several rounds, read again (from L2) each pass.
-// Bound by latency: the passes' barriers.
+// the block's position; among equal keys the lowest positions.  A radix pass
+// over the range that the keys take finds the digit in which the smallest
+// chosen key lies.  Mostly few keys share it: they are ranked against each
+// other by (key, position), which ends the search; else the next 8 bits are
+// looked at.  An ordered scan then writes the positions.  A thread holds PER
+// consecutive keys in registers; a longer row goes through in several rounds,
+// read again (from L2) each time.  Bound by latency: the barriers, and the fetch
+// of code that runs once (2048 bins of 11 bits took longer than 256 of 8).
 template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
 {
-    __shared__ uint32_t hist[1 << kDigit], warp_sums[32], range[2][32], found[3];
+    __shared__ uint32_t hist[1 << kDigit], warp_sums[32], seen[3][32], found[3], candidates;
+    __shared__ uint2 candidate[kCandidates]; // distance, position
+    __shared__ uint2 edge;                   // the smallest chosen one
     griddep_wait();
     griddep_launch_dependents();
     const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
@@ -311,94 +316,142 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
     }
     lo = __reduce_min_sync(~0u, lo);
     hi = __reduce_max_sync(~0u, hi);
+    kept = __reduce_add_sync(~0u, kept);
     if (lane == 0) {
-        range[0][warp] = lo;
-        range[1][warp] = hi;
+        seen[0][warp] = lo;
+        seen[1][warp] = hi;
+        seen[2][warp] = kept;
     }
-    for (int i = tid; i < 1 << kDigit; i += THREADS)
-        hist[i] = 0;
-    uint32_t all;
-    block_scan<THREADS>(kept, warp_sums, all);
-    lo = __reduce_min_sync(~0u, lane < THREADS / 32 ? range[0][lane] : ~0u);
-    hi = __reduce_max_sync(~0u, lane < THREADS / 32 ? range[1][lane] : 0u);
-    uint32_t need = p.most - all;    // of the scored ones
-    const int bits = 32 - __clz(hi - lo);
-    // distance d = key - lo; `border` is the found digits of the smallest chosen
-    uint32_t border = 0, ties = need;
-    for (int top = bits; top > 0 && need > 0;) {
+    if (tid < 1 << kDigit)
+        hist[tid] = 0;
+    if (tid == 0)
+        candidates = 0;
+    __syncthreads();
+    const bool some = lane < THREADS / 32;
+    lo = __reduce_min_sync(~0u, some ? seen[0][lane] : ~0u);
+    hi = __reduce_max_sync(~0u, some ? seen[1][lane] : 0u);
+    const uint32_t all = __reduce_add_sync(~0u, some ? seen[2][lane] : 0u);
+    uint32_t need = p.most - all; // of the scored ones
+    // Distances d = key - lo from the smallest key; of the smallest chosen one
+    // the bits from `top` up are known, and `need` of the `left` keys that
+    // share them are to be chosen.
+    uint32_t border = 0, left = ~0u;
+    int top = 32 - __clz(hi - lo);
+    auto shares = [&](uint32_t key) {
+        return key != 0 && key != kKeyKept && (top == 32 || ((key - lo) ^ border) >> top == 0);
+    };
+    while (top > 0 && left > kCandidates && left != need && need > 0) {
         const int shift = max(top - kDigit, 0);
         for (int round = 0; round < rounds; ++round) {
             if (rounds > 1)
                 load(round);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t d = k[i] - lo;
-                if (k[i] != 0 && k[i] != kKeyKept && (top == 32 || (d ^ border) >> top == 0))
-                    atomicAdd(&hist[d >> shift & ((1 << kDigit) - 1)], 1u);
-            }
+            for (int i = 0; i < PER; ++i)
+                if (shares(k[i]))
+                    atomicAdd(&hist[(k[i] - lo) >> shift & ((1 << kDigit) - 1)], 1u);
         }
         __syncthreads();
-        // digits from the largest down, kEach a thread
-        constexpr int kEach = (1 << kDigit) / THREADS;
-        uint32_t c[kEach], sum = 0, total;
+        if (warp == 0) { // lane l: the digits 255 - 8 l .. 248 - 8 l
+            constexpr int kEach = (1 << kDigit) / 32;
+            uint32_t c[kEach], sum = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            uint32_t &bin = hist[(1 << kDigit) - 1 - tid * kEach - i];
-            sum += c[i] = bin;
-            bin = 0;
-        }
-        uint32_t before = block_scan<THREADS>(sum, warp_sums, total);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (before < need && before + c[i] >= need) {
-                found[0] = (1 << kDigit) - 1 - tid * kEach - i;
-                found[1] = need - before;
-                found[2] = c[i];
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t &bin = hist[(1 << kDigit) - 1 - lane * kEach - i];
+                sum += c[i] = bin;
+                bin = 0;
             }
-            before += c[i];
+            uint32_t x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            uint32_t before = x - sum;
+            if (before < need && x >= need) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    if (before < need && before + c[i] >= need) {
+                        found[0] = (1 << kDigit) - 1 - lane * kEach - i;
+                        found[1] = need - before;
+                        found[2] = c[i];
+                    }
+                    before += c[i];
+                }
+            }
         }
         __syncthreads();
         border |= found[0] << shift;
-        ties = need = found[1];
+        need = found[1];
+        left = found[2];
         top = shift;
-        if (found[2] == need) { // all that share the digits are chosen
-            ties = ~0u;
-            break;
+    }
+    // Chosen: the kept, those above the edge's key, and those of its key up to
+    // its position.
+    uint32_t edge_d = border, edge_at = 0x7FFFFFFFu;
+    if (need == 0) { // only the kept
+        edge_d = ~0u;
+    } else if (left == need) { // all that share the border's bits
+    } else if (left <= kCandidates) {
+        for (int round = 0; round < rounds; ++round) {
+            if (rounds > 1)
+                load(round);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (shares(k[i]))
+                    candidate[atomicAdd(&candidates, 1u)] =
+                        make_uint2(k[i] - lo, (round * THREADS + tid) * PER + i);
         }
         __syncthreads();
+        if (tid < (int)left) {
+            const uint2 mine = candidate[tid];
+            uint32_t rank = 0;
+            for (uint32_t j = 0; j < left; ++j) {
+                const uint2 other = candidate[j];
+                rank += other.x > mine.x || (other.x == mine.x && other.y < mine.y);
+            }
+            if (rank == need - 1)
+                edge = mine;
+        }
+        __syncthreads();
+        edge_d = edge.x;
+        edge_at = edge.y;
+    } else { // many equal keys: the position of the need-th of them
+        uint32_t equal = 0;
+        for (int round = 0; round < rounds; ++round) {
+            if (rounds > 1)
+                load(round);
+            uint32_t e = 0, total;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                e += shares(k[i]);
+            uint32_t at = equal + block_scan<THREADS>(e, warp_sums, total);
+            equal += total;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (shares(k[i]) && ++at == need)
+                    edge.y = (round * THREADS + tid) * PER + i;
+        }
+        __syncthreads();
+        edge_at = edge.y;
     }
-    // Chosen: the kept, those above the border, the first `ties` on it (where
-    // the search stopped early, everything from the border up).
-    const bool some = p.most > all;
-    const uint32_t most_e = some ? ties : 0;
-    uint32_t above = 0, equal = 0;
+    uint32_t written = 0;
     for (int round = 0; round < rounds; ++round) {
         if (rounds > 1)
             load(round);
-        uint32_t a = 0, e = 0;
+        const uint32_t i0 = (round * THREADS + tid) * PER;
+        uint32_t chosen = 0, total; // a bit for each key
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t d = k[i] - lo;
-            const bool scored = k[i] != 0 && k[i] != kKeyKept;
-            a += k[i] == kKeyKept || (scored && some && d > border);
-            e += scored && d == border;
+            const bool yes = k[i] == kKeyKept ||
+                             (k[i] != 0 && (d > edge_d || (d == edge_d && i0 + i <= edge_at)));
+            chosen |= (yes ? 1u : 0u) << i;
         }
-        uint32_t total_a, total_e;
-        uint32_t at_a = above + block_scan<THREADS>(a, warp_sums, total_a);
-        uint32_t at_e = equal + block_scan<THREADS>(e, warp_sums, total_e);
-        above += total_a;
-        equal += total_e;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t d = k[i] - lo;
-            const bool scored = k[i] != 0 && k[i] != kKeyKept;
-            const bool gt = k[i] == kKeyKept || (scored && some && d > border);
-            const bool eq = scored && d == border;
-            if (gt || (eq && at_e < most_e))
-                list[at_a + min(at_e, most_e)] = (round * THREADS + tid) * PER + i;
-            at_a += gt;
-            at_e += eq;
-        }
+        uint32_t at = written + block_scan<THREADS>(__popc(chosen), warp_sums, total);
+        written += total;
+        for (; chosen; chosen &= chosen - 1)
+            list[at++] = i0 + __ffs(chosen) - 1;
     }
 }
 
