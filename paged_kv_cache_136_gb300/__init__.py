@@ -9,6 +9,8 @@ Importing this package fails loudly if libpa.so has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -89,25 +91,10 @@ _lib.pa_decode_splitk_fp8_workspace_size.argtypes = [_I, _I, _I, _I, _I]
 _lib.pa_decode_splitk_fp8.restype = _I
 _lib.pa_decode_splitk_fp8.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F,
                                       _F, _I, _I, _I, _P, _SZ, _P]
-_lib.pa_reshape_and_cache_fp8_block.restype = _I
-_lib.pa_reshape_and_cache_fp8_block.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I,
-                                                _I, _I, _I, _I, _I64, _I64, _I, _P]
 _lib.pa_block_decode_workspace_size.restype = _SZ
 _lib.pa_block_decode_workspace_size.argtypes = [_I, _I, _I]
-_lib.pa_decode_fp8_block.restype = _I
-_lib.pa_decode_fp8_block.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
-                                     _I, _I, _P, _SZ, _P]
-_lib.pa_update_block_bounds.restype = _I
-_lib.pa_update_block_bounds.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I,
-                                        _I, _I, _P]
 _lib.pa_select_blocks_workspace_size.restype = _SZ
 _lib.pa_select_blocks_workspace_size.argtypes = [_I, _I, _I, _I]
-_lib.pa_select_blocks.restype = _I
-_lib.pa_select_blocks.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
-                                  _I, _I, _I, _P, _SZ, _P]
-_lib.pa_decode_sparse.restype = _I
-_lib.pa_decode_sparse.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
-                                  _I, _F, _I, _P, _SZ, _P]
 _lib.pa_prefill.restype = _I
 _lib.pa_prefill.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                             _I, _F, _I, _I, _P]
@@ -497,85 +484,23 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
     return out
 
 
-# The block-scaled and block-sparse calls.  The checks are written for few
-# Python operations: a decode step makes several of these calls per layer.
-_I32, _F32, _U8, _I8 = torch.int32, torch.float32, torch.uint8, torch.int8
+# The block-scaled and block-sparse calls.  Their checks and marshalling are
+# native (csrc/pa_block_calls.c): a decode step makes several of these calls per
+# layer, and each costs the host little more than its launch.
+def _load_block_calls():
+    path = os.path.join(os.path.dirname(_LIB_PATH), "pa_block_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} not found; build the library first")
+    loader = importlib.machinery.ExtensionFileLoader("pa_block_calls", path)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location("pa_block_calls", path, loader=loader))
+    loader.exec_module(module)
+    module.bind(PAError, _current_device or torch.cuda.current_device,
+                _raw_current_stream or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return module
 
 
-def _here(names: str, *tensors) -> None:
-    """All tensors lie on the current device: a pointer of another one would
-    reach this device's kernels."""
-    d = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != d:
-            break
-    else:
-        if d >= 0 and d == (torch.cuda.current_device() if _current_device is None
-                            else _current_device()):
-            return
-    for name, t in zip(names.split(), tensors):
-        if t.get_device() < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device() if _current_device is None else _current_device()
-    for name, t in zip(names.split(), tensors):
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current device, cuda:{dev}")
-
-
-def _block_pool(kv_cache, kv_scales, block_size: int):
-    """Dimensions of an e4m3 pool (with scales) or a 16-bit one (kv_scales None)."""
-    shape = kv_cache.shape
-    if len(shape) != 5 or shape[0] != 2 or shape[2] != block_size:
-        raise ValueError("kv_cache must be [2, num_blocks, block_size, num_kv_heads, head_size]")
-    if not kv_cache.is_contiguous():
-        raise ValueError("kv_cache must be contiguous")
-    _, nb, _, hkv, d = shape
-    if kv_scales is None:
-        if kv_cache.dtype not in _DTYPE:
-            raise ValueError("a pool without kv_scales must be float16 or bfloat16")
-    else:
-        if kv_cache.dtype is not _U8:
-            raise ValueError("a pool with kv_scales must be a uint8 tensor of e4m3 codes")
-        if kv_scales.dtype is not _F32 or kv_scales.shape != (2, nb, hkv) or \
-                not kv_scales.is_contiguous():
-            raise ValueError("kv_scales must be contiguous float32 [2, num_blocks, num_kv_heads]")
-    return nb, hkv, d
-
-
-def _requests(block_tables, seq_lens, query_start_loc):
-    """(requests, blocks of a table row, stride of the rows)."""
-    r = seq_lens.numel()
-    if seq_lens.dtype is not _I32 or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous int32 [R]")
-    shape, stride = block_tables.shape, block_tables.stride()
-    if block_tables.dtype is not _I32 or len(shape) != 2 or shape[0] != r or \
-            (stride[1] != 1 and shape[1] != 1) or (stride[0] < shape[1] and r > 1):
-        raise ValueError("block_tables must be int32 [R, max_blocks] with contiguous rows")
-    if query_start_loc.dtype is not _I32 or query_start_loc.numel() != r + 1 or \
-            not query_start_loc.is_contiguous():
-        raise ValueError("query_start_loc must be contiguous int32 [R + 1]")
-    return r, shape[1], max(stride[0], shape[1])
-
-
-def _block_queries(q, d: int, block_tables, seq_lens):
-    """(sequences, query heads, blocks of a table row)."""
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != d or q.dtype not in _DTYPE or not q.is_contiguous():
-        raise ValueError("q must be contiguous fp16/bf16 [B, H, head_size]")
-    b, h, _ = shape
-    shape = block_tables.shape
-    if block_tables.dtype is not _I32 or len(shape) != 2 or shape[0] != b or \
-            not block_tables.is_contiguous():
-        raise ValueError("block_tables must be contiguous int32 [B, max_blocks_per_seq]")
-    if seq_lens.dtype is not _I32 or seq_lens.numel() != b or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous int32 [B]")
-    return b, h, shape[1]
-
-
-def _workspace_bytes(workspace) -> int:
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace.nbytes
+_block_calls = _load_block_calls()
 
 
 def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor,
@@ -588,29 +513,8 @@ def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor,
     positions) to e4m3 with one power-of-two scale for each (plane, block, kv
     head) and append them to the uint8 pool; ``kv_scales`` (float32 [2,
     num_blocks, Hkv]) is updated with it."""
-    if kv_scales is None:
-        raise ValueError("kv_scales is required")
-    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
-    r, mb, table_stride = _requests(block_tables, seq_lens, query_start_loc)
-    shape, ks, vs, dtype = key.shape, key.stride(), value.stride(), key.dtype
-    if dtype not in _DTYPE or value.dtype is not dtype or value.shape != shape or \
-            len(shape) != 3 or shape[1] != hkv or shape[2] != d:
-        raise ValueError("key and value must be fp16/bf16 [T, num_kv_heads, head_size] alike")
-    if ks[2] != 1 or vs[2] != 1 or ((ks[1] != d or vs[1] != d) and hkv > 1):
-        raise ValueError("key and value must have contiguous rows")
-    tokens = shape[0]
-    if r == 0 or tokens == 0:
-        return
-    _here("key value kv_cache kv_scales block_tables seq_lens query_start_loc", key, value,
-          kv_cache, kv_scales, block_tables, seq_lens, query_start_loc)
-    row = hkv * d
-    st = _lib.pa_reshape_and_cache_fp8_block(
-        key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(),
-        block_tables.data_ptr(), table_stride, seq_lens.data_ptr(), query_start_loc.data_ptr(), r,
-        tokens, int(max_query_len), hkv, d, block_size, nb, mb, ks[0] if tokens > 1 else row,
-        vs[0] if tokens > 1 else row, _DTYPE[dtype], _stream(stream))
-    if st:
-        raise PAError(st, "pa_reshape_and_cache_fp8_block")
+    _block_calls.write_block(key, value, kv_cache, kv_scales, block_tables, seq_lens,
+                             query_start_loc, block_size, max_query_len, stream)
 
 
 def pa_block_decode_workspace_size(num_heads: int, num_kv_heads: int, head_size: int) -> int:
@@ -627,34 +531,9 @@ def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tens
     returns ``out``, and the natural-log softmax denominators into ``lse``
     (float32 [B, H]) if given.  ``workspace`` holds
     pa_block_decode_workspace_size bytes."""
-    if kv_scales is None:
-        raise ValueError("kv_scales is required")
-    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
-    b, h, mb = _block_queries(q, d, block_tables, seq_lens)
-    if out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
-        raise ValueError("out must be contiguous and match q")
-    _here("out q kv_cache kv_scales block_tables seq_lens workspace", out, q, kv_cache, kv_scales,
-          block_tables, seq_lens, workspace)
-    lp = None
-    if lse is not None:
-        lp = _lse_arg(lse, b, h)
-        _here("lse", lse)
-    st = _lib.pa_decode_fp8_block(
-        out.data_ptr(), lp, q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(),
-        block_tables.data_ptr(), seq_lens.data_ptr(), b, h, hkv, d, block_size, nb, mb, float(scale),
-        _DTYPE[q.dtype], int(max_seq_len), workspace.data_ptr(), _workspace_bytes(workspace),
-        _stream(stream))
-    if st:
-        raise PAError(st, "pa_decode_fp8_block")
+    _block_calls.decode_block(out, q, kv_cache, kv_scales, block_tables, seq_lens, workspace, lse,
+                              scale, block_size, max_seq_len, stream)
     return out
-
-
-def _check_bounds(bounds, bounds_scale, nb: int, hkv: int, d: int) -> None:
-    if bounds.dtype is not _I8 or bounds.shape != (nb, hkv, 2, d) or not bounds.is_contiguous():
-        raise ValueError("bounds must be contiguous int8 [num_blocks, num_kv_heads, 2, head_size]")
-    if bounds_scale.dtype is not _F32 or bounds_scale.shape != (nb, hkv) or \
-            not bounds_scale.is_contiguous():
-        raise ValueError("bounds_scale must be contiguous float32 [num_blocks, num_kv_heads]")
 
 
 def pa_update_block_bounds(bounds: torch.Tensor, bounds_scale: torch.Tensor,
@@ -666,41 +545,14 @@ def pa_update_block_bounds(bounds: torch.Tensor, bounds_scale: torch.Tensor,
     [num_blocks, Hkv] scales) of every block that holds a new token of a
     request; the tokens are already in the pool (16-bit, or e4m3 with
     ``kv_scales``)."""
-    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
-    _check_bounds(bounds, bounds_scale, nb, hkv, d)
-    r, mb, table_stride = _requests(block_tables, seq_lens, query_start_loc)
-    if r == 0:
-        return
-    _here("bounds bounds_scale kv_cache block_tables seq_lens query_start_loc", bounds,
-          bounds_scale, kv_cache, block_tables, seq_lens, query_start_loc)
-    sp, code = None, 0
-    if kv_scales is None:
-        code = _DTYPE[kv_cache.dtype]
-    else:
-        _here("kv_scales", kv_scales)
-        sp = kv_scales.data_ptr()
-    st = _lib.pa_update_block_bounds(
-        bounds.data_ptr(), bounds_scale.data_ptr(), kv_cache.data_ptr(), sp,
-        block_tables.data_ptr(), table_stride, seq_lens.data_ptr(), query_start_loc.data_ptr(), r,
-        int(max_query_len), hkv, d, block_size, nb, mb, code, _stream(stream))
-    if st:
-        raise PAError(st, "pa_update_block_bounds")
+    _block_calls.update_bounds(bounds, bounds_scale, kv_cache, block_tables, seq_lens,
+                               query_start_loc, kv_scales, block_size, max_query_len, stream)
 
 
 def pa_select_blocks_workspace_size(num_seqs: int, num_kv_heads: int, max_seq_len: int,
                                     block_size: int) -> int:
     return int(_lib.pa_select_blocks_workspace_size(num_seqs, num_kv_heads, max_seq_len,
                                                     block_size))
-
-
-def _lists_arg(block_lists, list_lens, b: int, hkv: int) -> int:
-    shape = block_lists.shape
-    if block_lists.dtype is not _I32 or len(shape) != 3 or shape[0] != b or shape[1] != hkv or \
-            not block_lists.is_contiguous():
-        raise ValueError("block_lists must be contiguous int32 [B, num_kv_heads, max_selected]")
-    if list_lens.dtype is not _I32 or list_lens.numel() != b or not list_lens.is_contiguous():
-        raise ValueError("list_lens must be contiguous int32 [B]")
-    return shape[2]
 
 
 def pa_select_blocks(block_lists: torch.Tensor, list_lens: torch.Tensor, q: torch.Tensor,
@@ -714,22 +566,9 @@ def pa_select_blocks(block_lists: torch.Tensor, list_lens: torch.Tensor, q: torc
     ``list_lens`` (int32 [B]) their number; both are returned.  The first
     ``num_sink_blocks`` and the last ``num_recent_blocks`` are always chosen.
     ``workspace`` holds pa_select_blocks_workspace_size bytes."""
-    shape = bounds.shape
-    if len(shape) != 4:
-        raise ValueError("bounds must be contiguous int8 [num_blocks, num_kv_heads, 2, head_size]")
-    nb, hkv, _, d = shape
-    _check_bounds(bounds, bounds_scale, nb, hkv, d)
-    b, h, mb = _block_queries(q, d, block_tables, seq_lens)
-    k = _lists_arg(block_lists, list_lens, b, hkv)
-    _here("block_lists list_lens q bounds bounds_scale block_tables seq_lens workspace",
-          block_lists, list_lens, q, bounds, bounds_scale, block_tables, seq_lens, workspace)
-    st = _lib.pa_select_blocks(
-        block_lists.data_ptr(), list_lens.data_ptr(), q.data_ptr(), bounds.data_ptr(),
-        bounds_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), b, h, hkv, d,
-        block_size, nb, mb, k, int(num_sink_blocks), int(num_recent_blocks), _DTYPE[q.dtype],
-        int(max_seq_len), workspace.data_ptr(), _workspace_bytes(workspace), _stream(stream))
-    if st:
-        raise PAError(st, "pa_select_blocks")
+    _block_calls.select_blocks(block_lists, list_lens, q, bounds, bounds_scale, block_tables,
+                               seq_lens, workspace, block_size, max_seq_len, num_sink_blocks,
+                               num_recent_blocks, stream)
     return block_lists, list_lens
 
 
@@ -743,29 +582,8 @@ def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
     head), of a 16-bit pool or of an e4m3 pool with ``kv_scales``; writes and
     returns ``out`` (and ``lse``, float32 [B, H], if given).  ``workspace``
     holds pa_block_decode_workspace_size bytes."""
-    nb, hkv, d = _block_pool(kv_cache, kv_scales, block_size)
-    b, h, mb = _block_queries(q, d, block_tables, seq_lens)
-    if out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
-        raise ValueError("out must be contiguous and match q")
-    if kv_scales is None and q.dtype is not kv_cache.dtype:
-        raise ValueError("q and a 16-bit kv_cache must share their dtype")
-    k = _lists_arg(block_lists, list_lens, b, hkv)
-    _here("out q kv_cache block_tables seq_lens block_lists list_lens workspace", out, q, kv_cache,
-          block_tables, seq_lens, block_lists, list_lens, workspace)
-    sp = lp = None
-    if kv_scales is not None:
-        _here("kv_scales", kv_scales)
-        sp = kv_scales.data_ptr()
-    if lse is not None:
-        lp = _lse_arg(lse, b, h)
-        _here("lse", lse)
-    st = _lib.pa_decode_sparse(
-        out.data_ptr(), lp, q.data_ptr(), kv_cache.data_ptr(), sp, block_tables.data_ptr(),
-        seq_lens.data_ptr(), block_lists.data_ptr(), list_lens.data_ptr(), b, h, hkv, d,
-        block_size, nb, mb, k, float(scale), _DTYPE[q.dtype], workspace.data_ptr(),
-        _workspace_bytes(workspace), _stream(stream))
-    if st:
-        raise PAError(st, "pa_decode_sparse")
+    _block_calls.decode_sparse(out, q, kv_cache, block_tables, seq_lens, block_lists, list_lens,
+                               workspace, kv_scales, lse, scale, block_size, stream)
     return out
 
 

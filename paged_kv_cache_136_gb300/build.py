@@ -3,7 +3,9 @@
 The library is a handful of translation units compiled in parallel (the decode
 kernel instantiations are split by dtype and head_size) and linked into
 ``paged_kv_cache_136_gb300/_lib/libpa.so``, plus ``_lib/pa_latency``, a host
-program that times the C ABI on the 4-sequence workload.  Run ``python
+program that times the C ABI on the 4-sequence workload, and
+``_lib/pa_block_calls.so``, the Python binding of the block calls (gcc, CPython
+headers).  Run ``python
 paged_kv_cache_136_gb300/build.py`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +25,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libpa.so")
 LATENCY_TOOL = os.path.join(LIB_DIR, "pa_latency")
+BLOCK_CALLS = os.path.join(LIB_DIR, "pa_block_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -56,9 +60,10 @@ def _sources() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(LATENCY_TOOL):
+    made = (LIB, LATENCY_TOOL, BLOCK_CALLS)
+    if not all(os.path.exists(p) for p in made):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(LATENCY_TOOL))
+    t = min(os.path.getmtime(p) for p in made)
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
@@ -104,13 +109,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    # The C-ABI latency tool links against the library it measures.
+    # The C-ABI latency tool and the block calls link against the library.
     tmp = LATENCY_TOOL + f".{os.getpid()}.tmp"
     cmd = [_nvcc(), *ARCH, tool_obj, "-L", LIB_DIR, "-lpa", "-Xlinker", "-rpath=$ORIGIN", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LATENCY_TOOL)
+    tmp = BLOCK_CALLS + f".{os.getpid()}.tmp"
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "pa_block_calls.c"), "-L", LIB_DIR, "-lpa", "-Wl,-rpath,$ORIGIN",
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BLOCK_CALLS)
     return LIB
 
 

@@ -167,16 +167,45 @@ def test_binding_wants_cuda_tensors(pa, name):
         _calls(pa, _args())[name]()
 
 
-def test_binding_wants_the_current_device(pa, monkeypatch):
-    monkeypatch.setattr(pa, "_current_device", lambda: 0)
-    here, there, host = (types.SimpleNamespace(get_device=lambda i=i: i) for i in (0, 1, -1))
-    pa._here("a b", here, here)
-    with pytest.raises(ValueError, match="b must be a CUDA tensor"):
-        pa._here("a b", here, host)
-    with pytest.raises(ValueError, match="b must be on the current device, cuda:0"):
-        pa._here("a b", here, there)
-    with pytest.raises(ValueError, match="a must be on the current device, cuda:0"):
-        pa._here("a b", there, there)
+class _Elsewhere:
+    """A CPU tensor that says it lies on another device."""
+
+    def __init__(self, tensor, device):
+        self.tensor, self.device = tensor, device
+
+    def get_device(self):
+        return self.device
+
+    def __getattr__(self, name):
+        return getattr(self.tensor, name)
+
+
+def test_binding_wants_the_current_device(pa):
+    """Every tensor of a call on cuda:1 while cuda:0 is current, or one of them."""
+    calls = pa._block_calls
+    calls.bind(pa.PAError, lambda: 0, lambda device: 0)
+    try:
+        fields = [f for f in vars(_args()) if f != "bs"]
+        a = _args()
+        for f in fields:
+            setattr(a, f, _Elsewhere(getattr(a, f), 1))
+        for name, first in (("write", "key"), ("bounds", "bounds"), ("select", "block_lists")):
+            with pytest.raises(ValueError, match=first + " must be on the current device, cuda:0"):
+                _calls(pa, a)[name]()
+        for call in (lambda out: pa.pa_decode_fp8_block(out, a.q, a.pool, a.scales, a.tables, a.sl,
+                                                        0.1, a.bs, 16, a.ws),
+                     lambda out: pa.pa_decode_sparse(out, a.q, a.pool16, a.tables, a.sl, a.lists,
+                                                     a.lens, 0.1, a.bs, a.ws)):
+            with pytest.raises(ValueError, match="out must be on the current device, cuda:0"):
+                call(a.q)
+        a = _args()
+        for f in fields:
+            setattr(a, f, _Elsewhere(getattr(a, f), 1 if f == "sl" else 0))
+        for name in ("write", "bounds", "select"):
+            with pytest.raises(ValueError, match="seq_lens must be on the current device, cuda:0"):
+                _calls(pa, a)[name]()
+    finally:
+        calls.bind(pa.PAError, pa._current_device, pa._raw_current_stream)
 
 
 @pytest.mark.parametrize("field,value,names", [
@@ -217,12 +246,38 @@ def test_binding_checks_shapes(pa, field, value, names):
         assert "CUDA" not in str(e.value), (name, e.value)
 
 
-def test_a_broadcast_key_is_refused(pa, monkeypatch):
-    """A row stride of zero is no row stride: the C call refuses it."""
-    monkeypatch.setattr(pa, "_here", lambda *a: None)
-    monkeypatch.setattr(pa, "_stream", lambda stream: 0)
+def test_a_broadcast_key_is_refused(pa):
+    """A row stride of zero is no row stride."""
     a = _args()
     a.key = torch.zeros(1, 2, 64, dtype=torch.float16).expand(3, 2, 64)
-    with pytest.raises(pa.PAError) as e:
+    with pytest.raises(ValueError, match="contiguous rows"):
         _calls(pa, a)["write"]()
-    assert e.value.status == INVALID
+
+
+def test_what_is_no_tensor_is_refused(pa):
+    for field, value in (("pool", None), ("pool", 7), ("sl", [1, 2, 3]), ("tables", "x")):
+        a = _args()
+        setattr(a, field, value)
+        with pytest.raises((AttributeError, TypeError, ValueError)):
+            _calls(pa, a)["write"]()
+    with pytest.raises(ValueError, match="32 bits"):
+        pa.pa_update_block_bounds(*[None] * 6, 2 ** 40, 1)
+    with pytest.raises(TypeError):
+        pa.pa_decode_fp8_block(*[None] * 6, "0.1", 16, 16, None)
+
+
+def test_a_failed_call_raises_its_status(pa):
+    """The C call's own refusal comes out as PAError (no launch: the workspace
+    is too small)."""
+    calls = pa._block_calls
+    calls.bind(pa.PAError, lambda: 0, lambda device: 0)
+    try:
+        a = _args()
+        for f in vars(a):
+            if f != "bs":
+                setattr(a, f, _Elsewhere(getattr(a, f), 0))
+        with pytest.raises(pa.PAError) as e:
+            _calls(pa, a)["select"]()
+        assert e.value.status in (INVALID, WORKSPACE) and "pa_select_blocks" in str(e.value)
+    finally:
+        calls.bind(pa.PAError, pa._current_device, pa._raw_current_stream)
