@@ -41,8 +41,8 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) // unsign
 // once, coalesced, and stay in registers while their largest magnitude is
 // formed.  The block's older codes are touched only when the scale grows.
 // Bound by HBM: 2 bytes read and 1 written a value.
-// Grid: x = chunks of kWriteWarps (block of the request, piece of the row,
-// plane) units, y = request.
+// Grid: x = chunks of kWriteWarps (block of the request, plane, piece of the
+// row) units, y = request.
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(32 * kWriteWarps) write_block_kernel(const WriteParams p)
 {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_block_kernel(const Wri
     const int lane = threadIdx.x & 31;
     const int unit = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
     const int r = blockIdx.y;
-    const int plane = unit % 2, piece = unit / 2 % p.pieces, jj = unit / 2 / p.pieces;
+    const int piece = unit % p.pieces, plane = unit / p.pieces % 2, jj = unit / p.pieces / 2;
     Request q;
     if (!read_request(q, r, p.seq_lens, p.query_start_loc, p.num_tokens, p.max_query_len,
                       p.len_cap, unit == 0 && lane == 0, p.err))
@@ -210,7 +210,7 @@ template <> __device__ __forceinline__ uint32_t pair_min<__nv_bfloat16>(uint32_t
 // Bound by HBM: the keys, and 2 D + 4 bytes written a head.  T: type of a
 // 16-bit pool (e4m3 codes become halves).  Grid as the write's, without planes.
 template <typename T, bool E4M3, int D, int BS>
-__global__ void __launch_bounds__(32 * kBoundsWarps, 2) block_bounds_kernel(const BoundsParams p)
+__global__ void __launch_bounds__(32 * kBoundsWarps, 4) block_bounds_kernel(const BoundsParams p)
 {
     constexpr int kWords = BS == 16 ? 4 : 2;      // 32-bit words of a lane and row
     constexpr int kVals = kWords * (E4M3 ? 4 : 2);
