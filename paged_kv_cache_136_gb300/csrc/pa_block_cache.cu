@@ -50,7 +50,6 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_block_kernel(const Wri
     constexpr int kVals = 2 * kWords;             // values of a lane and row
     constexpr int kLanes = D / kVals;             // lanes of a head
     griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int unit = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
     const int r = blockIdx.y;
@@ -217,7 +216,6 @@ __global__ void __launch_bounds__(32 * kBoundsWarps, 4) block_bounds_kernel(cons
     constexpr int kPairs = kVals / 2;
     constexpr int kLanes = D / kVals;             // lanes of a head
     griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int unit = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
     const int r = blockIdx.y, piece = unit % p.pieces, jj = unit / p.pieces;

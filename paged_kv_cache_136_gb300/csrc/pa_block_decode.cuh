@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
         prefetch_tensormap(&pool_map);
     __syncwarp();
     griddep_wait();
-    griddep_launch_dependents();
 
     // ---- this CTA's run: [begin, end) of the line of tiles ----
     int run = 0, begin = 0, end;
@@ -731,6 +730,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
             }
         }
     }
+    griddep_launch_dependents();
 }
 
 // Merge of the (sequence, group)s that a cut divides: with M = max m_i,
@@ -754,7 +754,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
     __shared__ float part[kMergeWarps][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
-    griddep_launch_dependents();
     int4 seen = make_int4(0, 0, 0, 0);
     if ((int)threadIdx.x < ctas)
         seen = p.cuts[threadIdx.x];

@@ -35,7 +35,9 @@ struct SelectParams {
     uint32_t *keys;              // [B, Hkv, stride]
     unsigned int *err;
     int num_heads, num_kv_heads, group, num_blocks, max_blocks, block_size, len_cap, most, sink,
-        recent, stride, heads_log2, chunk; // kv heads and 16-block tiles of a score CTA
+        recent, stride;
+    int heads_log2;              // kv heads that a CTA scores
+    int chunk;                   // score_kernel: tiles of a CTA; pick_kernel: keys of shared memory
 };
 
 __device__ __forceinline__ int checked_len(const SelectParams &p, int s, bool report)
@@ -68,26 +70,18 @@ constexpr int kScoreWarps = 8;
 //
 // Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's 8
 // warps are 8 kv heads (or fewer, times several tiles), so that the bounds of a
-// block, which lie together, are read at one time, and go through p.chunk tiles.
-// A tile's bounds are asked for while the tile before it (or the queries) are
-// worked on.
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const SelectParams p)
+// block, which lie together, are read at one time.  A tile's bounds are asked
+// for while the tile before it (or the queries) are worked on.
+//
+// Scores the blocks j0 .. j0 + 15, then those `step` further, below `last`, of
+// a sequence of n blocks, and gives their keys to put(position, key).
+template <typename T, int D, typename Put>
+__device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int head, int n, int j0,
+                                             int step, int last, Put put)
 {
     constexpr int kPieces = 2 * D / 64;           // 16-byte pieces of a lane and row
-    griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int warp = threadIdx.x >> 5, groups = p.num_kv_heads >> p.heads_log2;
-    const int head = (blockIdx.x % groups << p.heads_log2) + (warp & ((1 << p.heads_log2) - 1));
-    const int step = 16 * (kScoreWarps >> p.heads_log2); // blocks the CTA takes at a time
-    const int s = blockIdx.y;
-    const int len = checked_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
-    const int n = (len + p.block_size - 1) / p.block_size;
-    const int first = blockIdx.x / groups * p.chunk * 16;
-    const int last = min(n, first + p.chunk * 16);
-    int j0 = first + (warp >> p.heads_log2) * 16;
-    if (j0 >= last || n <= p.most)
+    if (j0 >= last)
         return;
     const int32_t *const row = p.tables + (int64_t)s * p.max_blocks;
     // Rows g and g + 8 of a tile: blocks, then bounds and scales.
@@ -174,7 +168,6 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const Select
     // Columns 2t and 2t + 1 are queries 2t and 2t + 1 of the group.
     const float q0 = __shfl_sync(~0u, qs, 8 * t), q1 = __shfl_sync(~0u, qs, 8 * t + 4);
     const float off0 = __shfl_sync(~0u, off, 8 * t), off1 = __shfl_sync(~0u, off, 8 * t + 4);
-    uint32_t *const keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
 
     for (; j0 < last; j0 += step) {
         uint4 now[2][kPieces];
@@ -216,102 +209,79 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const Select
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
             if (t == r && j < last)
-                keys[j] = j < p.sink || j >= n - p.recent
-                              ? kKeyKept
-                              : key_of(scale[r] == INFINITY ? INFINITY : best + 0.f);
+                put(j, j < p.sink || j >= n - p.recent
+                           ? kKeyKept
+                           : key_of(scale[r] == INFINITY ? INFINITY : best + 0.f));
         }
     }
 }
 
-// Exclusive prefix of a count over the block's threads, and the total.
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total)
+// The keys of p.chunk tiles of one (sequence, head group) into the workspace.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const SelectParams p)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    if (lane == 31)
-        warp_sums[warp] = x;
-    __syncthreads();
-    uint32_t sum = lane < THREADS / 32 ? warp_sums[lane] : 0, up = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, up, o);
-        if (lane >= o)
-            up += y;
-    }
-    total = __shfl_sync(~0u, up, 31);
-    const uint32_t base = __shfl_sync(~0u, up - sum, warp);
-    __syncthreads();
-    return base + x - v;
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, groups = p.num_kv_heads >> p.heads_log2;
+    const int head = (blockIdx.x % groups << p.heads_log2) + (warp & ((1 << p.heads_log2) - 1));
+    const int s = blockIdx.y;
+    const int len = checked_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
+    const int n = (len + p.block_size - 1) / p.block_size;
+    if (n <= p.most)
+        return;
+    const int first = blockIdx.x / groups * p.chunk * 16;
+    uint32_t *const keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
+    score_blocks<T, D>(p, s, head, n, first + (warp >> p.heads_log2) * 16,
+                       16 * (kScoreWarps >> p.heads_log2), min(n, first + p.chunk * 16),
+                       [&](int j, uint32_t key) { keys[j] = key; });
+    // Not before: the picking CTAs would crowd on the SMs that are free first
+    // (27 against 20 us for 8 sequences of 4096 blocks).
+    griddep_launch_dependents();
 }
 
 constexpr int kDigit = 8;        // bits of a pass
 constexpr int kCandidates = 256; // keys that are ranked against each other
 
-// The `most` largest keys of one (sequence, kv head), in ascending order of
-// the block's position; among equal keys the lowest positions.  A radix pass
-// over the range that the keys take finds the digit in which the smallest
-// chosen key lies.  Mostly few keys share it: they are ranked against each
-// other by (key, position), which ends the search; else the next 8 bits are
-// looked at.  An ordered scan then writes the positions.  A thread holds PER
-// consecutive keys in registers; a longer row goes through in several rounds,
-// read again (from L2) each time.  Bound by latency: the barriers, and the fetch
-// of code that runs once (2048 bins of 11 bits took longer than 256 of 8).
-template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
+// The p.most largest of n > p.most keys of one (sequence, kv head), in
+// ascending order of their positions; among equal keys the lowest positions.
+// A radix pass over the range that the keys take finds the digit in which the
+// smallest chosen key lies.  Mostly few keys share it: they are ranked against
+// each other by (key, position), which ends the search; else the next 8 bits
+// are looked at.  A warp then counts and writes what is chosen of its own run of
+// the keys.  Bound by latency: the barriers, and the fetch of code that runs
+// once a launch, so that the loops are rolled but for the four keys of a load.
+// `keys` is aligned to 16 bytes and may be read up to a multiple of four.
+template <int THREADS>
+__device__ __forceinline__ void pick_blocks(const SelectParams &p, int n, int32_t *list,
+                                            const uint32_t *keys)
 {
-    __shared__ uint32_t hist[1 << kDigit], warp_sums[32], seen[3][32], found[3], candidates;
+    constexpr int kWarps = THREADS / 32;
+    __shared__ uint32_t hist[1 << kDigit], seen[4][32], found[3], candidates;
     __shared__ uint2 candidate[kCandidates]; // distance, position
     __shared__ uint2 edge;                   // the smallest chosen one
-    griddep_wait();
-    griddep_launch_dependents();
-    const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
-    const int lane = tid & 31, warp = tid >> 5;
-    const int len = checked_len(p, s, false);
-    const int n = (len + p.block_size - 1) / p.block_size;
-    const int count = min(n, p.most);
-    int32_t *list = p.lists + ((int64_t)s * p.num_kv_heads + head) * p.most;
-    if (head == 0 && tid == 0)
-        p.list_lens[s] = count;
-    for (int i = count + tid; i < p.most; i += THREADS)
-        list[i] = -1;
-    if (n <= p.most) {
-        for (int i = tid; i < n; i += THREADS)
-            list[i] = i;
-        return;
-    }
-    const uint32_t *keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
-    const int rounds = (n + THREADS * PER - 1) / (THREADS * PER);
-    uint32_t k[PER];
-    auto load = [&](int round) { // keys past the end are 0, below every score
-        const int i0 = (round * THREADS + tid) * PER;
-#pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i0 + i < n)
-                v = *reinterpret_cast<const uint4 *>(keys + i0 + i);
-            k[i] = v.x;
-            k[i + 1] = i0 + i + 1 < n ? v.y : 0;
-            k[i + 2] = i0 + i + 2 < n ? v.z : 0;
-            k[i + 3] = i0 + i + 3 < n ? v.w : 0;
-        }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    struct Quad {
+        uint32_t k[4];
+    };
+    auto read = [&](int i) { // keys i .. i + 3; past the end 0, below every score
+        Quad q;
+        const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);
+        q.k[0] = v.x;
+        q.k[1] = i + 1 < n ? v.y : 0;
+        q.k[2] = i + 2 < n ? v.z : 0;
+        q.k[3] = i + 3 < n ? v.w : 0;
+        return q;
     };
     // how many are kept anyway, and the range of the others
     uint32_t lo = ~0u, hi = 0, kept = 0;
-    for (int round = 0; round < rounds; ++round) {
-        load(round);
+#pragma unroll 1
+    for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+        const Quad q = read(i);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const bool scored = k[i] != 0 && k[i] != kKeyKept;
-            lo = scored ? min(lo, k[i]) : lo;
-            hi = scored ? max(hi, k[i]) : hi;
-            kept += k[i] == kKeyKept;
+        for (int c = 0; c < 4; ++c) {
+            const bool scored = q.k[c] != 0 && q.k[c] != kKeyKept;
+            lo = scored ? min(lo, q.k[c]) : lo;
+            hi = scored ? max(hi, q.k[c]) : hi;
+            kept += q.k[c] == kKeyKept;
         }
     }
     lo = __reduce_min_sync(~0u, lo);
@@ -327,7 +297,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
     if (tid == 0)
         candidates = 0;
     __syncthreads();
-    const bool some = lane < THREADS / 32;
+    const bool some = lane < kWarps;
     lo = __reduce_min_sync(~0u, some ? seen[0][lane] : ~0u);
     hi = __reduce_max_sync(~0u, some ? seen[1][lane] : 0u);
     const uint32_t all = __reduce_add_sync(~0u, some ? seen[2][lane] : 0u);
@@ -340,45 +310,44 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
     auto shares = [&](uint32_t key) {
         return key != 0 && key != kKeyKept && (top == 32 || ((key - lo) ^ border) >> top == 0);
     };
+#pragma unroll 1
     while (top > 0 && left > kCandidates && left != need && need > 0) {
         const int shift = max(top - kDigit, 0);
-        for (int round = 0; round < rounds; ++round) {
-            if (rounds > 1)
-                load(round);
+#pragma unroll 1
+        for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+            const Quad q = read(i);
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (shares(k[i]))
-                    atomicAdd(&hist[(k[i] - lo) >> shift & ((1 << kDigit) - 1)], 1u);
+            for (int c = 0; c < 4; ++c)
+                if (shares(q.k[c]))
+                    atomicAdd(&hist[(q.k[c] - lo) >> shift & ((1 << kDigit) - 1)], 1u);
         }
         __syncthreads();
         if (warp == 0) { // lane l: the digits 255 - 8 l .. 248 - 8 l
             constexpr int kEach = (1 << kDigit) / 32;
-            uint32_t c[kEach], sum = 0;
+            uint32_t sum = 0;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                uint32_t &bin = hist[(1 << kDigit) - 1 - lane * kEach - i];
-                sum += c[i] = bin;
-                bin = 0;
-            }
+            for (int i = 0; i < kEach; ++i)
+                sum += hist[(1 << kDigit) - 1 - lane * kEach - i];
             uint32_t x = sum;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t y = __shfl_up_sync(~0u, x, o);
-                if (lane >= o)
-                    x += y;
+                x += lane >= o ? y : 0;
             }
             uint32_t before = x - sum;
             if (before < need && x >= need) {
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    if (before < need && before + c[i] >= need) {
-                        found[0] = (1 << kDigit) - 1 - lane * kEach - i;
-                        found[1] = need - before;
-                        found[2] = c[i];
-                    }
-                    before += c[i];
-                }
+                int digit = (1 << kDigit) - 1 - lane * kEach;
+#pragma unroll 1
+                for (; before + hist[digit] < need; --digit)
+                    before += hist[digit];
+                found[0] = digit;
+                found[1] = need - before;
+                found[2] = hist[digit];
             }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = lane; i < 1 << kDigit; i += 32)
+                hist[i] = 0;
         }
         __syncthreads();
         border |= found[0] << shift;
@@ -393,19 +362,19 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
         edge_d = ~0u;
     } else if (left == need) { // all that share the border's bits
     } else if (left <= kCandidates) {
-        for (int round = 0; round < rounds; ++round) {
-            if (rounds > 1)
-                load(round);
+#pragma unroll 1
+        for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+            const Quad q = read(i);
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (shares(k[i]))
-                    candidate[atomicAdd(&candidates, 1u)] =
-                        make_uint2(k[i] - lo, (round * THREADS + tid) * PER + i);
+            for (int c = 0; c < 4; ++c)
+                if (shares(q.k[c]))
+                    candidate[atomicAdd(&candidates, 1u)] = make_uint2(q.k[c] - lo, i + c);
         }
         __syncthreads();
         if (tid < (int)left) {
             const uint2 mine = candidate[tid];
             uint32_t rank = 0;
+#pragma unroll 4
             for (uint32_t j = 0; j < left; ++j) {
                 const uint2 other = candidate[j];
                 rank += other.x > mine.x || (other.x == mine.x && other.y < mine.y);
@@ -416,44 +385,108 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
         __syncthreads();
         edge_d = edge.x;
         edge_at = edge.y;
-    } else { // many equal keys: the position of the need-th of them
-        uint32_t equal = 0;
-        for (int round = 0; round < rounds; ++round) {
-            if (rounds > 1)
-                load(round);
-            uint32_t e = 0, total;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                e += shares(k[i]);
-            uint32_t at = equal + block_scan<THREADS>(e, warp_sums, total);
-            equal += total;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (shares(k[i]) && ++at == need)
-                    edge.y = (round * THREADS + tid) * PER + i;
-        }
-        __syncthreads();
-        edge_at = edge.y;
     }
-    uint32_t written = 0;
-    for (int round = 0; round < rounds; ++round) {
-        if (rounds > 1)
-            load(round);
-        const uint32_t i0 = (round * THREADS + tid) * PER;
-        uint32_t chosen = 0, total; // a bit for each key
+    // A warp's run of the keys, and what is chosen of those before it.  Where
+    // many keys are equal to the border, the first `need` of them are.
+    const bool equals = need != 0 && left != need && left > kCandidates;
+    const int run = ((n + kWarps - 1) / kWarps + 127) / 128 * 128;
+    const int first = warp * run + 4 * lane, last = min(n, (warp + 1) * run);
+    // of four keys, which are chosen for certain and which are on the border
+    auto look = [&](int i, uint32_t &sure, uint32_t &maybe) {
+        const Quad q = read(i);
+        sure = maybe = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t d = k[i] - lo;
-            const bool yes = k[i] == kKeyKept ||
-                             (k[i] != 0 && (d > edge_d || (d == edge_d && i0 + i <= edge_at)));
-            chosen |= (yes ? 1u : 0u) << i;
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t d = q.k[c] - lo;
+            const bool scored = q.k[c] != 0 && q.k[c] != kKeyKept, on = scored && d == edge_d;
+            if (q.k[c] == kKeyKept || (scored && d > edge_d) ||
+                (on && !equals && (uint32_t)(i + c) <= edge_at))
+                sure |= 1u << c;
+            else if (on && equals)
+                maybe |= 1u << c;
         }
-        uint32_t at = written + block_scan<THREADS>(__popc(chosen), warp_sums, total);
-        written += total;
-        for (; chosen; chosen &= chosen - 1)
-            list[at++] = i0 + __ffs(chosen) - 1;
+    };
+    uint32_t sums[2] = {0, 0};
+#pragma unroll 1
+    for (int i = first; i < last; i += 128) {
+        uint32_t a, b;
+        look(i, a, b);
+        sums[0] += __popc(a);
+        sums[1] += __popc(b);
+    }
+    sums[0] = __reduce_add_sync(~0u, sums[0]);
+    sums[1] = __reduce_add_sync(~0u, sums[1]);
+    if (lane == 0) {
+        seen[2][warp] = sums[0];
+        seen[3][warp] = sums[1];
+    }
+    __syncthreads();
+    uint32_t above = __reduce_add_sync(~0u, lane < warp ? seen[2][lane] : 0u);
+    uint32_t on = __reduce_add_sync(~0u, lane < warp ? seen[3][lane] : 0u);
+    const uint32_t most_on = equals ? need : 0;
+#pragma unroll 1
+    for (int i = first; i - 4 * lane < last; i += 128) {
+        uint32_t a = 0, b = 0;
+        if (i < last)
+            look(i, a, b);
+        const uint32_t counts = __popc(a) | __popc(b) << 16;
+        uint32_t x = counts;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(~0u, x, o);
+            x += lane >= o ? y : 0;
+        }
+        const uint32_t total = __shfl_sync(~0u, x, 31);
+        x -= counts;
+        uint32_t at_a = above + (x & 0xFFFF), at_b = on + (x >> 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const bool sure = a >> c & 1, maybe = b >> c & 1;
+            if (sure || (maybe && at_b < most_on))
+                list[at_a + min(at_b, most_on)] = i + c;
+            at_a += sure;
+            at_b += maybe;
+        }
+        above += total & 0xFFFF;
+        on += total >> 16;
     }
 }
+
+// The list of a sequence of n <= p.most blocks (all of them), and what lies
+// behind every list.
+__device__ __forceinline__ void fill_list(const SelectParams &p, int n, int32_t *list)
+{
+    for (int i = threadIdx.x; i < p.most; i += blockDim.x)
+        if (i >= n || n <= p.most)
+            list[i] = i < n ? i : -1;
+}
+
+// The lists of the keys in the workspace; rows that fit p.chunk keys of shared
+// memory are read from there.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectParams p)
+{
+    extern __shared__ __align__(16) uint32_t near_keys[];
+    griddep_wait();
+    const int head = blockIdx.x, s = blockIdx.y;
+    const int n = (checked_len(p, s, false) + p.block_size - 1) / p.block_size;
+    const int64_t row = (int64_t)s * p.num_kv_heads + head;
+    if (head == 0 && threadIdx.x == 0)
+        p.list_lens[s] = min(n, p.most);
+    fill_list(p, n, p.lists + row * p.most);
+    if (n <= p.most)
+        return;
+    const uint32_t *keys = p.keys + row * p.stride;
+    if (n <= p.chunk) {
+        for (int i = threadIdx.x * 4; i < n; i += THREADS * 4)
+            *reinterpret_cast<uint4 *>(near_keys + i) = *reinterpret_cast<const uint4 *>(keys + i);
+        __syncthreads();
+        keys = near_keys;
+    }
+    pick_blocks<THREADS>(p, n, p.lists + row * p.most, keys);
+}
+
+constexpr int kPickSmem = 40 << 10;   // keys of a row in shared memory, without asking for more
 
 static bool aligned(const void *p, uintptr_t a)
 {
@@ -550,12 +583,12 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     p.recent = num_recent_blocks;
     p.stride = stride;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = sm_count(&e);
+    if (!sms)
+        return PA_ERR_CUDA;
     if (stride > max_selected) { // else every block of every sequence is chosen
         // Tiles of a CTA: about two CTAs an SM in all, so that the queries'
         // codes are formed few times, but no more than 16 tiles a warp.
-        const int sms = sm_count(&e);
-        if (!sms)
-            return PA_ERR_CUDA;
         const int64_t all = row_tiles * num_kv_heads * num_seqs, slots = 2ll * sms * kScoreWarps;
         const int64_t each = std::min<int64_t>((all + slots - 1) / slots, 16);
         p.heads_log2 = heads_log2(num_kv_heads);
@@ -575,11 +608,11 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
         if (e != cudaSuccess)
             return PA_ERR_CUDA;
     }
-    // Rows that fit the registers of 512 threads of 8 keys; longer ones, 16384
-    // keys at a time.
     const dim3 rows(num_kv_heads, num_seqs);
-    e = stride <= 4096 ? launch_after_previous(pick_kernel<512, 8>, rows, dim3(512), 0, st, p)
-                       : launch_after_previous(pick_kernel<1024, 16>, rows, dim3(1024), 0, st, p);
+    const bool small = stride * 4 <= kPickSmem;
+    p.chunk = small ? stride : 0;
+    e = small ? launch_after_previous(pick_kernel<512>, rows, dim3(512), stride * 4, st, p)
+              : launch_after_previous(pick_kernel<1024>, rows, dim3(1024), 0, st, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -195,6 +195,25 @@ def test_select_odd_values(pa):
     assert 150 in got[0][0, 1].tolist()
 
 
+@pytest.mark.parametrize("b,h,hkv,n,most", [
+    (1, 2, 1, 5000, 200),      # one CTA cluster, keys in two rounds
+    (40, 32, 8, 90, 7),        # more (sequence, head)s than CTAs fit: eight heads a cluster
+    (10, 16, 8, 333, 64), (3, 24, 12, 150, 31), (2, 4, 4, 70000, 100)])
+def test_select_shapes_of_the_grid(pa, b, h, hkv, n, most):
+    """Small codes, so that scores tie often, also at the border."""
+    d, bs, g = 64, 16, R.gen(b, "cuda")
+    lens = [bs * n - 3 * i for i in range(b)]
+    tables, nb = R.make_tables(lens, bs, seed=b)
+    up = torch.randint(0, 4, (nb, hkv, 1, d), generator=g, device="cuda")
+    bounds = torch.cat((up, up - 1), 2).to(torch.int8)
+    bsc = torch.exp2(torch.randint(-1, 2, (nb, hkv), generator=g, device="cuda").float())
+    q = torch.randn(b, h, d, generator=g, device="cuda").to(torch.bfloat16)
+    got = _select(pa, q, bounds, bsc, tables, R.ints(lens), bs, most, 1, 2, max(lens))
+    want = R.ref_select(q, bounds, bsc, tables, R.ints(lens), bs, most, 1, 2)
+    assert pa.pa_device_errors(clear=True) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_select_many_blocks(pa):
     h, hkv, d, bs = 16, 2, 64, 16
     lens = [16 * 20000, 5000]
