@@ -116,7 +116,7 @@ __device__ __forceinline__ void locate(const DecodeArgs &p, int s, int head, int
     if (p.lists) {
         if (j >= listed)
             return;
-        j = __ldg(p.lists + ((int64_t)s * p.num_kv_heads + head) * p.max_listed + j);
+        j = p.lists[((int64_t)s * p.num_kv_heads + head) * p.max_listed + j];
         if (j < 0)
             return; // padding
         if (j >= blocks) {
@@ -127,7 +127,7 @@ __device__ __forceinline__ void locate(const DecodeArgs &p, int s, int head, int
     live = j >= blocks ? 0 : max(0, min(kTile, len - (j << p.block_log2) - sub * kTile));
     if (live == 0)
         return;
-    const int blk = __ldg(p.tables + (int64_t)s * p.max_blocks + j);
+    const int blk = p.tables[(int64_t)s * p.max_blocks + j];
     if (blk < 0 || blk >= p.num_blocks) {
         atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
         return;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
             const int seg_end = w.seg + w.tiles, stop = min(end, seg_end);
             w.flags = (w.at == w.seg ? kBegins : 0) | (stop == seg_end ? kEnds : 0);
             w.len = length_of(p, w.seq, lane == 0 && warp == 0);
-            w.listed = p.lists ? min(__ldg(p.list_lens + w.seq), p.max_listed) : 0;
+            w.listed = p.lists ? min(p.list_lens[w.seq], p.max_listed) : 0;
             w.next = w.at - w.seg + tw;
             // a warp without a tile takes an empty one: all meet at the part's end
             w.left = max(1, (stop - w.at - tw + tws - 1) / tws);
@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
             if (n_row >= 0) {
                 const float *sc = p.scales + (int64_t)(n_row >> p.block_log2) * p.num_kv_heads +
                                   head;
-                n_ks = __ldg(sc);
-                n_vs = __ldg(sc + (int64_t)p.num_blocks * p.num_kv_heads);
+                n_ks = *sc;
+                n_vs = sc[(int64_t)p.num_blocks * p.num_kv_heads];
             }
         }
         w.next += 32 * tws;

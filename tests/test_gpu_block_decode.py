@@ -429,6 +429,80 @@ def test_serving_steps_in_a_graph(pa):
     assert pa.pa_device_errors(clear=True) == 0
 
 
+def test_two_graphs_share_a_workspace(pa):
+    """Captured apart, replayed in turn: each leaves nothing that the other sees."""
+    runs, ws = [], _workspace(pa, 16, 2, 128)
+    for i, lens in enumerate(([5000, 70], [33, 2500, 900, 1])):
+        q, pool, scales, tables, sl = _inputs(lens, 16, 2, 128, 16, torch.float16, True, seed=60 + i)
+        out = torch.empty_like(q)
+        args = (out, q, pool, scales, tables, sl, 0.1, 16, max(lens), ws)
+        pa.pa_decode_fp8_block(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.pa_decode_fp8_block(*args)
+        runs.append((graph, out, R.ref_decode(q, pool, scales, tables, sl, 16, 0.1), args))
+    for graph, out, ref, _ in (runs[0], runs[1], runs[0], runs[0], runs[1]):
+        out.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        R.check_decode(out, ref, True, True)
+
+
+def test_offsets_beyond_32_bits(pa):
+    """A pool of 6 GB: the blocks in use lie in its last part, whose byte offsets
+    pass 2^31 in a plane; every operator on them."""
+    h, hkv, d, bs, lens = 16, 8, 128, 16, [200, 40]
+    nb = 190_000
+    tables, used = R.make_tables(lens, bs, extra=0)
+    tables = torch.where(tables >= 0, tables + nb - used, -1).int()
+    pool = torch.zeros(2, nb, bs, hkv, d, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(2, nb, hkv, device="cuda")
+    bounds = torch.zeros(nb, hkv, 2, d, dtype=torch.int8, device="cuda")
+    bsc = torch.ones(nb, hkv, device="cuda")
+    g, sl, qsl = R.gen(1, "cuda"), R.ints(lens), R.starts(lens)
+    k, v = (torch.randn(sum(lens), hkv, d, generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn(2, h, d, generator=g, device="cuda").half()
+    pa.pa_reshape_and_cache_fp8_block(k, v, pool, scales, tables, sl, qsl, bs, max(lens))
+    pa.pa_update_block_bounds(bounds, bsc, pool, tables, sl, qsl, bs, max(lens), kv_scales=scales)
+    lists, counts = _select(pa, q, bounds, bsc, tables, sl, bs, 5, 1, 1, 200)
+    ws, out, sparse = _workspace(pa, h, hkv, d), torch.empty_like(q), torch.empty_like(q)
+    pa.pa_decode_fp8_block(out, q, pool, scales, tables, sl, 0.1, bs, 200, ws)
+    pa.pa_decode_sparse(sparse, q, pool, tables, sl, lists, counts, 0.1, bs, ws, kv_scales=scales)
+    torch.cuda.synchronize()
+    assert pa.pa_device_errors(clear=True) == 0
+    assert not pool[:, :nb - used].any()
+    # the same on a pool of the used blocks alone
+    near = torch.where(tables >= 0, tables - (nb - used), -1).int()
+    tail = slice(nb - used, nb)
+    zero = torch.zeros(2, used, bs, hkv, d, dtype=torch.uint8, device="cuda")
+    want = R.ref_write(k, v, zero, torch.ones(2, used, hkv, device="cuda"), near, sl, qsl, bs)
+    assert torch.equal(pool[:, tail], want[0]) and torch.equal(scales[:, tail], want[1])
+    wb = R.ref_bounds(bounds[tail], bsc[tail], *want, near, sl, qsl, bs)
+    assert torch.equal(bounds[tail], wb[0]) and torch.equal(bsc[tail], wb[1])
+    wl = R.ref_select(q, *wb, near, sl, bs, 5, 1, 1)
+    assert torch.equal(lists, wl[0]) and torch.equal(counts, wl[1])
+    R.check_decode(out, R.ref_decode(q, *want, near, sl, bs, 0.1), True, True)
+    R.check_decode(sparse, R.ref_decode(q, *want, near, sl, bs, 0.1, lists, counts), True, True)
+
+
+def test_decode_of_not_finite_values(pa):
+    """A NaN key or value in the cache reaches its rows and no others; what lies
+    behind the last token does not."""
+    lens, h, hkv, d, bs = [50, 50, 50], 4, 2, 128, 16
+    q, pool, scales, tables, sl = _inputs(lens, h, hkv, d, bs, torch.float16, True)
+    ref = R.ref_decode(q, pool, scales, tables, sl, bs, 0.1)
+    pool[0, tables[0, 1], 3, 0, 5] = 0x7F              # a key of head 0
+    pool[1, tables[2, 3], 1, 1, 7] = 0xFF              # a value of head 1: token 49
+    out = torch.empty_like(q)
+    pa.pa_decode_fp8_block(out, q, pool, scales, tables, sl, 0.1, bs, 50, _workspace(pa, h, hkv, d))
+    assert torch.isnan(out[0, :2]).all() and torch.isnan(out[2, 2:, 7]).all()
+    assert torch.isnan(out).sum() == 2 * d + 2
+    fine = ~torch.isnan(out)
+    part = tuple(torch.where(fine, x, 0.0) if x.dim() == 3 else x for x in ref)
+    R.check_decode(torch.where(fine, out, 0.0), part, True, True)
+
+
 def test_two_streams_with_their_own_workspaces(pa):
     """Decodes of different problems in flight at once on two streams."""
     runs = []
