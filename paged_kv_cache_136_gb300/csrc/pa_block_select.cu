@@ -609,10 +609,10 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
             return PA_ERR_CUDA;
     }
     const dim3 rows(num_kv_heads, num_seqs);
-    const bool small = stride * 4 <= kPickSmem;
-    p.chunk = small ? stride : 0;
-    e = small ? launch_after_previous(pick_kernel<512>, rows, dim3(512), stride * 4, st, p)
-              : launch_after_previous(pick_kernel<1024>, rows, dim3(1024), 0, st, p);
+    p.chunk = stride * 4 <= kPickSmem ? stride : 0;
+    e = stride <= 1024
+            ? launch_after_previous(pick_kernel<256>, rows, dim3(256), p.chunk * 4, st, p)
+            : launch_after_previous(pick_kernel<1024>, rows, dim3(1024), p.chunk * 4, st, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
