@@ -133,11 +133,14 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
     return r;
 }
 
-// kv heads that a CTA of eight warps takes side by side: the largest of 8, 4,
-// 2, 1 that divides them.
-inline int heads_log2(int num_kv_heads)
+// kv heads that a CTA of up to eight warps takes side by side: the most, up to
+// 8, that divide them, so that what lies together is read together.
+inline int heads_together(int num_kv_heads)
 {
-    return num_kv_heads % 8 == 0 ? 3 : num_kv_heads % 4 == 0 ? 2 : num_kv_heads % 2 == 0 ? 1 : 0;
+    int h = 8;
+    while (num_kv_heads % h)
+        --h;
+    return h;
 }
 
 // 16- and 8-byte loads that do not stay in L1.

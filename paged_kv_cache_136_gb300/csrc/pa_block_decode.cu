@@ -23,7 +23,8 @@ cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap
 template <typename T, bool E4M3, int D>
 static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
 {
-    const int smem = decode_smem<E4M3, D>(1 << p.heads_log2 < kWarps);
+    const int warps = p.heads * p.tiles_at_once;
+    const int smem = decode_smem<E4M3, D>(warps, p.tiles_at_once > 1);
     // once a device: a CTA of this kernel takes most of an SM's shared memory
     static bool ready[64];
     int dev = 0;
@@ -31,12 +32,12 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
     if (e == cudaSuccess && !ready[dev & 63]) {
         e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 decode_smem<E4M3, D>(true));
+                                 decode_smem<E4M3, D>(kWarps, true));
         ready[dev & 63] = e == cudaSuccess;
     }
     if (e != cudaSuccess)
         return e;
-    e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas), dim3(32 * kWarps), smem,
+    e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas), dim3(32 * warps), smem,
                               s, map, p);
     if (e != cudaSuccess)
         return e;
@@ -44,7 +45,7 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
         return cudaSuccess;
     // A warp for each query row of the most cuts there can be, as far as three
     // CTAs an SM go.
-    const int rows = p.group << p.heads_log2;
+    const int rows = p.group * p.heads;
     const int merge = std::min((ctas * rows + kMergeWarps - 1) / kMergeWarps, 3 * kMaxCtas / 2);
     return launch_after_previous(block_merge_kernel<T, E4M3, D>, dim3(merge),
                                  dim3(32 * kMergeWarps), 0, s, p, ctas);
@@ -113,6 +114,15 @@ static bool make_map(CUtensorMap *map, const void *pool, bool e4m3, int dtype, i
     return r == CUDA_SUCCESS;
 }
 
+// Tiles that the warps of a CTA of `heads` heads take at a time: 1, 2, 4 or 8.
+static int tiles_at_once(int heads)
+{
+    int t = 1;
+    while (2 * t * heads <= kWarps)
+        t *= 2;
+    return t;
+}
+
 // Workspace: the cuts, then two partial states of each CTA.
 struct Layout {
     size_t ml, o, total;
@@ -120,8 +130,8 @@ struct Layout {
 
 static Layout layout(int num_heads, int num_kv_heads, int head_size)
 {
-    const size_t rows = (size_t)kMaxCtas * 2 * (num_heads / num_kv_heads)
-                        << heads_log2(num_kv_heads);
+    const size_t rows = (size_t)kMaxCtas * 2 * (num_heads / num_kv_heads) *
+                        heads_together(num_kv_heads);
     Layout w;
     w.ml = round_up(kMaxCtas * sizeof(int4));
     w.o = w.ml + round_up(rows * 2 * sizeof(float));
@@ -170,18 +180,33 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     const int sms = sm_count(&e);
     if (!sms)
         return PA_ERR_CUDA;
-    // Short work is not cut: one CTA a (sequence, head group), of as many heads
-    // as leave a warp 8 tiles at most, if all of them fit the GPU at once.  (A
-    // cut and its merge cost about as much as those 8 tiles.)
+    // Cut into equal runs of the largest head groups, or one CTA for each
+    // (sequence, head group) of some size: whichever takes less by these costs,
+    // in tiles of a warp (about 0.35 us): what a launch takes besides its tiles
+    // 10, a merge 11, each further (sequence, group) of a CTA 6.  (Cut and whole:
+    // 152 sequences of 41 tokens, 5 kv heads 33 and 5.6 us; 64 lists of 64
+    // 16-token blocks, 8 kv heads 32.7 and 28.4 us.)
     const int slots = std::min((head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2) * sms, kMaxCtas);
-    int hl = heads_log2(num_kv_heads);
+    // tiles of a sequence, for this choice: a list rarely names a block twice
+    const int64_t usual = std::min(most, cap / kTile + 1);
+    int heads = heads_together(num_kv_heads), at_once = tiles_at_once(heads);
+    const int64_t groups = (int64_t)num_seqs * (num_kv_heads / heads);
+    double best = 21 + (double)groups * usual / ((double)slots * at_once) + 6.0 * groups / slots;
     bool whole = false;
-    for (int h = hl; h >= 0 && !whole; --h)
-        if (most <= 8ll << (3 - h) && (int64_t)num_seqs * (num_kv_heads >> h) <= slots) {
+    for (int h = heads; h >= 1; --h) {
+        if (num_kv_heads % h)
+            continue;
+        const int64_t ctas = (int64_t)num_seqs * (num_kv_heads / h);
+        const int t = tiles_at_once(h);
+        const double cost = (double)((ctas + slots - 1) / slots) * (10 + (usual + t - 1) / t);
+        if (cost < best && ctas <= INT32_MAX) {
+            best = cost;
             whole = true;
-            hl = h;
+            heads = h;
+            at_once = t;
         }
-    const int64_t tiles = most * num_seqs * (num_kv_heads >> hl);
+    }
+    const int64_t tiles = most * num_seqs * (num_kv_heads / heads);
     DecodeArgs p = {};
     p.err = device_error_word(&e);
     if (!p.err)
@@ -202,8 +227,9 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.group = group;
-    p.heads_log2 = hl;
-    p.num_groups = num_kv_heads >> hl;
+    p.heads = heads;
+    p.tiles_at_once = at_once;
+    p.num_groups = num_kv_heads / heads;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks;
     p.block_log2 = block_size == 16 ? 4 : 5;
@@ -213,7 +239,7 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     p.whole = whole;
     // Else equal runs, of at least kMinRun tiles a warp.
     const int64_t ctas = whole ? (int64_t)num_seqs * p.num_groups
-                               : std::min<int64_t>(tiles / (kMinRun * (kWarps >> hl)) + 1, slots);
+                               : std::min<int64_t>(tiles / (kMinRun * at_once) + 1, slots);
     alignas(64) CUtensorMap map;
     if (!make_map(&map, kv_cache, kv_scales != nullptr, dtype, num_blocks, block_size,
                   num_kv_heads, head_size))

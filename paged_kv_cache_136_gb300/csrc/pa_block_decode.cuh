@@ -23,8 +23,8 @@
 //
 // Work.  The (sequence, group of HG kv heads, 16-token tile) triples are laid
 // out in one line and cut into equal runs, one for each CTA, so that any mix
-// of lengths balances.  Inside a CTA the 8 warps are HG heads times 8 / HG
-// interleaved tiles.  A (sequence, group) that a cut divides leaves partial
+// of lengths balances.  Inside a CTA the (up to 8) warps are HG heads, the most
+// that divide the kv heads, times 1, 2, 4 or 8 interleaved tiles.  A (sequence, group) that a cut divides leaves partial
 // states, which a second kernel merges.
 //
 // e4m3 scales: the score takes the key scale; the value scale multiplies the
@@ -48,7 +48,7 @@
 namespace pa {
 namespace block {
 
-constexpr int kWarps = 8;      // warps of a CTA
+constexpr int kWarps = 8;      // warps of a CTA, at most
 constexpr int kMaxCtas = 304;  // CTAs of a launch, at most (workspace size)
 constexpr int kTile = 16;      // tokens a warp takes at a time
 constexpr int kMinRun = 4;     // tiles a warp takes at least before work is cut
@@ -66,8 +66,9 @@ struct DecodeArgs {
     int4 *cuts;                // [CTAs] {sequence, head group, CTAs sharing it, -}
     float *ws_o;               // [CTAs, 2, HG * G, D]
     float *ws_ml;              // [CTAs, 2, HG * G, 2]
-    int num_seqs, num_heads, num_kv_heads, group, heads_log2, num_groups, num_blocks, max_blocks,
+    int num_seqs, num_heads, num_kv_heads, group, num_groups, num_blocks, max_blocks,
         block_log2, max_listed, len_cap;
+    int heads, tiles_at_once;  // warps of a CTA: kv heads times interleaved tiles
     int whole;                 // a CTA is one (sequence, head group): nothing is cut
     float qscale;              // scale * log2 e
 };
@@ -164,10 +165,10 @@ constexpr int kEnds = 4;   // ... and ends it
 // Shared memory of a CTA: the rings (aligned to 1024), their Metas, and half of
 // the states that a head's upper warps hand to its lower ones
 // (none where every warp has a head of its own).
-template <bool E4M3, int D> constexpr int decode_smem(bool hand_over)
+template <bool E4M3, int D> constexpr int decode_smem(int warps, bool hand_over)
 {
-    return 1024 + kWarps * stages_of<E4M3, D>() * (tile_bytes<E4M3, D>() + (int)sizeof(Meta)) +
-           (hand_over ? kWarps / 2 * 4 * (D + 2) * 4 : 0);
+    return 1024 + warps * stages_of<E4M3, D>() * (tile_bytes<E4M3, D>() + (int)sizeof(Meta)) +
+           (hand_over ? warps / 2 * 4 * (D + 2) * 4 : 0);
 }
 
 // Where a warp's walk over its CTA's run stands.
@@ -228,12 +229,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 
     char *const smem = smem_raw + (-smem_addr(smem_raw) & 1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int heads = 1 << p.heads_log2;         // kv heads of the CTA
-    const int hl = warp & (heads - 1), tw = warp >> p.heads_log2, tws = kWarps >> p.heads_log2;
+    const int heads = p.heads, tws = p.tiles_at_once, warps = heads * tws;
+    const int tw = warp / heads, hl = warp - tw * heads;
     char *const ring = smem + warp * kStages * kTileBytes;
-    Meta *const meta = reinterpret_cast<Meta *>(smem + kWarps * kStages * kTileBytes) +
+    Meta *const meta = reinterpret_cast<Meta *>(smem + warps * kStages * kTileBytes) +
                        warp * kStages;
-    float *const handed = reinterpret_cast<float *>(smem + kWarps * kStages *
+    float *const handed = reinterpret_cast<float *>(smem + warps * kStages *
                                                     (kTileBytes + (int)sizeof(Meta)));
     if (lane < kStages)
         mbar_init(&meta[lane].bar, 1);
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
         f_seg = 0;
         end = f_tiles = tiles_of(p, f_seq, warp == 0);
     } else {
-        const int slice = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
+        const int slice = (p.num_seqs + 32 * warps - 1) / (32 * warps);
         const int s_lo = min(tid * slice, p.num_seqs), s_hi = min(s_lo + slice, p.num_seqs);
         int mine = 0;
         for (int s = s_lo; s < s_hi; ++s)
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             base += w < warp ? warp_sums[w] : 0;
-            total += warp_sums[w];
+            total += w < warps ? warp_sums[w] : 0;
         }
         base += x - mine;
         run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinRun * tws);
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     make_int4(w.seq, w.grp, (seg_end - 1) / run - (int)blockIdx.x + 1, 0);
             w.at = stop;
         }
-        const int head = (w.grp << p.heads_log2) + hl, n = min(32, w.left);
+        const int head = w.grp * heads + hl, n = min(32, w.left);
         n_whose = w.seq << 16 | head;
         w.left -= n;
         int live = 0;
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
         // time, and of their queries the even ones, then the odd ones.
         for (int half = tws >> 1; half; half >>= 1) {
             float *const box =
-                handed + ((((tw & (half - 1)) << p.heads_log2) + hl) * 4 + t) * (D + 2);
+                handed + (((tw & (half - 1)) * heads + hl) * 4 + t) * (D + 2);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float &m = k ? m1 : m0, &l = k ? l1 : l0;
@@ -716,8 +717,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                 if (p.lse && g == 0)
                     p.lse[row] = l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
             } else {
-                const int64_t row = ((int64_t)(2 * blockIdx.x + slot) << p.heads_log2) * p.group +
-                                    hl * p.group + col;
+                const int64_t row =
+                    ((int64_t)(2 * blockIdx.x + slot) * heads + hl) * p.group + col;
                 float *dst = p.ws_o + row * D;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
@@ -775,7 +776,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
     if (seen.z >= 2)
         list[at] = seen;
     __syncthreads();
-    const int rows = p.group << p.heads_log2, items = found * rows;
+    const int rows = p.group * p.heads, items = found * rows;
     // warps of a row: 1, 2, 5 or all 10, with at least kAtOnce states each
     int each = 1;
 #pragma unroll

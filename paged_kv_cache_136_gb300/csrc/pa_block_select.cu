@@ -36,7 +36,7 @@ struct SelectParams {
     unsigned int *err;
     int num_heads, num_kv_heads, group, num_blocks, max_blocks, block_size, len_cap, most, sink,
         recent, stride;
-    int heads_log2;              // kv heads that a CTA scores
+    int heads;                   // kv heads that a scoring CTA takes side by side
     int chunk;                   // score_kernel: tiles of a CTA; pick_kernel: keys of shared memory
 };
 
@@ -68,9 +68,9 @@ constexpr int kScoreWarps = 8;
 // exact in the fp32 accumulator; 128 sum c is taken off at the end.  The two
 // scales are powers of two.  So a score has one value, whatever the order.
 //
-// Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's 8
-// warps are 8 kv heads (or fewer, times several tiles), so that the bounds of a
-// block, which lie together, are read at one time.  A tile's bounds are asked
+// Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's
+// warps are up to 8 kv heads (times several tiles where that is 8 at most), so
+// that the bounds of a block, which lie together, are read at one time.  A tile's bounds are asked
 // for while the tile before it (or the queries) are worked on.
 //
 // Scores the blocks j0 .. j0 + 15, then those `step` further, below `last`, of
@@ -221,8 +221,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const SelectParams p)
 {
     griddep_wait();
-    const int warp = threadIdx.x >> 5, groups = p.num_kv_heads >> p.heads_log2;
-    const int head = (blockIdx.x % groups << p.heads_log2) + (warp & ((1 << p.heads_log2) - 1));
+    const int warp = threadIdx.x >> 5, groups = p.num_kv_heads / p.heads;
+    const int head = blockIdx.x % groups * p.heads + warp % p.heads;
     const int s = blockIdx.y;
     const int len = checked_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
     const int n = (len + p.block_size - 1) / p.block_size;
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2) score_kernel(const Select
         return;
     const int first = blockIdx.x / groups * p.chunk * 16;
     uint32_t *const keys = p.keys + ((int64_t)s * p.num_kv_heads + head) * p.stride;
-    score_blocks<T, D>(p, s, head, n, first + (warp >> p.heads_log2) * 16,
-                       16 * (kScoreWarps >> p.heads_log2), min(n, first + p.chunk * 16),
+    score_blocks<T, D>(p, s, head, n, first + warp / p.heads * 16,
+                       16 * (kScoreWarps / p.heads), min(n, first + p.chunk * 16),
                        [&](int j, uint32_t key) { keys[j] = key; });
     // Not before: the picking CTAs would crowd on the SMs that are free first
     // (27 against 20 us for 8 sequences of 4096 blocks).
@@ -587,16 +587,23 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     if (!sms)
         return PA_ERR_CUDA;
     if (stride > max_selected) { // else every block of every sequence is chosen
-        // Tiles of a CTA: about two CTAs an SM in all, so that the queries'
-        // codes are formed few times, but no more than 16 tiles a warp.
-        const int64_t all = row_tiles * num_kv_heads * num_seqs, slots = 2ll * sms * kScoreWarps;
-        const int64_t each = std::min<int64_t>((all + slots - 1) / slots, 16);
-        p.heads_log2 = heads_log2(num_kv_heads);
-        p.chunk = (int)each * (kScoreWarps >> p.heads_log2);
-        const dim3 grid((unsigned)((row_tiles + p.chunk - 1) / p.chunk *
-                                   (num_kv_heads >> p.heads_log2)),
+        // Tiles of a warp: those that take the fewest steps in waves of two
+        // CTAs an SM, with the start of a CTA (its queries' codes) as 3.
+        p.heads = heads_together(num_kv_heads);
+        const int at_once = kScoreWarps / p.heads; // tiles
+        const int64_t rows = (int64_t)(num_kv_heads / p.heads) * num_seqs, slots = 2 * sms;
+        int64_t best = INT64_MAX;
+        for (int each = 1; each <= 64; ++each) {
+            const int64_t runs = (row_tiles + each * at_once - 1) / (each * at_once);
+            const int64_t steps = (runs * rows + slots - 1) / slots * (3 + each);
+            if (steps < best) {
+                best = steps;
+                p.chunk = each * at_once;
+            }
+        }
+        const dim3 grid((unsigned)((row_tiles + p.chunk - 1) / p.chunk * (num_kv_heads / p.heads)),
                         num_seqs);
-        const dim3 threads(32 * kScoreWarps);
+        const dim3 threads(32 * p.heads * at_once);
         if (dtype == PA_BF16)
             e = head_size == 128
                     ? launch_after_previous(score_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, p)
@@ -610,7 +617,8 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
     }
     const dim3 rows(num_kv_heads, num_seqs);
     p.chunk = stride * 4 <= kPickSmem ? stride : 0;
-    e = stride <= 1024
+    // Long rows get 1024 threads, if there are no more of them than fit at once.
+    e = stride <= 1024 || (int64_t)num_kv_heads * num_seqs > 2 * sms
             ? launch_after_previous(pick_kernel<256>, rows, dim3(256), p.chunk * 4, st, p)
             : launch_after_previous(pick_kernel<1024>, rows, dim3(1024), p.chunk * 4, st, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
