@@ -588,12 +588,13 @@ pa_status pa_select_blocks(int32_t *block_lists, int32_t *list_lens, const void 
         return PA_ERR_CUDA;
     if (stride > max_selected) { // else every block of every sequence is chosen
         // Tiles of a warp: those that take the fewest steps in waves of two
-        // CTAs an SM, with the start of a CTA (its queries' codes) as 3.
+        // CTAs an SM, with the start of a CTA (its queries' codes) as 3; at most
+        // 16, so that sequences shorter than max_seq_len still spread.
         p.heads = heads_together(num_kv_heads);
         const int at_once = kScoreWarps / p.heads; // tiles
         const int64_t rows = (int64_t)(num_kv_heads / p.heads) * num_seqs, slots = 2 * sms;
         int64_t best = INT64_MAX;
-        for (int each = 1; each <= 64; ++each) {
+        for (int each = 1; each <= 16; ++each) {
             const int64_t runs = (row_tiles + each * at_once - 1) / (each * at_once);
             const int64_t steps = (runs * rows + slots - 1) / slots * (3 + each);
             if (steps < best) {
