@@ -469,9 +469,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     atomicOr(p.err, PA_DEVERR_TIMEOUT_);
             }
         }
-        // every lane has left the stage before this one: refill it
-        fetch(stage == 0 ? kStages - 1 : stage - 1);
-
         const int live = lost ? 0 : info.x;
 
         if (fresh) {
@@ -543,6 +540,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     }
                 }
             }
+            // every lane has left the stage before this one: refill it, while the
+            // products run
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
             const float f0 = E4M3 ? qmul0 * ks : qmul0, f1 = E4M3 ? qmul1 * ks : qmul1;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -651,6 +651,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     mma_16816<M>(o[i], a0, a1, a2, a3, lo[0], lo[1]);
             }
         }
+        else
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
         if (++stage == kStages) {
             stage = 0;
             parity ^= 1;
