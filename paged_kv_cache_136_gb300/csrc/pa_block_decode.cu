@@ -20,12 +20,12 @@ cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap
                                     const DecodeArgs &p, int ctas,
                                      cudaStream_t s);
 
-template <typename T, bool E4M3, int D>
-static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
+int block_decode_resident_f16(bool e4m3, int head_size, int warps, bool hand_over);
+int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_over);
+
+// The kernel's shared memory is allowed once a device (it takes most of an SM's).
+template <typename T, bool E4M3, int D> static cudaError_t prepare()
 {
-    const int warps = p.heads * p.tiles_at_once;
-    const int smem = decode_smem<E4M3, D>(warps, p.tiles_at_once > 1);
-    // once a device: a CTA of this kernel takes most of an SM's shared memory
     static bool ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -35,6 +35,32 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
                                  decode_smem<E4M3, D>(kWarps, true));
         ready[dev & 63] = e == cudaSuccess;
     }
+    return e;
+}
+
+// CTAs of so many warps that an SM holds at once; 0 on an error.
+template <typename T, bool E4M3, int D> static int resident(int warps, bool hand_over)
+{
+    static int known[kWarps + 1][2];
+    int &n = known[warps][hand_over];
+    int now = n;
+    if (!now) {
+        if (prepare<T, E4M3, D>() != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &now, block_decode_kernel<T, E4M3, D>, 32 * warps,
+                decode_smem<E4M3, D>(warps, hand_over)) != cudaSuccess)
+            return 0;
+        n = now;
+    }
+    return now;
+}
+
+template <typename T, bool E4M3, int D>
+static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
+{
+    const int warps = p.heads * p.tiles_at_once;
+    const int smem = decode_smem<E4M3, D>(warps, p.tiles_at_once > 1);
+    cudaError_t e = prepare<T, E4M3, D>();
     if (e != cudaSuccess)
         return e;
     e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas), dim3(32 * warps), smem,
@@ -43,10 +69,10 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
         return e;
     if (p.whole)
         return cudaSuccess;
-    // A warp for each query row of the most cuts there can be, as far as three
-    // CTAs an SM go.
+    // A warp for each query row of the most cuts there can be, as far as two CTAs
+    // an SM go.
     const int rows = p.group * p.heads;
-    const int merge = std::min((ctas * rows + kMergeWarps - 1) / kMergeWarps, 3 * kMaxCtas / 2);
+    const int merge = std::min((ctas * rows + kMergeWarps - 1) / kMergeWarps, 2 * kMaxCtas / 3);
     return launch_after_previous(block_merge_kernel<T, E4M3, D>, dim3(merge),
                                  dim3(32 * kMergeWarps), 0, s, p, ctas);
 }
@@ -60,6 +86,15 @@ cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap
         return e4m3 ? launch<__nv_bfloat16, true, 128>(map, p, ctas, s) : launch<__nv_bfloat16, false, 128>(map, p, ctas, s);
     return e4m3 ? launch<__nv_bfloat16, true, 64>(map, p, ctas, s) : launch<__nv_bfloat16, false, 64>(map, p, ctas, s);
 }
+
+int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_over)
+{
+    if (head_size == 128)
+        return e4m3 ? resident<__nv_bfloat16, true, 128>(warps, hand_over)
+                    : resident<__nv_bfloat16, false, 128>(warps, hand_over);
+    return e4m3 ? resident<__nv_bfloat16, true, 64>(warps, hand_over)
+                : resident<__nv_bfloat16, false, 64>(warps, hand_over);
+}
 #else
 cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap &map,
                                     const DecodeArgs &p, int ctas,
@@ -68,6 +103,15 @@ cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap 
     if (head_size == 128)
         return e4m3 ? launch<__half, true, 128>(map, p, ctas, s) : launch<__half, false, 128>(map, p, ctas, s);
     return e4m3 ? launch<__half, true, 64>(map, p, ctas, s) : launch<__half, false, 64>(map, p, ctas, s);
+}
+
+int block_decode_resident_f16(bool e4m3, int head_size, int warps, bool hand_over)
+{
+    if (head_size == 128)
+        return e4m3 ? resident<__half, true, 128>(warps, hand_over)
+                    : resident<__half, false, 128>(warps, hand_over);
+    return e4m3 ? resident<__half, true, 64>(warps, hand_over)
+                : resident<__half, false, 64>(warps, hand_over);
 }
 
 static bool aligned(const void *p, uintptr_t a)
@@ -123,6 +167,13 @@ static int tiles_at_once(int heads)
     return t;
 }
 
+// CTAs of a launch that cuts, at most: three an SM of 152 where its warps are
+// few or its tiles small, else two.
+static int max_ctas(int heads, int head_size)
+{
+    return heads <= 5 || head_size == 64 ? kMaxCtas : kMaxCtas / 3 * 2;
+}
+
 // Workspace: the cuts, then two partial states of each CTA.
 struct Layout {
     size_t ml, o, total;
@@ -130,8 +181,8 @@ struct Layout {
 
 static Layout layout(int num_heads, int num_kv_heads, int head_size)
 {
-    const size_t rows = (size_t)kMaxCtas * 2 * (num_heads / num_kv_heads) *
-                        heads_together(num_kv_heads);
+    const int heads = heads_together(num_kv_heads);
+    const size_t rows = (size_t)max_ctas(heads, head_size) * 2 * (num_heads / num_kv_heads) * heads;
     Layout w;
     w.ml = round_up(kMaxCtas * sizeof(int4));
     w.o = w.ml + round_up(rows * 2 * sizeof(float));
@@ -183,15 +234,23 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     // Cut into equal runs of the largest head groups, or one CTA for each
     // (sequence, head group) of some size: whichever takes less by these costs,
     // in tiles of a warp (about 0.35 us): what a launch takes besides its tiles
-    // 10, a merge 11, each further (sequence, group) of a CTA 6.  (Cut and whole:
-    // 152 sequences of 41 tokens, 5 kv heads 33 and 5.6 us; 64 lists of 64
-    // 16-token blocks, 8 kv heads 32.7 and 28.4 us.)
-    const int slots = std::min((head_size * (kv_scales ? 1 : 2) > 128 ? 1 : 2) * sms, kMaxCtas);
+    // 10, a merge 11, each further (sequence, group) of a CTA 6.  Cut runs take
+    // the tiles there are, whole ones those of the longest sequence: a sequence
+    // is taken for half of max_seq_len on average, a list for full.  (Cut and
+    // whole: 152 sequences of 41 tokens, 5 kv heads 33 and 5.6 us; 64 lists of 64
+    // 16-token blocks, 8 kv heads 32.7 and 28.4 us; 37 sequences of 3120 to 24966
+    // tokens, 6 kv heads of 64 49 and 158 us.)
     // tiles of a sequence, for this choice: a list rarely names a block twice
     const int64_t usual = std::min(most, cap / kTile + 1);
     int heads = heads_together(num_kv_heads), at_once = tiles_at_once(heads);
+    const auto resident = dtype == PA_BF16 ? block_decode_resident_bf16 : block_decode_resident_f16;
+    const int per_sm = resident(kv_scales != nullptr, head_size, heads * at_once, at_once > 1);
+    if (!per_sm)
+        return PA_ERR_CUDA;
+    const int slots = std::min(per_sm * sms, max_ctas(heads, head_size));
     const int64_t groups = (int64_t)num_seqs * (num_kv_heads / heads);
-    double best = 21 + (double)groups * usual / ((double)slots * at_once) + 6.0 * groups / slots;
+    double best = 21 + (double)groups * usual * (lists ? 1 : 0.5) / ((double)slots * at_once) +
+                  6.0 * groups / slots;
     bool whole = false;
     for (int h = heads; h >= 1; --h) {
         if (num_kv_heads % h)

@@ -32,8 +32,10 @@
 // heads 89 us, 6.2 TB/s.  A warp's products (m16n8k16: the 8 query rows of a
 // group are the narrow side, so no row of a product is idle at 8) take a third
 // of the issue slots.  On listed blocks each 128- or 256-byte row of a head is
-// read apart from its neighbours', which HBM serves at about 5.8 TB/s.  Besides,
-// a launch takes 3.5 us until its first tiles are in, and a merge 3 to 5 us.
+// read apart from its neighbours', which HBM serves at about 5.8 TB/s.  Tiles of
+// 2 KB (e4m3, head_size 64) are bound by a warp's latency for a tile: about 2.4
+// times the time of their bytes.  Besides, a launch takes 3.5 us until its first
+// tiles are in, and a merge 3 to 5 us.
 //
 // e4m3 scales: the score takes the key scale; the value scale multiplies the
 // probability before it is rounded to 16 bits.  The softmax's reference m is
@@ -57,7 +59,7 @@ namespace pa {
 namespace block {
 
 constexpr int kWarps = 8;      // warps of a CTA, at most
-constexpr int kMaxCtas = 304;  // CTAs of a launch, at most (workspace size)
+constexpr int kMaxCtas = 456;  // CTAs of a launch that cuts, at most
 constexpr int kTile = 16;      // tokens a warp takes at a time
 constexpr int kMinRun = 4;     // tiles a warp takes at least before work is cut
 
@@ -151,8 +153,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // it; bf16 has fp32's range and needs none.
 template <typename M> constexpr float lift_of() { return std::is_same<M, __half>::value ? 15.f : 0.f; }
 
-// Tiles of up to 4 KB: two CTAs an SM, 12 KB of tiles in flight a warp.  Tiles
-// of 8 KB: one CTA, 24 KB a warp.
+// Tiles of up to 4 KB: two CTAs of eight warps an SM, 12 KB of tiles in flight a
+// warp.  Tiles of 8 KB: one CTA, 24 KB a warp.  (Three CTAs for 2 KB tiles, with
+// 80 registers, were slower: 322 against 204 us for 227 sequences of up to 7111
+// tokens, 8 kv heads of 64.)
 template <bool E4M3, int D> constexpr int tile_bytes() { return 2 * kTile * D * (E4M3 ? 1 : 2); }
 template <bool E4M3, int D> constexpr int ctas_per_sm() { return tile_bytes<E4M3, D>() > 4096 ? 1 : 2; }
 template <bool E4M3, int D> constexpr int stages_of()
@@ -396,9 +400,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     if constexpr (kRow == 256)
                         tma_load_5d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row, 0,
                                          b_whose & 0xFFFF, 0, policy);
-                    else
+                    else if constexpr (kRow == 128)
                         tma_load_4d_hint(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row,
                                          b_whose & 0xFFFF, 0, policy);
+                    else // half a line of L2: the other half is another warp's
+                        tma_load_4d(ring + stage * kTileBytes, &pool_map, &m.bar, 0, row,
+                                    b_whose & 0xFFFF, 0);
                     if constexpr (E4M3)
                         *reinterpret_cast<float2 *>(&m.k_scale) = make_float2(b_ks, b_vs);
                 } else {
@@ -746,15 +753,15 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 
 // Merge of the (sequence, group)s that a cut divides: with M = max m_i,
 // out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Every CTA lists the cuts;
-// the (cut, query row) pairs then go round the warps, or round pairs, halves
-// or wholes of a CTA's warps, which split the states, where there are many
+// the (cut, query row) pairs then go round the warps, or round 3, 5 or all of a
+// CTA's warps, which split the states, where there are many
 // states and too few rows to fill the warps.  Bound by latency, so that what a
 // row needs is asked for at once: four states' m, l and o at a time.
-constexpr int kMergeWarps = 10; // a thread for each cut there can be
+constexpr int kMergeWarps = 15; // a thread for each cut there can be
 static_assert(32 * kMergeWarps >= kMaxCtas, "one look at the cuts");
 
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const DecodeArgs p, int ctas)
+__global__ void __launch_bounds__(32 * kMergeWarps, 2) block_merge_kernel(const DecodeArgs p, int ctas)
 {
     constexpr float kLift = lift_of<typename std::conditional<E4M3, __half, T>::type>();
     constexpr int kCols = D / 32;                // columns of a lane
@@ -787,10 +794,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Dec
         list[at] = seen;
     __syncthreads();
     const int rows = p.group * p.heads, items = found * rows;
-    // warps of a row: 1, 2, 5 or all 10, with at least kAtOnce states each
+    // warps of a row: 1, 3, 5 or all 15, with some kAtOnce states each
     int each = 1;
 #pragma unroll
-    for (int e = 2; e <= 10; e = e == 2 ? 5 : e + 5)
+    for (int e = 3; e <= 15; e = e == 3 ? 5 : e + 10)
         if (states > kAtOnce * (e - 1) && items * e <= (int)gridDim.x * kMergeWarps)
             each = e;
     const int at_once = kMergeWarps / each, mine = warp / each, lead = mine * each;
