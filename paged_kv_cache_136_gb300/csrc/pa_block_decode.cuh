@@ -28,7 +28,7 @@
 // states, which a second kernel merges.
 //
 // What bounds it.  HBM on long work: 8 sequences of 131072 tokens (64 query, 8
-// kv heads, e4m3, 2.15 GB) take 330 us, 6.5 TB/s; 64 of up to 2048 with 32 kv
+// kv heads, e4m3, 2.15 GB) take 323 us, 6.7 TB/s; 64 of up to 2048 with 32 kv
 // heads 89 us, 6.2 TB/s.  A warp's products (m16n8k16: the 8 query rows of a
 // group are the narrow side, so no row of a product is idle at 8) take a third
 // of the issue slots.  On listed blocks each 128- or 256-byte row of a head is
