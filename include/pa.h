@@ -330,6 +330,9 @@ pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *
  *                 positions j (entries of the sequence's table) in ascending
  *                 order, -1 behind the last
  *   list_lens     int32 [num_seqs]: min(max_selected, the sequence's blocks)
+ *   max_seq_len   an upper bound of every seq_len; a longer one is clamped and
+ *                 flagged (PA_DEVERR_SEQ_LEN).  A block outside the pool scores
+ *                 0 and is flagged (PA_DEVERR_BLOCK_ID).
  *   workspace     pa_select_blocks_workspace_size bytes, 256-byte aligned,
  *                 with the rules of pa_decode_splitk's
  *

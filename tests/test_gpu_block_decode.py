@@ -40,7 +40,8 @@ def _check(pa, got, lse, ref, dtype, eight):
                    two_parts=not (eight and dtype == torch.bfloat16), lse=lse)
 
 
-HEADS = [(4, 4), (8, 1), (16, 8), (12, 3), (32, 32), (10, 5), (64, 8), (24, 12)]
+HEADS = [(4, 4), (8, 1), (16, 8), (12, 3), (32, 32), (10, 5), (64, 8), (24, 12), (14, 7), (11, 11),
+         (36, 9)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
@@ -57,7 +58,8 @@ def test_decode_fp8_block(pa, d, bs, h, hkv, dtype):
     _check(pa, out, lse, R.ref_decode(q, pool, scales, tables, sl, bs, scale), dtype, True)
 
 
-@pytest.mark.parametrize("h,hkv,d,bs", [(8, 1, 128, 16), (64, 8, 128, 32), (4, 4, 64, 16)])
+@pytest.mark.parametrize("h,hkv,d,bs", [(8, 1, 128, 16), (64, 8, 128, 32), (4, 4, 64, 16),
+                                        (24, 3, 128, 16), (5, 5, 64, 32), (14, 7, 128, 32)])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_decode_fp8_block_long(pa, h, hkv, d, bs, dtype):
     """Cut over many CTAs, beside short sequences; a group of few heads."""
@@ -261,7 +263,7 @@ def _random_lists(lens, hkv, most, bs, seed, shuffle=True):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("h,hkv,d,bs,most", [
     (4, 4, 64, 16, 7), (8, 1, 128, 16, 64), (64, 8, 128, 32, 20), (12, 3, 64, 32, 5),
-    (32, 32, 128, 16, 1), (10, 5, 128, 32, 40)])
+    (32, 32, 128, 16, 1), (10, 5, 128, 32, 40), (7, 7, 64, 16, 3), (12, 6, 128, 16, 12)])
 def test_sparse(pa, h, hkv, d, bs, most, dtype, eight):
     lens = [1, 0, 500, 17, 2000, 31]
     q, pool, scales, tables, sl = _inputs(lens, h, hkv, d, bs, dtype, eight, seed=31)
