@@ -24,14 +24,14 @@
 // Work.  The (sequence, group of HG kv heads, 16-token tile) triples are laid
 // out in one line and cut into equal runs, one for each CTA, so that any mix
 // of lengths balances.  Inside a CTA the (up to 8) warps are HG heads, the most
-// that divide the kv heads, times 1, 2, 4 or 8 interleaved tiles.  A (sequence, group) that a cut divides leaves partial
-// states, which a second kernel merges.
+// that divide the kv heads, times 1, 2, 4 or 8 interleaved tiles.  A (sequence,
+// group) that a cut divides leaves partial states, which a second kernel merges.
 //
 // What bounds it.  HBM on long work: 8 sequences of 131072 tokens (64 query, 8
 // kv heads, e4m3, 2.15 GB) take 323 us, 6.7 TB/s; 64 of up to 2048 with 32 kv
-// heads 89 us, 6.2 TB/s.  A warp's products (m16n8k16: the 8 query rows of a
-// group are the narrow side, so no row of a product is idle at 8) take a third
-// of the issue slots.  On listed blocks each 128- or 256-byte row of a head is
+// heads 89 us, 6.2 TB/s.  The products (m16n8k16: the 8 query rows of a group are
+// the narrow side, so no part of a product is idle at 8) keep the tensor pipe
+// busy for a quarter of that.  On listed blocks each 128- or 256-byte row of a head is
 // read apart from its neighbours', which HBM serves at about 5.8 TB/s.  Tiles of
 // 2 KB (e4m3, head_size 64) are bound by a warp's latency for a tile: about 2.4
 // times the time of their bytes.  Besides, a launch takes 3.5 us until its first
