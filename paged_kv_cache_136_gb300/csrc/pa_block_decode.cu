@@ -257,7 +257,10 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
             continue;
         const int64_t ctas = (int64_t)num_seqs * (num_kv_heads / h);
         const int t = tiles_at_once(h);
-        const double cost = (double)((ctas + slots - 1) / slots) * (10 + (usual + t - 1) / t);
+        const int64_t once = (int64_t)resident(kv_scales != nullptr, head_size, h * t, t > 1) * sms;
+        if (!once)
+            return PA_ERR_CUDA;
+        const double cost = (double)((ctas + once - 1) / once) * (10 + (usual + t - 1) / t);
         if (cost < best && ctas <= INT32_MAX) {
             best = cost;
             whole = true;
