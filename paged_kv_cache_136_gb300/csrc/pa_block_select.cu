@@ -255,7 +255,7 @@ __device__ __forceinline__ void pick_blocks(const SelectParams &p, int n, int32_
                                             const uint32_t *keys)
 {
     constexpr int kWarps = THREADS / 32;
-    __shared__ uint32_t hist[1 << kDigit], seen[4][32], found[3], candidates;
+    __shared__ uint32_t hist[1 << kDigit], seen[5][32], found[3], candidates;
     __shared__ uint2 candidate[kCandidates]; // distance, position
     __shared__ uint2 edge;                   // the smallest chosen one
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -416,13 +416,15 @@ __device__ __forceinline__ void pick_blocks(const SelectParams &p, int n, int32_
     }
     sums[0] = __reduce_add_sync(~0u, sums[0]);
     sums[1] = __reduce_add_sync(~0u, sums[1]);
+    // Rows of their own: where no digit was looked at and nothing ranked, no
+    // barrier lies between here and the other warps' reads of the first three.
     if (lane == 0) {
-        seen[2][warp] = sums[0];
-        seen[3][warp] = sums[1];
+        seen[3][warp] = sums[0];
+        seen[4][warp] = sums[1];
     }
     __syncthreads();
-    uint32_t above = __reduce_add_sync(~0u, lane < warp ? seen[2][lane] : 0u);
-    uint32_t on = __reduce_add_sync(~0u, lane < warp ? seen[3][lane] : 0u);
+    uint32_t above = __reduce_add_sync(~0u, lane < warp ? seen[3][lane] : 0u);
+    uint32_t on = __reduce_add_sync(~0u, lane < warp ? seen[4][lane] : 0u);
     const uint32_t most_on = equals ? need : 0;
 #pragma unroll 1
     for (int i = first; i - 4 * lane < last; i += 128) {

@@ -1,0 +1,89 @@
+"""pa_select_blocks where little is left to choose by score, or the bounds are
+at the ends of their range: the lists against what the definition gives."""
+import math
+
+import pytest
+import torch
+
+from tests import _block_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    from __graft_entry__ import build_library
+    build_library()
+    import paged_kv_cache_136_gb300 as pa
+    pa.pa_device_errors(clear=True)
+    return pa
+
+
+GUARD = 64  # entries before and behind the lists that no call may touch
+
+
+def _select(pa, q, bounds, bsc, tables, sl, bs, most, sink, recent):
+    b, hkv = q.shape[0], bounds.shape[1]
+    msl = tables.shape[1] * bs
+    n = b * hkv * most
+    room = torch.full((n + 2 * GUARD,), -7, dtype=torch.int32, device="cuda")
+    lists = room[GUARD:GUARD + n].view(b, hkv, most)
+    counts = torch.full((b,), -7, dtype=torch.int32, device="cuda")
+    ws = torch.full((pa.pa_select_blocks_workspace_size(b, hkv, msl, bs),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    pa.pa_select_blocks(lists, counts, q, bounds, bsc, tables, sl, bs, msl, ws,
+                        num_sink_blocks=sink, num_recent_blocks=recent)
+    assert (room[:GUARD] == -7).all() and (room[GUARD + n:] == -7).all()
+    return lists, counts
+
+
+# (sequences, heads, kv heads, blocks of the longest): rows beyond what one pass
+# of a row's threads reads, 1024 of them where the rows fit the GPU at once, 256
+# where there are more; rows of odd lengths, and shorter ones beside them
+ROWS = [(2, 8, 2, 6001), (3, 4, 1, 4097), (1, 2, 1, 20000), (40, 16, 8, 2100), (77, 4, 4, 1025),
+        (320, 1, 1, 4500)]
+
+
+def _rows(b, h, hkv, n, d=64, bs=16):
+    """Every sequence reads the same blocks in another order."""
+    g = R.gen(b + n, "cuda")
+    order = torch.stack([torch.randperm(n, generator=g, device="cuda") for _ in range(b)])
+    blocks = [n - (i * 7) % 40 for i in range(b)]
+    bounds = torch.randint(0, 100, (n, hkv, 2, d), generator=g, device="cuda")
+    bounds = bounds.sort(2, descending=True).values.to(torch.int8)
+    q = torch.randn(b, h, d, generator=g, device="cuda").half()
+    sl = R.ints([k * bs - i % bs for i, k in enumerate(blocks)])
+    return q, bounds, torch.ones(n, hkv, device="cuda"), order.int(), sl, blocks
+
+
+@pytest.mark.parametrize("b,h,hkv,n", ROWS)
+@pytest.mark.parametrize("sink,recent", [(40, 24), (0, 64), (64, 0), (1, 0)])
+def test_nothing_left_to_choose(pa, b, h, hkv, n, sink, recent):
+    """sinks + recents == max_selected: the scores do not matter."""
+    q, bounds, bsc, tables, sl, blocks = _rows(b, h, hkv, n)
+    want = torch.tensor([list(range(sink)) + list(range(k - recent, k)) for k in blocks],
+                        dtype=torch.int32, device="cuda")[:, None].expand(-1, hkv, -1)
+    for _ in range(10):
+        lists, counts = _select(pa, q, bounds, bsc, tables, sl, 16, sink + recent, sink, recent)
+        assert torch.equal(lists, want) and (counts == sink + recent).all()
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("b,h,hkv,n", ROWS)
+@pytest.mark.parametrize("kind", ["zero queries", "infinite scales", "bounds of zeros"])
+def test_all_scores_equal(pa, b, h, hkv, n, kind):
+    """The kept blocks, then the lowest positions."""
+    q, bounds, bsc, tables, sl, blocks = _rows(b, h, hkv, n)
+    if kind == "zero queries":
+        q.zero_()
+    elif kind == "infinite scales":
+        bsc.fill_(math.inf)
+    else:
+        bounds.zero_()
+    most, sink, recent = 50, 3, 5
+    want = torch.tensor([list(range(most - recent)) + list(range(k - recent, k)) for k in blocks],
+                        dtype=torch.int32, device="cuda")[:, None].expand(-1, hkv, -1)
+    for _ in range(10):
+        lists, counts = _select(pa, q, bounds, bsc, tables, sl, 16, most, sink, recent)
+        assert torch.equal(lists, want) and (counts == most).all()
+    assert pa.pa_device_errors(clear=True) == 0
