@@ -324,7 +324,8 @@ pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *
  * +-127; NaN counts as 0).  The sum is an integer, so a score is exact and the
  * selection does not depend on the order of sums.  The first num_sink_blocks
  * and the last num_recent_blocks of a sequence (together at most
- * max_selected) are always chosen, then blocks with s = +inf, then the highest
+ * max_selected) are always chosen, then blocks whose s is not finite (+inf as
+ * above, or whatever lies where no bounds were written yet), then the highest
  * scores; equal ones from the lowest position.
  *   block_lists   int32 [num_seqs, num_kv_heads, max_selected]: the chosen
  *                 positions j (entries of the sequence's table) in ascending

@@ -16,7 +16,9 @@ namespace pa {
 namespace block {
 
 // Order-preserving keys of scores; a block that is kept whatever its score
-// comes before all of them (a score of +inf is 0xFF800000).
+// comes before all of them (a score of +inf is 0xFF800000).  Scores are never
+// NaN, whose keys are kKeyKept and 0: a block whose scale is not finite scores
+// +inf, and everything else a score is made of is finite.
 constexpr uint32_t kKeyKept = 0xFFFFFFFFu;
 
 __device__ __forceinline__ uint32_t key_of(float score)
@@ -210,7 +212,7 @@ __device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int h
             if (t == r && j < last)
                 put(j, j < p.sink || j >= n - p.recent
                            ? kKeyKept
-                           : key_of(scale[r] == INFINITY ? INFINITY : best + 0.f));
+                           : key_of(isfinite(scale[r]) ? best + 0.f : INFINITY));
         }
     }
 }

@@ -87,3 +87,29 @@ def test_all_scores_equal(pa, b, h, hkv, n, kind):
         lists, counts = _select(pa, q, bounds, bsc, tables, sl, 16, most, sink, recent)
         assert torch.equal(lists, want) and (counts == most).all()
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("b,h,hkv,n", ROWS[:1] + [(3, 8, 4, 300), (2, 4, 2, 1500)])
+def test_scales_that_are_not_finite(pa, b, h, hkv, n):
+    """Blocks whose bounds were never written may hold any bits: a scale of NaN
+    of either sign or of an infinity counts as +inf, before every score, and
+    never as a block that is kept anyway."""
+    q, bounds, bsc, tables, sl, blocks = _rows(b, h, hkv, n)
+    g = R.gen(3, "cuda")
+    odd = torch.rand(n, hkv, generator=g, device="cuda")
+    seen = torch.where(odd < 0.4, math.inf, bsc)           # what the definition sees
+    bits = torch.full((n, hkv), 0x7FFFFFFF, dtype=torch.int32, device="cuda")
+    bits[odd < 0.3] = 0x7F800001                           # NaN of other bits
+    bits[odd < 0.2] = -1                                   # 0xFFFFFFFF, a negative NaN
+    bits[odd < 0.1] = -0x800000                            # 0xFF800000, -inf
+    spoiled = torch.where(odd < 0.4, bits.view(torch.float32), bsc)
+    for most in (20, n // 2):                              # fewer and more than there are of them
+        got = _select(pa, q, bounds, spoiled, tables, sl, 16, most, 2, 3)
+        want = R.ref_select(q, bounds, seen, tables, sl, 16, most, 2, 3)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    spoiled.view(torch.int32).fill_(-1)                    # every block
+    got = _select(pa, q, bounds, spoiled, tables, sl, 16, 20, 2, 3)
+    want = torch.tensor([list(range(17)) + list(range(k - 3, k)) for k in blocks],
+                        dtype=torch.int32, device="cuda")
+    assert torch.equal(got[0], want[:, None].expand(-1, hkv, -1))
+    assert pa.pa_device_errors(clear=True) == 0
