@@ -16,8 +16,8 @@ namespace block {
 // Scales are 2^e with e in [-kExpRange, kExpRange].  A power of two multiplies
 // exactly, so codes can move to a larger scale without a second rounding
 // (except into e4m3's subnormals) and a sum of integer codes times scales has
-// one value whatever its order.  The range keeps every product of two scales
-// and a code sum a normal float.
+// one value whatever its order.  The range leaves every product of two scales
+// and a code sum (below 2^21) an exact fp32 number once 2^-16 is taken out.
 constexpr int kExpRange = 60;
 
 __device__ __forceinline__ float two_to(int e) // -126 <= e <= 127

@@ -167,7 +167,11 @@ __device__ __forceinline__ void score_blocks(const SelectParams &p, int s, int h
         off = 128.f * sum;
     }
     // Columns 2t and 2t + 1 are queries 2t and 2t + 1 of the group.
-    const float q0 = __shfl_sync(~0u, qs, 8 * t), q1 = __shfl_sync(~0u, qs, 8 * t + 4);
+    // Scores are formed 2^-16 times as large: a sum below 2^21 times two scales of
+    // up to 2^60 then stays below infinity, and the smallest, whole multiples of
+    // 2^-136, are fp32 numbers still (subnormal, kept: no flushing here).
+    const float qd = qs * 0x1p-16f;
+    const float q0 = __shfl_sync(~0u, qd, 8 * t), q1 = __shfl_sync(~0u, qd, 8 * t + 4);
     const float off0 = __shfl_sync(~0u, off, 8 * t), off1 = __shfl_sync(~0u, off, 8 * t + 4);
 
     for (; j0 < last; j0 += step) {

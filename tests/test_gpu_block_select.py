@@ -113,3 +113,30 @@ def test_scales_that_are_not_finite(pa, b, h, hkv, n):
                         dtype=torch.int32, device="cuda")
     assert torch.equal(got[0], want[:, None].expand(-1, hkv, -1))
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("e", [60, -60])
+def test_scores_at_the_ends_of_the_scales(pa, e, sign):
+    """Queries and blocks of the largest scale (scores of up to 2^140) and of the
+    smallest (down to 2^-120): more blocks than are chosen, all scores distinct,
+    positive or negative, and one block of infinite scale before them."""
+    h, hkv, d, bs, n, most = 4, 2, 64, 16, 400, 150
+    g = R.gen(5, "cuda")
+    tables = torch.randperm(n, generator=g, device="cuda").int()[None].contiguous()
+    steps = torch.arange(n, device="cuda") + 1
+    bounds = torch.zeros(n, hkv, 2, d, dtype=torch.int8, device="cuda")
+    for i in range(4):  # the sums are 127 * (1 .. n), in turn for each head
+        part = (steps - 100 * i).clamp(0, 100)
+        bounds[:, 0, :, i] = part[:, None].to(torch.int8)
+        bounds[:, 1, :, d - 1 - i] = part.flip(0)[:, None].to(torch.int8)
+    bsc = torch.full((n, hkv), 2.0 ** e, device="cuda")
+    bsc[7, 0] = math.inf
+    q = torch.full((1, h, d), sign * 127 * 2.0 ** e, device="cuda").to(torch.bfloat16)
+    if e > 0:
+        q[0, 1, 20], q[0, 2, 20] = math.inf, -math.inf         # met by codes of zero
+    sl = R.ints([n * bs])
+    got = _select(pa, q, bounds, bsc, tables, sl, bs, most, 0, 0)
+    want = R.ref_select(q, bounds, bsc, tables, sl, bs, most, 0, 0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert int((tables[0] == 7).nonzero()) in got[0][0, 0].tolist()
