@@ -223,10 +223,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
     block_decode_kernel(const __grid_constant__ CUtensorMap pool_map, const DecodeArgs p)
 {
     using M = typename std::conditional<E4M3, __half, T>::type; // type of the products
-    // P is split into a 16-bit high part and the rounded remainder where one
-    // part would add an error like the output's own rounding: not for a bf16
-    // output of products in halves (11 bits against 8).
-    constexpr bool kTwoParts = !(E4M3 && std::is_same<T, __nv_bfloat16>::value);
     constexpr float kLift = lift_of<M>();
     constexpr int kRow = D * (E4M3 ? 1 : 2);     // bytes of a head's row
     constexpr int kKPieces = kRow / 64;          // 16-byte pieces of a lane and row of K
@@ -600,15 +596,15 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     c[k] *= vs;
+            // P as a 16-bit part and the rounded remainder: 22 bits in halves, 16 in
+            // bf16.  One part alone (11, 8) would show where the values cancel.
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t h = pair_of<M>(c[2 * k], c[2 * k + 1]);
+                const float2 back = float2_of<M>(h);
                 hi[k] = transpose_8x8(h);
-                if constexpr (kTwoParts) {
-                    const float2 back = float2_of<M>(h);
-                    lo[k] = transpose_8x8(pair_of<M>(c[2 * k] - back.x, c[2 * k + 1] - back.y));
-                }
+                lo[k] = transpose_8x8(pair_of<M>(c[2 * k] - back.x, c[2 * k + 1] - back.y));
             }
 
             // O^T: rows are channels 2i and 2i + 1 of each lane's list
@@ -654,8 +650,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<E4M3, D>())
                     a3 = __byte_perm(vr[2][i], vr[3][i], 0x7632);
                 }
                 mma_16816<M>(o[i], a0, a1, a2, a3, hi[0], hi[1]);
-                if constexpr (kTwoParts)
-                    mma_16816<M>(o[i], a0, a1, a2, a3, lo[0], lo[1]);
+                mma_16816<M>(o[i], a0, a1, a2, a3, lo[0], lo[1]);
             }
         }
         else
