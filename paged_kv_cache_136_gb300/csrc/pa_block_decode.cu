@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "pa.h"
@@ -23,34 +24,45 @@ cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap
 int block_decode_resident_f16(bool e4m3, int head_size, int warps, bool hand_over);
 int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_over);
 
+// What is looked up once for each device.  Host threads that come at the same
+// time look up, and store, the same; a device past the array looks up each time.
+constexpr int kKnownDevices = 64;
+
 // The kernel's shared memory is allowed once a device (it takes most of an SM's).
 template <typename T, bool E4M3, int D> static cudaError_t prepare()
 {
-    static bool ready[64];
+    static std::atomic<bool> ready[kKnownDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && !ready[dev & 63]) {
+    const bool known = dev < kKnownDevices;
+    if (e == cudaSuccess && !(known && ready[dev])) {
         e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  decode_smem<E4M3, D>(kWarps, true));
-        ready[dev & 63] = e == cudaSuccess;
+        if (known)
+            ready[dev] = e == cudaSuccess;
     }
     return e;
 }
 
-// CTAs of so many warps that an SM holds at once; 0 on an error.
+// CTAs of so many warps that an SM of the current device holds at once; 0 on an
+// error.
 template <typename T, bool E4M3, int D> static int resident(int warps, bool hand_over)
 {
-    static int known[kWarps + 1][2];
-    int &n = known[warps][hand_over];
-    int now = n;
+    static std::atomic<int> seen[kKnownDevices][kWarps + 1][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    const bool known = dev < kKnownDevices;
+    int now = known ? seen[dev][warps][hand_over].load() : 0;
     if (!now) {
         if (prepare<T, E4M3, D>() != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                 &now, block_decode_kernel<T, E4M3, D>, 32 * warps,
                 decode_smem<E4M3, D>(warps, hand_over)) != cudaSuccess)
             return 0;
-        n = now;
+        if (known)
+            seen[dev][warps][hand_over] = now;
     }
     return now;
 }
