@@ -182,6 +182,14 @@ static int stream_of(PyObject *stream, int device, void **out)
     return PyErr_Occurred() ? -1 : 0;
 }
 
+/* Without the interpreter's lock, as through ctypes: a launch waits where the
+ * device's queue is full, and other threads go on meanwhile.  The caller holds
+ * the tensors. */
+#define UNLOCKED(call)      \
+    Py_BEGIN_ALLOW_THREADS  \
+    call;                   \
+    Py_END_ALLOW_THREADS
+
 static PyObject *done(pa_status st, const char *where)
 {
     if (st == PA_OK)
@@ -410,12 +418,13 @@ static PyObject *write_block(PyObject *self, PyObject *const *a, Py_ssize_t n)
                         *const starts = pointer(a[6]);
     if (PyErr_Occurred())
         return NULL;
-    return done(pa_reshape_and_cache_fp8_block(
-                    key, value, p.pool, p.scales, tables, r.stride, lens, starts, (int)r.count,
-                    (int)s[0], most, (int)p.kv_heads, (int)p.head_size, bs, (int)p.num_blocks,
-                    (int)r.blocks, s[0] > 1 ? ks[0] : row, s[0] > 1 ? vs[0] : row, (pa_dtype)kind,
-                    stream),
-                "pa_reshape_and_cache_fp8_block");
+    pa_status st;
+    UNLOCKED(st = pa_reshape_and_cache_fp8_block(
+                      key, value, p.pool, p.scales, tables, r.stride, lens, starts, (int)r.count,
+                      (int)s[0], most, (int)p.kv_heads, (int)p.head_size, bs, (int)p.num_blocks,
+                      (int)r.blocks, s[0] > 1 ? ks[0] : row, s[0] > 1 ? vs[0] : row, (pa_dtype)kind,
+                      stream));
+    return done(st, "pa_reshape_and_cache_fp8_block");
 }
 
 /* out, q, kv_cache, kv_scales, block_tables, seq_lens, workspace, lse, scale,
@@ -450,11 +459,12 @@ static PyObject *decode_block(PyObject *self, PyObject *const *a, Py_ssize_t n)
     float *const lse = all[7] ? pointer(all[7]) : NULL;
     if (PyErr_Occurred())
         return NULL;
-    return done(pa_decode_fp8_block(out, lse, q, p.pool, p.scales, tables, lens, (int)r.seqs,
-                                    (int)r.heads, (int)p.kv_heads, (int)p.head_size, bs,
-                                    (int)p.num_blocks, (int)r.blocks, (float)scale,
-                                    (pa_dtype)r.kind, most, ws, bytes, stream),
-                "pa_decode_fp8_block");
+    pa_status st;
+    UNLOCKED(st = pa_decode_fp8_block(out, lse, q, p.pool, p.scales, tables, lens, (int)r.seqs,
+                                      (int)r.heads, (int)p.kv_heads, (int)p.head_size, bs,
+                                      (int)p.num_blocks, (int)r.blocks, (float)scale,
+                                      (pa_dtype)r.kind, most, ws, bytes, stream));
+    return done(st, "pa_decode_fp8_block");
 }
 
 /* bounds, bounds_scale, kv_cache, block_tables, seq_lens, query_start_loc,
@@ -484,11 +494,12 @@ static PyObject *update_bounds(PyObject *self, PyObject *const *a, Py_ssize_t n)
                         *const starts = pointer(a[5]);
     if (PyErr_Occurred())
         return NULL;
-    return done(pa_update_block_bounds(bounds, scale, p.pool, p.scales, tables, r.stride, lens,
-                                       starts, (int)r.count, most, (int)p.kv_heads,
-                                       (int)p.head_size, bs, (int)p.num_blocks, (int)r.blocks,
-                                       (pa_dtype)p.kind, stream),
-                "pa_update_block_bounds");
+    pa_status st;
+    UNLOCKED(st = pa_update_block_bounds(bounds, scale, p.pool, p.scales, tables, r.stride, lens,
+                                         starts, (int)r.count, most, (int)p.kv_heads,
+                                         (int)p.head_size, bs, (int)p.num_blocks, (int)r.blocks,
+                                         (pa_dtype)p.kind, stream));
+    return done(st, "pa_update_block_bounds");
 }
 
 /* block_lists, list_lens, q, bounds, bounds_scale, block_tables, seq_lens,
@@ -525,11 +536,12 @@ static PyObject *select_blocks(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const int32_t *const tables = pointer(a[5]), *const seq_lens = pointer(a[6]);
     if (PyErr_Occurred())
         return NULL;
-    return done(pa_select_blocks(lists, lens, q, bounds, scale, tables, seq_lens, (int)r.seqs,
-                                 (int)r.heads, (int)s[1], (int)s[3], bs, (int)s[0], (int)r.blocks,
-                                 (int)listed, sink, recent, (pa_dtype)r.kind, most, ws, bytes,
-                                 stream),
-                "pa_select_blocks");
+    pa_status st;
+    UNLOCKED(st = pa_select_blocks(lists, lens, q, bounds, scale, tables, seq_lens, (int)r.seqs,
+                                   (int)r.heads, (int)s[1], (int)s[3], bs, (int)s[0], (int)r.blocks,
+                                   (int)listed, sink, recent, (pa_dtype)r.kind, most, ws, bytes,
+                                   stream));
+    return done(st, "pa_select_blocks");
 }
 
 /* out, q, kv_cache, block_tables, seq_lens, block_lists, list_lens, workspace,
@@ -569,11 +581,12 @@ static PyObject *decode_sparse(PyObject *self, PyObject *const *a, Py_ssize_t n)
     float *const lse = all[9] ? pointer(all[9]) : NULL;
     if (PyErr_Occurred())
         return NULL;
-    return done(pa_decode_sparse(out, lse, q, p.pool, p.scales, tables, seq_lens, lists, lens,
-                                 (int)r.seqs, (int)r.heads, (int)p.kv_heads, (int)p.head_size, bs,
-                                 (int)p.num_blocks, (int)r.blocks, (int)listed, (float)scale,
-                                 (pa_dtype)r.kind, ws, bytes, stream),
-                "pa_decode_sparse");
+    pa_status st;
+    UNLOCKED(st = pa_decode_sparse(out, lse, q, p.pool, p.scales, tables, seq_lens, lists, lens,
+                                   (int)r.seqs, (int)r.heads, (int)p.kv_heads, (int)p.head_size, bs,
+                                   (int)p.num_blocks, (int)r.blocks, (int)listed, (float)scale,
+                                   (pa_dtype)r.kind, ws, bytes, stream));
+    return done(st, "pa_decode_sparse");
 }
 
 /* The exception class of a failed call, and torch's functions for the current

@@ -1,6 +1,7 @@
 """The block calls from several host threads at once."""
 import ctypes
 import threading
+import time
 
 import pytest
 import torch
@@ -81,6 +82,59 @@ def test_c_calls_from_many_threads(pa):
                     r.tables.shape[1], 0.1, int(r.q.dtype == torch.bfloat16), r.msl,
                     r.ws.data_ptr(), r.ws.numel(), r.stream.cuda_stream)
             assert st == 0
+
+    _run([lambda r=r: calls(r) for r in runs])
+    torch.cuda.synchronize()
+    assert pa.pa_device_errors(clear=True) == 0
+    for r in runs:
+        r.check()
+
+
+def test_a_launch_that_waits_stops_no_other_thread(pa):
+    """A stream whose queue is full makes the launching thread wait; another
+    thread of the interpreter runs on meanwhile."""
+    hkv, d, bs = 2, 64, 16
+    tables, nb = R.make_tables([bs], bs)
+    pool, scales = R.make_pool(nb, bs, hkv, d, torch.float16, True)
+    bounds = torch.zeros(nb, hkv, 2, d, dtype=torch.int8, device="cuda")
+    bsc = torch.zeros(nb, hkv, device="cuda")
+    args = (bounds, bsc, pool, tables, R.ints([bs]), R.starts([bs]), bs, bs)
+    pa.pa_update_block_bounds(*args, kv_scales=scales)
+    torch.cuda.synchronize()
+    stream, done, gaps = torch.cuda.Stream(), threading.Event(), []
+
+    def watch():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    t = threading.Thread(target=watch)
+    t.start()
+    try:
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(1_000_000_000)           # about half a second
+        for _ in range(4000):                          # more than a queue holds
+            pa.pa_update_block_bounds(*args, kv_scales=scales, stream=stream)
+    finally:
+        done.set()
+        t.join()
+    torch.cuda.synchronize()
+    # a thread that has the lock gives it up every 5 ms; a wait for the whole
+    # sleep with the lock held shows as one gap of hundreds
+    assert max(gaps) < 0.2
+
+
+def test_binding_calls_from_many_threads(pa):
+    runs = [_Decode(pa, i, *PROBLEMS[i % len(PROBLEMS)]) for i in range(12)]
+    torch.cuda.synchronize()
+
+    def calls(r):
+        for _ in range(50):
+            pa.pa_decode_fp8_block(r.out, r.q, r.pool, r.scales, r.tables, r.sl, 0.1, r.bs, r.msl,
+                                   r.ws, stream=r.stream)
 
     _run([lambda r=r: calls(r) for r in runs])
     torch.cuda.synchronize()
