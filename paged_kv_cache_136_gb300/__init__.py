@@ -12,6 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 
 import torch
 
@@ -488,9 +489,10 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
 # native (csrc/pa_block_calls.c): a decode step makes several of these calls per
 # layer, and each costs the host little more than its launch.
 def _load_block_calls():
-    path = os.path.join(os.path.dirname(_LIB_PATH), "pa_block_calls.so")
+    path = os.path.join(os.path.dirname(_LIB_PATH),
+                        "pa_block_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
     if not os.path.exists(path):
-        raise ImportError(f"{path} not found; build the library first")
+        raise ImportError(f"{path} not found; build the library with this interpreter first")
     loader = importlib.machinery.ExtensionFileLoader("pa_block_calls", path)
     module = importlib.util.module_from_spec(
         importlib.util.spec_from_file_location("pa_block_calls", path, loader=loader))

@@ -4,9 +4,9 @@ The library is a handful of translation units compiled in parallel (the decode
 kernel instantiations are split by dtype and head_size) and linked into
 ``paged_kv_cache_136_gb300/_lib/libpa.so``, plus ``_lib/pa_latency``, a host
 program that times the C ABI on the 4-sequence workload, and
-``_lib/pa_block_calls.so``, the Python binding of the block calls (gcc, CPython
-headers).  Run ``python
-paged_kv_cache_136_gb300/build.py`` or call :func:`build`.
+``_lib/pa_block_calls.<interpreter>.so``, the Python binding of the block calls
+(gcc, CPython headers).  Run ``python paged_kv_cache_136_gb300/build.py`` or
+call :func:`build`.
 """
 from __future__ import annotations
 
@@ -25,7 +25,9 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libpa.so")
 LATENCY_TOOL = os.path.join(LIB_DIR, "pa_latency")
-BLOCK_CALLS = os.path.join(LIB_DIR, "pa_block_calls.so")
+# Named for the interpreter whose headers it was built with, as extension modules
+# are: another one does not find it, and builds its own.
+BLOCK_CALLS = os.path.join(LIB_DIR, "pa_block_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
