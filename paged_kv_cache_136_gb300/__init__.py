@@ -13,6 +13,7 @@ import importlib.machinery
 import importlib.util
 import os
 import sysconfig
+import threading
 
 import torch
 
@@ -487,12 +488,14 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
 
 # The block-scaled and block-sparse calls.  Their checks and marshalling are
 # native (csrc/pa_block_calls.c): a decode step makes several of these calls per
-# layer, and each costs the host little more than its launch.
+# layer, and each costs the host little more than its launch.  The binding is
+# loaded when the first of them is made, so that the other calls do not need it.
 def _load_block_calls():
     path = os.path.join(os.path.dirname(_LIB_PATH),
                         "pa_block_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
     if not os.path.exists(path):
-        raise ImportError(f"{path} not found; build the library with this interpreter first")
+        raise ImportError(f"{path} not found; the block calls need the library built with this "
+                          "interpreter, its headers installed")
     loader = importlib.machinery.ExtensionFileLoader("pa_block_calls", path)
     module = importlib.util.module_from_spec(
         importlib.util.spec_from_file_location("pa_block_calls", path, loader=loader))
@@ -502,7 +505,21 @@ def _load_block_calls():
     return module
 
 
-_block_calls = _load_block_calls()
+class _BlockCalls:
+    """Stands for the binding until it is loaded, and takes its own place then."""
+
+    def __init__(self):
+        self._lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _block_calls
+        with self._lock:
+            if _block_calls is self:
+                _block_calls = _load_block_calls()
+        return getattr(_block_calls, name)
+
+
+_block_calls = _BlockCalls()
 
 
 def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor,

@@ -5,8 +5,9 @@ kernel instantiations are split by dtype and head_size) and linked into
 ``paged_kv_cache_136_gb300/_lib/libpa.so``, plus ``_lib/pa_latency``, a host
 program that times the C ABI on the 4-sequence workload, and
 ``_lib/pa_block_calls.<interpreter>.so``, the Python binding of the block calls
-(gcc, CPython headers).  Run ``python paged_kv_cache_136_gb300/build.py`` or
-call :func:`build`.
+(gcc; left out, with a message, where CPython's headers are not installed: the
+other calls do not need it).  Run ``python paged_kv_cache_136_gb300/build.py``
+or call :func:`build`.
 """
 from __future__ import annotations
 
@@ -61,8 +62,14 @@ def _sources() -> list[str]:
                                                   os.path.abspath(__file__)])
 
 
+def _python_headers() -> str | None:
+    """The folder of Python.h, or None where it is not installed."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def _stale() -> bool:
-    made = (LIB, LATENCY_TOOL, BLOCK_CALLS)
+    made = [LIB, LATENCY_TOOL] + ([BLOCK_CALLS] if _python_headers() else [])
     if not all(os.path.exists(p) for p in made):
         return True
     t = min(os.path.getmtime(p) for p in made)
@@ -92,6 +99,22 @@ def _compile_tool() -> str:
     return obj
 
 
+def _build_block_calls() -> None:
+    """The binding of the block calls, against the library."""
+    headers = _python_headers()
+    if headers is None:
+        sys.stderr.write("Python.h is not installed: built without the block calls' binding\n")
+        return
+    tmp = BLOCK_CALLS + f".{os.getpid()}.tmp"
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", headers, "-I", INCLUDE,
+           os.path.join(CSRC, "pa_block_calls.c"), "-L", LIB_DIR, "-lpa", "-Wl,-rpath,$ORIGIN",
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BLOCK_CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libpa.so if any source changed; return its path."""
     if not force and not _stale():
@@ -118,14 +141,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LATENCY_TOOL)
-    tmp = BLOCK_CALLS + f".{os.getpid()}.tmp"
-    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-           os.path.join(CSRC, "pa_block_calls.c"), "-L", LIB_DIR, "-lpa", "-Wl,-rpath,$ORIGIN",
-           "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BLOCK_CALLS)
+    _build_block_calls()
     return LIB
 
 
