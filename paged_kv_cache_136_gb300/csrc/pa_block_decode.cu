@@ -14,12 +14,11 @@
 namespace pa {
 namespace block {
 
-cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap &map,
-                                    const DecodeArgs &p, int ctas,
-                                    cudaStream_t s);
-cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap &map,
-                                    const DecodeArgs &p, int ctas,
-                                     cudaStream_t s);
+// `nearest`: for an e4m3 pool (block_decode_kernel); a 16-bit one always is.
+cudaError_t launch_block_decode_f16(bool e4m3, bool nearest, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas, cudaStream_t s);
+cudaError_t launch_block_decode_bf16(bool e4m3, bool nearest, int head_size, const CUtensorMap &map,
+                                     const DecodeArgs &p, int ctas, cudaStream_t s);
 
 int block_decode_resident_f16(bool e4m3, int head_size, int warps, bool hand_over);
 int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_over);
@@ -29,14 +28,14 @@ int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_ov
 constexpr int kKnownDevices = 64;
 
 // The kernel's shared memory is allowed once a device (it takes most of an SM's).
-template <typename T, bool E4M3, int D> static cudaError_t prepare()
+template <typename T, bool E4M3, int D, bool NEAREST> static cudaError_t prepare()
 {
     static std::atomic<bool> ready[kKnownDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     const bool known = dev < kKnownDevices;
     if (e == cudaSuccess && !(known && ready[dev])) {
-        e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D>,
+        e = cudaFuncSetAttribute(block_decode_kernel<T, E4M3, D, NEAREST>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  decode_smem<E4M3, D>(kWarps, true));
         if (known)
@@ -45,8 +44,8 @@ template <typename T, bool E4M3, int D> static cudaError_t prepare()
     return e;
 }
 
-// CTAs of so many warps that an SM of the current device holds at once; 0 on an
-// error.
+// CTAs of so many warps that an SM of the current device holds at once (both
+// kernels of an e4m3 pool take as many registers); 0 on an error.
 template <typename T, bool E4M3, int D> static int resident(int warps, bool hand_over)
 {
     static std::atomic<int> seen[kKnownDevices][kWarps + 1][2];
@@ -56,9 +55,9 @@ template <typename T, bool E4M3, int D> static int resident(int warps, bool hand
     const bool known = dev < kKnownDevices;
     int now = known ? seen[dev][warps][hand_over].load() : 0;
     if (!now) {
-        if (prepare<T, E4M3, D>() != cudaSuccess ||
+        if (prepare<T, E4M3, D, !E4M3>() != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &now, block_decode_kernel<T, E4M3, D>, 32 * warps,
+                &now, block_decode_kernel<T, E4M3, D, !E4M3>, 32 * warps,
                 decode_smem<E4M3, D>(warps, hand_over)) != cudaSuccess)
             return 0;
         if (known)
@@ -67,15 +66,15 @@ template <typename T, bool E4M3, int D> static int resident(int warps, bool hand
     return now;
 }
 
-template <typename T, bool E4M3, int D>
+template <typename T, bool E4M3, int D, bool NEAREST>
 static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas, cudaStream_t s)
 {
     const int warps = p.heads * p.tiles_at_once;
     const int smem = decode_smem<E4M3, D>(warps, p.tiles_at_once > 1);
-    cudaError_t e = prepare<T, E4M3, D>();
+    cudaError_t e = prepare<T, E4M3, D, NEAREST>();
     if (e != cudaSuccess)
         return e;
-    e = launch_after_previous(block_decode_kernel<T, E4M3, D>, dim3(ctas), dim3(32 * warps), smem,
+    e = launch_after_previous(block_decode_kernel<T, E4M3, D, NEAREST>, dim3(ctas), dim3(32 * warps), smem,
                               s, map, p);
     if (e != cudaSuccess)
         return e;
@@ -89,14 +88,21 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
                                  dim3(32 * kMergeWarps), 0, s, p, ctas);
 }
 
-#if PA_INST_DTYPE == 1
-cudaError_t launch_block_decode_bf16(bool e4m3, int head_size, const CUtensorMap &map,
-                                    const DecodeArgs &p, int ctas,
-                                     cudaStream_t s)
+template <typename T, int D>
+static cudaError_t launch_of(bool e4m3, bool nearest, const CUtensorMap &map, const DecodeArgs &p,
+                             int ctas, cudaStream_t s)
 {
-    if (head_size == 128)
-        return e4m3 ? launch<__nv_bfloat16, true, 128>(map, p, ctas, s) : launch<__nv_bfloat16, false, 128>(map, p, ctas, s);
-    return e4m3 ? launch<__nv_bfloat16, true, 64>(map, p, ctas, s) : launch<__nv_bfloat16, false, 64>(map, p, ctas, s);
+    return !e4m3     ? launch<T, false, D, true>(map, p, ctas, s)
+           : nearest ? launch<T, true, D, true>(map, p, ctas, s)
+                     : launch<T, true, D, false>(map, p, ctas, s);
+}
+
+#if PA_INST_DTYPE == 1
+cudaError_t launch_block_decode_bf16(bool e4m3, bool nearest, int head_size, const CUtensorMap &map,
+                                     const DecodeArgs &p, int ctas, cudaStream_t s)
+{
+    return head_size == 128 ? launch_of<__nv_bfloat16, 128>(e4m3, nearest, map, p, ctas, s)
+                            : launch_of<__nv_bfloat16, 64>(e4m3, nearest, map, p, ctas, s);
 }
 
 int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_over)
@@ -108,13 +114,11 @@ int block_decode_resident_bf16(bool e4m3, int head_size, int warps, bool hand_ov
                 : resident<__nv_bfloat16, false, 64>(warps, hand_over);
 }
 #else
-cudaError_t launch_block_decode_f16(bool e4m3, int head_size, const CUtensorMap &map,
-                                    const DecodeArgs &p, int ctas,
-                                    cudaStream_t s)
+cudaError_t launch_block_decode_f16(bool e4m3, bool nearest, int head_size, const CUtensorMap &map,
+                                    const DecodeArgs &p, int ctas, cudaStream_t s)
 {
-    if (head_size == 128)
-        return e4m3 ? launch<__half, true, 128>(map, p, ctas, s) : launch<__half, false, 128>(map, p, ctas, s);
-    return e4m3 ? launch<__half, true, 64>(map, p, ctas, s) : launch<__half, false, 64>(map, p, ctas, s);
+    return head_size == 128 ? launch_of<__half, 128>(e4m3, nearest, map, p, ctas, s)
+                            : launch_of<__half, 64>(e4m3, nearest, map, p, ctas, s);
 }
 
 int block_decode_resident_f16(bool e4m3, int head_size, int warps, bool hand_over)
@@ -314,14 +318,17 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     // Else equal runs, of at least kMinRun tiles a warp.
     const int64_t ctas = whole ? (int64_t)num_seqs * p.num_groups
                                : std::min<int64_t>(tiles / (kMinRun * at_once) + 1, slots);
+    // the most tiles that a warp can have of one (sequence, head group)
+    const int64_t run = whole ? most : std::min(most, (tiles + ctas - 1) / ctas);
+    const bool nearest = run > (int64_t)kTruncated * at_once;
     alignas(64) CUtensorMap map;
     if (!make_map(&map, kv_cache, kv_scales != nullptr, dtype, num_blocks, block_size,
                   num_kv_heads, head_size))
         return PA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     e = dtype == PA_BF16
-            ? launch_block_decode_bf16(kv_scales != nullptr, head_size, map, p, (int)ctas, st)
-            : launch_block_decode_f16(kv_scales != nullptr, head_size, map, p, (int)ctas, st);
+            ? launch_block_decode_bf16(kv_scales != nullptr, nearest, head_size, map, p, (int)ctas, st)
+            : launch_block_decode_f16(kv_scales != nullptr, nearest, head_size, map, p, (int)ctas, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 #endif

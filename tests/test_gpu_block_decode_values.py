@@ -60,3 +60,41 @@ def test_probabilities_keep_two_parts(pa, h, hkv, d, bs, dtype, eight):
     for out in outs:
         R.check_decode(out, ref, half_products=eight or dtype == torch.float16, two_parts=True)
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("eight", [True, False])
+@pytest.mark.parametrize("length", [8176, 8192, 524288])
+def test_long_runs_do_not_lose_weight(pa, length, eight, dtype):
+    """Values of 1 in a run of tokens that one warp sums: the output is 1.
+
+    Additions that round to nearest are off by at most 2^-24 of the sum so far,
+    with either sign alike: over the 32768 of the longest run their sum has a
+    standard deviation of at most 2^-24 sqrt(32768 / 3) = 6.3e-6, and the
+    normaliser's the same.  An e4m3 pool's sums of up to 512 tiles are truncated,
+    by at most 2^-23 of the sum so far in each of a tile's two products: at most
+    2^-14 = 6.1e-5 of a sum that grows evenly.  The nearest 16-bit number is 1 as
+    long as all that is within 2^-12 = 2.4e-4 (fp16), 2^-9 (bf16)."""
+    b, h, hkv, d, bs, nb = 304, 8, 8, 128, 16, 64
+    if length > 10 ** 5:
+        b, bs = 152, 32
+    g = R.gen(4, "cuda")
+    pool, scales = R.make_pool(nb, bs, hkv, d, dtype, eight, seed=4)
+    pool[1] = 0x38 if eight else 1.0
+    if eight:
+        scales[1] = 1.0
+    # a few blocks in random order, so that no table of that length needs a pool
+    n = length // bs
+    tables = torch.randint(0, nb, (b, n), generator=g, device="cuda").int()
+    sl = torch.full((b,), length, dtype=torch.int32, device="cuda")
+    q = torch.randn(b, h, d, generator=g, device="cuda").to(dtype)
+    out, ws = torch.zeros_like(q), _workspace(pa, h, hkv, d)
+    if eight:
+        pa.pa_decode_fp8_block(out, q, pool, scales, tables, sl, 0.05, bs, length, ws)
+    else:
+        lists = torch.arange(n, dtype=torch.int32, device="cuda").expand(b, hkv, n).contiguous()
+        counts = torch.full((b,), n, dtype=torch.int32, device="cuda")
+        pa.pa_decode_sparse(out, q, pool, tables, sl, lists, counts, 0.05, bs, ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_errors(clear=True) == 0
+    assert (out == 1.0).all(), (out.double() - 1).abs().max()
