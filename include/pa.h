@@ -261,7 +261,8 @@ pa_status pa_decode_splitk_fp8(void *out, const void *q, const void *kv_cache,
  *           exact except for values that fall among e4m3's subnormals.
  * Other rows and scales are left as they were.  Every scale is a power of two;
  * kv_scales need not be initialised.  The blocks that receive tokens belong to
- * one request each; no other call writes them at the same time.
+ * one request each; no other call writes them at the same time.  (pa_prefill and
+ * pa_copy_blocks take 16-bit pools only.)
  *   key, value       rows as in pa_reshape_and_cache (strides in elements,
  *                    multiples of 8), num_tokens of them.
  *   block_tables     as in pa_prefill, row r at block_tables +
@@ -271,8 +272,9 @@ pa_status pa_decode_splitk_fp8(void *out, const void *q, const void *kv_cache,
  * (PA_DEVERR_SEQ_LEN), a block outside the pool likewise (PA_DEVERR_BLOCK_ID).
  *
  * pa_decode_fp8_block is pa_decode over such a pool:  keys scale * e4m3(K),
- * values scale * e4m3(V), q and out in `dtype`, fp32 softmax and sums; the
- * scales must lie in [2^-64, 2^64].  lse is NULL or receives each row's
+ * values scale * e4m3(V), q and out in `dtype`, fp32 softmax and sums, each
+ * probability with 22 bits in its product with a value; the scales must lie in
+ * [2^-64, 2^64].  lse is NULL or receives each row's
  * natural log-sum-exp as pa_decode_splitk_lse's (float32 [num_seqs,
  * num_heads]).  max_seq_len bounds every seq_len (a longer one is clamped and
  * flagged).  The call splits the work by itself; its workspace holds
@@ -319,8 +321,8 @@ pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *
  *
  * pa_select_blocks scores block j of sequence s for kv head h as
  *   max over the group's queries of 2^e_q 2^e_j sum_d c_d (c_d > 0 ? U_d : L_d),
- * with U and L its upper and lower bounds: an upper bound of the block's scores up to the rounding of the query's codes
- * c = rint(q / 2^e_q) (e_q the smallest in [-60, 60] that keeps them within
+ * with U and L its upper and lower bounds: an upper bound of the block's scores
+ * up to the rounding of the query's codes c = rint(q / 2^e_q) (e_q the smallest in [-60, 60] that keeps them within
  * +-127; NaN counts as 0).  The sum is an integer, so a score is exact and the
  * selection does not depend on the order of sums.  The first num_sink_blocks
  * and the last num_recent_blocks of a sequence (together at most
@@ -342,7 +344,10 @@ pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *
  * appears twice counts twice, a negative one is skipped, one past the
  * sequence's last block is skipped and flagged (PA_DEVERR_BLOCK_ID), and
  * entries behind list_lens[s] (at most max_selected, or clamped and flagged)
- * are not read.  A row that attends nothing is zero, its lse -inf.
+ * are not read.  A row that attends nothing is zero, its lse -inf.  Softmax and
+ * sums are fp32; each probability has 22 bits in its product with a value (16
+ * with a bf16 pool).  An infinite value that is attended gives an infinity or
+ * NaN in its channel, as in pa_decode.
  * Workspace and lse as in pa_decode_fp8_block.
  */
 pa_status pa_update_block_bounds(int8_t *bounds, float *bounds_scale, const void *kv_cache,
@@ -563,7 +568,8 @@ pa_status pa_selftest_wait_timeout(void *stream);
 /*
  * Measurement aid.  For every later decode call made by the calling host
  * thread (pa_decode, pa_decode_splitk, pa_decode_splitk_lse,
- * pa_decode_splitk_noalloc and the FP8 decodes), record the CUDA event
+ * pa_decode_splitk_noalloc, pa_decode_fp8 and pa_decode_splitk_fp8; not
+ * pa_decode_fp8_block or pa_decode_sparse), record the CUDA event
  * `before` on the call's stream just before its main attention kernel is
  * launched and `after` just after, so that the elapsed time between them is
  * that kernel's alone (the split-K plan and reduce kernels fall outside).

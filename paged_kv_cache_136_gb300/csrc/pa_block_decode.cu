@@ -74,8 +74,8 @@ static cudaError_t launch(const CUtensorMap &map, const DecodeArgs &p, int ctas,
     cudaError_t e = prepare<T, E4M3, D, NEAREST>();
     if (e != cudaSuccess)
         return e;
-    e = launch_after_previous(block_decode_kernel<T, E4M3, D, NEAREST>, dim3(ctas), dim3(32 * warps), smem,
-                              s, map, p);
+    e = launch_after_previous(block_decode_kernel<T, E4M3, D, NEAREST>, dim3(ctas),
+                              dim3(32 * warps), smem, s, map, p);
     if (e != cudaSuccess)
         return e;
     if (p.whole)
@@ -183,8 +183,8 @@ static int tiles_at_once(int heads)
     return t;
 }
 
-// CTAs of a launch that cuts, at most: three an SM of 152 where its warps are
-// few or its tiles small, else two.
+// CTAs of a launch that cuts, at most: 456, three for each of GB300's 152 SMs,
+// where its warps are few or its tiles small, else two.
 static int max_ctas(int heads, int head_size)
 {
     return heads <= 5 || head_size == 64 ? kMaxCtas : kMaxCtas / 3 * 2;
@@ -250,12 +250,16 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
     // Cut into equal runs of the largest head groups, or one CTA for each
     // (sequence, head group) of some size: whichever takes less by these costs,
     // in tiles of a warp (about 0.35 us): what a launch takes besides its tiles
-    // 10, a merge 11, each further (sequence, group) of a CTA 6.  Cut runs take
-    // the tiles there are, whole ones those of the longest sequence: a sequence
-    // is taken for half of max_seq_len on average, a list for full.  (Cut and
-    // whole: 152 sequences of 41 tokens, 5 kv heads 33 and 5.6 us; 64 lists of 64
-    // 16-token blocks, 8 kv heads 32.7 and 28.4 us; 37 sequences of 3120 to 24966
-    // tokens, 6 kv heads of 64 49 and 158 us.)
+    // 10, a merge 11, each further (sequence, group) of a CTA 6, fitted to what
+    // was measured.  Cut runs take the tiles there are, whole ones those of the
+    // longest sequence.  The lengths are on the device, so a sequence is taken for
+    // half of max_seq_len on average, as in a batch of requests of any age, and a
+    // list for full.  (Cut and whole: 152 sequences of 41 tokens, 5 kv heads 33
+    // and 5.6 us; 64 lists of 64 16-token blocks, 8 kv heads 32.7 and 28.4 us; 37
+    // sequences of 3120 to 24966 tokens, 6 kv heads of 64 49 and 158 us.)  Where
+    // all are as long as max_seq_len the cut is priced too low: at worst 256
+    // sequences of 512 tokens, 64 query and 8 kv heads, are cut in 55.2 us and
+    // would take 47.0 whole; 18 of 120 such batches lose more than 3 % by it.
     // tiles of a sequence, for this choice: a list rarely names a block twice
     const int64_t usual = std::min(most, cap / kTile + 1);
     int heads = heads_together(num_kv_heads), at_once = tiles_at_once(heads);
@@ -326,9 +330,8 @@ static pa_status decode(void *out, float *lse, const void *q, const void *kv_cac
                   num_kv_heads, head_size))
         return PA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = dtype == PA_BF16
-            ? launch_block_decode_bf16(kv_scales != nullptr, nearest, head_size, map, p, (int)ctas, st)
-            : launch_block_decode_f16(kv_scales != nullptr, nearest, head_size, map, p, (int)ctas, st);
+    const auto launch = dtype == PA_BF16 ? launch_block_decode_bf16 : launch_block_decode_f16;
+    e = launch(kv_scales != nullptr, nearest, head_size, map, p, (int)ctas, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 #endif

@@ -21,15 +21,18 @@
 // read at once meet eight different 16-byte columns of the 128-byte swizzle.
 // e4m3 codes become halves (exactly) in registers.
 //
-// Work.  The (sequence, group of HG kv heads, 16-token tile) triples are laid
-// out in one line and cut into equal runs, one for each CTA, so that any mix
-// of lengths balances.  Inside a CTA the (up to 8) warps are HG heads, the most
-// that divide the kv heads, times 1, 2, 4 or 8 interleaved tiles.  A (sequence,
-// group) that a cut divides leaves partial states, which a second kernel merges.
+// Work.  Inside a CTA the (up to 8) warps are HG kv heads times 1, 2, 4 or 8
+// interleaved tiles.  The host splits the work one of two ways, whichever costs
+// less.  Cut: the (sequence, group of HG heads, 16-token tile) triples are laid
+// out in one line and cut into equal runs, one for each CTA that fits at once,
+// so that any mix of lengths balances; HG is the most, up to 8, that divide the
+// kv heads.  A (sequence, group) that a cut divides leaves partial states, which
+// a second kernel merges.  Whole: a CTA is one (sequence, group), HG any divisor
+// of the kv heads, and nothing is merged.
 //
 // What bounds it.  HBM on long work: 8 sequences of 131072 tokens (64 query, 8
-// kv heads, e4m3, 2.15 GB) take 323 us, 6.7 TB/s; 64 of up to 2048 with 32 kv
-// heads 89 us, 6.2 TB/s.  The products (m16n8k16: the 8 query rows of a group are
+// kv heads, e4m3, 2.15 GB) take 321 to 327 us, 6.6 TB/s; 64 of up to 2048 with 32
+// kv heads 90 us, 6.2 TB/s.  The products (m16n8k16: the 8 query rows of a group are
 // the narrow side, so no part of a product is idle at 8) keep the tensor pipe
 // busy for a quarter of that.  On listed blocks each 128- or 256-byte row of a head is
 // read apart from its neighbours', which HBM serves at about 5.8 TB/s.  Tiles of
@@ -40,8 +43,8 @@
 // e4m3 scales: the score takes the key scale; the value scale multiplies the
 // probability before it is rounded to 16 bits.  The softmax's reference m is
 // the maximum of score + log2(value scale), so that the largest product
-// p * scale is 1 and halves hold the products of every block to the same
-// absolute precision.
+// p * scale is 2^lift (2^15 in halves, see lift_of) and halves hold the products
+// of every block to the same absolute precision.
 #pragma once
 
 #include <cuda.h>
@@ -228,8 +231,8 @@ constexpr float kNone = -3.402823466e38f;
 // additions that round to nearest; else they begin at the sums, to which the
 // matrix unit adds by truncation.  That takes up to 2^-23 of the sum so far off
 // it in each of a tile's two products (1.5e-3 measured in a run of 32768 tiles of
-// one sign), so at most 2^-14 in the kTruncated tiles it is used for, a quarter of
-// half a step of fp16.  A 16-bit pool always rounds: it costs nothing there (30.6
+// one sign): at most 2^-13 in the kTruncated tiles it is used for, 2^-14 of a sum
+// that grows evenly, where half a step of fp16 is 2^-12.  A 16-bit pool always rounds: it costs nothing there (30.6
 // against 30.5 us at 8 x 131072 tokens, 128 blocks each).  An e4m3 pool, at 128
 // registers, would take 83.5 instead of 79.0 us at 256 sequences of up to 4096
 // and 330 instead of 327 at 8 x 131072, runs of up to 216 tiles.
