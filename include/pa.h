@@ -322,8 +322,8 @@ pa_status pa_decode_fp8_block(void *out, float *lse, const void *q, const void *
  * pa_select_blocks scores block j of sequence s for kv head h as
  *   max over the group's queries of 2^e_q 2^e_j sum_d c_d (c_d > 0 ? U_d : L_d),
  * with U and L its upper and lower bounds: an upper bound of the block's scores
- * up to the rounding of the query's codes c = rint(q / 2^e_q) (e_q the smallest in [-60, 60] that keeps them within
- * +-127; NaN counts as 0).  The sum is an integer, so a score is exact and the
+ * up to the rounding of the query's codes c = rint(q / 2^e_q) (e_q the smallest
+ * in [-60, 60] that keeps them within +-127; NaN counts as 0).  The sum is an integer, so a score is exact and the
  * selection does not depend on the order of sums.  The first num_sink_blocks
  * and the last num_recent_blocks of a sequence (together at most
  * max_selected) are always chosen, then blocks whose s is not finite (+inf as
