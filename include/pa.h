@@ -16,6 +16,12 @@
  *                         one scale for each (plane, block, kv head)
  *   pa_update_block_bounds, pa_select_blocks, pa_decode_sparse
  *                         decode over the blocks that can score highest
+ *   pa_linear_prefill, pa_linear_decode
+ *                         linear attention with a decay for each head, over a
+ *                         pool of states
+ *   pa_fork_sequences, pa_extend_sequences, pa_compact_blocks
+ *                         the life of sequences in a block pool: copies of
+ *                         rows, room for new tokens, live blocks to the front
  *   pa_stage_copy         move a step's data between pinned host memory and
  *                         the device on the SMs
  *
@@ -96,6 +102,9 @@ typedef enum pa_dtype { PA_FP16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_TIMEOUT 0x8u  /* a bounded in-kernel wait ran out */
 #define PA_DEVERR_PREFIX 0x10u  /* cascade: a table does not start with the shared
                                    prefix blocks, or a seq_len is shorter than it */
+#define PA_DEVERR_STATE 0x20u   /* a state id at or beyond num_states */
+#define PA_DEVERR_PARENT 0x40u  /* fork: a parent at or beyond num_seqs */
+#define PA_DEVERR_POOL 0x80u    /* extend: too few free blocks, or slot_mapping too short */
 
 /*
  * Write new tokens into the pool ("PagedAttention 在 vLLM 中的实现分析",
@@ -506,6 +515,147 @@ pa_status pa_prefill(void *out, float *lse, const void *q, const void *kv_cache,
 pa_status pa_copy_blocks(void *kv_cache, const int64_t *block_mapping, int num_pairs,
                          int num_blocks, int block_size, int num_kv_heads, int head_size,
                          pa_dtype dtype, void *stream);
+
+/*
+ * Linear attention with a decay for each head.  The pages have no counterpart: it
+ * is the other kind of attention layer of models whose softmax layers use the
+ * paged cache.  Every (sequence, kv head) has a state S, a float32 matrix
+ * [head_size, head_size] (key channel, value channel), and each token t makes
+ *   S_t = exp(g_t) S_(t-1) + k_t v_t^T,   out_t[h] = scale * q_t[h] S_t
+ * for every query head h of the kv head (grouped as in pa_decode).
+ *
+ *   states       float32 [num_states, num_kv_heads, head_size, head_size]
+ *   src_states   int32 [num_seqs]: the state that sequence s continues;
+ *                negative: zeros.
+ *   dst_states   int32 [num_seqs]: where its state behind the last token is
+ *                written, which may be src_states[s]; negative: a padding row,
+ *                of which nothing is read or written, out included.
+ *                No state that a sequence writes may be read or written by
+ *                another one in the same call.  Ids at or beyond num_states are
+ *                flagged (PA_DEVERR_STATE), read as zeros and not written.
+ *   q            [num_tokens, num_heads, head_size], k and v [num_tokens,
+ *                num_kv_heads, head_size], dtype; row t of each at its own token
+ *                stride (elements, a multiple of 8, at least the row).
+ *   out          [num_tokens, num_heads, head_size], dtype, contiguous.
+ *   log_decay    float32: g of token t and kv head h at t * decay_stride + h;
+ *                decay_stride 0: one for each head.  At most 0 (-inf is a decay
+ *                of 0); growth may overflow.
+ * num_heads is any multiple of num_kv_heads; head_size 64 or 128.  States and sums
+ * are fp32.  Whatever is not finite in q, k, v or a state gives infinity or NaN in
+ * the outputs and states that depend on it, and in no others.
+ *
+ * pa_linear_decode is the step of one token for each sequence (token s is
+ * sequence s's).  pa_linear_prefill takes prompts, chunks of prompts, or the few
+ * tokens of a speculation, packed by query_start_loc as in pa_prefill:
+ *   query_start_loc  int32 [num_seqs + 1], non-decreasing, from 0 to at most
+ *                    num_tokens; rows of out outside it are left untouched.  A
+ *                    sequence without tokens moves its state from src to dst.
+ *   max_query_len    an upper bound of every q_len; a sequence that breaks these
+ *                    rules is skipped and flagged (PA_DEVERR_SEQ_LEN).
+ *   workspace        pa_linear_prefill_workspace_size bytes, 256-byte aligned,
+ *                    with the rules of pa_decode_splitk's
+ * Its products run on the tensor cores with 16-bit operands.  Scores times decays
+ * (P), decayed values and states go in as a rounded 16-bit part plus the rounded
+ * remainder: 2^-17 of their size with bf16 and 2^-22 with fp16, so that the one
+ * visible rounding is the output's own.
+ */
+pa_status pa_linear_decode(void *out, const void *q, const void *k, const void *v,
+                           const float *log_decay, int64_t decay_stride, float *states,
+                           const int32_t *src_states, const int32_t *dst_states, int num_seqs,
+                           int num_heads, int num_kv_heads, int head_size, int num_states,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                           pa_dtype dtype, void *stream);
+size_t pa_linear_prefill_workspace_size(int num_seqs, int num_tokens, int max_query_len,
+                                        int num_kv_heads, int head_size);
+pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void *v,
+                            const float *log_decay, int64_t decay_stride, float *states,
+                            const int32_t *src_states, const int32_t *dst_states,
+                            const int32_t *query_start_loc, int num_seqs, int num_tokens,
+                            int max_query_len, int num_heads, int num_kv_heads, int head_size,
+                            int num_states, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * The life of sequences in a block pool, on the device, so that a step that forks
+ * or frees sequences or needs new blocks can be captured.  The state is plain
+ * metadata: block tables int32 [rows, max_blocks_per_seq], seq_lens int32 [rows]
+ * and
+ *   ref_counts   int32 [num_blocks]: in how many rows a block stands; a block
+ *                with count 0 is free.
+ * A row's entries at and past ceil(seq_len / block_size) are neither read nor
+ * written.  block_size is any positive number: a pool of one state for each
+ * sequence (pa_linear_*) is one whose block_size no sequence outgrows.  Results
+ * are whole numbers and do not depend on the order in which anything runs.  Each
+ * metadata output may be the input itself where nothing else is said, and must
+ * not overlap it otherwise: separate ones leave the inputs to the step that still
+ * runs.  At most 65535 rows; max_blocks_per_seq * block_size < 2^31.  A seq_len
+ * outside [0, max_blocks_per_seq * block_size] is clamped and flagged
+ * (PA_DEVERR_SEQ_LEN), a block id outside the pool has no count and no bytes and
+ * is flagged (PA_DEVERR_BLOCK_ID).
+ *
+ * Extend and compact also move blocks' bytes, in every pool that is indexed by
+ * these block ids (layers' caches, scales, bounds, states), given as a HOST array:
+ */
+typedef struct pa_block_pool {
+    void *data;          /* device memory [planes, num_blocks, block_bytes] */
+    int64_t block_bytes; /* 16-byte moves where it and data are multiples of 16 */
+    int32_t planes;      /* 2 for [2, num_blocks, ...] keys and values */
+} pa_block_pool;
+#define PA_MAX_POOLS 256
+
+/*
+ * pa_fork_sequences: new row s is a copy of old row parents[s], or empty where
+ * parents[s] is negative; an old row that is nobody's parent is freed.  So one
+ * call forks, frees and reorders rows (the step of a beam search, requests that
+ * end).  Counts follow: a block loses one for each old row it stands in and gains
+ * one for each new row.  No bytes move: a fork shares every block.
+ *   tables_out, seq_lens_out   [num_seqs_out] rows; they must not overlap the
+ *                              inputs (rows trade places)
+ *   parents                    int32 [num_seqs_out]; one at or beyond num_seqs
+ *                              gives an empty row, flagged (PA_DEVERR_PARENT)
+ *
+ * pa_extend_sequences: room for num_new[s] more tokens in every row s.  Blocks are
+ * taken lowest id first, in the order of rows; a row whose partly filled last
+ * block is shared gets a copy of it in a new block (as if rows were taken one
+ * after the other: where all holders of a block go on in it, the last keeps it).
+ *   num_new        int32 [num_seqs]; a negative one, or one past the table's end,
+ *                  counts as 0, flagged (PA_DEVERR_SEQ_LEN)
+ *   slot_mapping   int64 [num_tokens]: the new tokens' slots, row after row, for
+ *                  pa_reshape_and_cache; -1 behind the last
+ *   info           int32 [2]: blocks that the call needs, and free blocks less
+ *                  those.  Where that is negative, or slot_mapping is too short,
+ *                  nothing is taken: tables, lengths and counts stay as they were,
+ *                  slots are -1, flagged (PA_DEVERR_POOL).
+ *   workspace      pa_sequences_workspace_size bytes, 256-byte aligned, with the
+ *                  rules of pa_decode_splitk's
+ *
+ * pa_compact_blocks: with n blocks in use, the k-th live id at or above n becomes
+ * the k-th free id below n, bytes and counts with it, so that the pool's tail is
+ * free.
+ *   new_ids        int32 [num_blocks]: every live block's id now, -1 for others
+ *   info           int32 [2]: n, and how many blocks moved
+ * An entry of a table whose block has count 0 becomes -1, flagged
+ * (PA_DEVERR_BLOCK_ID).
+ */
+pa_status pa_fork_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_t *ref_counts_out,
+                            const int32_t *block_tables, const int32_t *seq_lens,
+                            const int32_t *ref_counts, const int32_t *parents, int num_seqs,
+                            int num_seqs_out, int num_blocks, int max_blocks_per_seq,
+                            int block_size, void *stream);
+size_t pa_sequences_workspace_size(int num_seqs, int num_blocks);
+pa_status pa_extend_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_t *ref_counts_out,
+                              int64_t *slot_mapping, int32_t *info, const int32_t *block_tables,
+                              const int32_t *seq_lens, const int32_t *ref_counts,
+                              const int32_t *num_new, const pa_block_pool *pools, int num_pools,
+                              int num_seqs, int num_tokens, int num_blocks, int max_blocks_per_seq,
+                              int block_size, void *workspace, size_t workspace_bytes,
+                              void *stream);
+pa_status pa_compact_blocks(int32_t *tables_out, int32_t *ref_counts_out, int32_t *new_ids,
+                            int32_t *info, const int32_t *block_tables, const int32_t *seq_lens,
+                            const int32_t *ref_counts, const pa_block_pool *pools, int num_pools,
+                            int num_seqs, int num_blocks, int max_blocks_per_seq, int block_size,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Copy bytes from src to dst on the GPU's SMs (16-byte moves), stream-

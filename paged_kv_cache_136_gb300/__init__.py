@@ -29,10 +29,12 @@ __all__ = [
     "pa_decode_splitk_fp8", "pa_decode_splitk_fp8_workspace_size",
     "pa_reshape_and_cache_fp8_block", "pa_decode_fp8_block", "pa_block_decode_workspace_size",
     "pa_update_block_bounds", "pa_select_blocks", "pa_select_blocks_workspace_size",
-    "pa_decode_sparse",
+    "pa_decode_sparse", "pa_linear_decode", "pa_linear_prefill", "pa_linear_prefill_workspace_size",
+    "pa_fork_sequences", "pa_extend_sequences", "pa_compact_blocks", "pa_sequences_workspace_size",
     "pa_validate_block_mapping", "pa_status_string", "pa_version", "pa_profile_kernel_events",
     "DEVERR_BLOCK_ID",
-    "DEVERR_SEQ_LEN", "DEVERR_SLOT", "DEVERR_TIMEOUT",
+    "DEVERR_SEQ_LEN", "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_STATE", "DEVERR_PARENT",
+    "DEVERR_POOL",
 ]
 
 PA_OK = 0
@@ -41,6 +43,9 @@ DEVERR_SEQ_LEN = 0x2
 DEVERR_SLOT = 0x4
 DEVERR_TIMEOUT = 0x8
 DEVERR_PREFIX = 0x10
+DEVERR_STATE = 0x20
+DEVERR_PARENT = 0x40
+DEVERR_POOL = 0x80
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1}
 
@@ -97,6 +102,10 @@ _lib.pa_block_decode_workspace_size.restype = _SZ
 _lib.pa_block_decode_workspace_size.argtypes = [_I, _I, _I]
 _lib.pa_select_blocks_workspace_size.restype = _SZ
 _lib.pa_select_blocks_workspace_size.argtypes = [_I, _I, _I, _I]
+_lib.pa_linear_prefill_workspace_size.restype = _SZ
+_lib.pa_linear_prefill_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+_lib.pa_sequences_workspace_size.restype = _SZ
+_lib.pa_sequences_workspace_size.argtypes = [_I, _I]
 _lib.pa_prefill.restype = _I
 _lib.pa_prefill.argtypes = [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                             _I, _F, _I, _I, _P]
@@ -486,8 +495,8 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
     return out
 
 
-# The block-scaled and block-sparse calls.  Their checks and marshalling are
-# native (csrc/pa_block_calls.c): a decode step makes several of these calls per
+# The block-scaled and block-sparse calls, linear attention and the sequence
+# calls.  Their checks and marshalling are native (csrc/pa_block_calls.c): a decode step makes several of these calls per
 # layer, and each costs the host little more than its launch.  The binding is
 # loaded when the first of them is made, so that the other calls do not need it.
 def _load_block_calls():
@@ -604,6 +613,88 @@ def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
     _block_calls.decode_sparse(out, q, kv_cache, block_tables, seq_lens, block_lists, list_lens,
                                workspace, kv_scales, lse, scale, block_size, stream)
     return out
+
+
+def pa_linear_decode(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: torch.Tensor, states: torch.Tensor, src_states: torch.Tensor,
+                     dst_states: torch.Tensor, scale: float, stream=None) -> torch.Tensor:
+    """One token of linear attention with a decay for each kv head, for every
+    sequence: S = exp(log_decay) S + k v^T, out = scale q S.  ``states`` is
+    float32 [num_states, Hkv, D, D]; sequence s continues ``src_states[s]``
+    (negative: zeros) and leaves its state in ``dst_states[s]`` (negative: a
+    padding row, left alone).  ``log_decay`` is float32 [Hkv] or [B, Hkv].
+    q [B, H, D], k and v [B, Hkv, D] may be slices of wider rows.  Writes and
+    returns ``out``."""
+    _block_calls.linear_decode(out, q, k, v, log_decay, states, src_states, dst_states, scale,
+                               stream)
+    return out
+
+
+def pa_linear_prefill_workspace_size(num_seqs: int, num_tokens: int, max_query_len: int,
+                                     num_kv_heads: int, head_size: int) -> int:
+    return int(_lib.pa_linear_prefill_workspace_size(num_seqs, num_tokens, max_query_len,
+                                                     num_kv_heads, head_size))
+
+
+def pa_linear_prefill(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      log_decay: torch.Tensor, states: torch.Tensor, src_states: torch.Tensor,
+                      dst_states: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                      max_query_len: int, workspace: torch.Tensor, stream=None) -> torch.Tensor:
+    """pa_linear_decode for prompts, chunks of prompts or speculated tokens: the
+    rows query_start_loc[s]:query_start_loc[s+1] of q, k, v, out (and of
+    ``log_decay`` [T, Hkv]) are sequence s's next tokens.  ``workspace`` holds
+    pa_linear_prefill_workspace_size bytes.  Writes and returns ``out``."""
+    _block_calls.linear_prefill(out, q, k, v, log_decay, states, src_states, dst_states,
+                                query_start_loc, workspace, scale, max_query_len, stream)
+    return out
+
+
+def pa_fork_sequences(tables_out: torch.Tensor, seq_lens_out: torch.Tensor,
+                      ref_counts_out: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, ref_counts: torch.Tensor, parents: torch.Tensor,
+                      block_size: int, stream=None) -> None:
+    """Row s of the new tables becomes a copy of old row ``parents[s]`` (int32;
+    negative: an empty row); old rows without children are freed.  ``ref_counts``
+    (int32 [num_blocks], 0 for a free block) follow; ``ref_counts_out`` may be
+    ``ref_counts``, the other outputs are tensors of their own."""
+    _block_calls.fork_sequences(tables_out, seq_lens_out, ref_counts_out, block_tables, seq_lens,
+                                ref_counts, parents, block_size, stream)
+
+
+def pa_sequences_workspace_size(num_seqs: int, num_blocks: int) -> int:
+    """Workspace bytes of pa_extend_sequences and pa_compact_blocks."""
+    return int(_lib.pa_sequences_workspace_size(num_seqs, num_blocks))
+
+
+def pa_extend_sequences(tables_out: torch.Tensor, seq_lens_out: torch.Tensor,
+                        ref_counts_out: torch.Tensor, slot_mapping: torch.Tensor,
+                        info: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                        ref_counts: torch.Tensor, num_new: torch.Tensor, pools,
+                        block_size: int, workspace: torch.Tensor, stream=None) -> None:
+    """Room for ``num_new[s]`` more tokens in every row: the lowest free blocks in
+    the order of rows, copies of last blocks that are shared (in every tensor of
+    ``pools``, each [planes, num_blocks, ...]), and the new tokens' slots (int64,
+    -1 behind the last).  ``info`` (int32 [2]) receives the blocks needed and the
+    free blocks less those; if that is negative, or slot_mapping too short,
+    nothing is taken.  Each output may be its input.  ``workspace`` holds
+    pa_sequences_workspace_size bytes."""
+    _block_calls.extend_sequences(tables_out, seq_lens_out, ref_counts_out, slot_mapping, info,
+                                  block_tables, seq_lens, ref_counts, num_new, workspace, pools,
+                                  block_size, stream)
+
+
+def pa_compact_blocks(tables_out: torch.Tensor, ref_counts_out: torch.Tensor,
+                      new_ids: torch.Tensor, info: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, ref_counts: torch.Tensor, pools, block_size: int,
+                      workspace: torch.Tensor, stream=None) -> None:
+    """Move the live blocks (in every tensor of ``pools``, each [planes,
+    num_blocks, ...]) to the front of the pool.  ``new_ids`` (int32 [num_blocks])
+    receives each live block's id now (-1 for others), ``info`` (int32 [2]) the
+    number of live blocks and of those that moved.  tables_out and
+    ref_counts_out may be the inputs.  ``workspace`` holds
+    pa_sequences_workspace_size bytes."""
+    _block_calls.compact_blocks(tables_out, ref_counts_out, new_ids, info, block_tables, seq_lens,
+                                ref_counts, workspace, pools, block_size, stream)
 
 
 def pa_copy_blocks(kv_cache: torch.Tensor, block_mapping: torch.Tensor, block_size: int,

@@ -45,6 +45,8 @@ UNITS = [
     ("pa_decode_fp8_f16", "pa_decode_fp8_inst.cu", ["-DPA_INST_DTYPE=0"]),
     ("pa_decode_fp8_bf16", "pa_decode_fp8_inst.cu", ["-DPA_INST_DTYPE=1"]),
     ("pa_prefill_bf16", "pa_prefill_inst.cu", ["-DPA_INST_DTYPE=1"]),
+    ("pa_linear", "pa_linear.cu", []),
+    ("pa_sequences", "pa_sequences.cu", []),
     ("pa_block_cache", "pa_block_cache.cu", []),
     ("pa_block_select", "pa_block_select.cu", []),
     ("pa_block_decode_f16", "pa_block_decode.cu", ["-DPA_INST_DTYPE=0"]),

@@ -1,7 +1,7 @@
 /*
- * pa_block_calls.c -- the binding of the block-scaled and block-sparse calls
- * (CPython C API): checks of torch tensors' types, shapes and devices, and the
- * calls of include/pa.h, in one step.  A decode step makes several of these
+ * pa_block_calls.c -- the binding of the block-scaled and block-sparse calls, of
+ * linear attention and of the sequence calls (CPython C API): checks of torch
+ * tensors' types, shapes and devices, and the calls of include/pa.h, in one step.  A decode step makes several of these
  * calls a layer; through ctypes the checks and the marshalling of about 20
  * arguments took longer than the launch (8 against 4 us a call).
  */
@@ -12,7 +12,7 @@
 
 #include "pa.h"
 
-static PyObject *t_i32, *t_f32, *t_u8, *t_i8, *t_f16, *t_bf16; /* torch dtypes */
+static PyObject *t_i32, *t_i64, *t_f32, *t_u8, *t_i8, *t_f16, *t_bf16; /* torch dtypes */
 static PyObject *error_class, *current_device, *raw_stream;    /* given by bind() */
 static PyObject *n_shape, *n_dtype, *n_stride, *n_is_contiguous, *n_data_ptr, *n_get_device,
     *n_numel, *n_nbytes, *n_cuda_stream;
@@ -589,6 +589,323 @@ static PyObject *decode_sparse(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return done(st, "pa_decode_sparse");
 }
 
+/* ---- linear attention ---- */
+
+/* Rows [T, heads, head_size] of a tensor, contiguous but for the token stride. */
+typedef struct {
+    int64_t tokens, heads, head_size, stride;
+    int kind;
+} Rows;
+
+static int read_rows(PyObject *t, Rows *r, const char *what)
+{
+    int64_t s[3], st[3];
+    const int n = shape_of(t, s, 3);
+    if (n < 0)
+        return -1;
+    if (n != 3)
+        return bad(what);
+    r->kind = half_kind(t);
+    if (r->kind < 0 || strides_of(t, st, 3) < 0)
+        return -1;
+    r->tokens = s[0], r->heads = s[1], r->head_size = s[2];
+    const int64_t row = s[1] * s[2];
+    if (r->kind == 2 || (s[2] > 1 && st[2] != 1) || (s[1] > 1 && st[1] != s[2]) ||
+        (s[0] > 1 && st[0] < row))
+        return bad(what);
+    r->stride = s[0] > 1 ? st[0] : row;
+    return 0;
+}
+
+typedef struct {
+    Rows q, k, v;
+    int64_t decay_stride, num_states, seqs;
+} Linear;
+
+/* out, q, k, v, log_decay, states, src_states, dst_states */
+static int read_linear(PyObject *const *a, Linear *l)
+{
+    int64_t s[4], st[2];
+    if (read_rows(a[1], &l->q, "q must be fp16/bf16 [T, H, head_size] with contiguous rows") ||
+        read_rows(a[2], &l->k, "k must be fp16/bf16 [T, num_kv_heads, head_size] with contiguous rows") ||
+        read_rows(a[3], &l->v, "v must be fp16/bf16 [T, num_kv_heads, head_size] with contiguous rows"))
+        return -1;
+    if (l->k.kind != l->q.kind || l->v.kind != l->q.kind || l->k.tokens != l->q.tokens ||
+        l->v.tokens != l->q.tokens || l->k.head_size != l->q.head_size ||
+        l->v.head_size != l->q.head_size || l->v.heads != l->k.heads)
+        return bad("q, k and v must share dtype, token count and head_size, k and v their heads");
+    const int64_t want[3] = {l->q.tokens, l->q.heads, l->q.head_size};
+    if (is(a[0], l->q.kind == PA_BF16 ? t_bf16 : t_f16, want, 3, "out must be contiguous and match q"))
+        return -1;
+    static const char *const decays =
+        "log_decay must be float32 [num_kv_heads] or [T, num_kv_heads] with contiguous rows";
+    const int n = shape_of(a[4], s, 4), f = has_dtype(a[4], t_f32);
+    if (n < 0 || f < 0)
+        return -1;
+    if (!f || n < 1 || n > 2 || s[n - 1] != l->k.heads || (n == 2 && s[0] != l->q.tokens))
+        return bad(decays);
+    if (strides_of(a[4], st, 2) < 0)
+        return -1;
+    if (s[n - 1] > 1 && st[n - 1] != 1)
+        return bad(decays);
+    l->decay_stride = n == 1 ? 0 : s[0] > 1 ? st[0] : l->k.heads;
+    const int m = shape_of(a[5], s, 4);
+    if (m < 0)
+        return -1;
+    const int64_t states[4] = {m == 4 ? s[0] : 0, l->k.heads, l->q.head_size, l->q.head_size};
+    if (is(a[5], t_f32, states, 4,
+           "states must be contiguous float32 [num_states, num_kv_heads, head_size, head_size]"))
+        return -1;
+    l->num_states = s[0];
+    l->seqs = int_of(PyObject_CallMethodNoArgs(a[7], n_numel));
+    if (l->seqs < 0)
+        return -1;
+    if (is_i32_of(a[6], l->seqs, "src_states must be contiguous int32 [num_seqs]") ||
+        is_i32_of(a[7], l->seqs, "dst_states must be contiguous int32 [num_seqs]"))
+        return -1;
+    const int64_t sizes[] = {l->q.tokens, l->q.heads, l->num_states, l->seqs};
+    return fit(sizes, 4);
+}
+
+/* out, q, k, v, log_decay, states, src_states, dst_states, scale, stream */
+static PyObject *linear_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    static const char *const names[] = {"out",       "q",      "k",          "v",
+                                        "log_decay", "states", "src_states", "dst_states"};
+    Linear l;
+    int device;
+    void *stream, *p[8];
+    if (count(n, 10))
+        return NULL;
+    const double scale = PyFloat_AsDouble(a[8]);
+    if ((scale == -1.0 && PyErr_Occurred()) || read_linear(a, &l))
+        return NULL;
+    if (l.seqs != l.q.tokens) {
+        bad("src_states and dst_states must have one number for each token");
+        return NULL;
+    }
+    if ((device = here(names, a, 8)) < 0 || stream_of(a[9], device, &stream))
+        return NULL;
+    for (int i = 0; i < 8; ++i)
+        p[i] = pointer(a[i]);
+    if (PyErr_Occurred())
+        return NULL;
+    pa_status st;
+    UNLOCKED(st = pa_linear_decode(p[0], p[1], p[2], p[3], p[4], l.decay_stride, p[5], p[6], p[7],
+                                   (int)l.seqs, (int)l.q.heads, (int)l.k.heads, (int)l.q.head_size,
+                                   (int)l.num_states, l.q.stride, l.k.stride, l.v.stride,
+                                   (float)scale, (pa_dtype)l.q.kind, stream));
+    return done(st, "pa_linear_decode");
+}
+
+/* out, q, k, v, log_decay, states, src_states, dst_states, query_start_loc,
+ * workspace, scale, max_query_len, stream */
+static PyObject *linear_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    static const char *const names[] = {"out",        "q",          "k",      "v",
+                                        "log_decay",  "states",     "src_states",
+                                        "dst_states", "query_start_loc", "workspace"};
+    Linear l;
+    int device, most;
+    void *stream, *ws, *p[9];
+    size_t bytes;
+    if (count(n, 13) || to_int(a[11], &most))
+        return NULL;
+    const double scale = PyFloat_AsDouble(a[10]);
+    if ((scale == -1.0 && PyErr_Occurred()) || read_linear(a, &l) ||
+        is_i32_of(a[8], l.seqs + 1, "query_start_loc must be contiguous int32 [num_seqs + 1]") ||
+        read_workspace(a[9], &ws, &bytes))
+        return NULL;
+    if ((device = here(names, a, 10)) < 0 || stream_of(a[12], device, &stream))
+        return NULL;
+    for (int i = 0; i < 9; ++i)
+        p[i] = pointer(a[i]);
+    if (PyErr_Occurred())
+        return NULL;
+    pa_status st;
+    UNLOCKED(st = pa_linear_prefill(p[0], p[1], p[2], p[3], p[4], l.decay_stride, p[5], p[6], p[7],
+                                    p[8], (int)l.seqs, (int)l.q.tokens, most, (int)l.q.heads,
+                                    (int)l.k.heads, (int)l.q.head_size, (int)l.num_states,
+                                    l.q.stride, l.k.stride, l.v.stride, (float)scale,
+                                    (pa_dtype)l.q.kind, ws, bytes, stream));
+    return done(st, "pa_linear_prefill");
+}
+
+/* ---- sequences ---- */
+
+typedef struct {
+    int64_t rows, blocks, num_blocks; /* rows, entries of one, blocks of the pool */
+} Tables;
+
+/* block_tables, seq_lens, ref_counts */
+static int read_tables(PyObject *tables, PyObject *lens, PyObject *refs, Tables *t)
+{
+    int64_t s[2];
+    const int n = shape_of(tables, s, 2);
+    if (n < 0)
+        return -1;
+    int ok = n == 2 ? has_dtype(tables, t_i32) : 0;
+    if (ok == 1)
+        ok = contiguous(tables);
+    if (ok != 1)
+        return ok < 0 ? -1 : bad("block_tables must be contiguous int32 [rows, max_blocks_per_seq]");
+    t->rows = s[0], t->blocks = s[1];
+    t->num_blocks = int_of(PyObject_CallMethodNoArgs(refs, n_numel));
+    if (t->num_blocks < 0)
+        return -1;
+    return is_i32_of(lens, t->rows, "seq_lens must be contiguous int32 [rows]") ||
+                   is_i32_of(refs, t->num_blocks, "ref_counts must be contiguous int32 [num_blocks]")
+               ? -1
+               : fit(&t->num_blocks, 1);
+}
+
+static int read_tables_out(PyObject *tables, PyObject *lens, PyObject *refs, int64_t rows,
+                           const Tables *t)
+{
+    const int64_t want[2] = {rows, t->blocks};
+    if (is(tables, t_i32, want, 2,
+           "tables_out must be contiguous int32 [rows, max_blocks_per_seq] as wide as block_tables"))
+        return -1;
+    if (lens && is_i32_of(lens, rows, "seq_lens_out must be contiguous int32 [rows]"))
+        return -1;
+    return is_i32_of(refs, t->num_blocks, "ref_counts_out must be contiguous int32 [num_blocks]");
+}
+
+/* A list or tuple of tensors [planes, num_blocks, ...] on `device`; their number. */
+static int read_block_pools(PyObject *pools, int64_t num_blocks, int device, pa_block_pool *to)
+{
+    static const char *const wanted =
+        "pools must be a list of contiguous CUDA tensors [planes, num_blocks, ...]";
+    PyObject *list = PySequence_Fast(pools, wanted);
+    if (!list)
+        return -1;
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
+    int st = n <= PA_MAX_POOLS ? 0 : bad("too many pools for one call");
+    for (Py_ssize_t i = 0; i < n && !st; ++i) {
+        PyObject *const t = PySequence_Fast_GET_ITEM(list, i);
+        int64_t s[2];
+        const int dims = shape_of(t, s, 2);
+        const int c = dims < 0 ? -1 : contiguous(t);
+        if (c < 0) {
+            st = -1;
+            break;
+        }
+        const int64_t bytes = int_of(PyObject_GetAttr(t, n_nbytes));
+        const int64_t on = int_of(PyObject_CallMethodNoArgs(t, n_get_device));
+        if (PyErr_Occurred())
+            st = -1;
+        else if (!c || dims < 2 || s[1] != num_blocks || s[0] < 1 || s[0] > INT32_MAX || bytes <= 0)
+            st = bad(wanted);
+        else if (on != device)
+            st = bad("pools must be on the current device");
+        else {
+            to[i].data = pointer(t);
+            to[i].block_bytes = bytes / (s[0] * s[1]);
+            to[i].planes = (int32_t)s[0];
+            st = PyErr_Occurred() ? -1 : 0;
+        }
+    }
+    Py_DECREF(list);
+    return st ? -1 : (int)n;
+}
+
+/* tables_out, seq_lens_out, ref_counts_out, block_tables, seq_lens, ref_counts,
+ * parents, block_size, stream */
+static PyObject *fork_sequences(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    static const char *const names[] = {"tables_out", "seq_lens_out", "ref_counts_out", "block_tables",
+                                        "seq_lens",   "ref_counts",   "parents"};
+    Tables t;
+    int bs, device;
+    void *stream, *p[7];
+    if (count(n, 9) || to_int(a[7], &bs) || read_tables(a[3], a[4], a[5], &t))
+        return NULL;
+    const int64_t rows = int_of(PyObject_CallMethodNoArgs(a[6], n_numel));
+    if (rows < 0 || is_i32_of(a[6], rows, "parents must be contiguous int32 [rows of tables_out]") ||
+        read_tables_out(a[0], a[1], a[2], rows, &t))
+        return NULL;
+    const int64_t sizes[] = {rows, t.rows, t.blocks};
+    if (fit(sizes, 3) || (device = here(names, a, 7)) < 0 || stream_of(a[8], device, &stream))
+        return NULL;
+    for (int i = 0; i < 7; ++i)
+        p[i] = pointer(a[i]);
+    if (PyErr_Occurred())
+        return NULL;
+    pa_status st;
+    UNLOCKED(st = pa_fork_sequences(p[0], p[1], p[2], p[3], p[4], p[5], p[6], (int)t.rows, (int)rows,
+                                    (int)t.num_blocks, (int)t.blocks, bs, stream));
+    return done(st, "pa_fork_sequences");
+}
+
+/* tables_out, seq_lens_out, ref_counts_out, slot_mapping, info, block_tables,
+ * seq_lens, ref_counts, num_new, workspace, pools, block_size, stream */
+static PyObject *extend_sequences(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    static const char *const names[] = {"tables_out", "seq_lens_out", "ref_counts_out", "slot_mapping",
+                                        "info",       "block_tables", "seq_lens",       "ref_counts",
+                                        "num_new",    "workspace"};
+    Tables t;
+    int bs, device, pools;
+    size_t bytes;
+    void *stream, *ws, *p[9];
+    pa_block_pool pool[PA_MAX_POOLS];
+    if (count(n, 13) || to_int(a[11], &bs) || read_tables(a[5], a[6], a[7], &t) ||
+        read_tables_out(a[0], a[1], a[2], t.rows, &t) ||
+        is_i32_of(a[4], 2, "info must be contiguous int32 [2]") ||
+        is_i32_of(a[8], t.rows, "num_new must be contiguous int32 [rows]"))
+        return NULL;
+    const int64_t tokens = int_of(PyObject_CallMethodNoArgs(a[3], n_numel));
+    if (tokens < 0 || is(a[3], t_i64, &tokens, 1, "slot_mapping must be contiguous int64 [T]") ||
+        read_workspace(a[9], &ws, &bytes))
+        return NULL;
+    const int64_t sizes[] = {tokens, t.rows, t.blocks};
+    if (fit(sizes, 3) || (device = here(names, a, 10)) < 0 ||
+        (pools = read_block_pools(a[10], t.num_blocks, device, pool)) < 0 ||
+        stream_of(a[12], device, &stream))
+        return NULL;
+    for (int i = 0; i < 9; ++i)
+        p[i] = pointer(a[i]);
+    if (PyErr_Occurred())
+        return NULL;
+    pa_status st;
+    UNLOCKED(st = pa_extend_sequences(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], pool,
+                                      pools, (int)t.rows, (int)tokens, (int)t.num_blocks,
+                                      (int)t.blocks, bs, ws, bytes, stream));
+    return done(st, "pa_extend_sequences");
+}
+
+/* tables_out, ref_counts_out, new_ids, info, block_tables, seq_lens, ref_counts,
+ * workspace, pools, block_size, stream */
+static PyObject *compact_blocks(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    static const char *const names[] = {"tables_out",   "ref_counts_out", "new_ids",    "info",
+                                        "block_tables", "seq_lens",       "ref_counts", "workspace"};
+    Tables t;
+    int bs, device, pools;
+    size_t bytes;
+    void *stream, *ws, *p[7];
+    pa_block_pool pool[PA_MAX_POOLS];
+    if (count(n, 11) || to_int(a[9], &bs) || read_tables(a[4], a[5], a[6], &t) ||
+        read_tables_out(a[0], NULL, a[1], t.rows, &t) ||
+        is_i32_of(a[2], t.num_blocks, "new_ids must be contiguous int32 [num_blocks]") ||
+        is_i32_of(a[3], 2, "info must be contiguous int32 [2]") || read_workspace(a[7], &ws, &bytes))
+        return NULL;
+    const int64_t sizes[] = {t.rows, t.blocks};
+    if (fit(sizes, 2) || (device = here(names, a, 8)) < 0 ||
+        (pools = read_block_pools(a[8], t.num_blocks, device, pool)) < 0 ||
+        stream_of(a[10], device, &stream))
+        return NULL;
+    for (int i = 0; i < 7; ++i)
+        p[i] = pointer(a[i]);
+    if (PyErr_Occurred())
+        return NULL;
+    pa_status st;
+    UNLOCKED(st = pa_compact_blocks(p[0], p[1], p[2], p[3], p[4], p[5], p[6], pool, pools,
+                                    (int)t.rows, (int)t.num_blocks, (int)t.blocks, bs, ws, bytes,
+                                    stream));
+    return done(st, "pa_compact_blocks");
+}
+
 /* The exception class of a failed call, and torch's functions for the current
  * device and its current raw stream. */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -604,6 +921,8 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
 #define CALL(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {CALL(bind),          CALL(write_block),   CALL(decode_block),
                                 CALL(update_bounds), CALL(select_blocks), CALL(decode_sparse),
+                                CALL(linear_decode), CALL(linear_prefill),
+                                CALL(fork_sequences), CALL(extend_sequences), CALL(compact_blocks),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "pa_block_calls", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};
@@ -616,7 +935,8 @@ PyMODINIT_FUNC PyInit_pa_block_calls(void)
     struct {
         PyObject **to;
         const char *name;
-    } types[] = {{&t_i32, "int32"}, {&t_f32, "float32"}, {&t_u8, "uint8"},
+    } types[] = {{&t_i32, "int32"}, {&t_i64, "int64"},
+                 {&t_f32, "float32"}, {&t_u8, "uint8"},
                  {&t_i8, "int8"},   {&t_f16, "float16"}, {&t_bf16, "bfloat16"}},
       names[] = {{&n_shape, "shape"},         {&n_dtype, "dtype"},
                  {&n_stride, "stride"},       {&n_is_contiguous, "is_contiguous"},

@@ -15,6 +15,9 @@
 #define PA_DEVERR_SEQ_LEN_ 0x2u
 #define PA_DEVERR_SLOT_ 0x4u
 #define PA_DEVERR_TIMEOUT_ 0x8u
+#define PA_DEVERR_STATE_ 0x20u
+#define PA_DEVERR_PARENT_ 0x40u
+#define PA_DEVERR_POOL_ 0x80u
 
 namespace pa {
 

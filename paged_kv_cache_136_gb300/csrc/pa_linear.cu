@@ -1,0 +1,256 @@
+// pa_linear.cu -- linear attention with a decay for each head: the recurrent
+// kernel (single tokens, short prompts) and the host side of both entry points.
+#include <cuda_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pa.h"
+#include "pa_block.cuh"
+#include "pa_internal.h"
+#include "pa_linear.cuh"
+
+namespace pa {
+namespace lin {
+
+constexpr int kHeadsAtOnce = 8; // query heads whose products share the state in registers
+
+// One CTA walks one sequence's tokens for one kv head with the state in registers:
+// a thread has 4 value channels (16 bytes of a state's row) of every 8th key
+// channel, so the state is read and written once, in whole rows, with all of a
+// CTA's loads in flight, and a token's products cost one pass over registers and a
+// sum over the 8 row groups in shared memory.
+template <typename T, int D, bool kPrompt>
+__global__ void __launch_bounds__(2 * D) linear_step_kernel(const LinearParams p)
+{
+    constexpr int kLanes = D / 4, kGroups = 8, kRows = D / kGroups;
+    __shared__ float sk[D], sq[kHeadsAtOnce][D];
+    __shared__ float part[kGroups][kHeadsAtOnce][D];
+    griddep_wait();
+    const int tid = threadIdx.x, head = blockIdx.x, s = blockIdx.y;
+    const int col = tid % kLanes * 4, group = tid / kLanes;
+    const int dst = p.dst_states[s], src = p.src_states[s];
+    int t0 = s, t1 = s + 1;
+    if constexpr (kPrompt) {
+        t0 = p.query_start_loc[s], t1 = p.query_start_loc[s + 1];
+        if (t0 < 0 || t1 > p.num_tokens || t1 < t0 || t1 - t0 > p.max_query_len) {
+            if (tid == 0 && head == 0)
+                atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
+            return;
+        }
+    }
+    if (dst < 0)
+        return;
+    if (tid == 0 && head == 0 && (src >= p.num_states || dst >= p.num_states))
+        atomicOr(p.err, PA_DEVERR_STATE_);
+    const int64_t at = (int64_t)group * D + col, one = (int64_t)D * D;
+    float4 S[kRows];
+    if (src >= 0 && src < p.num_states) {
+        const float *const from = p.states + ((int64_t)src * p.num_kv_heads + head) * one + at;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            S[i] = *reinterpret_cast<const float4 *>(from + (int64_t)i * kGroups * D);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int per = p.num_heads / p.num_kv_heads;
+    for (int t = t0; t < t1; ++t) {
+        // The decay less one: a decay near one, rounded to 24 bits, would be off by
+        // the same 2^-25 in every step, and 256 steps of memory by 2^-17.
+        const float a = expm1f(p.log_decay[t * p.decay_stride + head]);
+        const T *const k = static_cast<const T *>(p.k) + t * p.k_stride + head * D;
+        const T *const v = static_cast<const T *>(p.v) + t * p.v_stride + head * D;
+        const T *const q = static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)head * per * D;
+        T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + head * per) * D;
+        const float2 v01 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col));
+        const float2 v23 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col + 2));
+        for (int g0 = 0; g0 < per; g0 += kHeadsAtOnce) {
+            const int n = min(kHeadsAtOnce, per - g0);
+            if (g0 == 0)
+                for (int i = tid; i < D; i += 2 * D)
+                    sk[i] = (float)k[i];
+            for (int i = tid; i < n * D; i += 2 * D)
+                sq[i / D][i % D] = (float)q[g0 * D + i] * p.scale;
+            __syncthreads();
+            if (g0 == 0) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const float kk = sk[group + i * kGroups];
+                    S[i].x = fmaf(kk, v01.x, fmaf(a, S[i].x, S[i].x));
+                    S[i].y = fmaf(kk, v01.y, fmaf(a, S[i].y, S[i].y));
+                    S[i].z = fmaf(kk, v23.x, fmaf(a, S[i].z, S[i].z));
+                    S[i].w = fmaf(kk, v23.y, fmaf(a, S[i].w, S[i].w));
+                }
+            }
+            for (int g = 0; g < n; ++g) {
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const float qq = sq[g][group + i * kGroups];
+                    o.x = fmaf(qq, S[i].x, o.x);
+                    o.y = fmaf(qq, S[i].y, o.y);
+                    o.z = fmaf(qq, S[i].z, o.z);
+                    o.w = fmaf(qq, S[i].w, o.w);
+                }
+                *reinterpret_cast<float4 *>(&part[group][g][col]) = o;
+            }
+            __syncthreads();
+            for (int i = tid; i < n * D; i += 2 * D) {
+                float o = 0.f;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+                    o += part[j][i / D][i % D];
+                out[g0 * D + i] = (T)o;
+            }
+            __syncthreads();
+        }
+    }
+    if (dst < p.num_states) {
+        float *const to = p.states + ((int64_t)dst * p.num_kv_heads + head) * one + at;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            *reinterpret_cast<float4 *>(to + (int64_t)i * kGroups * D) = S[i];
+    }
+}
+
+static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Checks that both entry points share, and the parameters.
+static pa_status read_args(LinearParams *p, void *out, const void *q, const void *k, const void *v,
+                           const float *log_decay, int64_t decay_stride, float *states,
+                           const int32_t *src_states, const int32_t *dst_states, int num_seqs,
+                           int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                           int num_states, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           float scale, pa_dtype dtype)
+{
+    if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        num_states <= 0 || num_heads % num_kv_heads || !isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if ((head_size != 64 && head_size != 128) || (dtype != PA_FP16 && dtype != PA_BF16) ||
+        num_seqs > 65535 || num_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t kv = (int64_t)num_kv_heads * head_size;
+    if (q_stride < (int64_t)num_heads * head_size || k_stride < kv || v_stride < kv ||
+        q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        (decay_stride != 0 && decay_stride < num_kv_heads))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!states || !src_states || !dst_states))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && num_tokens > 0 && (!out || !q || !k || !v || !log_decay))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(states, 16) || !aligned(log_decay, 4) || !aligned(src_states, 4) ||
+        !aligned(dst_states, 4))
+        return PA_ERR_INVALID_ARG;
+    *p = {};
+    p->out = out;
+    p->q = q;
+    p->k = k;
+    p->v = v;
+    p->log_decay = log_decay;
+    p->decay_stride = decay_stride;
+    p->states = states;
+    p->src_states = src_states;
+    p->dst_states = dst_states;
+    p->num_tokens = num_tokens;
+    p->num_heads = num_heads;
+    p->num_kv_heads = num_kv_heads;
+    p->num_states = num_states;
+    p->q_stride = q_stride;
+    p->k_stride = k_stride;
+    p->v_stride = v_stride;
+    p->scale = scale;
+    return PA_OK;
+}
+
+template <bool kPrompt>
+static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_size, pa_dtype dtype,
+                               cudaStream_t s)
+{
+    const dim3 grid(p.num_kv_heads, num_seqs), threads(2 * head_size);
+    if (head_size == 128)
+        return dtype == PA_BF16
+                   ? launch_after_previous(linear_step_kernel<__nv_bfloat16, 128, kPrompt>, grid, threads, 0, s, p)
+                   : launch_after_previous(linear_step_kernel<__half, 128, kPrompt>, grid, threads, 0, s, p);
+    return dtype == PA_BF16
+               ? launch_after_previous(linear_step_kernel<__nv_bfloat16, 64, kPrompt>, grid, threads, 0, s, p)
+               : launch_after_previous(linear_step_kernel<__half, 64, kPrompt>, grid, threads, 0, s, p);
+}
+
+} // namespace lin
+} // namespace pa
+
+using namespace pa;
+using namespace pa::lin;
+
+extern "C" {
+
+pa_status pa_linear_decode(void *out, const void *q, const void *k, const void *v,
+                           const float *log_decay, int64_t decay_stride, float *states,
+                           const int32_t *src_states, const int32_t *dst_states, int num_seqs,
+                           int num_heads, int num_kv_heads, int head_size, int num_states,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                           pa_dtype dtype, void *stream)
+{
+    LinearParams p;
+    const pa_status st = read_args(&p, out, q, k, v, log_decay, decay_stride, states, src_states,
+                                   dst_states, num_seqs, num_seqs, num_heads, num_kv_heads,
+                                   head_size, num_states, q_stride, k_stride, v_stride, scale, dtype);
+    if (st != PA_OK)
+        return st;
+    if (num_seqs == 0)
+        return PA_OK;
+    cudaError_t e;
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    e = launch_step<false>(p, num_seqs, head_size, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_linear_prefill_workspace_size(int num_seqs, int num_tokens, int max_query_len,
+                                        int num_kv_heads, int head_size)
+{
+    if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || num_kv_heads <= 0 || head_size <= 0)
+        return 0;
+    return 256;
+}
+
+pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void *v,
+                            const float *log_decay, int64_t decay_stride, float *states,
+                            const int32_t *src_states, const int32_t *dst_states,
+                            const int32_t *query_start_loc, int num_seqs, int num_tokens,
+                            int max_query_len, int num_heads, int num_kv_heads, int head_size,
+                            int num_states, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                            void *stream)
+{
+    LinearParams p;
+    const pa_status st = read_args(&p, out, q, k, v, log_decay, decay_stride, states, src_states,
+                                   dst_states, num_seqs, num_tokens, num_heads, num_kv_heads,
+                                   head_size, num_states, q_stride, k_stride, v_stride, scale, dtype);
+    if (st != PA_OK)
+        return st;
+    if (max_query_len < 0 || (num_seqs > 0 && !query_start_loc) || !aligned(query_start_loc, 4))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < pa_linear_prefill_workspace_size(num_seqs, num_tokens, max_query_len,
+                                                           num_kv_heads, head_size))
+        return PA_ERR_WORKSPACE;
+    cudaError_t e;
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.query_start_loc = query_start_loc;
+    p.max_query_len = max_query_len;
+    e = launch_step<true>(p, num_seqs, head_size, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+} // extern "C"

@@ -1,0 +1,875 @@
+// pa_sequences.cu -- the life of sequences in a block pool: forking and freeing
+// rows of the block tables, room for new tokens (blocks taken, shared last
+// blocks copied, slots), and moving the live blocks to the front of the pool.
+//
+// All of it is whole numbers and copied bytes, so every result has one right
+// value whatever the order in which CTAs run: a block is taken by its rank among
+// the free ones, counts are changed by integer atomics.
+#include <cuda_runtime.h>
+
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "pa.h"
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+
+namespace pa {
+namespace seqs {
+
+constexpr int kThreads = 256;      // of the wide kernels
+constexpr int kChunk = 1024;       // table entries of a CTA
+constexpr int kRankThreads = 1024; // of a CTA of the ranking kernels
+constexpr int kCluster = 8;        // CTAs of a ranking kernel, at most
+constexpr int kTile = 4 * kRankThreads; // counts that a CTA ranks at once
+constexpr int kUnit = 16384;       // bytes of a block that a CTA copies at once
+// A sum of at most 65535 rows' needs: blocks, fewer than 2^31 a row, and above
+// them the rows that copy a block.
+constexpr int kCopyBit = 47;
+
+// ---------------------------------------------------------------------------
+// Pools: what a block's bytes are, for the copies of extend and compact
+// ---------------------------------------------------------------------------
+struct Pool {
+    uint8_t *data;       // [planes, num_blocks, block_bytes]
+    int64_t block_bytes, plane_bytes;
+    int first_unit;      // units of the pools before this one
+    int plane_units;     // units of a block of one plane
+    int planes;
+    int width;           // bytes of a load: 16, 4 or 1
+};
+
+template <int N> struct Pools {
+    Pool pool[N];
+    int count, units;    // units of a block, over all pools
+};
+
+// One CTA copies unit `u` of block src to block dst.
+template <typename W>
+__device__ __forceinline__ void copy_bytes(uint8_t *dst, const uint8_t *src, int64_t bytes)
+{
+    const W *const s = reinterpret_cast<const W *>(src);
+    W *const d = reinterpret_cast<W *>(dst);
+    const int n = (int)(bytes / (int)sizeof(W));
+    // four loads in flight a thread
+    for (int i = threadIdx.x; i < n; i += 4 * kThreads) {
+        W v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k * kThreads < n)
+                v[k] = s[i + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k * kThreads < n)
+                d[i + k * kThreads] = v[k];
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void copy_unit(const Pools<N> &ps, int u, int64_t src, int64_t dst)
+{
+    int lo = 0, hi = ps.count - 1; // the last pool that begins at or before u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (ps.pool[mid].first_unit <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const Pool &p = ps.pool[lo];
+    const int at = u - p.first_unit, plane = at / p.plane_units;
+    const int64_t off = (int64_t)(at - plane * p.plane_units) * kUnit;
+    const int64_t bytes = min((int64_t)kUnit, p.block_bytes - off);
+    uint8_t *const base = p.data + plane * p.plane_bytes + off;
+    uint8_t *const d = base + dst * p.block_bytes;
+    const uint8_t *const s = base + src * p.block_bytes;
+    if (p.width == 16)
+        copy_bytes<uint4>(d, s, bytes);
+    else if (p.width == 4)
+        copy_bytes<uint32_t>(d, s, bytes);
+    else
+        copy_bytes<uint8_t>(d, s, bytes);
+}
+
+// ---------------------------------------------------------------------------
+// Fork
+// ---------------------------------------------------------------------------
+struct ForkParams {
+    int32_t *tables_out, *lens_out, *refs;
+    const int32_t *tables, *lens, *parents;
+    unsigned int *err;
+    int rows_in, rows_out, num_blocks, max_blocks, block_size, len_cap;
+};
+
+__device__ __forceinline__ int blocks_of(int len, int bs) { return len / bs + (len % bs != 0); }
+
+// A row's length, held to what its table can hold.
+__device__ __forceinline__ int length_of(const int32_t *lens, int r, int cap, bool tell,
+                                         unsigned int *err)
+{
+    const int n = lens[r];
+    if (n >= 0 && n <= cap)
+        return n;
+    if (tell)
+        atomicOr(err, PA_DEVERR_SEQ_LEN_);
+    return n < 0 ? 0 : cap;
+}
+
+__global__ void __launch_bounds__(kThreads) copy_counts_kernel(int32_t *__restrict__ out,
+                                                               const int32_t *__restrict__ in, int n)
+{
+    griddep_wait();
+    const int first = blockIdx.x * (4 * kThreads) + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (first + k * kThreads < n)
+            out[first + k * kThreads] = in[first + k * kThreads];
+}
+
+// CTA (r, c): entries [c kChunk, (c + 1) kChunk) of new row r, and of old row r,
+// whose blocks' counts change by its children less one.  Rows with one child, the
+// most of a beam search's, touch no count.
+__global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p)
+{
+    griddep_wait();
+    const int r = blockIdx.x, base = blockIdx.y * kChunk, tid = threadIdx.x;
+    const bool first = blockIdx.y == 0 && tid == 0;
+    if (r < p.rows_out) {
+        const int parent = p.parents[r];
+        int n = 0;
+        if (parent >= 0 && parent < p.rows_in)
+            n = length_of(p.lens, parent, p.len_cap, first, p.err);
+        else if (parent >= p.rows_in && first)
+            atomicOr(p.err, PA_DEVERR_PARENT_);
+        if (first)
+            p.lens_out[r] = n;
+        const int end = min(blocks_of(n, p.block_size), base + kChunk);
+        const int32_t *const src = p.tables + (int64_t)parent * p.max_blocks;
+        int32_t *const dst = p.tables_out + (int64_t)r * p.max_blocks;
+        int32_t v[kChunk / kThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / kThreads; ++k)
+            if (base + tid + k * kThreads < end)
+                v[k] = src[base + tid + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / kThreads; ++k)
+            if (base + tid + k * kThreads < end)
+                dst[base + tid + k * kThreads] = v[k];
+    }
+    if (r >= p.rows_in)
+        return;
+    const int n = blocks_of(length_of(p.lens, r, p.len_cap, first, p.err), p.block_size);
+    if (base >= n)
+        return;
+    int children = 0;
+    for (int i = 0; i < p.rows_out; i += kThreads)
+        children += __syncthreads_count(i + tid < p.rows_out && p.parents[i + tid] == r);
+    if (children == 1)
+        return;
+    const int end = min(n, base + kChunk);
+    for (int j = base + tid; j < end; j += kThreads) {
+        const int b = p.tables[(int64_t)r * p.max_blocks + j];
+        if (b >= 0 && b < p.num_blocks)
+            atomicAdd(p.refs + b, children - 1);
+        else
+            atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Ranks, by one cluster
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// What a CTA of the cluster tells the others, in the workspace.
+struct Told {
+    int64_t a, b, c;
+};
+
+// Exclusive prefix of v over the CTA's threads, and the sum; `sums` has a slot
+// for each of the 32 warps.  Two barriers.
+__device__ __forceinline__ int64_t prefix(int64_t v, int64_t *sums, int64_t *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        sums[warp] = x;
+    __syncthreads();
+    int64_t w = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t y = __shfl_up_sync(~0u, w, o);
+        if (lane >= o)
+            w += y;
+    }
+    *total = __shfl_sync(~0u, w, 31);
+    const int64_t before = warp ? __shfl_sync(~0u, w, warp - 1) : 0;
+    return before + x - v;
+}
+
+// f(id, free, number of free ids in [begin, id)) for every id of [begin, end), in
+// tiles of kTile: a warp has 128 consecutive ids, 32 at a time.
+template <typename F>
+__device__ __forceinline__ void ranked(const int32_t *refs, int begin, int end, int64_t *sums, F f)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int carry = 0;
+    for (int t = begin; t < end; t += kTile) {
+        const int at = t + warp * 128 + lane;
+        int v[4];
+        unsigned m[4];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[k] = at + 32 * k < end ? refs[at + 32 * k] : 1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            m[k] = __ballot_sync(~0u, v[k] == 0);
+            mine += __popc(m[k]);
+        }
+        int64_t total;
+        // one lane of a warp brings its sum: the others bring 0
+        int before = (int)prefix(lane == 0 ? mine : 0, sums, &total);
+        before = __shfl_sync(~0u, before, 0) + carry;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (at + 32 * k < end)
+                f(at + 32 * k, v[k], before + __popc(m[k] & ((1u << lane) - 1)));
+            before += __popc(m[k]);
+        }
+        carry += (int)total;
+    }
+}
+
+// Free ids of [begin, end), the same for every thread.
+__device__ __forceinline__ int count_free(const int32_t *refs, int begin, int end, int64_t *sums)
+{
+    int n = 0;
+    for (int i = begin + threadIdx.x; i < end; i += kRankThreads)
+        n += refs[i] == 0;
+    int64_t total;
+    prefix(n, sums, &total);
+    return (int)total;
+}
+
+struct ExtendParams {
+    int32_t *tables_out, *lens_out, *refs_out, *info;
+    int64_t *slots;
+    const int32_t *tables, *lens, *refs, *num_new;
+    unsigned int *err;
+    // workspace: per block
+    int32_t *writers, *latest, *free_ids;
+    // per row: old length, new tokens, first rank of its blocks, first token, and
+    // its old last block if that is copied, else -1; the rows that copy
+    int32_t *row_len, *row_new, *row_begin, *row_token, *row_copy, *copy_rows;
+    Told *told;          // of each CTA
+    int32_t *head;       // tokens, rows that copy
+    int rows, num_blocks, max_blocks, block_size, len_cap, num_tokens;
+};
+
+struct Row {
+    int len, fresh, last; // last: the block that new tokens go on in, or -1
+};
+
+__device__ __forceinline__ Row read_row(const ExtendParams &p, int r, bool tell)
+{
+    Row x;
+    x.len = length_of(p.lens, r, p.len_cap, tell, p.err);
+    x.fresh = p.num_new[r];
+    if (x.fresh < 0 || x.fresh > p.len_cap - x.len) {
+        if (tell)
+            atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
+        x.fresh = 0;
+    }
+    x.last = -1;
+    if (x.fresh > 0 && x.len % p.block_size) {
+        const int b = p.tables[(int64_t)r * p.max_blocks + x.len / p.block_size];
+        if (b >= 0 && b < p.num_blocks)
+            x.last = b;
+        else if (tell)
+            atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+    }
+    return x;
+}
+
+// One cluster: every row's needs, their prefix sums, and the ids of as many free
+// blocks.  A row that goes on in a shared block copies it, but for the last of its
+// holders where all of them go on; that is what row after row would come to.
+__global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendParams p)
+{
+    __shared__ int64_t sums[32];
+    griddep_wait();
+    const int rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
+    const int per = (p.rows + ctas - 1) / ctas;
+    const int r0 = min(p.rows, rank * per), r1 = min(p.rows, r0 + per);
+    const int part = ((p.num_blocks + ctas - 1) / ctas + 31) / 32 * 32;
+    const int b0 = min(p.num_blocks, rank * part), b1 = min(p.num_blocks, b0 + part);
+
+    for (int r = r0 + tid; r < r1; r += kRankThreads) {
+        const Row x = read_row(p, r, true);
+        if (x.last >= 0 && p.refs[x.last] > 1)
+            p.writers[x.last] = 0, p.latest[x.last] = -1;
+    }
+    const int free_here = count_free(p.refs, b0, b1, sums);
+    cluster_sync();
+    for (int r = r0 + tid; r < r1; r += kRankThreads) {
+        const Row x = read_row(p, r, false);
+        if (x.last >= 0 && p.refs[x.last] > 1) {
+            atomicAdd(p.writers + x.last, 1);
+            atomicMax(p.latest + x.last, r);
+        }
+    }
+    cluster_sync();
+    // need: blocks below kCopyBit, rows that copy above
+    constexpr int64_t low = (1ll << kCopyBit) - 1;
+    int64_t needs = 0, tokens = 0;
+    for (int t = r0; t < r1; t += kRankThreads) {
+        const int r = t + tid;
+        int64_t need = 0;
+        Row x = {0, 0, -1};
+        if (r < r1) {
+            x = read_row(p, r, false);
+            const int refs = x.last >= 0 ? p.refs[x.last] : 0;
+            if (refs <= 1 || (__ldcg(p.writers + x.last) == refs && __ldcg(p.latest + x.last) == r))
+                x.last = -1;
+            need = blocks_of(x.len + x.fresh, p.block_size) - blocks_of(x.len, p.block_size);
+            if (x.last >= 0)
+                need += 1 + (1ll << kCopyBit);
+        }
+        int64_t all_need, all_new;
+        const int64_t a = needs + prefix(need, sums, &all_need);
+        const int64_t b = tokens + prefix(x.fresh, sums, &all_new);
+        needs += all_need, tokens += all_new;
+        if (r < r1) {
+            p.row_len[r] = x.len;
+            p.row_new[r] = x.fresh;
+            p.row_copy[r] = x.last;
+            p.row_begin[r] = (int)(a & low);
+            p.row_token[r] = (int)b;
+        }
+    }
+    if (tid == 0)
+        p.told[rank] = {needs, tokens, free_here};
+    cluster_sync();
+    int64_t need_before = 0, new_before = 0, need_all = 0, total = 0, free = 0;
+    int free_before = 0;
+    for (int c = 0; c < ctas; ++c) {
+        const int64_t a = __ldcg(&p.told[c].a), b = __ldcg(&p.told[c].b), f = __ldcg(&p.told[c].c);
+        if (c < rank)
+            need_before += a, new_before += b, free_before += (int)f;
+        need_all += a, total += b, free += f;
+    }
+    const int64_t want = need_all & low;
+    const bool ok = want <= free && total <= p.num_tokens;
+    if (rank == 0 && tid == 0) {
+        if (!ok)
+            atomicOr(p.err, PA_DEVERR_POOL_);
+        p.info[0] = (int)min(want, (int64_t)INT32_MAX);
+        p.info[1] = (int)max(free - want, -(int64_t)INT32_MAX);
+        p.head[0] = ok ? (int)total : 0;
+        p.head[1] = ok ? (int)(need_all >> kCopyBit) : 0;
+    }
+    const int take = ok ? (int)want : 0;
+    ranked(p.refs, b0, b1, sums, [&](int id, int refs, int before) {
+        const int k = before + free_before;
+        const bool taken = refs == 0 && k < take;
+        if (taken)
+            p.free_ids[k] = id;
+        if (taken || p.refs_out != p.refs)
+            p.refs_out[id] = taken ? 1 : refs;
+    });
+    cluster_sync();
+    int copied = (int)(need_before >> kCopyBit); // rows before this one that copy
+    for (int t = r0; t < r1; t += kRankThreads) {
+        const int r = t + tid;
+        bool copies = false;
+        if (r < r1) {
+            copies = p.row_copy[r] >= 0 && ok;
+            p.row_begin[r] += (int)(need_before & low);
+            p.row_token[r] = ok ? p.row_token[r] + (int)(new_before & low) : 0;
+            if (!ok)
+                p.row_new[r] = 0, p.row_copy[r] = -1;
+            p.lens_out[r] = p.row_len[r] + (ok ? p.row_new[r] : 0);
+            if (copies)
+                atomicSub(p.refs_out + p.row_copy[r], 1);
+        }
+        int64_t all;
+        const int64_t at = prefix(copies, sums, &all);
+        if (copies)
+            p.copy_rows[copied + (int)at] = r;
+        copied += (int)all;
+    }
+}
+
+// The tables, the slots and the copies of extend: items of one list, CTA after
+// CTA.  Bound by the copies' bytes where there are any, else by latency.
+template <int N>
+__global__ void __launch_bounds__(kThreads) extend_apply_kernel(const ExtendParams p,
+                                                                const __grid_constant__ Pools<N> ps)
+{
+    griddep_wait();
+    const int tid = threadIdx.x, tokens = p.head[0], bs = p.block_size;
+    const int64_t copies = (int64_t)p.head[1] * ps.units;
+    const int chunks = (p.max_blocks + kChunk - 1) / kChunk;
+    const int64_t entries = (int64_t)p.rows * chunks;
+    const int64_t items = copies + entries + (p.num_tokens + kThreads - 1) / kThreads;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        if (item < copies) {
+            const int r = p.copy_rows[item / ps.units];
+            copy_unit(ps, (int)(item % ps.units), p.row_copy[r], p.free_ids[p.row_begin[r]]);
+            continue;
+        }
+        if (item < copies + entries) {
+            const int r = (int)((item - copies) / chunks);
+            const int base = (int)((item - copies) % chunks) * kChunk;
+            const int len = p.row_len[r], kept = blocks_of(len, bs) - (p.row_copy[r] >= 0);
+            const int end = min(base + kChunk, blocks_of(len + p.row_new[r], bs));
+            const int32_t *const got = p.free_ids + p.row_begin[r] - kept;
+            const int64_t row = (int64_t)r * p.max_blocks;
+            for (int j = base + tid; j < end; j += kThreads)
+                if (j >= kept)
+                    p.tables_out[row + j] = got[j];
+                else if (p.tables_out != p.tables)
+                    p.tables_out[row + j] = p.tables[row + j];
+            continue;
+        }
+        const int64_t t64 = (item - copies - entries) * kThreads + tid;
+        if (t64 >= p.num_tokens)
+            continue;
+        const int t = (int)t64;
+        int64_t slot = -1;
+        if (t < tokens) {
+            int lo = 0, hi = p.rows - 1; // the last row whose tokens begin at or before t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (p.row_token[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int len = p.row_len[lo], pos = len + t - p.row_token[lo], j = pos / bs;
+            const int kept = blocks_of(len, bs) - (p.row_copy[lo] >= 0);
+            const int block = j < kept ? p.tables[(int64_t)lo * p.max_blocks + j]
+                                       : p.free_ids[p.row_begin[lo] + j - kept];
+            if (block >= 0 && block < p.num_blocks)
+                slot = (int64_t)block * bs + pos % bs;
+        }
+        p.slots[t] = slot;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Compact
+// ---------------------------------------------------------------------------
+struct CompactParams {
+    int32_t *tables_out, *refs_out, *new_ids, *info;
+    const int32_t *tables, *lens, *refs;
+    unsigned int *err;
+    int32_t *holes, *movers; // workspace: free ids below the live blocks' number, and what goes there
+    Told *told;
+    int32_t *head;           // live blocks below their number; blocks that move
+    int rows, num_blocks, max_blocks, block_size, len_cap;
+};
+
+// One cluster: with n live blocks, the k-th live id at or above n moves to the
+// k-th free id below n.
+__global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const CompactParams p)
+{
+    __shared__ int64_t sums[32];
+    griddep_wait();
+    const int rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
+    const int part = ((p.num_blocks + ctas - 1) / ctas + 31) / 32 * 32;
+    const int b0 = min(p.num_blocks, rank * part), b1 = min(p.num_blocks, b0 + part);
+    const int mine = count_free(p.refs, b0, b1, sums);
+    if (tid == 0)
+        p.told[rank].a = mine;
+    if (rank == 0 && tid == 0)
+        p.head[0] = -1;
+    cluster_sync();
+    int free_before = 0, free = 0;
+    for (int c = 0; c < ctas; ++c) {
+        const int a = (int)__ldcg(&p.told[c].a);
+        free_before += c < rank ? a : 0;
+        free += a;
+    }
+    const int n = p.num_blocks - free;
+    ranked(p.refs, b0, b1, sums, [&](int id, int refs, int before) {
+        const int f = before + free_before, live = id - f; // free and live ids below this one
+        if (id == n)
+            p.head[0] = live;
+        // what moves is marked with its rank for the second pass
+        p.new_ids[id] = refs == 0 ? -1 : id < n ? id : -2 - live;
+        if (refs == 0 && id < n)
+            p.holes[f] = id;
+    });
+    cluster_sync();
+    const int low = n == p.num_blocks ? n : __ldcg(p.head); // live ids below n
+    if (rank == 0 && tid == 0) {
+        p.info[0] = n;
+        p.info[1] = n - low;
+        p.head[1] = n - low;
+    }
+    for (int id = b0 + tid; id < b1; id += kRankThreads) {
+        const int x = p.new_ids[id];
+        if (x <= -2) {
+            const int k = -2 - x - low, to = __ldcg(p.holes + k);
+            const int refs = p.refs[id];
+            p.movers[k] = id;
+            p.new_ids[id] = to;
+            p.refs_out[to] = refs;
+            p.refs_out[id] = 0;
+        } else if (p.refs_out != p.refs && (x >= 0 || id >= n)) {
+            p.refs_out[id] = x >= 0 ? p.refs[id] : 0; // a hole's is written by what goes there
+        }
+    }
+}
+
+// The moves and the tables of compact; as extend_apply_kernel.
+template <int N>
+__global__ void __launch_bounds__(kThreads) compact_apply_kernel(const CompactParams p,
+                                                                 const __grid_constant__ Pools<N> ps)
+{
+    griddep_wait();
+    const int64_t copies = (int64_t)p.head[1] * ps.units;
+    const int chunks = (p.max_blocks + kChunk - 1) / kChunk;
+    const int64_t items = copies + (int64_t)p.rows * chunks;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        if (item < copies) {
+            const int k = (int)(item / ps.units);
+            copy_unit(ps, (int)(item % ps.units), p.movers[k], p.holes[k]);
+            continue;
+        }
+        const int r = (int)((item - copies) / chunks);
+        const int base = (int)((item - copies) % chunks) * kChunk;
+        const int len = length_of(p.lens, r, p.len_cap, base == 0 && threadIdx.x == 0, p.err);
+        const int end = min(base + kChunk, blocks_of(len, p.block_size));
+        const int64_t row = (int64_t)r * p.max_blocks;
+        for (int j = base + threadIdx.x; j < end; j += kThreads) {
+            const int b = p.tables[row + j];
+            int to = -1;
+            if (b >= 0 && b < p.num_blocks)
+                to = p.new_ids[b];
+            if (to < 0)
+                atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+            p.tables_out[row + j] = to;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+static bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Rows and blocks of the tables and counts.
+static pa_status check_sizes(int rows, int num_blocks, int max_blocks, int block_size)
+{
+    if (rows < 0 || num_blocks <= 0 || max_blocks <= 0 || block_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (rows > 65535 || (int64_t)max_blocks * block_size > INT32_MAX ||
+        num_blocks > (1 << 29) || (max_blocks - 1) / kChunk + 1 > 65535)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+// Launch on one cluster of `ctas` CTAs, after the kernel before.
+template <typename P>
+static cudaError_t launch_cluster(void (*kern)(const P), int ctas, cudaStream_t s, const P &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kRankThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// CTAs of a ranking kernel: one while it holds everything in a tile, for its
+// barrier is the CTA's own then.
+static int rank_ctas(int rows, int num_blocks)
+{
+    return rows <= kRankThreads && num_blocks <= kTile ? 1 : kCluster;
+}
+
+static pa_status read_pools(Pools<PA_MAX_POOLS> *to, const pa_block_pool *from, int count,
+                            int num_blocks)
+{
+    if (count < 0 || (count > 0 && !from))
+        return PA_ERR_INVALID_ARG;
+    if (count > PA_MAX_POOLS)
+        return PA_ERR_UNSUPPORTED;
+    int64_t units = 0;
+    for (int i = 0; i < count; ++i) {
+        const pa_block_pool &f = from[i];
+        if (!f.data || f.block_bytes <= 0 || f.planes <= 0)
+            return PA_ERR_INVALID_ARG;
+        Pool &p = to->pool[i];
+        p.data = static_cast<uint8_t *>(f.data);
+        p.block_bytes = f.block_bytes;
+        p.plane_bytes = f.block_bytes * num_blocks;
+        p.planes = f.planes;
+        p.first_unit = (int)units;
+        const int64_t each = (f.block_bytes + kUnit - 1) / kUnit;
+        p.plane_units = (int)each;
+        const uintptr_t all = reinterpret_cast<uintptr_t>(f.data) | (uintptr_t)f.block_bytes;
+        p.width = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+        units += each * f.planes;
+        if (f.block_bytes > ((int64_t)1 << 40) / num_blocks || units > (1 << 30))
+            return PA_ERR_UNSUPPORTED;
+    }
+    to->count = count;
+    to->units = (int)units;
+    return PA_OK;
+}
+
+// Few pools travel in a small parameter block: a launch copies all of it.
+constexpr int kFewPools = 16;
+
+template <typename P>
+static cudaError_t launch_apply(void (*few)(const P, const Pools<kFewPools>),
+                                void (*many)(const P, const Pools<PA_MAX_POOLS>), const P &p,
+                                const Pools<PA_MAX_POOLS> &ps, int64_t items, cudaStream_t s)
+{
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * 8)));
+    if (ps.count > kFewPools)
+        return launch_after_previous(many, grid, dim3(kThreads), 0, s, p, ps);
+    Pools<kFewPools> f;
+    std::copy(ps.pool, ps.pool + ps.count, f.pool);
+    f.count = ps.count;
+    f.units = ps.units;
+    return launch_after_previous(few, grid, dim3(kThreads), 0, s, p, f);
+}
+
+} // namespace seqs
+} // namespace pa
+
+using namespace pa;
+using namespace pa::seqs;
+
+extern "C" {
+
+pa_status pa_fork_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_t *ref_counts_out,
+                            const int32_t *block_tables, const int32_t *seq_lens,
+                            const int32_t *ref_counts, const int32_t *parents, int num_seqs,
+                            int num_seqs_out, int num_blocks, int max_blocks_per_seq,
+                            int block_size, void *stream)
+{
+    pa_status st = check_sizes(num_seqs, num_blocks, max_blocks_per_seq, block_size);
+    if (st == PA_OK)
+        st = check_sizes(num_seqs_out, num_blocks, max_blocks_per_seq, block_size);
+    if (st != PA_OK)
+        return st;
+    if (!ref_counts || !ref_counts_out || !aligned(ref_counts, 4) || !aligned(ref_counts_out, 4) ||
+        (num_seqs > 0 && (!block_tables || !seq_lens)) ||
+        (num_seqs_out > 0 && (!tables_out || !seq_lens_out || !parents)) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(tables_out, 4) ||
+        !aligned(seq_lens_out, 4) || !aligned(parents, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t wide = (int64_t)max_blocks_per_seq * 4, counts = (int64_t)num_blocks * 4;
+    // rows trade places, so that they cannot be written where others are read
+    if (overlap(tables_out, num_seqs_out * wide, block_tables, num_seqs * wide) ||
+        overlap(seq_lens_out, num_seqs_out * 4ll, seq_lens, num_seqs * 4ll) ||
+        (ref_counts != ref_counts_out && overlap(ref_counts, counts, ref_counts_out, counts)))
+        return PA_ERR_INVALID_ARG;
+    cudaError_t e;
+    ForkParams p = {};
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.tables_out = tables_out;
+    p.lens_out = seq_lens_out;
+    p.refs = ref_counts_out;
+    p.tables = block_tables;
+    p.lens = seq_lens;
+    p.parents = parents;
+    p.rows_in = num_seqs;
+    p.rows_out = num_seqs_out;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.block_size = block_size;
+    p.len_cap = max_blocks_per_seq * block_size;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ref_counts_out != ref_counts) {
+        const unsigned n = (unsigned)((num_blocks + 4 * kThreads - 1) / (4 * kThreads));
+        if (launch_after_previous(copy_counts_kernel, dim3(n), dim3(kThreads), 0, s, ref_counts_out,
+                                  ref_counts, num_blocks) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    const int rows = std::max(num_seqs, num_seqs_out);
+    if (rows == 0)
+        return PA_OK;
+    const dim3 grid(rows, (max_blocks_per_seq + kChunk - 1) / kChunk);
+    return launch_after_previous(fork_kernel, grid, dim3(kThreads), 0, s, p) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_sequences_workspace_size(int num_seqs, int num_blocks)
+{
+    if (check_sizes(num_seqs, num_blocks, 1, 1) != PA_OK)
+        return 0;
+    // the CTAs' sums and two numbers, three numbers a block, six a row
+    return kCluster * sizeof(Told) + 16 + 4 * (3 * (size_t)num_blocks + 6 * (size_t)num_seqs);
+}
+
+pa_status pa_extend_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_t *ref_counts_out,
+                              int64_t *slot_mapping, int32_t *info, const int32_t *block_tables,
+                              const int32_t *seq_lens, const int32_t *ref_counts,
+                              const int32_t *num_new, const pa_block_pool *pools, int num_pools,
+                              int num_seqs, int num_tokens, int num_blocks, int max_blocks_per_seq,
+                              int block_size, void *workspace, size_t workspace_bytes, void *stream)
+{
+    pa_status st = check_sizes(num_seqs, num_blocks, max_blocks_per_seq, block_size);
+    if (st != PA_OK)
+        return st;
+    if (num_tokens < 0 || !info || !ref_counts || !ref_counts_out || (num_tokens > 0 && !slot_mapping) ||
+        (num_seqs > 0 &&
+         (!tables_out || !seq_lens_out || !block_tables || !seq_lens || !num_new)) ||
+        !aligned(tables_out, 4) || !aligned(seq_lens_out, 4) || !aligned(ref_counts_out, 4) ||
+        !aligned(slot_mapping, 8) || !aligned(info, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4) || !aligned(ref_counts, 4) || !aligned(num_new, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t wide = 4ll * num_seqs * max_blocks_per_seq;
+    if ((tables_out != block_tables && overlap(tables_out, wide, block_tables, wide)) ||
+        (seq_lens_out != seq_lens && overlap(seq_lens_out, 4ll * num_seqs, seq_lens, 4ll * num_seqs)) ||
+        (ref_counts_out != ref_counts &&
+         overlap(ref_counts_out, 4ll * num_blocks, ref_counts, 4ll * num_blocks)))
+        return PA_ERR_INVALID_ARG;
+    Pools<PA_MAX_POOLS> ps;
+    st = read_pools(&ps, pools, num_pools, num_blocks);
+    if (st != PA_OK)
+        return st;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < pa_sequences_workspace_size(num_seqs, num_blocks))
+        return PA_ERR_WORKSPACE;
+    cudaError_t e;
+    ExtendParams p = {};
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.tables_out = tables_out;
+    p.lens_out = seq_lens_out;
+    p.refs_out = ref_counts_out;
+    p.info = info;
+    p.slots = slot_mapping;
+    p.tables = block_tables;
+    p.lens = seq_lens;
+    p.refs = ref_counts;
+    p.num_new = num_new;
+    p.told = static_cast<Told *>(workspace);
+    p.head = reinterpret_cast<int32_t *>(p.told + kCluster);
+    p.writers = p.head + 4;
+    p.latest = p.writers + num_blocks;
+    p.free_ids = p.latest + num_blocks;
+    p.row_len = p.free_ids + num_blocks;
+    p.row_new = p.row_len + num_seqs;
+    p.row_begin = p.row_new + num_seqs;
+    p.row_token = p.row_begin + num_seqs;
+    p.row_copy = p.row_token + num_seqs;
+    p.copy_rows = p.row_copy + num_seqs;
+    p.rows = num_seqs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.block_size = block_size;
+    p.len_cap = max_blocks_per_seq * block_size;
+    p.num_tokens = num_tokens;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_cluster(extend_rank_kernel, rank_ctas(num_seqs, num_blocks), s, p) != cudaSuccess)
+        return PA_ERR_CUDA;
+    // as many items as there can be: every row may copy its last block
+    const int64_t items = (int64_t)num_seqs * ((max_blocks_per_seq + kChunk - 1) / kChunk) +
+                          (num_tokens + kThreads - 1) / kThreads + (int64_t)num_seqs * ps.units;
+    e = launch_apply(extend_apply_kernel<kFewPools>, extend_apply_kernel<PA_MAX_POOLS>, p, ps,
+                     items, s);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_compact_blocks(int32_t *tables_out, int32_t *ref_counts_out, int32_t *new_ids,
+                            int32_t *info, const int32_t *block_tables, const int32_t *seq_lens,
+                            const int32_t *ref_counts, const pa_block_pool *pools, int num_pools,
+                            int num_seqs, int num_blocks, int max_blocks_per_seq, int block_size,
+                            void *workspace, size_t workspace_bytes, void *stream)
+{
+    pa_status st = check_sizes(num_seqs, num_blocks, max_blocks_per_seq, block_size);
+    if (st != PA_OK)
+        return st;
+    if (!info || !new_ids || !ref_counts || !ref_counts_out ||
+        (num_seqs > 0 && (!tables_out || !block_tables || !seq_lens)) || !aligned(tables_out, 4) ||
+        !aligned(ref_counts_out, 4) || !aligned(new_ids, 4) || !aligned(info, 4) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(ref_counts, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t wide = 4ll * num_seqs * max_blocks_per_seq, counts = 4ll * num_blocks;
+    if ((tables_out != block_tables && overlap(tables_out, wide, block_tables, wide)) ||
+        (ref_counts_out != ref_counts && overlap(ref_counts_out, counts, ref_counts, counts)) ||
+        overlap(new_ids, counts, ref_counts, counts) ||
+        overlap(new_ids, counts, ref_counts_out, counts))
+        return PA_ERR_INVALID_ARG;
+    Pools<PA_MAX_POOLS> ps;
+    st = read_pools(&ps, pools, num_pools, num_blocks);
+    if (st != PA_OK)
+        return st;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < pa_sequences_workspace_size(num_seqs, num_blocks))
+        return PA_ERR_WORKSPACE;
+    cudaError_t e;
+    CompactParams p = {};
+    p.err = device_error_word(&e);
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.tables_out = tables_out;
+    p.refs_out = ref_counts_out;
+    p.new_ids = new_ids;
+    p.info = info;
+    p.tables = block_tables;
+    p.lens = seq_lens;
+    p.refs = ref_counts;
+    p.told = static_cast<Told *>(workspace);
+    p.head = reinterpret_cast<int32_t *>(p.told + kCluster);
+    p.holes = p.head + 4;
+    p.movers = p.holes + num_blocks;
+    p.rows = num_seqs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.block_size = block_size;
+    p.len_cap = max_blocks_per_seq * block_size;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_cluster(compact_rank_kernel, rank_ctas(0, num_blocks), s, p) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const int64_t items = (int64_t)num_seqs * ((max_blocks_per_seq + kChunk - 1) / kChunk) +
+                          (int64_t)num_blocks * ps.units;
+    e = launch_apply(compact_apply_kernel<kFewPools>, compact_apply_kernel<PA_MAX_POOLS>, p, ps,
+                     items, s);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+} // extern "C"

@@ -1,0 +1,292 @@
+"""Linear attention with a decay for each head on the GPU, against the 64-bit
+recurrence of tests/_linear_ref.py."""
+import math
+
+import pytest
+import torch
+
+from tests._linear_ref import check_out, check_states, inputs, ref_linear
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    from __graft_entry__ import build_library
+    build_library()
+    import paged_kv_cache_136_gb300 as pa
+    pa.pa_device_errors(clear=True)
+    return pa
+
+
+def decode(pa, x, out=None, stream=None):
+    out = torch.full_like(x["q"], 7.0, memory_format=torch.contiguous_format) if out is None else out
+    return pa.pa_linear_decode(out, x["q"], x["k"], x["v"], x["log_decay"], x["states"], x["src"],
+                               x["dst"], x["scale"], stream=stream)
+
+
+def longest(x):
+    return int((x["starts"][1:] - x["starts"][:-1]).max()) if len(x["starts"]) > 1 else 0
+
+
+def workspace(pa, x, most=None):
+    n = pa.pa_linear_prefill_workspace_size(len(x["src"]), len(x["q"]),
+                                            longest(x) if most is None else most,
+                                            x["k"].shape[1], x["q"].shape[2])
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def prefill(pa, x, out=None, most=None, ws=None, stream=None):
+    out = torch.full_like(x["q"], 7.0, memory_format=torch.contiguous_format) if out is None else out
+    most = longest(x) if most is None else most
+    return pa.pa_linear_prefill(out, x["q"], x["k"], x["v"], x["log_decay"], x["states"], x["src"],
+                                x["dst"], x["starts"], x["scale"], most,
+                                workspace(pa, x, most) if ws is None else ws, stream=stream)
+
+
+def check(pa, x, run, flags=0):
+    ref, states, mag, smag = ref_linear(x["q"], x["k"], x["v"], x["log_decay"], x["states"],
+                                        x["src"], x["dst"], x["starts"], x["scale"])
+    before = x["states"].clone()
+    out = run(pa, x)
+    check_out(out, ref, mag)
+    check_states(x["states"], states, smag, out.dtype)
+    assert bool((out[torch.isnan(mag)] == 7.0).all()), "rows that are nobody's were written"
+    wrote = torch.zeros(len(before), dtype=torch.bool, device=before.device)
+    wrote[[int(i) for i in x["dst"] if 0 <= int(i) < len(before)]] = True
+    assert torch.equal(x["states"][~wrote], before[~wrote]), "states that are nobody's were written"
+    assert pa.pa_device_errors(clear=True) == flags
+    return out
+
+
+HEADS = [(4, 4), (8, 1), (12, 3), (10, 2), (5, 5), (16, 1)]
+
+
+@pytest.mark.parametrize("heads,kv_heads", HEADS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decode(pa, heads, kv_heads, d, dtype):
+    for b, decay, fused in ((1, "head", False), (5, "token", True), (37, "token", False)):
+        x = inputs([1] * b, heads, kv_heads, d, dtype, decay, seed=b, fresh=range(0, b, 3), fused=fused)
+        check(pa, x, decode)
+
+
+LENS = [[1], [100], [128], [129, 0, 1, 127, 2, 256, 0], [300, 5], [1, 1, 1], [700]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (6, 2), (8, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill(pa, lens, heads, kv_heads, d, dtype):
+    for decay, fused in (("head", False), ("token", True)):
+        x = inputs(lens, heads, kv_heads, d, dtype, decay, seed=len(lens), fresh=range(1, len(lens), 2),
+                   fused=fused, tail=3)
+        check(pa, x, prefill)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill_equals_decode_steps(pa, d, dtype):
+    """A prompt in one call, in two chunks, and token by token: the same states and
+    outputs within the bounds of one call each."""
+    n = 150
+    x = inputs([n], 4, 2, d, dtype, "token", seed=3)
+    ref, states, mag, smag = ref_linear(x["q"], x["k"], x["v"], x["log_decay"], x["states"],
+                                        x["src"], x["dst"], x["starts"], x["scale"])
+    out = torch.empty_like(x["q"])
+    cut = 70
+    for lo, hi in [(0, cut), (cut, n)]:
+        y = {**x, **{key: x[key][lo:hi] for key in ("q", "k", "v", "log_decay")}}
+        y["starts"] = torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda")
+        y["src"] = x["src"] if lo == 0 else x["dst"]
+        prefill(pa, y, out=out[lo:hi])
+    check_out(out, ref, mag)
+    check_states(x["states"], states, smag, out.dtype)
+    x = inputs([n], 4, 2, d, dtype, "token", seed=3)
+    out.zero_()
+    for i in range(n):
+        y = {**x, **{key: x[key][i:i + 1] for key in ("q", "k", "v", "log_decay")}}
+        y["src"] = x["src"] if i == 0 else x["dst"]
+        decode(pa, y, out=out[i:i + 1])
+    check_out(out, ref, mag)
+    check_states(x["states"], states, smag, out.dtype)
+
+
+@pytest.mark.parametrize("run", [decode, prefill])
+def test_padding_and_bad_ids(pa, run):
+    lens = [1] * 6 if run is decode else [130, 3, 140, 0, 9, 1]
+    x = inputs(lens, 4, 2, 64, "bf16", "token", seed=5)
+    x["dst"][1] = -1                       # a padding row
+    x["dst"][2] = -(1 << 31)
+    x["src"][4] = -(1 << 31)               # zeros
+    check(pa, x, run)
+    y = inputs(lens, 4, 2, 64, "bf16", "token", seed=6)
+    y["src"][0] = len(y["states"])         # read as zeros
+    y["dst"][5] = (1 << 31) - 1            # not written
+    check(pa, y, run, flags=pa.DEVERR_STATE)
+
+
+def test_in_place(pa):
+    """src and dst the same: a step of a running batch."""
+    for run, lens in ((decode, [1] * 4), (prefill, [129, 1, 0, 260])):
+        x = inputs(lens, 8, 2, 128, "fp16", "head", seed=8)
+        x["dst"] = x["src"].clone()
+        check(pa, x, run)
+
+
+@pytest.mark.parametrize("run", [decode, prefill])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decays_at_both_ends(pa, run, dtype):
+    """Decays of one (0), of zero (-inf and very negative), between ordinary ones."""
+    lens = [1] * 12 if run is decode else [5, 260, 131]
+    x = inputs(lens, 4, 4, 64, dtype, "token", seed=9)
+    g = x["log_decay"]
+    pick = torch.rand(g.shape, generator=torch.Generator().manual_seed(1)).cuda()
+    g[pick < 0.3] = 0.0
+    g[pick > 0.9] = -1e4
+    g[pick > 0.95] = -math.inf
+    g[pick > 0.98] = -90.0
+    check(pa, x, run)
+
+
+def test_prefill_of_long_memory(pa):
+    """Decays of exactly one: the state is a plain sum over all tokens."""
+    x = inputs([513], 2, 1, 128, "bf16", "head", seed=10)
+    x["log_decay"].zero_()
+    check(pa, x, prefill)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_not_finite_stays_where_it_belongs(pa, dtype):
+    """NaN and infinities of a token reach that token's row and later ones of its
+    sequence, nothing before it, no neighbour, and no rows behind the last."""
+    lens = [140, 200, 60]
+    for which, value in (("v", math.inf), ("v", math.nan), ("k", math.nan), ("q", math.nan),
+                         ("log_decay", math.nan)):
+        x = inputs(lens, 4, 2, 64, dtype, "token", seed=11, fresh=(0, 1, 2), tail=70)
+        for name in ("q", "k", "v", "log_decay"):
+            x[name][sum(lens):] = math.nan
+        clean = {**x, "states": x["states"].clone()}
+        good = prefill(pa, clean)
+        hit = 140 + 150                    # token 150 of sequence 1
+        if which == "log_decay":
+            x[which][hit, 1] = value
+        else:
+            x[which][hit, 1, 5] = value
+        out = prefill(pa, x)
+        rows = torch.ones(len(out), dtype=torch.bool, device="cuda")
+        rows[hit:340] = False
+        assert torch.equal(out[rows], good[rows]), which
+        later = out[hit:340]
+        if which == "q":                   # that row's head alone
+            assert bool(torch.isnan(out[hit, 1]).all())
+            later = later[1:]
+            assert torch.equal(later, good[hit + 1:340])
+            assert torch.equal(x["states"], clean["states"])
+            continue
+        # kv head 1 serves query heads 2 and 3; kv head 0 is untouched
+        assert torch.equal(later[:, :2], good[hit:340, :2]), which
+        if which == "v":                   # value channel 5 alone
+            assert not torch.isfinite(later[:, 2:, 5]).any()
+            keep = torch.arange(64, device="cuda") != 5
+            assert torch.equal(later[:, 2:][..., keep], good[hit:340, 2:][..., keep])
+        else:
+            assert torch.isnan(later[:, 2:]).all(), which
+        S, good_S = x["states"][int(x["dst"][1])], clean["states"][int(x["dst"][1])]
+        assert torch.equal(S[0], good_S[0])
+        hurt = ~torch.isfinite(S[1])
+        if which == "v":
+            assert bool(hurt[:, 5].all()) and int(hurt.sum()) == 64
+        elif which == "k":
+            assert bool(hurt[5].all()) and int(hurt.sum()) == 64
+        else:
+            assert bool(hurt.all())
+        pa.pa_device_errors(clear=True)
+
+
+def test_prefill_skips_bad_sequences(pa):
+    x = inputs([40, 30, 20], 2, 2, 64, "fp16", "head", seed=12)
+    want = {**x, "states": x["states"].clone()}
+    good = prefill(pa, want)
+    out = prefill(pa, x, most=35)          # sequence 0 is longer than max_query_len
+    assert torch.equal(out[40:], good[40:]) and bool((out[:40] == 7.0).all())
+    assert pa.pa_device_errors(clear=True) == pa.DEVERR_SEQ_LEN
+    x["starts"] = torch.tensor([0, 40, 30, 95], dtype=torch.int32, device="cuda")
+    prefill(pa, x, most=100)               # a negative length, and rows past the end
+    assert pa.pa_device_errors(clear=True) == pa.DEVERR_SEQ_LEN
+
+
+@pytest.mark.parametrize("scale", [1.0, 3e-4, 40.0])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_sizes_of_values(pa, dtype, scale):
+    """Loud and quiet keys and values: what leaves fp16's range on the way (scores,
+    states) must not leave it in the operands."""
+    for lens, run in (([200, 70], prefill), ([1] * 5, decode)):
+        x = inputs(lens, 4, 2, 128, dtype, "token", seed=13)
+        x["k"] *= scale
+        x["q"] *= scale
+        x["states"] *= scale
+        if scale > 1:
+            x["v"] *= 1e-3
+        check(pa, x, run)
+
+
+def test_capture_and_replay(pa):
+    """Both calls in one graph; lengths, ids and inputs change between replays."""
+    x = inputs([200, 56], 4, 2, 64, "bf16", "token", seed=14)
+    y = inputs([1] * 3, 4, 2, 64, "bf16", "token", seed=15)
+    out, dec = torch.full_like(x["q"], 7.0), torch.full_like(y["q"], 7.0)
+    ws = workspace(pa, x, 256)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        prefill(pa, x, out=out, most=256, ws=ws)
+        decode(pa, y, out=dec)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        prefill(pa, x, out=out, most=256, ws=ws)
+        decode(pa, y, out=dec)
+    for seed, lens in ((20, [1, 255]), (21, [130, 126])):
+        nx, ny = (inputs(a, 4, 2, 64, "bf16", "token", seed=seed) for a in (lens, [1] * 3))
+        for old, new in ((x, nx), (y, ny)):
+            for key in old:
+                if isinstance(old[key], torch.Tensor):
+                    old[key].copy_(new[key])
+        rx = ref_linear(*(x[k] for k in ("q", "k", "v", "log_decay", "states", "src", "dst",
+                                         "starts", "scale")))
+        ry = ref_linear(*(y[k] for k in ("q", "k", "v", "log_decay", "states", "src", "dst",
+                                         "starts", "scale")))
+        g.replay()
+        torch.cuda.synchronize()
+        check_out(out, rx[0], rx[2])
+        check_states(x["states"], rx[1], rx[3], out.dtype)
+        check_out(dec, ry[0], ry[2])
+        check_states(y["states"], ry[1], ry[3], out.dtype)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_repeatable_and_on_streams(pa):
+    """The same bits every time, on two streams at once with a workspace each."""
+    lens = [400, 31, 260]
+    xs = [inputs(lens, 8, 2, 128, "bf16", "token", seed=16) for _ in range(3)]
+    outs = [torch.full_like(x["q"], 7.0) for x in xs]
+    wss = [workspace(pa, x) for x in xs]
+    prefill(pa, xs[0], out=outs[0], ws=wss[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i, s in enumerate(streams):
+        prefill(pa, xs[i + 1], out=outs[i + 1], ws=wss[i + 1], stream=s)
+    torch.cuda.synchronize()
+    for i in (1, 2):
+        assert torch.equal(outs[i], outs[0]) and torch.equal(xs[i]["states"], xs[0]["states"])
+
+
+def test_no_sequences_and_no_tokens(pa):
+    x = inputs([0, 0], 2, 2, 64, "fp16", "head", seed=17, fresh=(1,))
+    check(pa, x, prefill)
+    y = inputs([], 2, 2, 64, "fp16", "head", seed=18, tail=4)
+    out = prefill(pa, y)
+    assert bool((out == 7.0).all())
