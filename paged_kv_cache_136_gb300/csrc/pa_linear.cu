@@ -11,6 +11,7 @@
 #include "pa_block.cuh"
 #include "pa_internal.h"
 #include "pa_linear.cuh"
+#include "pa_linear_tc.cuh"
 
 namespace pa {
 namespace lin {
@@ -181,6 +182,86 @@ static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_siz
                : launch_after_previous(linear_step_kernel<__half, 64, kPrompt>, grid, threads, 0, s, p);
 }
 
+// ---------------------------------------------------------------------------
+// Prompts on the tensor cores
+// ---------------------------------------------------------------------------
+constexpr int kSms = 152;
+// The longest prompt, in tokens, that the recurrent kernel takes.
+constexpr int kShort = 16;
+
+// How prompts are cut.  A sequence and kv head is a chain of chunks that one CTA
+// walks.  Where the longest chain takes more than twice an SM's share of all work,
+// sequences are cut into segments (four for each SM, no shorter than four chunks)
+// whose states a first pass forms, at the price of reading K and V twice.
+struct Cut {
+    int segment, lines;
+};
+
+static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_kv_heads)
+{
+    const int64_t share = (int64_t)num_tokens * num_kv_heads / kSms;
+    if (max_query_len <= std::max<int64_t>(2 * share, 8 * kChunk))
+        return {INT32_MAX, num_seqs};
+    const int64_t segment = std::max<int64_t>(4, (share / 4 + kChunk - 1) / kChunk) * kChunk;
+    return {(int)segment, (int)(num_tokens / segment) + num_seqs + 1};
+}
+
+static bool rows_map(CUtensorMap *map, const void *x, pa_dtype dtype, int num_tokens, int heads,
+                     int head_size, int64_t stride)
+{
+    cudaError_t err;
+    const auto fn = encode_fn(&err);
+    if (!fn)
+        return false;
+    // {head_size, heads, tokens}; a box is 64 elements of one head of 128 tokens
+    cuuint64_t dims[3] = {(cuuint64_t)head_size, (cuuint64_t)heads, (cuuint64_t)num_tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_size * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, kChunk}, step[3] = {1, 1, 1};
+    return fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              3, const_cast<void *>(x), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+template <typename T, int D, bool kParts>
+static cudaError_t launch_pass(const Maps &maps, const LinearParams &p, cudaStream_t s)
+{
+    const auto kern = linear_chunk_kernel<T, D, kParts>;
+    constexpr int kSmem = tc_smem_bytes<D>();
+    static unsigned long long done_mask = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
+    }
+    return launch_after_previous(kern, dim3(p.num_kv_heads, p.lines), dim3(kTcThreads), kSmem, s, maps.q,
+                                 maps.k, maps.v, p);
+}
+
+template <typename T, int D>
+static cudaError_t launch_chunks(const Maps &maps, const LinearParams &p, cudaStream_t s)
+{
+    if (p.segment != INT32_MAX) {
+        cudaError_t e = launch_pass<T, D, true>(maps, p, s);
+        if (e == cudaSuccess)
+            e = launch_after_previous(linear_join_kernel<D>, dim3(D * D / 1024, p.num_kv_heads, p.num_seqs),
+                                      dim3(256), 0, s, p);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_pass<T, D, false>(maps, p, s);
+}
+
 } // namespace lin
 } // namespace pa
 
@@ -217,7 +298,11 @@ size_t pa_linear_prefill_workspace_size(int num_seqs, int num_tokens, int max_qu
 {
     if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || num_kv_heads <= 0 || head_size <= 0)
         return 0;
-    return 256;
+    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    if (cut.segment == INT32_MAX)
+        return 256;
+    const size_t each = (size_t)num_kv_heads * 4 * ((size_t)head_size * head_size + 1);
+    return (each * (size_t)cut.lines + 255) / 256 * 256;
 }
 
 pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void *v,
@@ -249,7 +334,30 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
         return PA_ERR_CUDA;
     p.query_start_loc = query_start_loc;
     p.max_query_len = max_query_len;
-    e = launch_step<true>(p, num_seqs, head_size, dtype, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_tokens == 0 || max_query_len <= kShort) {
+        e = launch_step<true>(p, num_seqs, head_size, dtype, s);
+        return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
+    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    if (cut.lines > 65535)
+        return PA_ERR_UNSUPPORTED;
+    p.num_seqs = num_seqs;
+    p.segment = cut.segment;
+    p.lines = cut.lines;
+    p.parts = static_cast<float *>(workspace);
+    p.part_decay = p.parts + (int64_t)cut.lines * num_kv_heads * head_size * head_size;
+    Maps maps;
+    if (!rows_map(&maps.q, q, dtype, num_tokens, num_heads, head_size, q_stride) ||
+        !rows_map(&maps.k, k, dtype, num_tokens, num_kv_heads, head_size, k_stride) ||
+        !rows_map(&maps.v, v, dtype, num_tokens, num_kv_heads, head_size, v_stride))
+        return PA_ERR_CUDA;
+    if (head_size == 128)
+        e = dtype == PA_BF16 ? launch_chunks<__nv_bfloat16, 128>(maps, p, s)
+                             : launch_chunks<__half, 128>(maps, p, s);
+    else
+        e = dtype == PA_BF16 ? launch_chunks<__nv_bfloat16, 64>(maps, p, s)
+                             : launch_chunks<__half, 64>(maps, p, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -17,6 +17,10 @@ struct LinearParams {
     const int32_t *query_start_loc; // [num_seqs + 1]; not read by the decode step
     unsigned int *err;
     int64_t decay_stride, q_stride, k_stride, v_stride; // elements
+    // prompts of several segments: the lines of the grid (a segment each, at most),
+    // tokens of a segment, and each line's state [lines, Hkv, D, D] and decay
+    float *parts, *part_decay;
+    int lines, segment, num_seqs;
     int num_tokens, max_query_len, num_heads, num_kv_heads, num_states;
     float scale;
 };

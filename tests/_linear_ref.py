@@ -91,7 +91,7 @@ def inputs(lens, heads, kv_heads, d, dtype, decay="token", seed=0, fresh=(), dev
     n = 2 * b + spare
     deal = torch.randperm(n, generator=g).int()
     src, dst = deal[:b].clone(), deal[b:2 * b].clone()
-    for i in fresh:
+    for i in (i for i in fresh if i < b):
         src[i] = -1
     starts = torch.tensor([sum(lens[:i]) for i in range(b + 1)], dtype=torch.int32)
     return dict(q=q, k=k, v=v, log_decay=rate.float().to(device),

@@ -85,6 +85,50 @@ def test_prefill(pa, lens, heads, kv_heads, d, dtype):
         check(pa, x, prefill)
 
 
+@pytest.mark.parametrize("lens", [[3000], [513, 0, 1500, 1, 2049, 40], [1024, 1025, 1537]], ids=str)
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (6, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill_in_segments(pa, lens, heads, kv_heads, d, dtype):
+    """Few chains that are long: sequences are cut, their segments' states joined."""
+    assert pa.pa_linear_prefill_workspace_size(len(lens), sum(lens) + 3, max(lens), kv_heads, d) > 256
+    for decay, fresh in (("head", ()), ("token", (0, 2, 5))):
+        x = inputs(lens, heads, kv_heads, d, dtype, decay, seed=len(lens), fresh=fresh, tail=3)
+        if decay == "head" and len(lens) > 1:
+            x["dst"][-1] = -1
+        check(pa, x, prefill)
+
+
+def test_bad_metadata_in_segments(pa):
+    """Sequences that overlap or break their bounds are flagged or read twice; no call
+    reads or writes outside its tensors."""
+    for starts in ([0, 3000, 100, 4000], [0, 4000, 0, 4000, 0, 4000], [-5, 100, 2000, 9000],
+                   [0, 1 << 30, 100, 300]):
+        x = inputs([4000 // (len(starts) - 1)] * (len(starts) - 1), 2, 1, 64, "fp16", "token", seed=1,
+                   tail=4000 % (len(starts) - 1))
+        x["starts"] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        prefill(pa, x, most=4000)
+        assert pa.pa_device_errors(clear=True) == pa.DEVERR_SEQ_LEN
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_not_finite_in_segments(pa, dtype):
+    """A value that is not finite reaches the segments behind its own."""
+    x = inputs([2000], 2, 2, 64, dtype, "token", seed=2)
+    clean = {**x, "states": x["states"].clone()}
+    good = prefill(pa, clean)
+    x["v"][700, 1, 9] = math.nan
+    out = prefill(pa, x)
+    keep = torch.arange(64, device="cuda") != 9
+    assert torch.equal(out[:700], good[:700]) and torch.equal(out[:, 0], good[:, 0])
+    assert torch.equal(out[..., keep], good[..., keep])
+    assert bool(torch.isnan(out[700:, 1, 9]).all())
+    to = int(x["dst"][0])
+    assert bool(torch.isnan(x["states"][to, 1, :, 9]).all())
+    assert torch.equal(x["states"][to, 1][:, keep], clean["states"][to, 1][:, keep])
+    pa.pa_device_errors(clear=True)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_prefill_equals_decode_steps(pa, d, dtype):
