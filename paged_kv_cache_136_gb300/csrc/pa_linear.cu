@@ -224,14 +224,14 @@ static bool rows_map(CUtensorMap *map, const void *x, pa_dtype dtype, int num_to
 }
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 template <typename T, int D, bool kParts>
 static cudaError_t launch_pass(const Maps &maps, const LinearParams &p, cudaStream_t s)
 {
     const auto kern = linear_chunk_kernel<T, D, kParts>;
-    constexpr int kSmem = tc_smem_bytes<D>();
+    constexpr int kSmem = tc_smem_bytes<T, D>();
     static unsigned long long done_mask = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -242,10 +242,17 @@ static cudaError_t launch_pass(const Maps &maps, const LinearParams &p, cudaStre
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess)
             return e;
+        // the registers that the warpgroups trade have to be there at the launch
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kern);
+        if (e != cudaSuccess)
+            return e;
+        if (a.numRegs * (kTcThreads / 128) < 4 * kRegsMany + kRegsFew)
+            return cudaErrorInvalidConfiguration;
         __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
     }
     return launch_after_previous(kern, dim3(p.num_kv_heads, p.lines), dim3(kTcThreads), kSmem, s, maps.q,
-                                 maps.k, maps.v, p);
+                                 maps.k, maps.v, maps.out, p);
 }
 
 template <typename T, int D>
@@ -348,7 +355,9 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
     p.parts = static_cast<float *>(workspace);
     p.part_decay = p.parts + (int64_t)cut.lines * num_kv_heads * head_size * head_size;
     Maps maps;
-    if (!rows_map(&maps.q, q, dtype, num_tokens, num_heads, head_size, q_stride) ||
+    if (!rows_map(&maps.out, out, dtype, num_tokens, num_heads, head_size,
+                  (int64_t)num_heads * head_size) ||
+        !rows_map(&maps.q, q, dtype, num_tokens, num_heads, head_size, q_stride) ||
         !rows_map(&maps.k, k, dtype, num_tokens, num_kv_heads, head_size, k_stride) ||
         !rows_map(&maps.v, v, dtype, num_tokens, num_kv_heads, head_size, v_stride))
         return PA_ERR_CUDA;

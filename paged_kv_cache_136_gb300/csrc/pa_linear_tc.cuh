@@ -20,18 +20,23 @@
 // additions that round to nearest.
 //
 // A CTA walks one segment of one sequence for one kv head with all of its query
-// heads.  Roles in a CTA of 320 threads:
-//   warp 8 (producer)  a chunk's decay sums, and its tiles by TMA: K (2 slots), the
-//                      query heads' Q (2 slots), V (1 slot)
-//   warp 9 (MMA)       per query head: scores = Q K^T, O = Q S, O += P V; per chunk,
-//                      after the first head: delta = V'^T K
-//   warps 0-3          one row of the chunk per thread: P from the scores, O scaled
-//                      by e^(b_i) between its two products, the output
-//   warps 4-7          one value channel per thread: V' from the V tile, and the
-//                      state's column (head_size floats in registers), which goes to
-//                      shared memory as the operand of the next chunk's Q S
-// Tensor memory: scores, then P over them, in columns 0-127; O at 128; delta at 256;
-// V' at 384 (high parts, then remainders at 448).
+// heads.  Roles in a CTA of 640 threads:
+//   warps 0-7    a row of the chunk and half of its columns per thread: P from the
+//                scores, O scaled by e^(b_i) between its two products, the output
+//                tile over the query tile that made it
+//   warps 8-15   a value channel and half of the key channels (and tokens) per thread:
+//                V' from the V tile, and the state (in registers), which goes to
+//                shared memory as the operand of the next chunk's Q S
+//   warp 16      a chunk's decay sums, and its tiles by TMA: K (2 slots), the query
+//                heads' Q (2 slots), V (1 slot)
+//   warp 17      the MMAs: per query head O = Q S, O += P V, the next head's scores;
+//                per chunk, after the first head's P V, delta = V'^T K
+//   warp 18      output tiles to global memory by TMA
+// Two threads share a row or a channel because one warp a scheduler is not enough to
+// hide the latency of tensor memory and of fetching a role's instructions; the loops
+// over blocks are rolled for the latter's sake.
+// Tensor memory: the scores in columns 0-127, in each block of 32 columns P over them
+// (16 columns of high parts, 16 of remainders); O at 128; delta at 256; V' behind.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,15 +53,24 @@ namespace lin {
 
 constexpr int kChunk = 128;        // tokens
 constexpr int kBlock = 32;         // tokens whose decays are summed as one
-constexpr int kTcThreads = 320;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kTcThreads = 640;
+constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18;
+// Five warpgroups are launched with 96 registers a thread; the last one, whose warps
+// issue copies and MMAs, hands some to the others: 4 * 112 + 32 = 5 * 96.
+constexpr int kRegsFew = 32, kRegsMany = 112;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 128, kTmemDelta = 256, kTmemV = 384;
+constexpr uint32_t kTmemO = 128, kTmemDelta = 256;
 constexpr int kRegion = kChunk * 128; // 128 token rows of 64 elements
 
-template <int D>
+template <typename T, int D>
 struct Geo {
+    // V' enters V'^T K in three parts with bf16, 2^-24 of its size: with two the states
+    // would be off by 2.6e-6 (measured), with fp16's longer parts two reach 2^-22.
+    static constexpr int kSplit = std::is_same<T, __half>::value ? 2 : 3;
+    // Three parts of 128 tokens leave 64 columns for delta: with head_size 128 it is
+    // formed for one half of the key channels, then for the other.
+    static constexpr bool kTwice = kSplit == 3 && D == 128;
+    static constexpr uint32_t kTmemV = kTmemCols - kSplit * (kChunk / 2);
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kRegion;      // a Q, K or V tile
     static constexpr int kStateRegion = D * 128;         // 64 key channels of all value channels
@@ -66,7 +80,7 @@ struct Geo {
 };
 
 // A chunk's decays, in log2 units where they are sums.
-struct Decays {
+struct alignas(16) Decays { // read four floats at a time
     float upto[kChunk];   // sum from the block's first token up to this one
     float rest[kChunk];   // 2^(sum behind this one to the block's end)
     float block[4];       // the blocks' sums
@@ -75,23 +89,26 @@ struct Decays {
 struct Misc {
     uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full, v_empty;
     uint64_t dec_full[2], dec_empty[2];
-    uint64_t s_full, p_full, o1_full, o_full, o_free;
-    uint64_t v1_full, d_full, st_full, qs_done, drain;
+    uint64_t s_full, p_full, o1_full, o_full, o_free, o_staged;
+    uint64_t v1_full, d_full, d_free, d2_full, st_full, qs_done, drain;
+    uint64_t hurt[2];        // a byte for each warp of channels: whether it met what is not finite
     Decays dec[2];
     float state_scale[2];    // what the state's operand was divided by
-    float warp_max[4];
     uint32_t tmem_base;
-    int unit[4];
-    uint8_t poison[2][128];  // by value channel: the chunk's first token that is not finite, or 128
+    int unit[3];
+    uint8_t first[2][128];   // by value channel: the chunk's first token whose value is not
+                             // finite, or 128
+    uint8_t exponent[2][128]; // fp16: largest exponent of a half of the tokens, by channel
+    float warp_max[2][8];
 };
 
-template <int D> constexpr int tc_smem_bytes()
+template <typename T, int D> constexpr int tc_smem_bytes()
 {
     // at least half of an SM's: two CTAs would wait for each other's tensor memory
-    return Geo<D>::kOffMisc + (int)sizeof(Misc) > 120 * 1024 ? Geo<D>::kOffMisc + (int)sizeof(Misc)
-                                                             : 120 * 1024;
+    constexpr int n = Geo<T, D>::kOffMisc + (int)sizeof(Misc);
+    return n > 120 * 1024 ? n : 120 * 1024;
 }
-static_assert(tc_smem_bytes<128>() <= 232448, "shared memory of an SM");
+static_assert(tc_smem_bytes<__half, 128>() <= 232448, "shared memory of an SM");
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
@@ -199,15 +216,20 @@ template <typename T, int D, bool kParts>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap k_map,
-                        const __grid_constant__ CUtensorMap v_map, const LinearParams p)
+                        const __grid_constant__ CUtensorMap v_map,
+                        const __grid_constant__ CUtensorMap out_map, const LinearParams p)
 {
-    using Gm = Geo<D>;
+    using Gm = Geo<T, D>;
     constexpr int TB = Gm::kTile;
+    constexpr int kSplit = Gm::kSplit;
+    constexpr bool kTwice = Gm::kTwice;
     constexpr bool kHalf = std::is_same<T, __half>::value;
+    constexpr int H = D / 2; // channels of a thread that has half of them
     constexpr uint32_t kFmt = kHalf ? 0u : 1u;
     constexpr uint32_t kIdescScores = idesc_f16_f32(kFmt, 0, 0, kChunk, kChunk);
-    constexpr uint32_t kIdescState = idesc_f16_f32(kFmt, 0, 0, kChunk, D); // Q S
-    constexpr uint32_t kIdescValue = idesc_f16_f32(kFmt, 0, 1, 128, D);    // P V, V'^T K
+    constexpr uint32_t kIdescState = idesc_f16_f32(kFmt, 0, 0, kChunk, D);             // Q S
+    constexpr uint32_t kIdescValue = idesc_f16_f32(kFmt, 0, 1, kChunk, D);             // P V
+    constexpr uint32_t kIdescDelta = idesc_f16_f32(kFmt, 0, 1, 128, kTwice ? D / 2 : D); // V'^T K
 
     extern __shared__ __align__(1024) uint8_t smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + Gm::kOffMisc);
@@ -230,25 +252,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0)
             m->unit[0] = s, m->unit[1] = j, m->unit[2] = n;
     }
-    if (tid == 0) {
+    if (tid == 32) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->k_full[i], 1);
             mbar_init(&m->k_empty[i], 1);
             mbar_init(&m->q_full[i], 1);
             mbar_init(&m->q_empty[i], 1);
             mbar_init(&m->dec_full[i], 1);
-            mbar_init(&m->dec_empty[i], kParts ? 4 : 8);
+            mbar_init(&m->dec_empty[i], kParts ? 8 : 16);
         }
         mbar_init(&m->v_full, 1);
         mbar_init(&m->v_empty, 1);
         mbar_init(&m->s_full, 1);
-        mbar_init(&m->p_full, 4);
+        mbar_init(&m->p_full, 8);
         mbar_init(&m->o1_full, 1);
         mbar_init(&m->o_full, 1);
-        mbar_init(&m->o_free, 4);
-        mbar_init(&m->v1_full, 4);
+        mbar_init(&m->o_free, 8);
+        mbar_init(&m->o_staged, 8);
+        mbar_init(&m->v1_full, 8);
         mbar_init(&m->d_full, 1);
-        mbar_init(&m->st_full, 4);
+        mbar_init(&m->d_free, 4);
+        mbar_init(&m->d2_full, 1);
+        mbar_init(&m->st_full, 8);
         mbar_init(&m->qs_done, 1);
         mbar_init(&m->drain, 1);
         fence_barrier_init();
@@ -262,6 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int len = min(q1 - t0, p.segment), n = (len + kChunk - 1) / kChunk;
     const int src = p.src_states[s], dst = p.dst_states[s];
     const int per = p.num_heads / p.num_kv_heads;
+    const int total = kParts ? n : n * per; // (chunk, query head) pairs
     if (tid == 0 && head == 0 && !kParts && (src >= p.num_states || dst >= p.num_states))
         atomicOr(p.err, PA_DEVERR_STATE_);
     if (warp == kMmaWarp) {
@@ -273,154 +299,171 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = m->tmem_base;
 
-    if (warp == kProducerWarp) {
-        // ================================================================ producer
-        if (lane == 0) {
-            prefetch_tensormap(&k_map);
-            prefetch_tensormap(&v_map);
-            if (!kParts)
-                prefetch_tensormap(&q_map);
-        }
-        auto load = [&](int off, const CUtensorMap *map, uint64_t *bar, int h, int t) {
-            mbar_arrive_expect_tx(bar, (uint32_t)TB);
-#pragma unroll
-            for (int hf = 0; hf < Gm::kHalves; ++hf)
-                tma_load_3d(smem + off + hf * kRegion, map, bar, hf * 64, h, t);
-        };
-        const float *const log_decay = p.log_decay + head;
-        // this lane's four tokens of chunk c, in log2 units; below 2^-128 is 0, and
-        // a difference of two such sums stays a number
-        auto read_decays = [&](int c, float (&g)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = c * kChunk + lane * 4 + i;
-                float x = 0.f;
-                if (t < len)
-                    x = log_decay[(int64_t)(t0 + t) * p.decay_stride] * 1.4426950408889634f;
-                g[i] = x < -128.f ? -128.f : x;
+    if (warp >= kProducerWarp) {
+        registers_down<kRegsFew>();
+        if (warp == kProducerWarp) {
+            // ============================================================ producer
+            if (lane == 0) {
+                prefetch_tensormap(&k_map);
+                prefetch_tensormap(&v_map);
+                if (!kParts)
+                    prefetch_tensormap(&q_map);
             }
-        };
-        float g[4];
-        bool ok = true;
-        int loaded_k = 0, loaded_q = 0, loaded_v = 0;
-        if (n > 0)
-            read_decays(0, g);
-        for (int c = 0, it = 0; ok && c < n; ++c) {
-            const int b = c & 1, t = t0 + c * kChunk;
-            const uint32_t again = (uint32_t)((c >> 1) - 1) & 1;
-            if (c >= 2 && !warp_wait(&m->k_empty[b], again, lane)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0)
-                load(Gm::kOffK + b * TB, &k_map, &m->k_full[b], head, t);
-            ++loaded_k;
-            if (c >= 2 && !warp_wait(&m->dec_empty[b], again, lane)) {
-                ok = false;
-                break;
-            }
-            Decays &d = m->dec[b];
-            float upto[4], rest[4], total;
-            upto[0] = g[0];
+            auto load = [&](int off, const CUtensorMap *map, uint64_t *bar, int h, int t) {
+                mbar_arrive_expect_tx(bar, (uint32_t)TB);
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
-                upto[i] = upto[i - 1] + g[i];
-            rest[3] = 0.f;
-#pragma unroll
-            for (int i = 2; i >= 0; --i)
-                rest[i] = rest[i + 1] + g[i + 1];
-            total = upto[3];
-            float up = total, down = total; // over the 8 lanes of a block
-#pragma unroll
-            for (int o = 1; o < 8; o *= 2) {
-                const float a = __shfl_up_sync(~0u, up, o, 8), z = __shfl_down_sync(~0u, down, o, 8);
-                if ((lane & 7) >= o)
-                    up += a;
-                if ((lane & 7) + o < 8)
-                    down += z;
-            }
-            float before = __shfl_up_sync(~0u, up, 1, 8), behind = __shfl_down_sync(~0u, down, 1, 8);
-            before = lane & 7 ? before : 0.f;
-            behind = (lane & 7) < 7 ? behind : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d.upto[lane * 4 + i] = before + upto[i];
-                d.rest[lane * 4 + i] = exp2f(behind + rest[i]);
-            }
-            if ((lane & 7) == 7)
-                d.block[lane >> 3] = up;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&m->dec_full[b]);
-            if (c + 1 < n)
-                read_decays(c + 1, g);
-            for (int h = 0; h < (kParts ? 1 : per); ++h, ++it) {
-                if (!kParts) {
-                    if (it >= 2 && !warp_wait(&m->q_empty[it & 1], (uint32_t)((it >> 1) - 1) & 1, lane)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0)
-                        load(Gm::kOffQ + (it & 1) * TB, &q_map, &m->q_full[it & 1], head * per + h, t);
-                    ++loaded_q;
-                }
-                if (h == 0) {
-                    if (c >= 1 && !warp_wait(&m->v_empty, (uint32_t)(c - 1) & 1, lane)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0)
-                        load(Gm::kOffV, &v_map, &m->v_full, head, t);
-                    ++loaded_v;
-                }
-            }
-        }
-        if (!ok && lane == 0) {
-            // Given up: no tile may land in a later CTA's memory, so the last load on
-            // each barrier is awaited, within the waits' own limit.
-            atomicOr(p.err, PA_DEVERR_TIMEOUT_);
-            auto settle = [](uint64_t *bar, int loads) {
-                if (loads > 0)
-                    mbar_wait(bar, (uint32_t)(loads - 1) & 1);
+                for (int hf = 0; hf < Gm::kHalves; ++hf)
+                    tma_load_3d(smem + off + hf * kRegion, map, bar, hf * 64, h, t);
             };
-            for (int b = 0; b < 2; ++b) {
-                settle(&m->k_full[b], (loaded_k + 1 - b) >> 1);
-                settle(&m->q_full[b], (loaded_q + 1 - b) >> 1);
-            }
-            settle(&m->v_full, loaded_v);
-        }
-    } else if (warp == kMmaWarp) {
-        // ============================================================== MMA issuer
-        const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), 16, 1024);
-        const uint64_t kt_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), kRegion, 1024);
-        const uint64_t q_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffQ), 16, 1024);
-        const uint64_t v_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffV), kRegion, 1024);
-        const uint64_t s_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffS), 16, 1024);
-        auto slot = [](int b) { return (uint64_t)((uint32_t)(b * TB) >> 4); };
-        bool ok = true;
-        int it = 0;
-        for (int c = 0; ok && c < n; ++c) {
-            const int kb = c & 1;
-            if (!(ok = warp_wait(&m->k_full[kb], (uint32_t)(c >> 1) & 1, lane)))
-                break;
-            for (int h = 0; h < (kParts ? 1 : per); ++h, ++it) {
-                const int qb = it & 1;
-                const uint64_t qd = q_desc + slot(qb);
-                if (!kParts) {
-                    // scores, over the P that the last product has read
-                    if (!(ok = warp_wait(&m->q_full[qb], (uint32_t)(it >> 1) & 1, lane)))
-                        break;
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint64_t kd = k_desc + slot(kb);
+            const float *const log_decay = p.log_decay + head;
+            // this lane's four tokens of chunk c, in log2 units; below 2^-128 is 0, and
+            // a difference of two such sums stays a number
+            auto read_decays = [&](int c, float (&g)[4]) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t o = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                            umma_f16(tmem, qd + o, kd + o, kIdescScores, kk > 0 ? 1u : 0u);
+                for (int i = 0; i < 4; ++i) {
+                    const int t = c * kChunk + lane * 4 + i;
+                    float x = 0.f;
+                    if (t < len)
+                        x = log_decay[(int64_t)(t0 + t) * p.decay_stride] * 1.4426950408889634f;
+                    g[i] = x < -128.f ? -128.f : x;
+                }
+            };
+            float g[4];
+            bool ok = true;
+            int loaded_k = 0, loaded_q = 0, loaded_v = 0;
+            if (n > 0)
+                read_decays(0, g);
+            for (int c = 0, it = 0; ok && c < n; ++c) {
+                const int b = c & 1, t = t0 + c * kChunk;
+                const uint32_t again = (uint32_t)((c >> 1) - 1) & 1;
+                if (c >= 2 && !warp_wait(&m->k_empty[b], again, lane)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0)
+                    load(Gm::kOffK + b * TB, &k_map, &m->k_full[b], head, t);
+                ++loaded_k;
+                if (c >= 2 && !warp_wait(&m->dec_empty[b], again, lane)) {
+                    ok = false;
+                    break;
+                }
+                Decays &d = m->dec[b];
+                float upto[4], rest[4];
+                upto[0] = g[0];
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    upto[i] = upto[i - 1] + g[i];
+                rest[3] = 0.f;
+#pragma unroll
+                for (int i = 2; i >= 0; --i)
+                    rest[i] = rest[i + 1] + g[i + 1];
+                float up = upto[3], down = upto[3]; // over the 8 lanes of a block
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2) {
+                    const float a = __shfl_up_sync(~0u, up, o, 8);
+                    const float z = __shfl_down_sync(~0u, down, o, 8);
+                    if ((lane & 7) >= o)
+                        up += a;
+                    if ((lane & 7) + o < 8)
+                        down += z;
+                }
+                float before = __shfl_up_sync(~0u, up, 1, 8), behind = __shfl_down_sync(~0u, down, 1, 8);
+                before = lane & 7 ? before : 0.f;
+                behind = (lane & 7) < 7 ? behind : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    d.upto[lane * 4 + i] = before + upto[i];
+                    d.rest[lane * 4 + i] = exp2f(behind + rest[i]);
+                }
+                if ((lane & 7) == 7)
+                    d.block[lane >> 3] = up;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&m->dec_full[b]);
+                if (c + 1 < n)
+                    read_decays(c + 1, g);
+                for (int h = 0; h < (kParts ? 1 : per); ++h, ++it) {
+                    if (!kParts) {
+                        if (it >= 2 &&
+                            !warp_wait(&m->q_empty[it & 1], (uint32_t)((it >> 1) - 1) & 1, lane)) {
+                            ok = false;
+                            break;
                         }
-                        umma_commit(&m->s_full);
+                        if (lane == 0)
+                            load(Gm::kOffQ + (it & 1) * TB, &q_map, &m->q_full[it & 1], head * per + h, t);
+                        ++loaded_q;
                     }
-                    __syncwarp();
+                    if (h == 0) {
+                        if (c >= 1 && !warp_wait(&m->v_empty, (uint32_t)(c - 1) & 1, lane)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0)
+                            load(Gm::kOffV, &v_map, &m->v_full, head, t);
+                        ++loaded_v;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                // Given up: no tile may land in a later CTA's memory, so the last load on
+                // each barrier is awaited, within the waits' own limit.
+                atomicOr(p.err, PA_DEVERR_TIMEOUT_);
+                auto settle = [](uint64_t *bar, int loads) {
+                    if (loads > 0)
+                        mbar_wait(bar, (uint32_t)(loads - 1) & 1);
+                };
+                for (int b = 0; b < 2; ++b) {
+                    settle(&m->k_full[b], (loaded_k + 1 - b) >> 1);
+                    settle(&m->q_full[b], (loaded_q + 1 - b) >> 1);
+                }
+                settle(&m->v_full, loaded_v);
+            }
+        } else if (warp == kMmaWarp) {
+            // ========================================================== MMA issuer
+            const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), 16, 1024);
+            const uint64_t kt_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), kRegion, 1024);
+            const uint64_t q_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffQ), 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffV), kRegion, 1024);
+            const uint64_t s_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffS), 16, 1024);
+            auto slot = [](int b) { return (uint64_t)((uint32_t)(b * TB) >> 4); };
+            // the scores of pair `it`, over the P that the last product has read
+            auto scores = [&](int it, int c, bool first) {
+                if (first && !warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1, lane))
+                    return false;
+                if (!warp_wait(&m->q_full[it & 1], (uint32_t)(it >> 1) & 1, lane))
+                    return false;
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    const uint64_t qd = q_desc + slot(it & 1), kd = k_desc + slot(c & 1);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
+                        umma_f16(tmem, qd + o, kd + o, kIdescScores, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&m->s_full);
+                }
+                __syncwarp();
+                return true;
+            };
+            // delta = V'^T K, for key channels from 64 `half` on where it is formed in two
+            auto delta = [&](int c, int half, uint64_t *bar) {
+                const uint64_t kd = kt_desc + slot(c & 1) + (uint64_t)((half * kRegion) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kChunk / 16; ++kk)
+#pragma unroll
+                    for (int part = 0; part < kSplit; ++part)
+                        umma_f16_tmem_a(tmem + kTmemDelta,
+                                        tmem + Gm::kTmemV + (uint32_t)(part * 64 + kk * 8),
+                                        kd + (uint64_t)((kk * 2048) >> 4), kIdescDelta,
+                                        kk + part > 0 ? 1u : 0u);
+                umma_commit(bar);
+            };
+            bool ok = n == 0 || kParts || scores(0, 0, true);
+            for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
+                const bool last = kParts || h == per - 1;
+                if (kParts) {
+                    ok = warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1, lane);
+                } else {
                     // O = Q S, both parts
                     if (h == 0)
                         ok = warp_wait(&m->st_full, (uint32_t)c & 1, lane);
@@ -430,6 +473,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         break;
                     tc_fence_after_sync();
                     if (lane == 0) {
+                        const uint64_t qd = q_desc + slot(it & 1);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t o = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
@@ -440,12 +484,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      kIdescState, 1u);
                         }
                         umma_commit(&m->o1_full);
-                        umma_commit(&m->q_empty[qb]);
-                        if (h == per - 1)
+                        if (last)
                             umma_commit(&m->qs_done);
                     }
                     __syncwarp();
-                    // O += P V
                     ok = warp_wait(&m->p_full, (uint32_t)it & 1, lane);
                 }
                 if (ok && h == 0)
@@ -454,106 +496,158 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 tc_fence_after_sync();
                 if (lane == 0) {
-                    if (!kParts) {
+                    if (!kParts) { // O += P V, both parts
 #pragma unroll
                         for (int kk = 0; kk < kChunk / 16; ++kk) {
                             const uint64_t vd = v_desc + (uint64_t)((kk * 2048) >> 4);
-                            umma_f16_tmem_a(tmem + kTmemO, tmem + (uint32_t)(kk * 8), vd, kIdescValue, 1u);
-                            umma_f16_tmem_a(tmem + kTmemO, tmem + (uint32_t)(64 + kk * 8), vd,
-                                            kIdescValue, 1u);
+                            const uint32_t pa = tmem + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8);
+                            umma_f16_tmem_a(tmem + kTmemO, pa, vd, kIdescValue, 1u);
+                            umma_f16_tmem_a(tmem + kTmemO, pa + 16, vd, kIdescValue, 1u);
                         }
                         umma_commit(&m->o_full);
+                        if (last)
+                            umma_commit(&m->v_empty);
                     }
-                    if (h == 0) { // delta = V'^T K
-                        const uint64_t kd = kt_desc + slot(kb);
-#pragma unroll
-                        for (int kk = 0; kk < kChunk / 16; ++kk) {
-                            const uint64_t o = (uint64_t)((kk * 2048) >> 4);
-                            umma_f16_tmem_a(tmem + kTmemDelta, tmem + kTmemV + (uint32_t)(kk * 8), kd + o,
-                                            kIdescValue, kk > 0 ? 1u : 0u);
-                            umma_f16_tmem_a(tmem + kTmemDelta, tmem + kTmemV + (uint32_t)(64 + kk * 8),
-                                            kd + o, kIdescValue, 1u);
-                        }
-                        umma_commit(&m->d_full);
-                    }
-                    if (kParts || h == per - 1) {
-                        umma_commit(&m->v_empty);
-                        umma_commit(&m->k_empty[kb]);
-                    }
+                    if (h == 0)
+                        delta(c, 0, &m->d_full);
                 }
                 __syncwarp();
+                const int next = last ? c + 1 : c;
+                if (!kParts && it + 1 < total)
+                    ok = scores(it + 1, next, last);
+                if (kTwice && h == 0 && ok) {
+                    ok = warp_wait(&m->d_free, (uint32_t)c & 1, lane);
+                    tc_fence_after_sync();
+                    if (ok && lane == 0)
+                        delta(c, 1, &m->d2_full);
+                    __syncwarp();
+                }
+                if (lane == 0 && last) {
+                    if (kParts)
+                        umma_commit(&m->v_empty);
+                    umma_commit(&m->k_empty[c & 1]);
+                }
+                __syncwarp();
+                c = next;
+                h = last ? 0 : h + 1;
+            }
+            if (!ok && lane == 0)
+                atomicOr(p.err, PA_DEVERR_TIMEOUT_);
+            if (lane == 0)
+                umma_commit(&m->drain);
+            warp_wait(&m->drain, 0, lane);
+        } else if (warp == kStoreWarp && !kParts) {
+            // ============================================================== outputs
+            bool ok = true;
+            for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
+                if (!(ok = warp_wait(&m->o_staged, (uint32_t)it & 1, lane)))
+                    break;
+                if (lane == 0) {
+                    if (len - c * kChunk >= kChunk) { // a tail's rows were written one by one
+#pragma unroll
+                        for (int hf = 0; hf < Gm::kHalves; ++hf)
+                            tma_store_3d(&out_map, smem + Gm::kOffQ + (it & 1) * TB + hf * kRegion,
+                                         hf * 64, head * per + h, t0 + c * kChunk);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                    mbar_arrive(&m->q_empty[it & 1]);
+                }
+                __syncwarp();
+                if (++h == per)
+                    h = 0, ++c;
+            }
+            if (lane == 0) {
+                bulk_wait();
+                if (!ok)
+                    atomicOr(p.err, PA_DEVERR_TIMEOUT_);
             }
         }
-        if (!ok && lane == 0)
-            atomicOr(p.err, PA_DEVERR_TIMEOUT_);
-        if (lane == 0)
-            umma_commit(&m->drain);
-        warp_wait(&m->drain, 0, lane);
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ===================================================== rows: P and outputs
-        const int row = tid, blk = warp;
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t s_addr = tmem + lane_base, o_addr = tmem + lane_base + kTmemO;
+        registers_up<kRegsMany>();
+        const int row = tid & 127, blk = warp & 3, half = warp >> 2;
+        const uint32_t lane_base = (uint32_t)(blk * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base;
+        const uint32_t o_addr = tmem + lane_base + kTmemO + (uint32_t)(half * H);
+        // this thread's column blocks: 0 and 3, or 1 and 2, which is as even as the
+        // triangle allows
+        const int block[2] = {half, 3 - half};
         bool ok = true;
-        int it = 0;
-        for (int c = 0; ok && !kParts && c < n; ++c) {
+        float upto = 0.f, inter = 0.f, f[2] = {0.f, 0.f};
+        // With fp16 the two warps of a row block meet at a barrier once a round: one that
+        // has given up goes on to the next one, where both leave.
+        for (int it = 0; !kParts && it < total; ++it) {
+            const int c = it / per, h = it - c * per;
             const Decays &d = m->dec[c & 1];
             const int live = min(kChunk, len - c * kChunk);
-            float upto = 0.f, inter = 0.f, f[3] = {0.f, 0.f, 0.f};
-            for (int h = 0; h < per; ++h, ++it) {
-                if (h == 0) {
-                    if (!(ok = warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1, lane)))
-                        break;
-                    // 2^(decays from the end of column block J to this row), J = blk - 1 - k
-                    upto = d.upto[row];
-                    float sum = upto;
+            if (h == 0)
+                ok = ok && warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1, lane);
+            if (h == 0 && ok) {
+                // decays from the end of a column block to this row, and from the
+                // chunk's beginning
+                upto = d.upto[row];
+                float sum = upto;
+                f[0] = f[1] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        if (k < blk) {
-                            f[k] = exp2f(sum) * p.scale;
-                            sum += d.block[blk - 1 - k];
-                        }
-                    inter = exp2f(sum) * p.scale; // from the chunk's beginning
+                for (int k = 3; k >= 0; --k)
+                    if (k < blk) {
+                        if (k == block[0])
+                            f[0] = exp2f(sum) * p.scale;
+                        if (k == block[1])
+                            f[1] = exp2f(sum) * p.scale;
+                        sum += d.block[k];
+                    }
+                inter = exp2f(sum) * p.scale;
+            }
+            ok = ok && warp_wait(&m->s_full, (uint32_t)it & 1, lane);
+            tc_fence_after_sync();
+            float down = 1.f, up = 1.f; // 2^-E, 2^E
+            if constexpr (kHalf) {
+                float most = 0.f; // of the whole row, by both of its threads
+#pragma unroll 1
+                for (int b = 0; ok && b <= blk; ++b) {
+                    uint32_t sv[32];
+                    tmem_ld32_nowait(s_addr + (uint32_t)(b * 32), sv);
+                    tmem_wait_ld();
+                    const int end = b < blk ? 31 : lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        most = fmaxf(most, i <= end ? fabsf(__uint_as_float(sv[i])) : 0.f);
                 }
-                if (!(ok = warp_wait(&m->s_full, (uint32_t)it & 1, lane)))
-                    break;
-                tc_fence_after_sync();
-                uint32_t sv[kChunk];
+                const int e = range_exponent(most * fabsf(p.scale));
+                down = power_of_two(-e);
+                up = power_of_two(e);
+                // P goes over the scores: both threads have seen all of them
+                ok = !bar_sync_or(2 + blk, 64, !ok);
+            }
+            if (!ok)
+                break;
+#pragma unroll 1
+            for (int z = 0; z < 2; ++z) {
+                const int b = z ? 3 - half : half;
+                const uint32_t at = s_addr + (uint32_t)(b * 32);
+                uint32_t hi[16], lo[16];
+                if (b > blk) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (b <= blk)
-                        tmem_ld32_nowait(s_addr + (uint32_t)(b * 32),
-                                         *reinterpret_cast<uint32_t(*)[32]>(sv + b * 32));
-                tmem_wait_ld();
-                float down = 1.f, up = 1.f; // 2^-E, 2^E
-                if constexpr (kHalf) {
-                    float most = 0.f;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (b <= blk)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (b < blk || i <= lane)
-                                    most = fmaxf(most, fabsf(__uint_as_float(sv[b * 32 + i])));
-                    const int e = range_exponent(most * fabsf(p.scale));
-                    down = power_of_two(-e);
-                    up = power_of_two(e);
-                }
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t hi[16], lo[16];
+                    for (int i = 0; i < 16; ++i)
+                        hi[i] = lo[i] = 0;
+                } else {
+                    uint32_t sv[32];
+                    tmem_ld32_nowait(at, sv);
+                    tmem_wait_ld();
                     if (b < blk) {
-                        const float fb = (b == blk - 1 ? f[0] : b == blk - 2 ? f[1] : f[2]) * down;
+                        const float fb = (z ? f[1] : f[0]) * down;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 r = *reinterpret_cast<const float4 *>(&d.rest[b * 32 + i * 4]);
-                            const uint32_t *const x = sv + b * 32 + i * 4;
+                            const uint32_t *const x = sv + i * 4;
                             split2<T>(__uint_as_float(x[0]) * (r.x * fb), __uint_as_float(x[1]) * (r.y * fb),
                                       hi[2 * i], lo[2 * i]);
                             split2<T>(__uint_as_float(x[2]) * (r.z * fb), __uint_as_float(x[3]) * (r.w * fb),
                                       hi[2 * i + 1], lo[2 * i + 1]);
                         }
-                    } else if (b == blk) {
+                    } else {
                         const float fb = p.scale * down;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -562,139 +656,150 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             float x[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                x[k] = i * 4 + k <= lane ? __uint_as_float(sv[b * 32 + i * 4 + k]) *
-                                                               (ex2(upto - l[k]) * fb)
-                                                         : 0.f;
+                                x[k] = i * 4 + k <= lane
+                                           ? __uint_as_float(sv[i * 4 + k]) * (ex2(upto - l[k]) * fb)
+                                           : 0.f;
                             split2<T>(x[0], x[1], hi[2 * i], lo[2 * i]);
                             split2<T>(x[2], x[3], hi[2 * i + 1], lo[2 * i + 1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            hi[i] = lo[i] = 0;
                     }
-                    // over the scores, which are all in registers
-                    tmem_st16(s_addr + (uint32_t)(b * 16), hi);
-                    tmem_st16(s_addr + (uint32_t)(64 + b * 16), lo);
                 }
-                if (h == 0) {
-                    // both before p_full lets their next phases begin
-                    ok = warp_wait(&m->st_full, (uint32_t)c & 1, lane) &&
-                         warp_wait(&m->v1_full, (uint32_t)c & 1, lane);
-                    if (ok && kHalf)
-                        inter *= m->state_scale[c & 1];
-                }
-                ok = ok && warp_wait(&m->o1_full, (uint32_t)it & 1, lane);
-                if (!ok)
-                    break;
-                tc_fence_after_sync();
-                const float of = inter * down;
+                tmem_st16(at, hi);
+                tmem_st16(at + 16, lo);
+            }
+            if (h == 0) {
+                // both before p_full lets their next phases begin
+                ok = warp_wait(&m->st_full, (uint32_t)c & 1, lane) &&
+                     warp_wait(&m->v1_full, (uint32_t)c & 1, lane);
+                if (ok && kHalf)
+                    inter *= m->state_scale[c & 1];
+            }
+            ok = ok && warp_wait(&m->o1_full, (uint32_t)it & 1, lane);
+            if (!ok)
+                continue;
+            tc_fence_after_sync();
+            const float of = inter * down;
+#pragma unroll 1
+            for (int b = 0; b < H / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld32_nowait(o_addr + (uint32_t)(b * 32), o);
+                tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(o_addr + (uint32_t)(b * 32), o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * of);
-                    tmem_st32(o_addr + (uint32_t)(b * 32), o);
-                }
-                tmem_wait_st();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&m->p_full);
-                if (!(ok = warp_wait(&m->o_full, (uint32_t)it & 1, lane)))
-                    break;
-                tc_fence_after_sync();
-                T *const out = static_cast<T *>(p.out) +
-                               ((int64_t)(t0 + c * kChunk + row) * p.num_heads + head * per + h) * D;
-                uint32_t w[D / 2];
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(o_addr + (uint32_t)(b * 32), o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[b * 16 + i] = pack2<T>(__uint_as_float(o[2 * i]) * up,
-                                                 __uint_as_float(o[2 * i + 1]) * up);
-                }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&m->o_free);
-                if (row < live) {
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i)
-                        reinterpret_cast<uint4 *>(out)[i] =
-                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int i = 0; i < 32; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * of);
+                tmem_st32(o_addr + (uint32_t)(b * 32), o);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&m->p_full);
+            if (!(ok = warp_wait(&m->o_full, (uint32_t)it & 1, lane)))
+                continue;
+            tc_fence_after_sync();
+            const bool hurt = m->hurt[c & 1] != 0;
+            uint8_t *const tile = smem + Gm::kOffQ + (it & 1) * TB + (half * H / 64) * kRegion + row * 128;
+            T *const out = static_cast<T *>(p.out) + half * H +
+                           ((int64_t)(t0 + c * kChunk + row) * p.num_heads + head * per + h) * D;
+#pragma unroll 1
+            for (int b = 0; b < H / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld32_nowait(o_addr + (uint32_t)(b * 32), o);
+                tmem_wait_ld();
+                if (hurt) {
                     // A value that is not finite was taken out of the product, where it
                     // would have reached the rows before it as 0 * NaN.
-                    const uint32_t *const hurt = reinterpret_cast<const uint32_t *>(m->poison[c & 1]);
-                    for (int i = 0; i < D / 4; ++i) {
-                        const uint32_t x = hurt[i];
-                        if (x != 0x80808080u)
-                            for (int k = 0; k < 4; ++k)
-                                if ((int)(x >> 8 * k & 255) <= row)
-                                    out[4 * i + k] = (T)__uint_as_float(0x7FFFFFFFu);
-                    }
+                    const uint8_t *const first = &m->first[c & 1][half * H + b * 32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (first[i] <= row)
+                            o[i] = 0x7FFFFFFFu;
                 }
-                if (h == per - 1) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&m->dec_empty[c & 1]);
+                uint4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t *const x = o + i * 8;
+                    w[i] = make_uint4(
+                        pack2<T>(__uint_as_float(x[0]) * up, __uint_as_float(x[1]) * up),
+                        pack2<T>(__uint_as_float(x[2]) * up, __uint_as_float(x[3]) * up),
+                        pack2<T>(__uint_as_float(x[4]) * up, __uint_as_float(x[5]) * up),
+                        pack2<T>(__uint_as_float(x[6]) * up, __uint_as_float(x[7]) * up));
                 }
+                if (live == kChunk) {
+                    const int piece = (half * H % 64) / 8 + b * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(tile + ((piece + i) ^ (row & 7)) * 16) = w[i];
+                } else if (row < live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4 *>(out)[b * 4 + i] = w[i];
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&m->o_free);
+                mbar_arrive(&m->o_staged);
+                if (h == per - 1)
+                    mbar_arrive(&m->dec_empty[c & 1]);
             }
         }
         if (!ok && lane == 0)
             atomicOr(p.err, PA_DEVERR_TIMEOUT_);
     } else {
         // ================================================= value channels: the state
-        const int wg = warp & 3, ch = tid & 127; // value channel, and token row in a tail
+        registers_up<kRegsMany>();
+        const int wg = warp & 3, ch = tid & 127, half = (warp - 8) >> 2;
         const uint32_t lane_base = (uint32_t)(wg * 32) << 16;
         const bool mine = ch < D;
-        const int64_t one = (int64_t)D * D;
-        float S[D];
+        const int64_t one = (int64_t)D * D, at0 = (int64_t)half * H * D + ch;
+        float S[H]; // key channels from half * H on
         {
             const float *from = nullptr;
             if (j > 0 && !kParts)
-                from = p.parts + ((int64_t)(y - 1) * p.num_kv_heads + head) * one;
+                from = p.parts + ((int64_t)(y - 1) * p.num_kv_heads + head) * one + at0;
             else if (j == 0 && src >= 0 && src < p.num_states)
-                from = p.states + ((int64_t)src * p.num_kv_heads + head) * one;
+                from = p.states + ((int64_t)src * p.num_kv_heads + head) * one + at0;
 #pragma unroll
-            for (int k = 0; k < D; ++k)
-                S[k] = mine && from ? from[(int64_t)k * D + ch] : 0.f;
+            for (int k = 0; k < H; ++k)
+                S[k] = mine && from ? from[(int64_t)k * D] : 0.f;
         }
         // The state as the operand of Q S: row = value channel, 64 key channels a
-        // region, 16-byte pieces in the 128-byte swizzle.
-        auto put_state = [&](int c) {
+        // region, 16-byte pieces in the 128-byte swizzle.  False where a thread of the
+        // group has given up.
+        auto put_state = [&](int c, bool ok) {
             float down = 1.f;
             if constexpr (kHalf) {
                 float most = 0.f;
 #pragma unroll
-                for (int k = 0; k < D; ++k)
+                for (int k = 0; k < H; ++k)
                     most = fmaxf(most, fabsf(S[k]) < INFINITY ? fabsf(S[k]) : 0.f);
                 const unsigned top = __reduce_max_sync(~0u, __float_as_uint(most));
                 if (lane == 0)
-                    m->warp_max[wg] = __uint_as_float(top);
-                bar_sync(1, 128);
-                most = fmaxf(fmaxf(m->warp_max[0], m->warp_max[1]), fmaxf(m->warp_max[2], m->warp_max[3]));
-                bar_sync(1, 128);
+                    m->warp_max[c & 1][warp - 8] = __uint_as_float(top);
+                if (bar_sync_or(1, 256, !ok))
+                    return false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    most = fmaxf(most, m->warp_max[c & 1][i]);
                 const int e = range_exponent(most);
                 down = power_of_two(-e);
-                if (ch == 0)
+                if (tid == 256)
                     m->state_scale[c & 1] = power_of_two(e);
+            } else if (!ok) {
+                return false;
             }
             if (mine) {
-                uint8_t *const at = smem + Gm::kOffS + ch * 128;
+                uint8_t *const at = smem + Gm::kOffS + ch * 128 + (half * H / 64) * Gm::kStateRegion;
 #pragma unroll
-                for (int k = 0; k < D; k += 8) {
+                for (int k = 0; k < H; k += 8) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         split2<T>(S[k + 2 * i] * down, S[k + 2 * i + 1] * down, hi[i], lo[i]);
-                    const int off = (k / 64) * Gm::kStateRegion + (((k % 64) / 8) ^ (ch & 7)) * 16;
+                    const int off = (((half * H % 64) / 8 + k / 8) ^ (ch & 7)) * 16;
                     *reinterpret_cast<uint4 *>(at + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(at + Gm::kState + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -703,106 +808,131 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&m->st_full);
+            return true;
         };
         if (!kParts && n > 0)
-            put_state(0);
+            put_state(0, true);
         float decay_log2 = 0.f; // of the whole segment
-        bool ok = true; // of this warp, until the next barrier
+        bool ok = true;         // of this warp, until the next barrier
         for (int c = 0; c < n; ++c) {
             const int b = c & 1, live = min(kChunk, len - c * kChunk);
             const Decays &d = m->dec[b];
             ok = ok && warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1, lane) &&
                  warp_wait(&m->v_full, (uint32_t)c & 1, lane);
-            if (ok && live < kChunk)
-                ok = warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1, lane);
-            // every thread of the group leaves or none does: barriers follow
-            ok = !bar_sync_or(1, 128, !ok);
-            if (!ok)
-                break;
             if (live < kChunk) {
-                // the tile's rows behind the sequence are a neighbour's: zeros
-                if (ch >= live)
+                // the tiles' rows behind the sequence are a neighbour's: zeros
+                ok = ok && warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1, lane);
+                if (ok && ch >= live && half < Gm::kHalves)
 #pragma unroll
-                    for (int hf = 0; hf < Gm::kHalves; ++hf)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int off = hf * kRegion + ch * 128 + i * 16;
-                            *reinterpret_cast<uint4 *>(smem + Gm::kOffV + off) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(smem + Gm::kOffK + b * TB + off) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                bar_sync(1, 128);
+                    for (int i = 0; i < 8; ++i) {
+                        const int off = half * kRegion + ch * 128 + i * 16;
+                        *reinterpret_cast<uint4 *>(smem + Gm::kOffV + off) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(smem + Gm::kOffK + b * TB + off) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                bar_sync(1, 256);
             }
-            // 2^(decays behind each block of 32, to the chunk's end)
-            float behind[4];
-            float sum = 0.f;
+            // 2^(decays behind the blocks of 32 to the chunk's end), of this half's two
+            float behind[2], sum = 0.f;
 #pragma unroll
             for (int k = 3; k >= 0; --k) {
-                behind[k] = exp2f(sum);
+                if (k >> 1 == half)
+                    behind[k & 1] = exp2f(sum);
                 sum += d.block[k];
             }
             const float decay = exp2f(sum);
             decay_log2 += sum;
-            // V': this channel of all tokens, decayed to the chunk's end
-            float back = 1.f;
-            bool hurt = false;
-            if (mine) {
-                const uint8_t *const col = smem + Gm::kOffV + (ch / 64) * kRegion + (ch % 8) * 2;
-                const int piece = (ch % 64) / 8;
-                auto value = [&](int t) {
-                    return value_of<T>(*reinterpret_cast<const uint16_t *>(
-                        col + t * 128 + ((piece ^ (t & 7)) * 16)));
-                };
-                float scale = 1.f;
-                if constexpr (kHalf) {
+            // V': this channel of this half's tokens, decayed to the chunk's end
+            float back = 1.f, scale = 1.f;
+            uint8_t *const col = smem + Gm::kOffV + (ch / 64) * kRegion + (ch % 8) * 2 + half * 64 * 128;
+            const int piece = (ch % 64) / 8;
+            auto value_at = [&](int t) { // t-th token of this half
+                return reinterpret_cast<uint16_t *>(col + t * 128 + ((piece ^ (t & 7)) * 16));
+            };
+            if constexpr (kHalf) {
+                if (mine) {
                     float most = 0.f;
-#pragma unroll 32
-                    for (int t = 0; t < kChunk; ++t)
-                        most = fmaxf(most, fabsf(value(t)));
-                    const int e = range_exponent(most < INFINITY ? most : 65504.f);
+#pragma unroll 1
+                    for (int t = 0; t < 64; t += 16)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            most = fmaxf(most, fabsf(value_of<T>(*value_at(t + i))));
+                    m->exponent[half][ch] =
+                        (uint8_t)(__float_as_uint(most < INFINITY ? most : 65504.f) >> 23);
+                }
+                bar_sync(2 + 4 + wg, 64);
+                if (mine) {
+                    const int e = max((int)max(m->exponent[0][ch], m->exponent[1][ch]) - 127 - 13, -40);
                     scale = power_of_two(-e);
                     back = power_of_two(e);
                 }
-                auto put = [&]() {
-                    float odd = 0.f; // NaN once a value is not finite
+            }
+            auto put_values = [&]() { // true if one is not finite
+                float odd = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const float f = (k < 2 ? behind[0] : behind[1]) * scale;
+                    uint32_t part[3][8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float f = behind[k] * scale;
-                        uint32_t hi[16], lo[16];
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 r = *reinterpret_cast<const float4 *>(
+                            &d.rest[half * 64 + k * 16 + i * 4]);
+                        const float w[4] = {r.x * f, r.y * f, r.z * f, r.w * f};
+                        float x[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 r = *reinterpret_cast<const float4 *>(&d.rest[k * 32 + i * 4]);
-                            float x[4];
+                        for (int z = 0; z < 4; ++z) {
+                            const float v = value_of<T>(*value_at(k * 16 + i * 4 + z));
+                            odd = fmaf(v, 0.f, odd);
+                            x[z] = v * w[z];
+                        }
 #pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                x[z] = value(k * 32 + i * 4 + z);
-                                odd = fmaf(x[z], 0.f, odd);
+                        for (int z = 0; z < 2; ++z) {
+                            float a = x[2 * z], e = x[2 * z + 1];
+#pragma unroll
+                            for (int q = 0; q < kSplit; ++q) {
+                                part[q][2 * i + z] = pack2<T>(a, e);
+                                const float2 u = unpack2<T>(part[q][2 * i + z]);
+                                a -= u.x, e -= u.y;
                             }
-                            split2<T>(x[0] * (r.x * f), x[1] * (r.y * f), hi[2 * i], lo[2 * i]);
-                            split2<T>(x[2] * (r.z * f), x[3] * (r.w * f), hi[2 * i + 1], lo[2 * i + 1]);
-                        }
-                        tmem_st16(tmem + lane_base + kTmemV + (uint32_t)(k * 16), hi);
-                        tmem_st16(tmem + lane_base + kTmemV + (uint32_t)(64 + k * 16), lo);
-                    }
-                    return odd;
-                };
-                const float odd = put();
-                hurt = odd != 0.f; // NaN compares unequal
-                int first = 128;
-                if (hurt) {
-                    for (int t = kChunk - 1; t >= 0; --t) {
-                        uint16_t *const at = reinterpret_cast<uint16_t *>(
-                            const_cast<uint8_t *>(col) + t * 128 + ((piece ^ (t & 7)) * 16));
-                        if (!(fabsf(value_of<T>(*at)) < INFINITY)) {
-                            first = t;
-                            *at = 0;
                         }
                     }
+#pragma unroll
+                    for (int q = 0; q < kSplit; ++q)
+                        tmem_st8(tmem + lane_base + Gm::kTmemV +
+                                     (uint32_t)(q * 64 + half * 32 + k * 8), part[q]);
                 }
-                if (__any_sync(~0u, hurt))
-                    put();
-                m->poison[b][ch] = (uint8_t)first;
+                return odd != 0.f; // NaN compares unequal
+            };
+            bool hurt = false;
+            int first = 128;
+            if (ok && mine) {
+                hurt = put_values();
+                if (hurt)
+                    for (int t = 63; t >= 0; --t)
+                        if (!(fabsf(value_of<T>(*value_at(t))) < INFINITY)) {
+                            first = half * 64 + t;
+                            *value_at(t) = 0;
+                        }
+                if (half == 0)
+                    m->first[b][ch] = (uint8_t)first;
+                const bool any = __any_sync(~0u, hurt);
+                if (any)
+                    put_values();
+                if (lane == 0)
+                    reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = any;
                 tmem_wait_st();
+            } else if (lane == 0) {
+                reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = 0;
+            }
+            // every thread of the group goes on or none does
+            ok = !bar_sync_or(1, 256, !ok);
+            if (!ok)
+                break;
+            if (m->hurt[b] != 0) { // the first of both halves, for both
+                if (half == 1 && first < 128 && m->first[b][ch] == 128)
+                    m->first[b][ch] = (uint8_t)first;
+                bar_sync(1, 256);
+                hurt = mine && m->first[b][ch] < 128;
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
@@ -811,13 +941,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_arrive(&m->dec_empty[b]);
                 mbar_arrive(&m->v1_full);
             }
-            ok = warp_wait(&m->d_full, (uint32_t)c & 1, lane);
+            ok = warp_wait(kTwice && half == 1 ? &m->d2_full : &m->d_full, (uint32_t)c & 1, lane);
             tc_fence_after_sync();
             if (ok && mine) {
+                const uint32_t from = tmem + lane_base + kTmemDelta + (uint32_t)(kTwice ? 0 : half * H);
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
+                for (int k = 0; k < H / 32; ++k) {
                     uint32_t x[32];
-                    tmem_ld32_nowait(tmem + lane_base + kTmemDelta + (uint32_t)(k * 32), x);
+                    tmem_ld32_nowait(from + (uint32_t)(k * 32), x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -825,16 +956,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (hurt)
 #pragma unroll
-                    for (int k = 0; k < D; ++k)
+                    for (int k = 0; k < H; ++k)
                         S[k] = __uint_as_float(0x7FFFFFFFu);
             }
             tc_fence_before_sync();
+            if (kTwice && half == 0) {
+                __syncwarp();
+                if (ok && lane == 0)
+                    mbar_arrive(&m->d_free);
+            }
             if (!kParts && c + 1 < n) {
                 ok = ok && warp_wait(&m->qs_done, (uint32_t)c & 1, lane);
-                ok = !bar_sync_or(1, 128, !ok);
-                if (!ok)
+                ok = put_state(c + 1, ok);
+                if (kHalf && !ok) // of the whole group then
                     break;
-                put_state(c + 1);
             }
         }
         if (!ok && lane == 0)
@@ -842,14 +977,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (ok && mine) {
             float *to = nullptr;
             if (kParts)
-                to = p.parts + ((int64_t)y * p.num_kv_heads + head) * one;
+                to = p.parts + ((int64_t)y * p.num_kv_heads + head) * one + at0;
             else if (j == nseg - 1 && dst < p.num_states)
-                to = p.states + ((int64_t)dst * p.num_kv_heads + head) * one;
+                to = p.states + ((int64_t)dst * p.num_kv_heads + head) * one + at0;
             if (to)
 #pragma unroll
-                for (int k = 0; k < D; ++k)
-                    to[(int64_t)k * D + ch] = S[k];
-            if (kParts && ch == 0)
+                for (int k = 0; k < H; ++k)
+                    to[(int64_t)k * D] = S[k];
+            if (kParts && tid == 256)
                 p.part_decay[(int64_t)y * p.num_kv_heads + head] = exp2f(decay_log2);
         }
     }
