@@ -140,13 +140,20 @@ template <> __device__ __forceinline__ float value_of<__nv_bfloat16>(uint16_t u)
     return __uint_as_float((uint32_t)u << 16);
 }
 
-// Two values as a 16-bit part and the rounded remainder.
-template <typename T>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+// Two values as N 16-bit parts, each the rounded remainder of those before it.
+template <typename T, int N>
+__device__ __forceinline__ void split(float2 x, uint32_t (&part)[N])
 {
-    hi = pack2<T>(a, b);
-    const float2 h = unpack2<T>(hi);
-    lo = pack2<T>(a - h.x, b - h.y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        part[i] = pack2<T>(x.x, x.y);
+        if (i + 1 < N)
+            x = __ffma2_rn(unpack2<T>(part[i]), make_float2(-1.f, -1.f), x);
+    }
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t *x)
+{
+    return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
 }
 
 // Exponent E that brings magnitudes up to m below 2^14 (or up to there): m 2^-E.
@@ -433,12 +440,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!warp_wait(&m->q_full[it & 1], (uint32_t)(it >> 1) & 1, lane))
                     return false;
                 tc_fence_after_sync();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t qd = q_desc + slot(it & 1), kd = k_desc + slot(c & 1);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t o = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                        umma_f16(tmem, qd + o, kd + o, kIdescScores, kk > 0 ? 1u : 0u);
+#pragma unroll 1
+                    for (uint32_t kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
+                        umma_f16(tmem, qd + o, kd + o, kIdescScores, kk);
                     }
                     umma_commit(&m->s_full);
                 }
@@ -448,14 +455,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // delta = V'^T K, for key channels from 64 `half` on where it is formed in two
             auto delta = [&](int c, int half, uint64_t *bar) {
                 const uint64_t kd = kt_desc + slot(c & 1) + (uint64_t)((half * kRegion) >> 4);
+#pragma unroll 1
+                for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < kChunk / 16; ++kk)
-#pragma unroll
-                    for (int part = 0; part < kSplit; ++part)
-                        umma_f16_tmem_a(tmem + kTmemDelta,
-                                        tmem + Gm::kTmemV + (uint32_t)(part * 64 + kk * 8),
-                                        kd + (uint64_t)((kk * 2048) >> 4), kIdescDelta,
-                                        kk + part > 0 ? 1u : 0u);
+                    for (uint32_t part = 0; part < kSplit; ++part)
+                        umma_f16_tmem_a(tmem + kTmemDelta, tmem + Gm::kTmemV + part * 64 + kk * 8,
+                                        kd + kk * (2048 >> 4), kIdescDelta, kk + part);
                 umma_commit(bar);
             };
             bool ok = n == 0 || kParts || scores(0, 0, true);
@@ -472,14 +477,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!ok)
                         break;
                     tc_fence_after_sync();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint64_t qd = q_desc + slot(it & 1);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t o = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                            const uint64_t so =
-                                (uint64_t)(((kk >> 2) * Gm::kStateRegion + (kk & 3) * 32) >> 4);
-                            umma_f16(tmem + kTmemO, qd + o, s_desc + so, kIdescState, kk > 0 ? 1u : 0u);
+#pragma unroll 1
+                        for (uint32_t kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t o = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
+                            const uint64_t so = ((kk >> 2) * Gm::kStateRegion + (kk & 3) * 32) >> 4;
+                            umma_f16(tmem + kTmemO, qd + o, s_desc + so, kIdescState, kk);
                             umma_f16(tmem + kTmemO, qd + o, s_desc + (Gm::kState >> 4) + so,
                                      kIdescState, 1u);
                         }
@@ -488,19 +492,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             umma_commit(&m->qs_done);
                     }
                     __syncwarp();
-                    ok = warp_wait(&m->p_full, (uint32_t)it & 1, lane);
                 }
-                if (ok && h == 0)
+                // delta before P V: the next chunk's state is being made meanwhile
+                if (ok && h == 0) {
                     ok = warp_wait(&m->v1_full, (uint32_t)c & 1, lane);
-                if (!ok)
-                    break;
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    if (!kParts) { // O += P V, both parts
-#pragma unroll
-                        for (int kk = 0; kk < kChunk / 16; ++kk) {
-                            const uint64_t vd = v_desc + (uint64_t)((kk * 2048) >> 4);
-                            const uint32_t pa = tmem + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8);
+                    tc_fence_after_sync();
+                    if (ok && elect_one())
+                        delta(c, 0, &m->d_full);
+                    __syncwarp();
+                }
+                if (!kParts) {
+                    ok = ok && warp_wait(&m->p_full, (uint32_t)it & 1, lane);
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    if (elect_one()) { // O += P V, both parts
+#pragma unroll 1
+                        for (uint32_t kk = 0; kk < kChunk / 16; ++kk) {
+                            const uint64_t vd = v_desc + kk * (2048 >> 4);
+                            const uint32_t pa = tmem + (kk >> 1) * 32 + (kk & 1) * 8;
                             umma_f16_tmem_a(tmem + kTmemO, pa, vd, kIdescValue, 1u);
                             umma_f16_tmem_a(tmem + kTmemO, pa + 16, vd, kIdescValue, 1u);
                         }
@@ -508,21 +518,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (last)
                             umma_commit(&m->v_empty);
                     }
-                    if (h == 0)
-                        delta(c, 0, &m->d_full);
+                    __syncwarp();
                 }
-                __syncwarp();
-                const int next = last ? c + 1 : c;
-                if (!kParts && it + 1 < total)
-                    ok = scores(it + 1, next, last);
                 if (kTwice && h == 0 && ok) {
                     ok = warp_wait(&m->d_free, (uint32_t)c & 1, lane);
                     tc_fence_after_sync();
-                    if (ok && lane == 0)
+                    if (ok && elect_one())
                         delta(c, 1, &m->d2_full);
                     __syncwarp();
                 }
-                if (lane == 0 && last) {
+                const int next = last ? c + 1 : c;
+                if (!kParts && ok && it + 1 < total)
+                    ok = scores(it + 1, next, last);
+                if (last && elect_one()) {
                     if (kParts)
                         umma_commit(&m->v_empty);
                     umma_commit(&m->k_empty[c & 1]);
@@ -533,8 +541,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok && lane == 0)
                 atomicOr(p.err, PA_DEVERR_TIMEOUT_);
-            if (lane == 0)
+            if (elect_one())
                 umma_commit(&m->drain);
+            __syncwarp();
             warp_wait(&m->drain, 0, lane);
         } else if (warp == kStoreWarp && !kParts) {
             // ============================================================== outputs
@@ -628,6 +637,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int b = z ? 3 - half : half;
                 const uint32_t at = s_addr + (uint32_t)(b * 32);
                 uint32_t hi[16], lo[16];
+                auto put = [&](int i, float2 x) {
+                    uint32_t part[2];
+                    split<T, 2>(x, part);
+                    hi[i] = part[0], lo[i] = part[1];
+                };
                 if (b > blk) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -638,29 +652,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_wait_ld();
                     if (b < blk) {
                         const float fb = (z ? f[1] : f[0]) * down;
+                        const float2 fb2 = make_float2(fb, fb);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 r = *reinterpret_cast<const float4 *>(&d.rest[b * 32 + i * 4]);
-                            const uint32_t *const x = sv + i * 4;
-                            split2<T>(__uint_as_float(x[0]) * (r.x * fb), __uint_as_float(x[1]) * (r.y * fb),
-                                      hi[2 * i], lo[2 * i]);
-                            split2<T>(__uint_as_float(x[2]) * (r.z * fb), __uint_as_float(x[3]) * (r.w * fb),
-                                      hi[2 * i + 1], lo[2 * i + 1]);
+                            put(2 * i, __fmul2_rn(pair_of(sv + i * 4), __fmul2_rn(make_float2(r.x, r.y), fb2)));
+                            put(2 * i + 1, __fmul2_rn(pair_of(sv + i * 4 + 2),
+                                                      __fmul2_rn(make_float2(r.z, r.w), fb2)));
                         }
                     } else {
-                        const float fb = p.scale * down;
+                        const float2 fb2 = make_float2(p.scale * down, p.scale * down);
+                        const float2 up2 = make_float2(upto, upto), less = make_float2(-1.f, -1.f);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 u = *reinterpret_cast<const float4 *>(&d.upto[b * 32 + i * 4]);
-                            const float l[4] = {u.x, u.y, u.z, u.w};
-                            float x[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                x[k] = i * 4 + k <= lane
-                                           ? __uint_as_float(sv[i * 4 + k]) * (ex2(upto - l[k]) * fb)
-                                           : 0.f;
-                            split2<T>(x[0], x[1], hi[2 * i], lo[2 * i]);
-                            split2<T>(x[2], x[3], hi[2 * i + 1], lo[2 * i + 1]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 l = __ffma2_rn(
+                                *reinterpret_cast<const float2 *>(&d.upto[b * 32 + i * 2]), less, up2);
+                            const float2 x = __fmul2_rn(
+                                pair_of(sv + i * 2), __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), fb2));
+                            put(i, make_float2(2 * i <= lane ? x.x : 0.f, 2 * i < lane ? x.y : 0.f));
                         }
                     }
                 }
@@ -678,15 +687,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok)
                 continue;
             tc_fence_after_sync();
-            const float of = inter * down;
+            const float2 of = make_float2(inter * down, inter * down);
 #pragma unroll 1
             for (int b = 0; b < H / 32; ++b) {
                 uint32_t o[32];
                 tmem_ld32_nowait(o_addr + (uint32_t)(b * 32), o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) * of);
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = __fmul2_rn(pair_of(o + i), of);
+                    o[i] = __float_as_uint(x.x), o[i + 1] = __float_as_uint(x.y);
+                }
                 tmem_st32(o_addr + (uint32_t)(b * 32), o);
             }
             tmem_wait_st();
@@ -715,25 +726,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (first[i] <= row)
                             o[i] = 0x7FFFFFFFu;
                 }
-                uint4 w[4];
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t *const x = o + i * 8;
-                    w[i] = make_uint4(
-                        pack2<T>(__uint_as_float(x[0]) * up, __uint_as_float(x[1]) * up),
-                        pack2<T>(__uint_as_float(x[2]) * up, __uint_as_float(x[3]) * up),
-                        pack2<T>(__uint_as_float(x[4]) * up, __uint_as_float(x[5]) * up),
-                        pack2<T>(__uint_as_float(x[6]) * up, __uint_as_float(x[7]) * up));
+                for (int i = 0; i < 16; ++i) {
+                    float2 x = pair_of(o + 2 * i);
+                    if constexpr (kHalf)
+                        x = __fmul2_rn(x, make_float2(up, up));
+                    w[i] = pack2<T>(x.x, x.y);
                 }
                 if (live == kChunk) {
                     const int piece = (half * H % 64) / 8 + b * 4;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(tile + ((piece + i) ^ (row & 7)) * 16) = w[i];
+                        *reinterpret_cast<uint4 *>(tile + ((piece + i) ^ (row & 7)) * 16) =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 } else if (row < live) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        reinterpret_cast<uint4 *>(out)[b * 4 + i] = w[i];
+                        reinterpret_cast<uint4 *>(out)[b * 4 + i] =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 }
             }
             fence_proxy_async_smem();
@@ -797,8 +808,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int k = 0; k < H; k += 8) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        split2<T>(S[k + 2 * i] * down, S[k + 2 * i + 1] * down, hi[i], lo[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        float2 x = make_float2(S[k + 2 * i], S[k + 2 * i + 1]);
+                        if constexpr (kHalf)
+                            x = __fmul2_rn(x, make_float2(down, down));
+                        uint32_t part[2];
+                        split<T, 2>(x, part);
+                        hi[i] = part[0], lo[i] = part[1];
+                    }
                     const int off = (((half * H % 64) / 8 + k / 8) ^ (ch & 7)) * 16;
                     *reinterpret_cast<uint4 *>(at + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(at + Gm::kState + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -842,82 +859,107 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const float decay = exp2f(sum);
             decay_log2 += sum;
-            // V': this channel of this half's tokens, decayed to the chunk's end
-            float back = 1.f, scale = 1.f;
-            uint8_t *const col = smem + Gm::kOffV + (ch / 64) * kRegion + (ch % 8) * 2 + half * 64 * 128;
-            const int piece = (ch % 64) / 8;
-            auto value_at = [&](int t) { // t-th token of this half
-                return reinterpret_cast<uint16_t *>(col + t * 128 + ((piece ^ (t & 7)) * 16));
+            // V': this warp's 32 channels of this half's tokens, decayed to the chunk's end.
+            // Transposed 8x8 matrices give a lane two tokens of a channel, as the operand
+            // in tensor memory wants them: 4 channels a lane, and a fourth of their tokens.
+            float back = 1.f;
+            const uint32_t tile = smem_addr(smem + Gm::kOffV + (wg / 2) * kRegion);
+            auto load_v = [&](uint32_t (&x)[4], int k, int g) { // 16 tokens from 16 k, 16 channels
+                const int t = half * 64 + k * 16 + (lane >> 4) * 8 + (lane & 7);
+                const int piece = (wg & 1) * 4 + g * 2 + (lane >> 3 & 1);
+                ldmatrix_x4_trans(x, tile + (uint32_t)(t * 128 + ((piece ^ (lane & 7)) * 16)));
             };
+            uint8_t *const col = smem + Gm::kOffV + (ch / 64) * kRegion + (ch % 8) * 2 + half * 64 * 128;
+            auto value_at = [&](int t) { // t-th token of this half, of the channel `ch`
+                return reinterpret_cast<uint16_t *>(col + t * 128 + (((ch % 64) / 8 ^ (t & 7)) * 16));
+            };
+            float scale[4] = {1.f, 1.f, 1.f, 1.f}; // of this lane's channels lane / 4 + 8 i
             if constexpr (kHalf) {
                 if (mine) {
-                    float most = 0.f;
+                    uint32_t most[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                    for (int t = 0; t < 64; t += 16)
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            most = fmaxf(most, fabsf(value_of<T>(*value_at(t + i))));
-                    m->exponent[half][ch] =
-                        (uint8_t)(__float_as_uint(most < INFINITY ? most : 65504.f) >> 23);
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t x[4];
+                            load_v(x, k, g);
+                            // magnitudes order as their bits; what is not finite counts as the largest
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                most[g * 2 + (i & 1)] = __vmaxu2(most[g * 2 + (i & 1)], x[i] & 0x7FFF7FFFu);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 1));
+                        most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 2));
+                        const uint32_t top = min(max(most[i] & 0xFFFFu, most[i] >> 16), 0x7BFFu);
+                        if ((lane & 3) == 0)
+                            m->exponent[half][wg * 32 + i * 8 + (lane >> 2)] =
+                                (uint8_t)(__float_as_uint(value_of<T>((uint16_t)top)) >> 23);
+                    }
                 }
                 bar_sync(2 + 4 + wg, 64);
                 if (mine) {
-                    const int e = max((int)max(m->exponent[0][ch], m->exponent[1][ch]) - 127 - 13, -40);
-                    scale = power_of_two(-e);
-                    back = power_of_two(e);
+                    auto exponent = [&](int i) {
+                        return max((int)max(m->exponent[0][i], m->exponent[1][i]) - 127 - 13, -40);
+                    };
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        scale[i] = power_of_two(-exponent(wg * 32 + i * 8 + (lane >> 2)));
+                    back = power_of_two(exponent(ch));
                 }
             }
             auto put_values = [&]() { // true if one is not finite
-                float odd = 0.f;
+                float2 odd = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
-                    const float f = (k < 2 ? behind[0] : behind[1]) * scale;
-                    uint32_t part[3][8];
+                    const float f = k < 2 ? behind[0] : behind[1];
+                    const float2 f2 = make_float2(f, f);
+                    float2 w[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 r = *reinterpret_cast<const float4 *>(
-                            &d.rest[half * 64 + k * 16 + i * 4]);
-                        const float w[4] = {r.x * f, r.y * f, r.z * f, r.w * f};
-                        float x[4];
+                    for (int i = 0; i < 2; ++i)
+                        w[i] = __fmul2_rn(*reinterpret_cast<const float2 *>(
+                                              &d.rest[half * 64 + k * 16 + i * 8 + (lane & 3) * 2]), f2);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const float v = value_of<T>(*value_at(k * 16 + i * 4 + z));
-                            odd = fmaf(v, 0.f, odd);
-                            x[z] = v * w[z];
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t x[4], part[kSplit][4];
+                        load_v(x, k, g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float2 v = unpack2<T>(x[i]);
+                            odd = __ffma2_rn(v, make_float2(0.f, 0.f), odd);
+                            v = __fmul2_rn(v, w[i >> 1]);
+                            if constexpr (kHalf)
+                                v = __fmul2_rn(v, make_float2(scale[g * 2 + (i & 1)], scale[g * 2 + (i & 1)]));
+                            uint32_t y[kSplit];
+                            split<T, kSplit>(v, y);
+#pragma unroll
+                            for (int q = 0; q < kSplit; ++q)
+                                part[q][i] = y[q];
                         }
 #pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            float a = x[2 * z], e = x[2 * z + 1];
-#pragma unroll
-                            for (int q = 0; q < kSplit; ++q) {
-                                part[q][2 * i + z] = pack2<T>(a, e);
-                                const float2 u = unpack2<T>(part[q][2 * i + z]);
-                                a -= u.x, e -= u.y;
-                            }
-                        }
+                        for (int q = 0; q < kSplit; ++q)
+                            tmem_st_16x128b_x2(tmem + lane_base + ((uint32_t)(g * 16) << 16) + Gm::kTmemV +
+                                                   (uint32_t)(q * 64 + half * 32 + k * 8), part[q]);
                     }
-#pragma unroll
-                    for (int q = 0; q < kSplit; ++q)
-                        tmem_st8(tmem + lane_base + Gm::kTmemV +
-                                     (uint32_t)(q * 64 + half * 32 + k * 8), part[q]);
                 }
-                return odd != 0.f; // NaN compares unequal
+                return odd.x != 0.f || odd.y != 0.f; // NaN compares unequal
             };
             bool hurt = false;
             int first = 128;
             if (ok && mine) {
-                hurt = put_values();
-                if (hurt)
+                const bool any = __any_sync(~0u, put_values());
+                if (any) {
                     for (int t = 63; t >= 0; --t)
                         if (!(fabsf(value_of<T>(*value_at(t))) < INFINITY)) {
                             first = half * 64 + t;
                             *value_at(t) = 0;
                         }
+                    __syncwarp();
+                    put_values();
+                }
                 if (half == 0)
                     m->first[b][ch] = (uint8_t)first;
-                const bool any = __any_sync(~0u, hurt);
-                if (any)
-                    put_values();
                 if (lane == 0)
                     reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = any;
                 tmem_wait_st();
@@ -951,8 +993,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_ld32_nowait(from + (uint32_t)(k * 32), x);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        S[k * 32 + i] = fmaf(decay, S[k * 32 + i], __uint_as_float(x[i]) * back);
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 add = pair_of(x + i);
+                        if constexpr (kHalf)
+                            add = __fmul2_rn(add, make_float2(back, back));
+                        const float2 to = __ffma2_rn(make_float2(S[k * 32 + i], S[k * 32 + i + 1]),
+                                                     make_float2(decay, decay), add);
+                        S[k * 32 + i] = to.x, S[k * 32 + i + 1] = to.y;
+                    }
                 }
                 if (hurt)
 #pragma unroll
