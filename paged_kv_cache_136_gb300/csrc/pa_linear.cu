@@ -247,7 +247,7 @@ static cudaError_t launch_pass(const Maps &maps, const LinearParams &p, cudaStre
         e = cudaFuncGetAttributes(&a, kern);
         if (e != cudaSuccess)
             return e;
-        if (a.numRegs * (kTcThreads / 128) < 4 * kRegsMany + kRegsFew)
+        if (a.numRegs < kRegsLaunched)
             return cudaErrorInvalidConfiguration;
         __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
     }

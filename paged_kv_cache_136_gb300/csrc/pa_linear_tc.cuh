@@ -56,9 +56,12 @@ constexpr int kBlock = 32;         // tokens whose decays are summed as one
 constexpr int kTcThreads = 640;
 constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18;
 // Five warpgroups are launched with 96 registers a thread; the last one, whose warps
-// issue copies and MMAs, hands some to the others: 4 * 112 + 32 = 5 * 96.
-constexpr int kRegsFew = 32, kRegsMany = 112;
+// issue copies and MMAs, hands some to the two that hold states: 2 * 128 + 2 * 96 + 32.
+constexpr int kRegsLaunched = 96, kRegsFew = 32, kRegsMany = 128;
 constexpr uint32_t kTmemCols = 512;
+// Named barriers: of all rows, of all channels, of a half of the channels (2), of the
+// two warps that share 32 rows (4) or channels (4).
+constexpr int kRowsBarrier = 1, kChannelsBarrier = 2, kHalfBarrier = 3, kPairBarrier = 5;
 constexpr uint32_t kTmemO = 128, kTmemDelta = 256;
 constexpr int kRegion = kChunk * 128; // 128 token rows of 64 elements
 
@@ -163,12 +166,28 @@ __device__ __forceinline__ int range_exponent(float m)
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane)
+// A phase of a barrier, awaited by a whole converged warp, with a limit of tries (16 M of
+// 20 cycles or more: a wait of these kernels takes microseconds).  One short loop that
+// all lanes run: it stands at twenty places of a kernel whose roles have to fit the
+// instruction cache together, and a loop of lane 0 alone leaves code behind it that is
+// compiled for diverged lanes, MMA issue above all (16 prompts of 32 heads: 453 us with
+// mbar_wait's unrolled tries in lane 0, 520 with a short loop there, 300 with this).
+constexpr int kTries = 1 << 24;
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
-    bool ok = true;
-    if (lane == 0)
-        ok = mbar_wait(bar, parity);
-    return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    int left = kTries;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity) && --left) {
+    }
+    return __all_sync(~0u, left > 0);
+}
+
+// A group of N threads goes on, or gives up, together: one of its warps waits on the
+// mbarriers (a waiting warp asks again and again, and takes issue slots and fetches from
+// those that work), the others at named barrier `id`.
+template <int N> __device__ __forceinline__ bool together(int id, bool ok)
+{
+    return !bar_sync_or(id, N, !ok);
 }
 
 // Where sequence s lies, and in how many segments; 0 if it is skipped.
@@ -343,14 +362,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c = 0, it = 0; ok && c < n; ++c) {
                 const int b = c & 1, t = t0 + c * kChunk;
                 const uint32_t again = (uint32_t)((c >> 1) - 1) & 1;
-                if (c >= 2 && !warp_wait(&m->k_empty[b], again, lane)) {
+                if (c >= 2 && !warp_wait(&m->k_empty[b], again)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0)
                     load(Gm::kOffK + b * TB, &k_map, &m->k_full[b], head, t);
                 ++loaded_k;
-                if (c >= 2 && !warp_wait(&m->dec_empty[b], again, lane)) {
+                if (c >= 2 && !warp_wait(&m->dec_empty[b], again)) {
                     ok = false;
                     break;
                 }
@@ -392,7 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int h = 0; h < (kParts ? 1 : per); ++h, ++it) {
                     if (!kParts) {
                         if (it >= 2 &&
-                            !warp_wait(&m->q_empty[it & 1], (uint32_t)((it >> 1) - 1) & 1, lane)) {
+                            !warp_wait(&m->q_empty[it & 1], (uint32_t)((it >> 1) - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -401,7 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         ++loaded_q;
                     }
                     if (h == 0) {
-                        if (c >= 1 && !warp_wait(&m->v_empty, (uint32_t)(c - 1) & 1, lane)) {
+                        if (c >= 1 && !warp_wait(&m->v_empty, (uint32_t)(c - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -411,14 +430,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
             }
-            if (!ok && lane == 0) {
+            if (!ok) {
                 // Given up: no tile may land in a later CTA's memory, so the last load on
                 // each barrier is awaited, within the waits' own limit.
-                atomicOr(p.err, PA_DEVERR_TIMEOUT_);
+                if (lane == 0)
+                    atomicOr(p.err, PA_DEVERR_TIMEOUT_);
                 auto settle = [](uint64_t *bar, int loads) {
                     if (loads > 0)
-                        mbar_wait(bar, (uint32_t)(loads - 1) & 1);
+                        warp_wait(bar, (uint32_t)(loads - 1) & 1);
                 };
+#pragma unroll 1
                 for (int b = 0; b < 2; ++b) {
                     settle(&m->k_full[b], (loaded_k + 1 - b) >> 1);
                     settle(&m->q_full[b], (loaded_q + 1 - b) >> 1);
@@ -435,9 +456,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto slot = [](int b) { return (uint64_t)((uint32_t)(b * TB) >> 4); };
             // the scores of pair `it`, over the P that the last product has read
             auto scores = [&](int it, int c, bool first) {
-                if (first && !warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1, lane))
+                if (first && !warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1))
                     return false;
-                if (!warp_wait(&m->q_full[it & 1], (uint32_t)(it >> 1) & 1, lane))
+                if (!warp_wait(&m->q_full[it & 1], (uint32_t)(it >> 1) & 1))
                     return false;
                 tc_fence_after_sync();
                 if (elect_one()) {
@@ -467,13 +488,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
                 const bool last = kParts || h == per - 1;
                 if (kParts) {
-                    ok = warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1, lane);
+                    ok = warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1);
                 } else {
                     // O = Q S, both parts
                     if (h == 0)
-                        ok = warp_wait(&m->st_full, (uint32_t)c & 1, lane);
+                        ok = warp_wait(&m->st_full, (uint32_t)c & 1);
                     if (ok && it > 0)
-                        ok = warp_wait(&m->o_free, (uint32_t)(it - 1) & 1, lane);
+                        ok = warp_wait(&m->o_free, (uint32_t)(it - 1) & 1);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
@@ -495,14 +516,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 // delta before P V: the next chunk's state is being made meanwhile
                 if (ok && h == 0) {
-                    ok = warp_wait(&m->v1_full, (uint32_t)c & 1, lane);
+                    ok = warp_wait(&m->v1_full, (uint32_t)c & 1);
                     tc_fence_after_sync();
                     if (ok && elect_one())
                         delta(c, 0, &m->d_full);
                     __syncwarp();
                 }
                 if (!kParts) {
-                    ok = ok && warp_wait(&m->p_full, (uint32_t)it & 1, lane);
+                    ok = ok && warp_wait(&m->p_full, (uint32_t)it & 1);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
@@ -521,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                 }
                 if (kTwice && h == 0 && ok) {
-                    ok = warp_wait(&m->d_free, (uint32_t)c & 1, lane);
+                    ok = warp_wait(&m->d_free, (uint32_t)c & 1);
                     tc_fence_after_sync();
                     if (ok && elect_one())
                         delta(c, 1, &m->d2_full);
@@ -544,12 +565,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (elect_one())
                 umma_commit(&m->drain);
             __syncwarp();
-            warp_wait(&m->drain, 0, lane);
+            warp_wait(&m->drain, 0);
         } else if (warp == kStoreWarp && !kParts) {
             // ============================================================== outputs
             bool ok = true;
             for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
-                if (!(ok = warp_wait(&m->o_staged, (uint32_t)it & 1, lane)))
+                if (!(ok = warp_wait(&m->o_staged, (uint32_t)it & 1)))
                     break;
                 if (lane == 0) {
                     if (len - c * kChunk >= kChunk) { // a tail's rows were written one by one
@@ -574,7 +595,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp < 8) {
         // ===================================================== rows: P and outputs
-        registers_up<kRegsMany>();
         const int row = tid & 127, blk = warp & 3, half = warp >> 2;
         const uint32_t lane_base = (uint32_t)(blk * 32) << 16;
         const uint32_t s_addr = tmem + lane_base;
@@ -584,15 +604,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int block[2] = {half, 3 - half};
         bool ok = true;
         float upto = 0.f, inter = 0.f, f[2] = {0.f, 0.f};
-        // With fp16 the two warps of a row block meet at a barrier once a round: one that
-        // has given up goes on to the next one, where both leave.
         for (int it = 0; !kParts && it < total; ++it) {
             const int c = it / per, h = it - c * per;
             const Decays &d = m->dec[c & 1];
             const int live = min(kChunk, len - c * kChunk);
-            if (h == 0)
-                ok = ok && warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1, lane);
-            if (h == 0 && ok) {
+            if (warp == 0)
+                ok = (h > 0 || warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1)) &&
+                     warp_wait(&m->s_full, (uint32_t)it & 1);
+            if (!(ok = together<256>(kRowsBarrier, ok)))
+                break;
+            if (h == 0) {
                 // decays from the end of a column block to this row, and from the
                 // chunk's beginning
                 upto = d.upto[row];
@@ -609,13 +630,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 inter = exp2f(sum) * p.scale;
             }
-            ok = ok && warp_wait(&m->s_full, (uint32_t)it & 1, lane);
             tc_fence_after_sync();
             float down = 1.f, up = 1.f; // 2^-E, 2^E
             if constexpr (kHalf) {
                 float most = 0.f; // of the whole row, by both of its threads
 #pragma unroll 1
-                for (int b = 0; ok && b <= blk; ++b) {
+                for (int b = 0; b <= blk; ++b) {
                     uint32_t sv[32];
                     tmem_ld32_nowait(s_addr + (uint32_t)(b * 32), sv);
                     tmem_wait_ld();
@@ -628,10 +648,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 down = power_of_two(-e);
                 up = power_of_two(e);
                 // P goes over the scores: both threads have seen all of them
-                ok = !bar_sync_or(2 + blk, 64, !ok);
+                bar_sync(kPairBarrier + blk, 64);
             }
-            if (!ok)
-                break;
 #pragma unroll 1
             for (int z = 0; z < 2; ++z) {
                 const int b = z ? 3 - half : half;
@@ -676,16 +694,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_st16(at, hi);
                 tmem_st16(at + 16, lo);
             }
-            if (h == 0) {
-                // both before p_full lets their next phases begin
-                ok = warp_wait(&m->st_full, (uint32_t)c & 1, lane) &&
-                     warp_wait(&m->v1_full, (uint32_t)c & 1, lane);
-                if (ok && kHalf)
-                    inter *= m->state_scale[c & 1];
-            }
-            ok = ok && warp_wait(&m->o1_full, (uint32_t)it & 1, lane);
-            if (!ok)
-                continue;
+            // The first two before p_full lets their next phases begin.
+            if (warp == 0)
+                ok = (h > 0 || (warp_wait(&m->st_full, (uint32_t)c & 1) &&
+                                warp_wait(&m->v1_full, (uint32_t)c & 1))) &&
+                     warp_wait(&m->o1_full, (uint32_t)it & 1);
+            if (!(ok = together<256>(kRowsBarrier, ok)))
+                break;
+            if (kHalf && h == 0)
+                inter *= m->state_scale[c & 1];
             tc_fence_after_sync();
             const float2 of = make_float2(inter * down, inter * down);
 #pragma unroll 1
@@ -705,8 +722,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&m->p_full);
-            if (!(ok = warp_wait(&m->o_full, (uint32_t)it & 1, lane)))
-                continue;
+            if (warp == 0)
+                ok = warp_wait(&m->o_full, (uint32_t)it & 1);
+            if (!(ok = together<256>(kRowsBarrier, ok)))
+                break;
             tc_fence_after_sync();
             const bool hurt = m->hurt[c & 1] != 0;
             uint8_t *const tile = smem + Gm::kOffQ + (it & 1) * TB + (half * H / 64) * kRegion + row * 128;
@@ -790,7 +809,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const unsigned top = __reduce_max_sync(~0u, __float_as_uint(most));
                 if (lane == 0)
                     m->warp_max[c & 1][warp - 8] = __uint_as_float(top);
-                if (bar_sync_or(1, 256, !ok))
+                if (!together<256>(kChannelsBarrier, ok))
                     return false;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -827,19 +846,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_arrive(&m->st_full);
             return true;
         };
-        if (!kParts && n > 0)
-            put_state(0, true);
         float decay_log2 = 0.f; // of the whole segment
         bool ok = true;         // of this warp, until the next barrier
-        for (int c = 0; c < n; ++c) {
+        for (int c = kParts ? 0 : -1; c < n; ++c) { // chunk -1 leaves the state it was given
+            if (c >= 0) {
             const int b = c & 1, live = min(kChunk, len - c * kChunk);
             const Decays &d = m->dec[b];
-            ok = ok && warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1, lane) &&
-                 warp_wait(&m->v_full, (uint32_t)c & 1, lane);
+            if (warp == 8)
+                ok = ok && warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1) &&
+                     warp_wait(&m->v_full, (uint32_t)c & 1) &&
+                     // V' is read until the second delta is done
+                     (!kTwice || c == 0 || warp_wait(&m->d2_full, (uint32_t)(c - 1) & 1)) &&
+                     (live == kChunk || warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1));
+            if (!(ok = together<256>(kChannelsBarrier, ok)))
+                break;
             if (live < kChunk) {
                 // the tiles' rows behind the sequence are a neighbour's: zeros
-                ok = ok && warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1, lane);
-                if (ok && ch >= live && half < Gm::kHalves)
+                if (ch >= live && half < Gm::kHalves)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int off = half * kRegion + ch * 128 + i * 16;
@@ -847,7 +870,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         *reinterpret_cast<uint4 *>(smem + Gm::kOffK + b * TB + off) =
                             make_uint4(0, 0, 0, 0);
                     }
-                bar_sync(1, 256);
+                bar_sync(kChannelsBarrier, 256);
             }
             // 2^(decays behind the blocks of 32 to the chunk's end), of this half's two
             float behind[2], sum = 0.f;
@@ -898,7 +921,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 (uint8_t)(__float_as_uint(value_of<T>((uint16_t)top)) >> 23);
                     }
                 }
-                bar_sync(2 + 4 + wg, 64);
+                bar_sync(kPairBarrier + 4 + wg, 64);
                 if (mine) {
                     auto exponent = [&](int i) {
                         return max((int)max(m->exponent[0][i], m->exponent[1][i]) - 127 - 13, -40);
@@ -912,51 +935,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto put_values = [&]() { // true if one is not finite
                 float2 odd = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    const float f = k < 2 ? behind[0] : behind[1];
+                for (int z = 0; z < 4; ++z) { // 32 tokens of 16 channels
+                    const int k = z >> 1, g = z & 1;
+                    const float f = k == 0 ? behind[0] : behind[1];
                     const float2 f2 = make_float2(f, f);
-                    float2 w[2];
+                    uint32_t x[2][4], part[kSplit][8];
+                    load_v(x[0], 2 * k, g);
+                    load_v(x[1], 2 * k + 1, g);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        w[i] = __fmul2_rn(*reinterpret_cast<const float2 *>(
-                                              &d.rest[half * 64 + k * 16 + i * 8 + (lane & 3) * 2]), f2);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t x[4], part[kSplit][4];
-                        load_v(x, k, g);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float2 v = unpack2<T>(x[i]);
-                            odd = __ffma2_rn(v, make_float2(0.f, 0.f), odd);
-                            v = __fmul2_rn(v, w[i >> 1]);
-                            if constexpr (kHalf)
-                                v = __fmul2_rn(v, make_float2(scale[g * 2 + (i & 1)], scale[g * 2 + (i & 1)]));
-                            uint32_t y[kSplit];
-                            split<T, kSplit>(v, y);
-#pragma unroll
-                            for (int q = 0; q < kSplit; ++q)
-                                part[q][i] = y[q];
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 w = __fmul2_rn(
+                            *reinterpret_cast<const float2 *>(
+                                &d.rest[half * 64 + k * 32 + (i >> 1) * 8 + (lane & 3) * 2]), f2);
+                        float2 v = unpack2<T>(x[i >> 2][i & 3]);
+                        odd = __ffma2_rn(v, make_float2(0.f, 0.f), odd);
+                        v = __fmul2_rn(v, w);
+                        if constexpr (kHalf) {
+                            const float s2 = g ? scale[2 + (i & 1)] : scale[i & 1];
+                            v = __fmul2_rn(v, make_float2(s2, s2));
                         }
+                        uint32_t y[kSplit];
+                        split<T, kSplit>(v, y);
 #pragma unroll
                         for (int q = 0; q < kSplit; ++q)
-                            tmem_st_16x128b_x2(tmem + lane_base + ((uint32_t)(g * 16) << 16) + Gm::kTmemV +
-                                                   (uint32_t)(q * 64 + half * 32 + k * 8), part[q]);
+                            part[q][i] = y[q];
                     }
+#pragma unroll
+                    for (int q = 0; q < kSplit; ++q)
+                        tmem_st_16x128b_x4(tmem + lane_base + ((uint32_t)(g * 16) << 16) + Gm::kTmemV +
+                                               (uint32_t)(q * 64 + half * 32 + k * 16), part[q]);
                 }
                 return odd.x != 0.f || odd.y != 0.f; // NaN compares unequal
             };
             bool hurt = false;
             int first = 128;
-            if (ok && mine) {
-                const bool any = __any_sync(~0u, put_values());
-                if (any) {
+            if (mine) {
+                bool any = false;
+#pragma unroll 1
+                while (__any_sync(~0u, put_values())) { // once more, without what is not finite
+                    any = true;
+#pragma unroll 1
                     for (int t = 63; t >= 0; --t)
                         if (!(fabsf(value_of<T>(*value_at(t))) < INFINITY)) {
                             first = half * 64 + t;
                             *value_at(t) = 0;
                         }
                     __syncwarp();
-                    put_values();
                 }
                 if (half == 0)
                     m->first[b][ch] = (uint8_t)first;
@@ -966,14 +990,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else if (lane == 0) {
                 reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = 0;
             }
-            // every thread of the group goes on or none does
-            ok = !bar_sync_or(1, 256, !ok);
-            if (!ok)
-                break;
+            bar_sync(kChannelsBarrier, 256);
             if (m->hurt[b] != 0) { // the first of both halves, for both
                 if (half == 1 && first < 128 && m->first[b][ch] == 128)
                     m->first[b][ch] = (uint8_t)first;
-                bar_sync(1, 256);
+                bar_sync(kChannelsBarrier, 256);
                 hurt = mine && m->first[b][ch] < 128;
             }
             fence_proxy_async_smem();
@@ -983,7 +1004,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_arrive(&m->dec_empty[b]);
                 mbar_arrive(&m->v1_full);
             }
-            ok = warp_wait(kTwice && half == 1 ? &m->d2_full : &m->d_full, (uint32_t)c & 1, lane);
+            // the halves go separate ways here where delta comes in two
+            if (wg == 0)
+                ok = warp_wait(kTwice && half == 1 ? &m->d2_full : &m->d_full, (uint32_t)c & 1);
+            ok = together<128>(kHalfBarrier + half, ok);
             tc_fence_after_sync();
             if (ok && mine) {
                 const uint32_t from = tmem + lane_base + kTmemDelta + (uint32_t)(kTwice ? 0 : half * H);
@@ -1014,11 +1038,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(&m->d_free);
             }
             if (!kParts && c + 1 < n) {
-                ok = ok && warp_wait(&m->qs_done, (uint32_t)c & 1, lane);
-                ok = put_state(c + 1, ok);
-                if (kHalf && !ok) // of the whole group then
-                    break;
+                if (wg == 0)
+                    ok = ok && warp_wait(&m->qs_done, (uint32_t)c & 1);
+                ok = together<128>(kHalfBarrier + half, ok);
             }
+            } // c >= 0
+            if (!kParts && c + 1 < n)
+                ok = put_state(c + 1, ok);
         }
         if (!ok && lane == 0)
             atomicOr(p.err, PA_DEVERR_TIMEOUT_);

@@ -446,13 +446,14 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// Store an 8-column piece of 16 TMEM lanes in the layout of transposed 8x8 matrices:
-// lane l has lane l / 4 (v[0], v[2]) and 8 + l / 4 (v[1], v[3]), columns l % 4 (v[0],
-// v[1]) and 4 + l % 4.
-__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&v)[4])
+// Store a 16-column piece of 16 TMEM lanes in the layout of transposed 8x8 matrices:
+// lane l has TMEM lane l / 4 (even v) and 8 + l / 4 (odd v) of columns 4 (i / 2) + l % 4,
+// i the index in v.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&v)[8])
 {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(
+                     taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
 
