@@ -32,6 +32,8 @@
 //   warp 17      the MMAs: per query head O = Q S, O += P V, the next head's scores;
 //                per chunk, after the first head's P V, delta = V'^T K
 //   warp 18      output tiles to global memory by TMA
+//   warp 19      looks through V tiles: rows behind the sequence and values that are not
+//                finite become zeros; with fp16 the channels' largest magnitudes
 // Two threads share a row or a channel because one warp a scheduler is not enough to
 // hide the latency of tensor memory and of fetching a role's instructions; the loops
 // over blocks are rolled for the latter's sake.
@@ -54,15 +56,14 @@ namespace lin {
 constexpr int kChunk = 128;        // tokens
 constexpr int kBlock = 32;         // tokens whose decays are summed as one
 constexpr int kTcThreads = 640;
-constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18;
+constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18, kLookWarp = 19;
 // Five warpgroups are launched with 96 registers a thread; the last one, whose warps
 // issue copies and MMAs, hands some to the two that hold states: 2 * 128 + 2 * 96 + 32.
 constexpr int kRegsLaunched = 96, kRegsFew = 32, kRegsMany = 128;
 constexpr uint32_t kTmemCols = 512;
-// Named barriers: of all rows, of all channels, of a half of the channels (2), of the
-// two warps that share 32 rows (4) or channels (4).
-constexpr int kRowsBarrier = 1, kChannelsBarrier = 2, kHalfBarrier = 3, kPairBarrier = 5;
-constexpr uint32_t kTmemO = 128, kTmemDelta = 256;
+// Named barriers: of all rows, of all channels, of the two warps that share 32 rows (4).
+constexpr int kRowsBarrier = 1, kChannelsBarrier = 2, kPairBarrier = 3;
+constexpr uint32_t kTmemO = 128, kTmemDelta = 256, kTmemV = 384;
 constexpr int kRegion = kChunk * 128; // 128 token rows of 64 elements
 
 template <typename T, int D>
@@ -70,14 +71,15 @@ struct Geo {
     // V' enters V'^T K in three parts with bf16, 2^-24 of its size: with two the states
     // would be off by 2.6e-6 (measured), with fp16's longer parts two reach 2^-22.
     static constexpr int kSplit = std::is_same<T, __half>::value ? 2 : 3;
-    // Three parts of 128 tokens leave 64 columns for delta: with head_size 128 it is
-    // formed for one half of the key channels, then for the other.
-    static constexpr bool kTwice = kSplit == 3 && D == 128;
-    static constexpr uint32_t kTmemV = kTmemCols - kSplit * (kChunk / 2);
+    // Tensor memory has 128 columns for V': a ring of blocks of 32 tokens, which are made
+    // while the MMAs take the ones before.
+    static constexpr int kRing = 128 / (kSplit * 16);
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kRegion;      // a Q, K or V tile
     static constexpr int kStateRegion = D * 128;         // 64 key channels of all value channels
     static constexpr int kState = kHalves * kStateRegion;
+    // Five tiles: K twice, then with one query head a kv head Q once and V twice, with
+    // more of them Q twice and V once.
     static constexpr int kOffK = 0, kOffQ = 2 * kTile, kOffV = 4 * kTile, kOffS = 5 * kTile;
     static constexpr int kOffMisc = kOffS + 2 * kState;
 };
@@ -90,18 +92,18 @@ struct alignas(16) Decays { // read four floats at a time
 };
 
 struct Misc {
-    uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full, v_empty;
+    uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];
     uint64_t dec_full[2], dec_empty[2];
     uint64_t s_full, p_full, o1_full, o_full, o_free, o_staged;
-    uint64_t v1_full, d_full, d_free, d2_full, st_full, qs_done, drain;
-    uint64_t hurt[2];        // a byte for each warp of channels: whether it met what is not finite
+    uint64_t vok_full[2], st_full[2], ring_full[4], ring_empty[4], d_full, qs_done, drain;
+    uint32_t hurt[2];        // whether a chunk had values that are not finite
     Decays dec[2];
     float state_scale[2];    // what the state's operand was divided by
     uint32_t tmem_base;
     int unit[3];
     uint8_t first[2][128];   // by value channel: the chunk's first token whose value is not
                              // finite, or 128
-    uint8_t exponent[2][128]; // fp16: largest exponent of a half of the tokens, by channel
+    uint8_t exponent[2][128]; // fp16: by value channel, the chunk's largest exponent
     float warp_max[2][8];
 };
 
@@ -143,6 +145,36 @@ template <> __device__ __forceinline__ float value_of<__nv_bfloat16>(uint16_t u)
     return __uint_as_float((uint32_t)u << 16);
 }
 
+// x less the two 16-bit values of `part`, by multiply-adds that take 16-bit factors: the
+// parts are not unpacked first, which would be twice the work on a narrower pipe.
+template <typename T> __device__ __forceinline__ float2 less(float2 x, uint32_t part);
+template <> __device__ __forceinline__ float2 less<__half>(float2 x, uint32_t part)
+{
+    asm("{\n"
+        "  .reg .b16 l, h, m;\n"
+        "  mov.b32 {l, h}, %2;\n"
+        "  mov.b16 m, 0xBC00;\n"
+        "  fma.rn.f32.f16 %0, l, m, %0;\n"
+        "  fma.rn.f32.f16 %1, h, m, %1;\n"
+        "}\n"
+        : "+f"(x.x), "+f"(x.y)
+        : "r"(part));
+    return x;
+}
+template <> __device__ __forceinline__ float2 less<__nv_bfloat16>(float2 x, uint32_t part)
+{
+    asm("{\n"
+        "  .reg .b16 l, h, m;\n"
+        "  mov.b32 {l, h}, %2;\n"
+        "  mov.b16 m, 0xBF80;\n"
+        "  fma.rn.f32.bf16 %0, l, m, %0;\n"
+        "  fma.rn.f32.bf16 %1, h, m, %1;\n"
+        "}\n"
+        : "+f"(x.x), "+f"(x.y)
+        : "r"(part));
+    return x;
+}
+
 // Two values as N 16-bit parts, each the rounded remainder of those before it.
 template <typename T, int N>
 __device__ __forceinline__ void split(float2 x, uint32_t (&part)[N])
@@ -151,12 +183,20 @@ __device__ __forceinline__ void split(float2 x, uint32_t (&part)[N])
     for (int i = 0; i < N; ++i) {
         part[i] = pack2<T>(x.x, x.y);
         if (i + 1 < N)
-            x = __ffma2_rn(unpack2<T>(part[i]), make_float2(-1.f, -1.f), x);
+            x = less<T>(x, part[i]);
     }
 }
 __device__ __forceinline__ float2 pair_of(const uint32_t *x)
 {
     return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+
+// max(m, |x.x|, |x.y|); a NaN is passed over.
+__device__ __forceinline__ float most_of(float m, float2 x)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(x.x), "f"(x.y));
+    return r;
 }
 
 // Exponent E that brings magnitudes up to m below 2^14 (or up to there): m 2^-E.
@@ -182,9 +222,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
     return __all_sync(~0u, left > 0);
 }
 
-// A group of N threads goes on, or gives up, together: one of its warps waits on the
-// mbarriers (a waiting warp asks again and again, and takes issue slots and fetches from
-// those that work), the others at named barrier `id`.
+// A group of N threads goes on, or gives up, together: one of its warps waits on an
+// mbarrier (a waiting warp asks again and again, and takes issue slots and fetches from
+// those that work), another one on the next if there is one, all of them at named
+// barrier `id`.
 template <int N> __device__ __forceinline__ bool together(int id, bool ok)
 {
     return !bar_sync_or(id, N, !ok);
@@ -248,14 +289,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     using Gm = Geo<T, D>;
     constexpr int TB = Gm::kTile;
     constexpr int kSplit = Gm::kSplit;
-    constexpr bool kTwice = Gm::kTwice;
     constexpr bool kHalf = std::is_same<T, __half>::value;
     constexpr int H = D / 2; // channels of a thread that has half of them
     constexpr uint32_t kFmt = kHalf ? 0u : 1u;
     constexpr uint32_t kIdescScores = idesc_f16_f32(kFmt, 0, 0, kChunk, kChunk);
     constexpr uint32_t kIdescState = idesc_f16_f32(kFmt, 0, 0, kChunk, D);             // Q S
     constexpr uint32_t kIdescValue = idesc_f16_f32(kFmt, 0, 1, kChunk, D);             // P V
-    constexpr uint32_t kIdescDelta = idesc_f16_f32(kFmt, 0, 1, 128, kTwice ? D / 2 : D); // V'^T K
+    constexpr uint32_t kIdescDelta = idesc_f16_f32(kFmt, 0, 1, 128, D);    // V'^T K
 
     extern __shared__ __align__(1024) uint8_t smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + Gm::kOffMisc);
@@ -265,12 +305,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     griddep_wait();
     // the last line is past every unit, so its search sees every sequence
     const bool tell = head == 0 && y == (int)gridDim.y - 1 && !kParts;
-    if (p.segment == INT32_MAX) { // one segment each: line y is sequence y
-        if (tid == 0) {
-            int q0, len;
-            m->unit[2] = segments_of(p, y, q0, len, head == 0);
-            m->unit[0] = m->unit[2] ? y : -1;
-            m->unit[1] = 0;
+    if (p.segment == INT32_MAX) {
+        // One segment each.  Of up to 32 sequences line y is the y-th longest, so that the
+        // long ones start first; with more of them their chains are many and even out.
+        if (warp == 0) {
+            int q0, len = -1, n = 0, s = y;
+            if (p.num_seqs > 32) {
+                n = segments_of(p, y, q0, len, head == 0 && lane == 0);
+            } else {
+                if (lane < p.num_seqs)
+                    n = segments_of(p, lane, q0, len, head == 0 && lane == y);
+                int rank = 0;
+                for (int i = 0; i < p.num_seqs; ++i) {
+                    const int other = __shfl_sync(~0u, len, i);
+                    rank += other > len || (other == len && i < lane);
+                }
+                s = __ffs(__ballot_sync(~0u, lane < p.num_seqs && rank == y)) - 1;
+                n = __shfl_sync(~0u, n, s);
+            }
+            if (lane == 0)
+                m->unit[0] = n ? s : -1, m->unit[1] = 0, m->unit[2] = n;
         }
     } else if (warp == 0) {
         int s, j = 0, n = 0;
@@ -284,22 +338,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&m->k_empty[i], 1);
             mbar_init(&m->q_full[i], 1);
             mbar_init(&m->q_empty[i], 1);
+            mbar_init(&m->vok_full[i], 1);
+            mbar_init(&m->st_full[i], 8);
+            mbar_init(&m->v_full[i], 1);
+            mbar_init(&m->v_empty[i], 1);
             mbar_init(&m->dec_full[i], 1);
             mbar_init(&m->dec_empty[i], kParts ? 8 : 16);
         }
-        mbar_init(&m->v_full, 1);
-        mbar_init(&m->v_empty, 1);
         mbar_init(&m->s_full, 1);
         mbar_init(&m->p_full, 8);
         mbar_init(&m->o1_full, 1);
         mbar_init(&m->o_full, 1);
         mbar_init(&m->o_free, 8);
         mbar_init(&m->o_staged, 8);
-        mbar_init(&m->v1_full, 8);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&m->ring_full[i], 8);
+            mbar_init(&m->ring_empty[i], 1);
+        }
         mbar_init(&m->d_full, 1);
-        mbar_init(&m->d_free, 4);
-        mbar_init(&m->d2_full, 1);
-        mbar_init(&m->st_full, 8);
         mbar_init(&m->qs_done, 1);
         mbar_init(&m->drain, 1);
         fence_barrier_init();
@@ -314,6 +370,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int src = p.src_states[s], dst = p.dst_states[s];
     const int per = p.num_heads / p.num_kv_heads;
     const int total = kParts ? n : n * per; // (chunk, query head) pairs
+    // With one query head a kv head (and without any, in the first pass) a chunk is short,
+    // and its chain -- V', delta, state -- sets the pace: V is loaded a chunk ahead, into
+    // what is the second Q slot otherwise, Q's slot is free after Q S, and the output
+    // goes over the K tile.
+    const bool solo = kParts || per == 1;
+    auto v_slot = [&](int c) { return solo ? c & 1 : 0; };
+    auto v_phase = [&](int c) { return (uint32_t)(solo ? c >> 1 : c) & 1; };
+    auto v_offset = [&](int c) { return Gm::kOffV - v_slot(c) * TB; };
+    auto q_slot = [&](int it) { return solo ? 0 : it & 1; };
+    auto q_phase = [&](int it) { return (uint32_t)(solo ? it : it >> 1) & 1; };
     if (tid == 0 && head == 0 && !kParts && (src >= p.num_states || dst >= p.num_states))
         atomicOr(p.err, PA_DEVERR_STATE_);
     if (warp == kMmaWarp) {
@@ -342,39 +408,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tma_load_3d(smem + off + hf * kRegion, map, bar, hf * 64, h, t);
             };
             const float *const log_decay = p.log_decay + head;
-            // this lane's four tokens of chunk c, in log2 units; below 2^-128 is 0, and
-            // a difference of two such sums stays a number
+            // this lane's four tokens of chunk c
             auto read_decays = [&](int c, float (&g)[4]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = c * kChunk + lane * 4 + i;
-                    float x = 0.f;
-                    if (t < len)
-                        x = log_decay[(int64_t)(t0 + t) * p.decay_stride] * 1.4426950408889634f;
-                    g[i] = x < -128.f ? -128.f : x;
+                    g[i] = t < len ? log_decay[(int64_t)(t0 + t) * p.decay_stride] : 0.f;
                 }
             };
             float g[4];
             bool ok = true;
             int loaded_k = 0, loaded_q = 0, loaded_v = 0;
-            if (n > 0)
-                read_decays(0, g);
-            for (int c = 0, it = 0; ok && c < n; ++c) {
-                const int b = c & 1, t = t0 + c * kChunk;
-                const uint32_t again = (uint32_t)((c >> 1) - 1) & 1;
-                if (c >= 2 && !warp_wait(&m->k_empty[b], again)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0)
-                    load(Gm::kOffK + b * TB, &k_map, &m->k_full[b], head, t);
-                ++loaded_k;
-                if (c >= 2 && !warp_wait(&m->dec_empty[b], again)) {
-                    ok = false;
-                    break;
-                }
+            auto put_decays = [&](int c) {
+                const int b = c & 1;
+                if (c >= 2 && !warp_wait(&m->dec_empty[b], (uint32_t)((c >> 1) - 1) & 1))
+                    return false;
                 Decays &d = m->dec[b];
                 float upto[4], rest[4];
+                // in log2 units; below 2^-128 is 0, and a difference of two such sums stays
+                // a number
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[i] *= 1.4426950408889634f;
+                    g[i] = g[i] < -128.f ? -128.f : g[i];
+                }
                 upto[0] = g[0];
 #pragma unroll
                 for (int i = 1; i < 4; ++i)
@@ -408,27 +465,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(&m->dec_full[b]);
                 if (c + 1 < n)
                     read_decays(c + 1, g);
-                for (int h = 0; h < (kParts ? 1 : per); ++h, ++it) {
-                    if (!kParts) {
-                        if (it >= 2 &&
-                            !warp_wait(&m->q_empty[it & 1], (uint32_t)((it >> 1) - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0)
-                            load(Gm::kOffQ + (it & 1) * TB, &q_map, &m->q_full[it & 1], head * per + h, t);
-                        ++loaded_q;
-                    }
-                    if (h == 0) {
-                        if (c >= 1 && !warp_wait(&m->v_empty, (uint32_t)(c - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0)
-                            load(Gm::kOffV, &v_map, &m->v_full, head, t);
-                        ++loaded_v;
-                    }
-                }
+                return true;
+            };
+            auto load_k = [&](int c) {
+                if (c >= 2 && !warp_wait(&m->k_empty[c & 1], (uint32_t)((c >> 1) - 1) & 1))
+                    return false;
+                if (lane == 0)
+                    load(Gm::kOffK + (c & 1) * TB, &k_map, &m->k_full[c & 1], head, t0 + c * kChunk);
+                ++loaded_k;
+                return true;
+            };
+            auto load_q = [&](int c, int h) { // the pairs in turn
+                const int it = loaded_q, b = q_slot(it), slots = solo ? 1 : 2;
+                if (kParts)
+                    return true;
+                if (it >= slots && !warp_wait(&m->q_empty[b], q_phase(it - slots)))
+                    return false;
+                if (lane == 0)
+                    load(Gm::kOffQ + b * TB, &q_map, &m->q_full[b], head * per + h, t0 + c * kChunk);
+                ++loaded_q;
+                return true;
+            };
+            auto load_v = [&](int c) {
+                const int b = v_slot(c), slots = solo ? 2 : 1;
+                if (c >= slots && !warp_wait(&m->v_empty[b], v_phase(c - slots)))
+                    return false;
+                if (lane == 0)
+                    load(v_offset(c), &v_map, &m->v_full[b], head, t0 + c * kChunk);
+                ++loaded_v;
+                return true;
+            };
+            if (n > 0) {
+                read_decays(0, g);
+                ok = load_k(0) && load_q(0, 0) && load_v(0) && put_decays(0);
+            }
+            // in the order in which their places come free
+#pragma unroll 1
+            for (int c = 0; ok && c < n; ++c) {
+                const bool more = c + 1 < n;
+                if (solo && more)
+                    ok = load_v(c + 1);
+                if (more)
+                    ok = ok && put_decays(c + 1);
+#pragma unroll 1
+                for (int h = 1; ok && h < per; ++h)
+                    ok = load_q(c, h);
+                if (ok && more)
+                    ok = load_k(c + 1) && load_q(c + 1, 0) && (solo || load_v(c + 1));
             }
             if (!ok) {
                 // Given up: no tile may land in a later CTA's memory, so the last load on
@@ -442,27 +525,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int b = 0; b < 2; ++b) {
                     settle(&m->k_full[b], (loaded_k + 1 - b) >> 1);
-                    settle(&m->q_full[b], (loaded_q + 1 - b) >> 1);
+                    settle(&m->q_full[b], solo ? (b ? 0 : loaded_q) : (loaded_q + 1 - b) >> 1);
+                    settle(&m->v_full[b], solo ? (loaded_v + 1 - b) >> 1 : (b ? 0 : loaded_v));
                 }
-                settle(&m->v_full, loaded_v);
             }
         } else if (warp == kMmaWarp) {
             // ========================================================== MMA issuer
             const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), 16, 1024);
             const uint64_t kt_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffK), kRegion, 1024);
             const uint64_t q_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffQ), 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffV), kRegion, 1024);
             const uint64_t s_desc = smem_desc_sw128(smem_addr(smem + Gm::kOffS), 16, 1024);
             auto slot = [](int b) { return (uint64_t)((uint32_t)(b * TB) >> 4); };
             // the scores of pair `it`, over the P that the last product has read
             auto scores = [&](int it, int c, bool first) {
                 if (first && !warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1))
                     return false;
-                if (!warp_wait(&m->q_full[it & 1], (uint32_t)(it >> 1) & 1))
+                if (!warp_wait(&m->q_full[q_slot(it)], q_phase(it)))
                     return false;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const uint64_t qd = q_desc + slot(it & 1), kd = k_desc + slot(c & 1);
+                    const uint64_t qd = q_desc + slot(q_slot(it)), kd = k_desc + slot(c & 1);
 #pragma unroll 1
                     for (uint32_t kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
@@ -473,33 +555,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 return true;
             };
-            // delta = V'^T K, for key channels from 64 `half` on where it is formed in two
-            auto delta = [&](int c, int half, uint64_t *bar) {
-                const uint64_t kd = kt_desc + slot(c & 1) + (uint64_t)((half * kRegion) >> 4);
+            // delta = V'^T K, block after block of V', the last tokens' first
+            auto delta = [&](int c) {
 #pragma unroll 1
-                for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const uint32_t block = (uint32_t)c * 4 + k, at = block % Gm::kRing;
+                    if (!warp_wait(&m->ring_full[at], (block / Gm::kRing) & 1))
+                        return false;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint64_t kd = kt_desc + slot(c & 1) + (3 - k) * (2 * 2048 >> 4);
+                        const uint32_t a = tmem + kTmemV + at * (kSplit * 16);
+#pragma unroll 1
+                        for (uint32_t kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (uint32_t part = 0; part < kSplit; ++part)
-                        umma_f16_tmem_a(tmem + kTmemDelta, tmem + Gm::kTmemV + part * 64 + kk * 8,
-                                        kd + kk * (2048 >> 4), kIdescDelta, kk + part);
-                umma_commit(bar);
+                            for (uint32_t part = 0; part < kSplit; ++part)
+                                umma_f16_tmem_a(tmem + kTmemDelta, a + part * 16 + kk * 8,
+                                                kd + kk * (2048 >> 4), kIdescDelta, k + kk + part);
+                        umma_commit(&m->ring_empty[at]);
+                        if (k == 3)
+                            umma_commit(&m->d_full);
+                    }
+                    __syncwarp();
+                }
+                return true;
             };
+            // with several query heads V arrives late in the first one's time
+            const int delta_head = solo ? 0 : 1;
             bool ok = n == 0 || kParts || scores(0, 0, true);
             for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
                 const bool last = kParts || h == per - 1;
-                if (kParts) {
+                const int next = last ? c + 1 : c;
+                if (kParts)
                     ok = warp_wait(&m->k_full[c & 1], (uint32_t)(c >> 1) & 1);
-                } else {
+                if (!kParts) {
                     // O = Q S, both parts
-                    if (h == 0)
-                        ok = warp_wait(&m->st_full, (uint32_t)c & 1);
+                    if (ok && h == 0)
+                        ok = warp_wait(&m->st_full[c & 1], (uint32_t)(c >> 1) & 1);
                     if (ok && it > 0)
                         ok = warp_wait(&m->o_free, (uint32_t)(it - 1) & 1);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint64_t qd = q_desc + slot(it & 1);
+                        const uint64_t qd = q_desc + slot(q_slot(it));
 #pragma unroll 1
                         for (uint32_t kk = 0; kk < D / 16; ++kk) {
                             const uint64_t o = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
@@ -511,50 +610,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         umma_commit(&m->o1_full);
                         if (last)
                             umma_commit(&m->qs_done);
+                        if (solo)
+                            umma_commit(&m->q_empty[0]);
                     }
                     __syncwarp();
                 }
-                // delta before P V: the next chunk's state is being made meanwhile
-                if (ok && h == 0) {
-                    ok = warp_wait(&m->v1_full, (uint32_t)c & 1);
-                    tc_fence_after_sync();
-                    if (ok && elect_one())
-                        delta(c, 0, &m->d_full);
-                    __syncwarp();
-                }
+                if (kParts || h == delta_head)
+                    ok = ok && delta(c);
                 if (!kParts) {
                     ok = ok && warp_wait(&m->p_full, (uint32_t)it & 1);
+                    if (ok && h == 0)
+                        ok = warp_wait(&m->vok_full[c & 1], (uint32_t)(c >> 1) & 1);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
                     if (elect_one()) { // O += P V, both parts
+                        const uint64_t vd0 =
+                            smem_desc_sw128(smem_addr(smem + v_offset(c)), kRegion, 1024);
 #pragma unroll 1
                         for (uint32_t kk = 0; kk < kChunk / 16; ++kk) {
-                            const uint64_t vd = v_desc + kk * (2048 >> 4);
+                            const uint64_t vd = vd0 + kk * (2048 >> 4);
                             const uint32_t pa = tmem + (kk >> 1) * 32 + (kk & 1) * 8;
                             umma_f16_tmem_a(tmem + kTmemO, pa, vd, kIdescValue, 1u);
                             umma_f16_tmem_a(tmem + kTmemO, pa + 16, vd, kIdescValue, 1u);
                         }
                         umma_commit(&m->o_full);
-                        if (last)
-                            umma_commit(&m->v_empty);
+                        if (last) // V' was made before delta
+                            umma_commit(&m->v_empty[v_slot(c)]);
                     }
                     __syncwarp();
+                    if (it + 1 < total)
+                        ok = scores(it + 1, next, last);
                 }
-                if (kTwice && h == 0 && ok) {
-                    ok = warp_wait(&m->d_free, (uint32_t)c & 1);
-                    tc_fence_after_sync();
-                    if (ok && elect_one())
-                        delta(c, 1, &m->d2_full);
-                    __syncwarp();
-                }
-                const int next = last ? c + 1 : c;
-                if (!kParts && ok && it + 1 < total)
-                    ok = scores(it + 1, next, last);
                 if (last && elect_one()) {
                     if (kParts)
-                        umma_commit(&m->v_empty);
-                    umma_commit(&m->k_empty[c & 1]);
+                        umma_commit(&m->v_empty[v_slot(c)]);
+                    if (kParts || !solo) // else free with the output's store
+                        umma_commit(&m->k_empty[c & 1]);
                 }
                 __syncwarp();
                 c = next;
@@ -576,12 +668,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (len - c * kChunk >= kChunk) { // a tail's rows were written one by one
 #pragma unroll
                         for (int hf = 0; hf < Gm::kHalves; ++hf)
-                            tma_store_3d(&out_map, smem + Gm::kOffQ + (it & 1) * TB + hf * kRegion,
+                            tma_store_3d(&out_map,
+                                         smem + (solo ? Gm::kOffK : Gm::kOffQ) + (it & 1) * TB + hf * kRegion,
                                          hf * 64, head * per + h, t0 + c * kChunk);
                         bulk_commit();
                         bulk_wait_read();
                     }
-                    mbar_arrive(&m->q_empty[it & 1]);
+                    mbar_arrive(solo ? &m->k_empty[it & 1] : &m->q_empty[it & 1]);
                 }
                 __syncwarp();
                 if (++h == per)
@@ -592,6 +685,100 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok)
                     atomicOr(p.err, PA_DEVERR_TIMEOUT_);
             }
+        } else if (warp == kLookWarp) {
+            // ======================================================== a look at V
+            bool ok = true;
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
+                const int b = c & 1, live = min(kChunk, len - c * kChunk);
+                uint8_t *const v = smem + v_offset(c);
+                ok = warp_wait(&m->v_full[v_slot(c)], v_phase(c)) &&
+                     // everyone is through with chunk c - 2, whose `first` is written over
+                     warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1) &&
+                     (live == kChunk || warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1));
+                if (!ok)
+                    break;
+                // the tiles' rows behind the sequence are a neighbour's: zeros
+#pragma unroll 1
+                for (int i = live * 8 + lane; i < kChunk * 8; i += 32)
+#pragma unroll
+                    for (int hf = 0; hf < Gm::kHalves; ++hf) {
+                        *reinterpret_cast<uint4 *>(v + hf * kRegion + i * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(smem + Gm::kOffK + b * TB + hf * kRegion + i * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                __syncwarp();
+                // whether all is finite
+                uint32_t odd = 0;
+                if constexpr (kHalf) {
+                    // 16 channels by 16 tokens at a time, a channel's pairs in a lane; magnitudes
+                    // order as their bits
+#pragma unroll 1
+                    for (int g = 0; g < D / 16; ++g) {
+                        uint32_t most[2] = {0, 0};
+                        const uint32_t at = smem_addr(v + (g / 4) * kRegion) +
+                                            (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 128 +
+                                                       (((g % 4 * 2 + (lane >> 3 & 1)) ^ (lane & 7)) * 16));
+#pragma unroll 4
+                        for (int k = 0; k < kChunk / 16; ++k) {
+                            uint32_t x[4];
+                            ldmatrix_x4_trans(x, at + (uint32_t)(k * 2048));
+                            most[0] = __vmaxu2(__vmaxu2(most[0], x[0] & 0x7FFF7FFFu), x[2] & 0x7FFF7FFFu);
+                            most[1] = __vmaxu2(__vmaxu2(most[1], x[1] & 0x7FFF7FFFu), x[3] & 0x7FFF7FFFu);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 1));
+                            most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 2));
+                            const uint32_t top = max(most[i] & 0xFFFFu, most[i] >> 16);
+                            odd |= (top + 0x0400u) << 16; // an exponent of ones carries to the top
+                            if ((lane & 3) == 0)
+                                m->exponent[b][g * 16 + i * 8 + (lane >> 2)] =
+                                    (uint8_t)(__float_as_uint(value_of<T>((uint16_t)top)) >> 23);
+                        }
+                    }
+                } else {
+#pragma unroll 4
+                    for (int i = 0; i < TB / 512; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(v + lane * 16 + i * 512);
+                        odd |= ((x.x & 0x7FFF7FFFu) + 0x00800080u) | ((x.y & 0x7FFF7FFFu) + 0x00800080u) |
+                               ((x.z & 0x7FFF7FFFu) + 0x00800080u) | ((x.w & 0x7FFF7FFFu) + 0x00800080u);
+                    }
+                }
+                const bool hurt = __any_sync(~0u, (odd & 0x80008000u) != 0);
+                if (hurt) {
+                    // What is not finite is taken out of the tile: in P V it would reach the
+                    // rows before it as 0 * NaN.  `first` is where a channel is lost from.
+#pragma unroll 1
+                    for (int ch = lane; ch < D; ch += 32) {
+                        int first = 128;
+                        float most = 0.f;
+#pragma unroll 1
+                        for (int t = kChunk - 1; t >= 0; --t) {
+                            uint16_t *const at = reinterpret_cast<uint16_t *>(
+                                v + (ch / 64) * kRegion + t * 128 + (((ch % 64) / 8 ^ (t & 7)) * 16) +
+                                (ch % 8) * 2);
+                            const float x = fabsf(value_of<T>(*at));
+                            if (!(x < INFINITY)) {
+                                first = t;
+                                *at = 0;
+                            } else {
+                                most = fmaxf(most, x);
+                            }
+                        }
+                        m->first[b][ch] = (uint8_t)first;
+                        m->exponent[b][ch] = (uint8_t)(__float_as_uint(most) >> 23);
+                    }
+                }
+                if (lane == 0)
+                    m->hurt[b] = hurt;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&m->vok_full[b]);
+            }
+            if (!ok && lane == 0)
+                atomicOr(p.err, PA_DEVERR_TIMEOUT_);
         }
     } else if (warp < 8) {
         // ===================================================== rows: P and outputs
@@ -609,8 +796,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Decays &d = m->dec[c & 1];
             const int live = min(kChunk, len - c * kChunk);
             if (warp == 0)
-                ok = (h > 0 || warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1)) &&
-                     warp_wait(&m->s_full, (uint32_t)it & 1);
+                ok = warp_wait(&m->s_full, (uint32_t)it & 1);
+            else if (h == 0 && warp == 1)
+                ok = warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1);
             if (!(ok = together<256>(kRowsBarrier, ok)))
                 break;
             if (h == 0) {
@@ -639,10 +827,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     uint32_t sv[32];
                     tmem_ld32_nowait(s_addr + (uint32_t)(b * 32), sv);
                     tmem_wait_ld();
-                    const int end = b < blk ? 31 : lane;
+                    if (b == blk)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        most = fmaxf(most, i <= end ? fabsf(__uint_as_float(sv[i])) : 0.f);
+                        for (int i = 1; i < 32; ++i)
+                            sv[i] = i <= lane ? sv[i] : 0;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        most = most_of(most, pair_of(sv + i));
                 }
                 const int e = range_exponent(most * fabsf(p.scale));
                 down = power_of_two(-e);
@@ -694,11 +885,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_st16(at, hi);
                 tmem_st16(at + 16, lo);
             }
-            // The first two before p_full lets their next phases begin.
             if (warp == 0)
-                ok = (h > 0 || (warp_wait(&m->st_full, (uint32_t)c & 1) &&
-                                warp_wait(&m->v1_full, (uint32_t)c & 1))) &&
-                     warp_wait(&m->o1_full, (uint32_t)it & 1);
+                ok = warp_wait(&m->o1_full, (uint32_t)it & 1);
+            else if (h == 0 && warp == 1)
+                ok = warp_wait(&m->st_full[c & 1], (uint32_t)(c >> 1) & 1);
+            else if (h == 0 && warp == 2)
+                ok = warp_wait(&m->vok_full[c & 1], (uint32_t)(c >> 1) & 1);
             if (!(ok = together<256>(kRowsBarrier, ok)))
                 break;
             if (kHalf && h == 0)
@@ -728,7 +920,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             tc_fence_after_sync();
             const bool hurt = m->hurt[c & 1] != 0;
-            uint8_t *const tile = smem + Gm::kOffQ + (it & 1) * TB + (half * H / 64) * kRegion + row * 128;
+            uint8_t *const tile = smem + (solo ? Gm::kOffK : Gm::kOffQ) + (it & 1) * TB +
+                                  (half * H / 64) * kRegion + row * 128;
             T *const out = static_cast<T *>(p.out) + half * H +
                            ((int64_t)(t0 + c * kChunk + row) * p.num_heads + head * per + h) * D;
 #pragma unroll 1
@@ -804,8 +997,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if constexpr (kHalf) {
                 float most = 0.f;
 #pragma unroll
-                for (int k = 0; k < H; ++k)
-                    most = fmaxf(most, fabsf(S[k]) < INFINITY ? fabsf(S[k]) : 0.f);
+                for (int k = 0; k < H; k += 2)
+                    most = most_of(most, make_float2(S[k], S[k + 1]));
+                if (most == INFINITY) { // the largest that is finite, then
+                    most = 0.f;
+#pragma unroll
+                    for (int k = 0; k < H; ++k)
+                        most = fmaxf(most, fabsf(S[k]) < INFINITY ? fabsf(S[k]) : 0.f);
+                }
                 const unsigned top = __reduce_max_sync(~0u, __float_as_uint(most));
                 if (lane == 0)
                     m->warp_max[c & 1][warp - 8] = __uint_as_float(top);
@@ -843,174 +1042,116 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&m->st_full);
+                mbar_arrive(&m->st_full[c & 1]);
             return true;
         };
         float decay_log2 = 0.f; // of the whole segment
         bool ok = true;         // of this warp, until the next barrier
-        for (int c = kParts ? 0 : -1; c < n; ++c) { // chunk -1 leaves the state it was given
-            if (c >= 0) {
-            const int b = c & 1, live = min(kChunk, len - c * kChunk);
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+            const int b = c & 1;
             const Decays &d = m->dec[b];
-            if (warp == 8)
-                ok = ok && warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1) &&
-                     warp_wait(&m->v_full, (uint32_t)c & 1) &&
-                     // V' is read until the second delta is done
-                     (!kTwice || c == 0 || warp_wait(&m->d2_full, (uint32_t)(c - 1) & 1)) &&
-                     (live == kChunk || warp_wait(&m->k_full[b], (uint32_t)(c >> 1) & 1));
-            if (!(ok = together<256>(kChannelsBarrier, ok)))
+            // Without other heads' products between, one wait serves a whole round (below).
+            if (!kParts) {
+                if (!solo && c > 0) {
+                    if (warp == 8)
+                        ok = ok && warp_wait(&m->qs_done, (uint32_t)(c - 1) & 1);
+                    ok = together<256>(kChannelsBarrier, ok);
+                }
+                ok = put_state(c, ok);
+            }
+            if (!solo || c == 0) {
+                if (warp == 8)
+                    ok = ok && warp_wait(&m->vok_full[b], (uint32_t)(c >> 1) & 1);
+                else if (warp == 9)
+                    ok = ok && warp_wait(&m->dec_full[b], (uint32_t)(c >> 1) & 1);
+                ok = together<256>(kChannelsBarrier, ok);
+            }
+            if (!ok)
                 break;
-            if (live < kChunk) {
-                // the tiles' rows behind the sequence are a neighbour's: zeros
-                if (ch >= live && half < Gm::kHalves)
+            const bool hurt = mine && m->hurt[b] && m->first[b][ch] < 128;
+            float scale[2] = {1.f, 1.f}, back = 1.f; // of channels lane / 4 and 8 + lane / 4 of 16
+            if (kHalf && mine) {
+                auto exponent = [&](int i) { return max((int)m->exponent[b][i] - 127 - 13, -40); };
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int off = half * kRegion + ch * 128 + i * 16;
-                        *reinterpret_cast<uint4 *>(smem + Gm::kOffV + off) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(smem + Gm::kOffK + b * TB + off) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                bar_sync(kChannelsBarrier, 256);
+                for (int i = 0; i < 2; ++i)
+                    scale[i] = power_of_two(-exponent(wg * 32 + half * 16 + i * 8 + (lane >> 2)));
+                back = power_of_two(exponent(ch));
             }
-            // 2^(decays behind the blocks of 32 to the chunk's end), of this half's two
-            float behind[2], sum = 0.f;
-#pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                if (k >> 1 == half)
-                    behind[k & 1] = exp2f(sum);
-                sum += d.block[k];
-            }
-            const float decay = exp2f(sum);
-            decay_log2 += sum;
-            // V': this warp's 32 channels of this half's tokens, decayed to the chunk's end.
-            // Transposed 8x8 matrices give a lane two tokens of a channel, as the operand
-            // in tensor memory wants them: 4 channels a lane, and a fourth of their tokens.
-            float back = 1.f;
-            const uint32_t tile = smem_addr(smem + Gm::kOffV + (wg / 2) * kRegion);
-            auto load_v = [&](uint32_t (&x)[4], int k, int g) { // 16 tokens from 16 k, 16 channels
-                const int t = half * 64 + k * 16 + (lane >> 4) * 8 + (lane & 7);
-                const int piece = (wg & 1) * 4 + g * 2 + (lane >> 3 & 1);
-                ldmatrix_x4_trans(x, tile + (uint32_t)(t * 128 + ((piece ^ (lane & 7)) * 16)));
+            // V', decayed to the chunk's end, from the last block on: of each block of 32
+            // tokens this warp has 16 channels.  Transposed 8x8 matrices give a lane two tokens of a channel, as the
+            // operand in tensor memory wants them.
+            const uint32_t tile = smem_addr(smem + v_offset(c) + (wg / 2) * kRegion) +
+                                  (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 128 +
+                                             ((((wg & 1) * 4 + half * 2 + (lane >> 3 & 1)) ^ (lane & 7)) * 16));
+            const float4 sums = *reinterpret_cast<const float4 *>(d.block);
+            const float behind[3] = {sums.w, sums.w + sums.z, sums.w + sums.z + sums.y};
+            const float factor[3] = {exp2f(behind[0]), exp2f(behind[1]), exp2f(behind[2])};
+            // a block is handed on while the next one is worked out
+            auto hand_on = [&](int i) {
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&m->ring_full[((uint32_t)c * 4 + i) % Gm::kRing]);
             };
-            uint8_t *const col = smem + Gm::kOffV + (ch / 64) * kRegion + (ch % 8) * 2 + half * 64 * 128;
-            auto value_at = [&](int t) { // t-th token of this half, of the channel `ch`
-                return reinterpret_cast<uint16_t *>(col + t * 128 + (((ch % 64) / 8 ^ (t & 7)) * 16));
-            };
-            float scale[4] = {1.f, 1.f, 1.f, 1.f}; // of this lane's channels lane / 4 + 8 i
-            if constexpr (kHalf) {
-                if (mine) {
-                    uint32_t most[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            uint32_t x[4];
-                            load_v(x, k, g);
-                            // magnitudes order as their bits; what is not finite counts as the largest
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                most[g * 2 + (i & 1)] = __vmaxu2(most[g * 2 + (i & 1)], x[i] & 0x7FFF7FFFu);
-                        }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 1));
-                        most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 2));
-                        const uint32_t top = min(max(most[i] & 0xFFFFu, most[i] >> 16), 0x7BFFu);
-                        if ((lane & 3) == 0)
-                            m->exponent[half][wg * 32 + i * 8 + (lane >> 2)] =
-                                (uint8_t)(__float_as_uint(value_of<T>((uint16_t)top)) >> 23);
-                    }
-                }
-                bar_sync(kPairBarrier + 4 + wg, 64);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t block = (uint32_t)c * 4 + i, at = block % Gm::kRing;
+                const int k = 3 - i;
+                uint32_t part[kSplit][8];
                 if (mine) {
-                    auto exponent = [&](int i) {
-                        return max((int)max(m->exponent[0][i], m->exponent[1][i]) - 127 - 13, -40);
-                    };
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        scale[i] = power_of_two(-exponent(wg * 32 + i * 8 + (lane >> 2)));
-                    back = power_of_two(exponent(ch));
-                }
-            }
-            auto put_values = [&]() { // true if one is not finite
-                float2 odd = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int z = 0; z < 4; ++z) { // 32 tokens of 16 channels
-                    const int k = z >> 1, g = z & 1;
-                    const float f = k == 0 ? behind[0] : behind[1];
+                    const float f = i == 0 ? 1.f : i == 1 ? factor[0] : i == 2 ? factor[1] : factor[2];
                     const float2 f2 = make_float2(f, f);
-                    uint32_t x[2][4], part[kSplit][8];
-                    load_v(x[0], 2 * k, g);
-                    load_v(x[1], 2 * k + 1, g);
+                    uint32_t x[2][4];
+                    ldmatrix_x4_trans(x[0], tile + (uint32_t)(k * 4096));
+                    ldmatrix_x4_trans(x[1], tile + (uint32_t)(k * 4096 + 2048));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int z = 0; z < 8; ++z) {
                         const float2 w = __fmul2_rn(
-                            *reinterpret_cast<const float2 *>(
-                                &d.rest[half * 64 + k * 32 + (i >> 1) * 8 + (lane & 3) * 2]), f2);
-                        float2 v = unpack2<T>(x[i >> 2][i & 3]);
-                        odd = __ffma2_rn(v, make_float2(0.f, 0.f), odd);
-                        v = __fmul2_rn(v, w);
-                        if constexpr (kHalf) {
-                            const float s2 = g ? scale[2 + (i & 1)] : scale[i & 1];
-                            v = __fmul2_rn(v, make_float2(s2, s2));
-                        }
+                            *reinterpret_cast<const float2 *>(&d.rest[k * 32 + (z >> 1) * 8 + (lane & 3) * 2]), f2);
+                        float2 v = __fmul2_rn(unpack2<T>(x[z >> 2][z & 3]), w);
+                        if constexpr (kHalf)
+                            v = __fmul2_rn(v, make_float2(scale[z & 1], scale[z & 1]));
                         uint32_t y[kSplit];
                         split<T, kSplit>(v, y);
 #pragma unroll
                         for (int q = 0; q < kSplit; ++q)
-                            part[q][i] = y[q];
+                            part[q][z] = y[q];
                     }
+                }
+                if (i > 0)
+                    hand_on(i - 1);
+                // the chunk before is through: its delta has been read
+                if (ok && i >= Gm::kRing)
+                    ok = warp_wait(&m->ring_empty[at], (block / Gm::kRing - 1) & 1);
+                if (mine) {
 #pragma unroll
                     for (int q = 0; q < kSplit; ++q)
-                        tmem_st_16x128b_x4(tmem + lane_base + ((uint32_t)(g * 16) << 16) + Gm::kTmemV +
-                                               (uint32_t)(q * 64 + half * 32 + k * 16), part[q]);
+                        tmem_st_16x128b_x4(tmem + lane_base + ((uint32_t)(half * 16) << 16) + kTmemV +
+                                               at * (kSplit * 16) + (uint32_t)(q * 16), part[q]);
                 }
-                return odd.x != 0.f || odd.y != 0.f; // NaN compares unequal
-            };
-            bool hurt = false;
-            int first = 128;
-            if (mine) {
-                bool any = false;
-#pragma unroll 1
-                while (__any_sync(~0u, put_values())) { // once more, without what is not finite
-                    any = true;
-#pragma unroll 1
-                    for (int t = 63; t >= 0; --t)
-                        if (!(fabsf(value_of<T>(*value_at(t))) < INFINITY)) {
-                            first = half * 64 + t;
-                            *value_at(t) = 0;
-                        }
-                    __syncwarp();
-                }
-                if (half == 0)
-                    m->first[b][ch] = (uint8_t)first;
-                if (lane == 0)
-                    reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = any;
-                tmem_wait_st();
-            } else if (lane == 0) {
-                reinterpret_cast<uint8_t *>(&m->hurt[b])[warp - 8] = 0;
             }
-            bar_sync(kChannelsBarrier, 256);
-            if (m->hurt[b] != 0) { // the first of both halves, for both
-                if (half == 1 && first < 128 && m->first[b][ch] == 128)
-                    m->first[b][ch] = (uint8_t)first;
-                bar_sync(kChannelsBarrier, 256);
-                hurt = mine && m->first[b][ch] < 128;
-            }
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
+            hand_on(3);
+            if (lane == 0)
                 mbar_arrive(&m->dec_empty[b]);
-                mbar_arrive(&m->v1_full);
+            const float sum = behind[2] + sums.x;
+            const float decay = exp2f(sum);
+            decay_log2 += sum;
+            if (warp == 8) {
+                ok = ok && warp_wait(&m->d_full, (uint32_t)c & 1);
+            } else if (solo && c + 1 < n) { // and what the next round wants
+                if (warp == 9)
+                    ok = ok && warp_wait(&m->vok_full[b ^ 1], (uint32_t)((c + 1) >> 1) & 1);
+                else if (warp == 10)
+                    ok = ok && warp_wait(&m->dec_full[b ^ 1], (uint32_t)((c + 1) >> 1) & 1);
+                else if (warp == 11 && !kParts)
+                    ok = ok && warp_wait(&m->qs_done, (uint32_t)c & 1);
             }
-            // the halves go separate ways here where delta comes in two
-            if (wg == 0)
-                ok = warp_wait(kTwice && half == 1 ? &m->d2_full : &m->d_full, (uint32_t)c & 1);
-            ok = together<128>(kHalfBarrier + half, ok);
+            ok = together<256>(kChannelsBarrier, ok);
             tc_fence_after_sync();
             if (ok && mine) {
-                const uint32_t from = tmem + lane_base + kTmemDelta + (uint32_t)(kTwice ? 0 : half * H);
+                const uint32_t from = tmem + lane_base + kTmemDelta + (uint32_t)(half * H);
 #pragma unroll
                 for (int k = 0; k < H / 32; ++k) {
                     uint32_t x[32];
@@ -1032,19 +1173,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         S[k] = __uint_as_float(0x7FFFFFFFu);
             }
             tc_fence_before_sync();
-            if (kTwice && half == 0) {
-                __syncwarp();
-                if (ok && lane == 0)
-                    mbar_arrive(&m->d_free);
-            }
-            if (!kParts && c + 1 < n) {
-                if (wg == 0)
-                    ok = ok && warp_wait(&m->qs_done, (uint32_t)c & 1);
-                ok = together<128>(kHalfBarrier + half, ok);
-            }
-            } // c >= 0
-            if (!kParts && c + 1 < n)
-                ok = put_state(c + 1, ok);
         }
         if (!ok && lane == 0)
             atomicOr(p.err, PA_DEVERR_TIMEOUT_);
