@@ -16,43 +16,50 @@
 namespace pa {
 namespace lin {
 
+constexpr int kStepThreads = 128, kCols = 64; // of a CTA of the recurrent kernel
 constexpr int kHeadsAtOnce = 8; // query heads whose products share the state in registers
 
-// One CTA walks one sequence's tokens for one kv head with the state in registers:
-// a thread has 4 value channels (16 bytes of a state's row) of every 8th key
-// channel, so the state is read and written once, in whole rows, with all of a
-// CTA's loads in flight, and a token's products cost one pass over registers and a
-// sum over the 8 row groups in shared memory.
+// One CTA walks one sequence's tokens for 64 value channels of one kv head with that
+// part of the state in registers: a thread has 4 value channels (16 bytes of a state's
+// row) of every 8th key channel, so the state is read and written once, in pieces of 256
+// bytes, with all of a CTA's loads in flight, and a token's products cost one pass over
+// registers and a sum over the 8 row groups in shared memory.  Bound by HBM.  Five small
+// CTAs an SM keep reads and writes going side by side, and the states, which the next
+// step wants, go past the caches: 64 x 32 states of 128 x 128 take 41 us, 6.5 TB/s, 256 x
+// 8 with four query heads each 43 (with cached loads and stores 43 and 46, with whole
+// states by 256 threads 51 and 56, with four heads in one pass over the state 45 and 47,
+// with the stores before the products 45 and 48).
 template <typename T, int D, bool kPrompt>
-__global__ void __launch_bounds__(2 * D) linear_step_kernel(const LinearParams p)
+__global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearParams p)
 {
-    constexpr int kLanes = D / 4, kGroups = 8, kRows = D / kGroups;
+    constexpr int kLanes = kCols / 4, kGroups = kStepThreads / kLanes, kRows = D / kGroups;
     __shared__ float sk[D], sq[kHeadsAtOnce][D];
-    __shared__ float part[kGroups][kHeadsAtOnce][D];
+    __shared__ float part[kGroups][kHeadsAtOnce][kCols];
     griddep_wait();
-    const int tid = threadIdx.x, head = blockIdx.x, s = blockIdx.y;
+    const int tid = threadIdx.x, head = blockIdx.x / (D / kCols), s = blockIdx.y;
+    const int col0 = blockIdx.x % (D / kCols) * kCols; // this CTA's value channels
     const int col = tid % kLanes * 4, group = tid / kLanes;
     const int dst = p.dst_states[s], src = p.src_states[s];
     int t0 = s, t1 = s + 1;
     if constexpr (kPrompt) {
         t0 = p.query_start_loc[s], t1 = p.query_start_loc[s + 1];
         if (t0 < 0 || t1 > p.num_tokens || t1 < t0 || t1 - t0 > p.max_query_len) {
-            if (tid == 0 && head == 0)
+            if (tid == 0 && blockIdx.x == 0)
                 atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
             return;
         }
     }
     if (dst < 0)
         return;
-    if (tid == 0 && head == 0 && (src >= p.num_states || dst >= p.num_states))
+    if (tid == 0 && blockIdx.x == 0 && (src >= p.num_states || dst >= p.num_states))
         atomicOr(p.err, PA_DEVERR_STATE_);
-    const int64_t at = (int64_t)group * D + col, one = (int64_t)D * D;
+    const int64_t at = (int64_t)group * D + col0 + col, one = (int64_t)D * D;
     float4 S[kRows];
     if (src >= 0 && src < p.num_states) {
         const float *const from = p.states + ((int64_t)src * p.num_kv_heads + head) * one + at;
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
-            S[i] = *reinterpret_cast<const float4 *>(from + (int64_t)i * kGroups * D);
+            S[i] = __ldcs(reinterpret_cast<const float4 *>(from + (int64_t)i * kGroups * D));
     } else {
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
@@ -64,17 +71,17 @@ __global__ void __launch_bounds__(2 * D) linear_step_kernel(const LinearParams p
         // the same 2^-25 in every step, and 256 steps of memory by 2^-17.
         const float a = expm1f(p.log_decay[t * p.decay_stride + head]);
         const T *const k = static_cast<const T *>(p.k) + t * p.k_stride + head * D;
-        const T *const v = static_cast<const T *>(p.v) + t * p.v_stride + head * D;
+        const T *const v = static_cast<const T *>(p.v) + t * p.v_stride + head * D + col0;
         const T *const q = static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)head * per * D;
-        T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + head * per) * D;
+        T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + head * per) * D + col0;
         const float2 v01 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col));
         const float2 v23 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col + 2));
         for (int g0 = 0; g0 < per; g0 += kHeadsAtOnce) {
             const int n = min(kHeadsAtOnce, per - g0);
             if (g0 == 0)
-                for (int i = tid; i < D; i += 2 * D)
+                for (int i = tid; i < D; i += kStepThreads)
                     sk[i] = (float)k[i];
-            for (int i = tid; i < n * D; i += 2 * D)
+            for (int i = tid; i < n * D; i += kStepThreads)
                 sq[i / D][i % D] = (float)q[g0 * D + i] * p.scale;
             __syncthreads();
             if (g0 == 0) {
@@ -100,12 +107,12 @@ __global__ void __launch_bounds__(2 * D) linear_step_kernel(const LinearParams p
                 *reinterpret_cast<float4 *>(&part[group][g][col]) = o;
             }
             __syncthreads();
-            for (int i = tid; i < n * D; i += 2 * D) {
+            for (int i = tid; i < n * kCols; i += kStepThreads) {
                 float o = 0.f;
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
-                    o += part[j][i / D][i % D];
-                out[g0 * D + i] = (T)o;
+                    o += part[j][i / kCols][i % kCols];
+                out[(g0 + i / kCols) * D + i % kCols] = (T)o;
             }
             __syncthreads();
         }
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(2 * D) linear_step_kernel(const LinearParams p
         float *const to = p.states + ((int64_t)dst * p.num_kv_heads + head) * one + at;
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
-            *reinterpret_cast<float4 *>(to + (int64_t)i * kGroups * D) = S[i];
+            __stcs(reinterpret_cast<float4 *>(to + (int64_t)i * kGroups * D), S[i]);
     }
 }
 
@@ -172,7 +179,7 @@ template <bool kPrompt>
 static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_size, pa_dtype dtype,
                                cudaStream_t s)
 {
-    const dim3 grid(p.num_kv_heads, num_seqs), threads(2 * head_size);
+    const dim3 grid(p.num_kv_heads * (head_size / kCols), num_seqs), threads(kStepThreads);
     if (head_size == 128)
         return dtype == PA_BF16
                    ? launch_after_previous(linear_step_kernel<__nv_bfloat16, 128, kPrompt>, grid, threads, 0, s, p)
