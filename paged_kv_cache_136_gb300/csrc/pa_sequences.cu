@@ -23,6 +23,7 @@ constexpr int kThreads = 256;      // of the wide kernels
 constexpr int kChunk = 1024;       // table entries of a CTA
 constexpr int kRankThreads = 1024; // of a CTA of the ranking kernels
 constexpr int kCluster = 8;        // CTAs of a ranking kernel, at most
+constexpr int kRows = 8;           // table rows of a thread of theirs: 65536 in all
 constexpr int kTile = 4 * kRankThreads; // counts that a CTA ranks at once
 constexpr int kUnit = 16384;       // bytes of a block that a CTA copies at once
 // A sum of at most 65535 rows' needs: blocks, fewer than 2^31 a row, and above
@@ -187,43 +188,78 @@ __device__ __forceinline__ void cluster_sync()
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// What a CTA of the cluster tells the others, in the workspace.
+// What a CTA of the cluster tells the others, in the workspace: at most three sums.
 struct Told {
-    int64_t a, b, c;
+    int64_t v[4];
 };
 
-// Exclusive prefix of v over the CTA's threads, and the sum; `sums` has a slot
-// for each of the 32 warps.  Two barriers.
-__device__ __forceinline__ int64_t prefix(int64_t v, int64_t *sums, int64_t *total)
+// The first N sums of the CTAs before this one, and of all: each lane reads one CTA's,
+// so that the reads take one latency.
+template <int N>
+__device__ __forceinline__ void hear(const Told *told, int rank, int ctas, int64_t (&before)[N],
+                                     int64_t (&all)[N])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
+    const int lane = threadIdx.x & 31;
+    int64_t x[N];
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int64_t y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    __syncthreads();
-    if (lane == 31)
-        sums[warp] = x;
-    __syncthreads();
-    int64_t w = sums[lane];
+    for (int n = 0; n < N; ++n)
+        x[n] = lane < ctas ? __ldcg(&told[lane].v[n]) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int64_t y = __shfl_up_sync(~0u, w, o);
-        if (lane >= o)
-            w += y;
+    for (int n = 0; n < N; ++n) {
+        int64_t y = lane < rank ? x[n] : 0;
+#pragma unroll
+        for (int o = kCluster / 2; o; o /= 2) {
+            x[n] += __shfl_xor_sync(~0u, x[n], o);
+            y += __shfl_xor_sync(~0u, y, o);
+        }
+        all[n] = __shfl_sync(~0u, x[n], 0);
+        before[n] = __shfl_sync(~0u, y, 0);
     }
-    *total = __shfl_sync(~0u, w, 31);
-    const int64_t before = warp ? __shfl_sync(~0u, w, warp - 1) : 0;
-    return before + x - v;
 }
 
-// f(id, free, number of free ids in [begin, id)) for every id of [begin, end), in
+// Exclusive prefixes of N values over the CTA's threads, and their sums; `sums` has a
+// slot for each of the 32 warps.  Two barriers.
+template <int N>
+__device__ __forceinline__ void prefix(int64_t (&v)[N], int64_t (*sums)[32], int64_t (&total)[N])
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        x[n] = v[n];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int64_t y = __shfl_up_sync(~0u, x[n], o);
+            if (lane >= o)
+                x[n] += y;
+        }
+    __syncthreads();
+    if (lane == 31)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            sums[n][warp] = x[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        int64_t w = sums[n][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t y = __shfl_up_sync(~0u, w, o);
+            if (lane >= o)
+                w += y;
+        }
+        total[n] = __shfl_sync(~0u, w, 31);
+        const int64_t before = __shfl_sync(~0u, w, (warp + 31) & 31);
+        v[n] = (warp ? before : 0) + x[n] - v[n];
+    }
+}
+
+// f(id, count, number of free ids in [begin, id)) for every id of [begin, end), in
 // tiles of kTile: a warp has 128 consecutive ids, 32 at a time.
 template <typename F>
-__device__ __forceinline__ void ranked(const int32_t *refs, int begin, int end, int64_t *sums, F f)
+__device__ __forceinline__ void ranked(const int32_t *refs, int begin, int end, int *sums, F f)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int carry = 0;
@@ -240,29 +276,40 @@ __device__ __forceinline__ void ranked(const int32_t *refs, int begin, int end, 
             m[k] = __ballot_sync(~0u, v[k] == 0);
             mine += __popc(m[k]);
         }
-        int64_t total;
-        // one lane of a warp brings its sum: the others bring 0
-        int before = (int)prefix(lane == 0 ? mine : 0, sums, &total);
-        before = __shfl_sync(~0u, before, 0) + carry;
+        __syncthreads();
+        if (lane == 0)
+            sums[warp] = mine;
+        __syncthreads();
+        const int other = sums[lane];
+        int before = __reduce_add_sync(~0u, lane < warp ? other : 0) + carry;
+        carry += __reduce_add_sync(~0u, other);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (at + 32 * k < end)
                 f(at + 32 * k, v[k], before + __popc(m[k] & ((1u << lane) - 1)));
             before += __popc(m[k]);
         }
-        carry += (int)total;
     }
 }
 
-// Free ids of [begin, end), the same for every thread.
-__device__ __forceinline__ int count_free(const int32_t *refs, int begin, int end, int64_t *sums)
+// This thread's free ids of [begin, end); the CTA's, the same for every thread.
+__device__ __forceinline__ int my_free(const int32_t *refs, int begin, int end)
 {
     int n = 0;
+#pragma unroll 8
     for (int i = begin + threadIdx.x; i < end; i += kRankThreads)
         n += refs[i] == 0;
-    int64_t total;
-    prefix(n, sums, &total);
-    return (int)total;
+    return n;
+}
+__device__ __forceinline__ int sum_of(int n, int *sums)
+{
+    n = __reduce_add_sync(~0u, n);
+    if ((threadIdx.x & 31) == 0)
+        sums[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = __reduce_add_sync(~0u, sums[threadIdx.x & 31]);
+    __syncthreads();
+    return n;
 }
 
 struct ExtendParams {
@@ -284,14 +331,13 @@ struct Row {
     int len, fresh, last; // last: the block that new tokens go on in, or -1
 };
 
-__device__ __forceinline__ Row read_row(const ExtendParams &p, int r, bool tell)
+__device__ __forceinline__ Row read_row(const ExtendParams &p, int r)
 {
     Row x;
-    x.len = length_of(p.lens, r, p.len_cap, tell, p.err);
     x.fresh = p.num_new[r];
+    x.len = length_of(p.lens, r, p.len_cap, true, p.err);
     if (x.fresh < 0 || x.fresh > p.len_cap - x.len) {
-        if (tell)
-            atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
+        atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
         x.fresh = 0;
     }
     x.last = -1;
@@ -299,7 +345,7 @@ __device__ __forceinline__ Row read_row(const ExtendParams &p, int r, bool tell)
         const int b = p.tables[(int64_t)r * p.max_blocks + x.len / p.block_size];
         if (b >= 0 && b < p.num_blocks)
             x.last = b;
-        else if (tell)
+        else
             atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
     }
     return x;
@@ -310,7 +356,8 @@ __device__ __forceinline__ Row read_row(const ExtendParams &p, int r, bool tell)
 // holders where all of them go on; that is what row after row would come to.
 __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendParams p)
 {
-    __shared__ int64_t sums[32];
+    __shared__ int64_t sums[2][32];
+    __shared__ int counts[32];
     griddep_wait();
     const int rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
     const int per = (p.rows + ctas - 1) / ctas;
@@ -318,61 +365,62 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
     const int part = ((p.num_blocks + ctas - 1) / ctas + 31) / 32 * 32;
     const int b0 = min(p.num_blocks, rank * part), b1 = min(p.num_blocks, b0 + part);
 
-    for (int r = r0 + tid; r < r1; r += kRankThreads) {
-        const Row x = read_row(p, r, true);
-        if (x.last >= 0 && p.refs[x.last] > 1)
-            p.writers[x.last] = 0, p.latest[x.last] = -1;
-    }
-    const int free_here = count_free(p.refs, b0, b1, sums);
-    cluster_sync();
-    for (int r = r0 + tid; r < r1; r += kRankThreads) {
-        const Row x = read_row(p, r, false);
-        if (x.last >= 0 && p.refs[x.last] > 1) {
-            atomicAdd(p.writers + x.last, 1);
-            atomicMax(p.latest + x.last, r);
+    // A thread's rows stay in registers over the barriers: the last block only where it
+    // is shared, and its count.
+    Row row[kRows];
+    int held[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        const int r = r0 + tid + k * kRankThreads;
+        row[k] = {0, 0, -1};
+        held[k] = 0;
+        if (r >= r1)
+            continue;
+        row[k] = read_row(p, r);
+        if (row[k].last >= 0) {
+            held[k] = p.refs[row[k].last];
+            if (held[k] > 1)
+                p.writers[row[k].last] = 0, p.latest[row[k].last] = -1;
+            else
+                row[k].last = -1;
         }
     }
+    const int free_here = sum_of(my_free(p.refs, b0, b1), counts);
     cluster_sync();
-    // need: blocks below kCopyBit, rows that copy above
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        if (row[k].last >= 0) {
+            atomicAdd(p.writers + row[k].last, 1);
+            atomicMax(p.latest + row[k].last, r0 + tid + k * kRankThreads);
+        }
+    cluster_sync();
     constexpr int64_t low = (1ll << kCopyBit) - 1;
-    int64_t needs = 0, tokens = 0;
-    for (int t = r0; t < r1; t += kRankThreads) {
-        const int r = t + tid;
-        int64_t need = 0;
-        Row x = {0, 0, -1};
-        if (r < r1) {
-            x = read_row(p, r, false);
-            const int refs = x.last >= 0 ? p.refs[x.last] : 0;
-            if (refs <= 1 || (__ldcg(p.writers + x.last) == refs && __ldcg(p.latest + x.last) == r))
-                x.last = -1;
-            need = blocks_of(x.len + x.fresh, p.block_size) - blocks_of(x.len, p.block_size);
-            if (x.last >= 0)
-                need += 1 + (1ll << kCopyBit);
-        }
-        int64_t all_need, all_new;
-        const int64_t a = needs + prefix(need, sums, &all_need);
-        const int64_t b = tokens + prefix(x.fresh, sums, &all_new);
-        needs += all_need, tokens += all_new;
-        if (r < r1) {
-            p.row_len[r] = x.len;
-            p.row_new[r] = x.fresh;
-            p.row_copy[r] = x.last;
-            p.row_begin[r] = (int)(a & low);
-            p.row_token[r] = (int)b;
-        }
+    int64_t needs = 0, tokens = 0, begin[kRows], token[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        if (r0 + k * kRankThreads >= r1) // no thread has a row
+            continue;
+        Row &x = row[k];
+        const int r = r0 + tid + k * kRankThreads;
+        if (x.last >= 0 && __ldcg(p.writers + x.last) == held[k] && __ldcg(p.latest + x.last) == r)
+            x.last = -1;
+        // need: blocks below kCopyBit, rows that copy above
+        int64_t v[2] = {blocks_of(x.len + x.fresh, p.block_size) - blocks_of(x.len, p.block_size), x.fresh};
+        if (x.last >= 0)
+            v[0] += 1 + (1ll << kCopyBit);
+        int64_t all[2];
+        prefix(v, sums, all);
+        begin[k] = needs + v[0];
+        token[k] = tokens + v[1];
+        needs += all[0], tokens += all[1];
     }
     if (tid == 0)
-        p.told[rank] = {needs, tokens, free_here};
+        p.told[rank].v[0] = needs, p.told[rank].v[1] = tokens, p.told[rank].v[2] = free_here;
     cluster_sync();
-    int64_t need_before = 0, new_before = 0, need_all = 0, total = 0, free = 0;
-    int free_before = 0;
-    for (int c = 0; c < ctas; ++c) {
-        const int64_t a = __ldcg(&p.told[c].a), b = __ldcg(&p.told[c].b), f = __ldcg(&p.told[c].c);
-        if (c < rank)
-            need_before += a, new_before += b, free_before += (int)f;
-        need_all += a, total += b, free += f;
-    }
-    const int64_t want = need_all & low;
+    int64_t before[3], all[3];
+    hear(p.told, rank, ctas, before, all);
+    const int64_t need_before = before[0], new_before = before[1], free_before = before[2];
+    const int64_t need_all = all[0], total = all[1], free = all[2], want = need_all & low;
     const bool ok = want <= free && total <= p.num_tokens;
     if (rank == 0 && tid == 0) {
         if (!ok)
@@ -383,35 +431,37 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
         p.head[1] = ok ? (int)(need_all >> kCopyBit) : 0;
     }
     const int take = ok ? (int)want : 0;
-    ranked(p.refs, b0, b1, sums, [&](int id, int refs, int before) {
-        const int k = before + free_before;
-        const bool taken = refs == 0 && k < take;
-        if (taken)
-            p.free_ids[k] = id;
-        if (taken || p.refs_out != p.refs)
-            p.refs_out[id] = taken ? 1 : refs;
-    });
-    cluster_sync();
-    int copied = (int)(need_before >> kCopyBit); // rows before this one that copy
-    for (int t = r0; t < r1; t += kRankThreads) {
-        const int r = t + tid;
-        bool copies = false;
-        if (r < r1) {
-            copies = p.row_copy[r] >= 0 && ok;
-            p.row_begin[r] += (int)(need_before & low);
-            p.row_token[r] = ok ? p.row_token[r] + (int)(new_before & low) : 0;
-            if (!ok)
-                p.row_new[r] = 0, p.row_copy[r] = -1;
-            p.lens_out[r] = p.row_len[r] + (ok ? p.row_new[r] : 0);
-            if (copies)
-                atomicSub(p.refs_out + p.row_copy[r], 1);
-        }
-        int64_t all;
-        const int64_t at = prefix(copies, sums, &all);
+    if (take > free_before || p.refs_out != p.refs)
+        ranked(p.refs, b0, b1, counts, [&](int id, int refs, int before) {
+            const int k = before + (int)free_before;
+            const bool taken = refs == 0 && k < take;
+            if (taken)
+                p.free_ids[k] = id;
+            if (taken || p.refs_out != p.refs)
+                p.refs_out[id] = taken ? 1 : refs;
+        });
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        const int r = r0 + tid + k * kRankThreads;
+        if (r >= r1)
+            continue;
+        const Row &x = row[k];
+        const bool copies = ok && x.last >= 0;
+        const int64_t need = need_before + begin[k];
+        p.row_len[r] = x.len;
+        p.row_new[r] = ok ? x.fresh : 0;
+        p.row_copy[r] = copies ? x.last : -1;
+        p.row_begin[r] = (int)(need & low);
+        p.row_token[r] = ok ? (int)(new_before + token[k]) : 0;
+        p.lens_out[r] = x.len + (ok ? x.fresh : 0);
         if (copies)
-            p.copy_rows[copied + (int)at] = r;
-        copied += (int)all;
+            p.copy_rows[need >> kCopyBit] = r;
     }
+    cluster_sync();
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        if (ok && row[k].last >= 0)
+            atomicSub(p.refs_out + row[k].last, 1);
 }
 
 // The tables, the slots and the copies of extend: items of one list, CTA after
@@ -488,25 +538,20 @@ struct CompactParams {
 // k-th free id below n.
 __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const CompactParams p)
 {
-    __shared__ int64_t sums[32];
+    __shared__ int counts[32];
     griddep_wait();
     const int rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
     const int part = ((p.num_blocks + ctas - 1) / ctas + 31) / 32 * 32;
     const int b0 = min(p.num_blocks, rank * part), b1 = min(p.num_blocks, b0 + part);
-    const int mine = count_free(p.refs, b0, b1, sums);
+    const int mine = sum_of(my_free(p.refs, b0, b1), counts);
     if (tid == 0)
-        p.told[rank].a = mine;
-    if (rank == 0 && tid == 0)
-        p.head[0] = -1;
+        p.told[rank].v[0] = mine;
     cluster_sync();
-    int free_before = 0, free = 0;
-    for (int c = 0; c < ctas; ++c) {
-        const int a = (int)__ldcg(&p.told[c].a);
-        free_before += c < rank ? a : 0;
-        free += a;
-    }
+    int64_t before[1], all[1];
+    hear(p.told, rank, ctas, before, all);
+    const int free_before = (int)before[0], free = (int)all[0];
     const int n = p.num_blocks - free;
-    ranked(p.refs, b0, b1, sums, [&](int id, int refs, int before) {
+    ranked(p.refs, b0, b1, counts, [&](int id, int refs, int before) {
         const int f = before + free_before, live = id - f; // free and live ids below this one
         if (id == n)
             p.head[0] = live;
@@ -610,11 +655,14 @@ static cudaError_t launch_cluster(void (*kern)(const P), int ctas, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// CTAs of a ranking kernel: one while it holds everything in a tile, for its
-// barrier is the CTA's own then.
+// CTAs of a ranking kernel: one for each two tiles, so that small pools pay for no
+// cluster.
 static int rank_ctas(int rows, int num_blocks)
 {
-    return rows <= kRankThreads && num_blocks <= kTile ? 1 : kCluster;
+    int n = 1;
+    while (n < kCluster && (num_blocks > 2 * kTile * n || rows > 2 * kRankThreads * n))
+        n *= 2;
+    return n;
 }
 
 static pa_status read_pools(Pools<PA_MAX_POOLS> *to, const pa_block_pool *from, int count,
