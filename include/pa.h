@@ -621,8 +621,8 @@ typedef struct pa_block_pool {
  * after the other: where all holders of a block go on in it, the last keeps it).
  *   num_new        int32 [num_seqs]; a negative one, or one past the table's end,
  *                  counts as 0, flagged (PA_DEVERR_SEQ_LEN)
- *   slot_mapping   int64 [num_tokens]: the new tokens' slots, row after row, for
- *                  pa_reshape_and_cache; -1 behind the last
+ *   slot_mapping   int64 [num_tokens]: the new tokens' slots, row after row without
+ *                  gaps, for pa_reshape_and_cache; -1 behind the last
  *   info           int32 [2]: blocks that the call needs, and free blocks less
  *                  those.  Where that is negative, or slot_mapping is too short,
  *                  nothing is taken: tables, lengths and counts stay as they were,

@@ -674,7 +674,7 @@ def pa_extend_sequences(tables_out: torch.Tensor, seq_lens_out: torch.Tensor,
     """Room for ``num_new[s]`` more tokens in every row: the lowest free blocks in
     the order of rows, copies of last blocks that are shared (in every tensor of
     ``pools``, each [planes, num_blocks, ...]), and the new tokens' slots (int64,
-    -1 behind the last).  ``info`` (int32 [2]) receives the blocks needed and the
+    row after row without gaps, -1 behind the last).  ``info`` (int32 [2]) receives the blocks needed and the
     free blocks less those; if that is negative, or slot_mapping too short,
     nothing is taken.  Each output may be its input.  ``workspace`` holds
     pa_sequences_workspace_size bytes."""

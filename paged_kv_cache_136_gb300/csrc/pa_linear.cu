@@ -210,7 +210,8 @@ static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_kv_he
     if (max_query_len <= std::max<int64_t>(2 * share, 8 * kChunk))
         return {INT32_MAX, num_seqs};
     const int64_t segment = std::max<int64_t>(4, (share / 4 + kChunk - 1) / kChunk) * kChunk;
-    return {(int)segment, (int)(num_tokens / segment) + num_seqs + 1};
+    const int64_t lines = num_tokens / segment + num_seqs + 1;
+    return lines <= 65535 ? Cut{(int)segment, (int)lines} : Cut{INT32_MAX, num_seqs};
 }
 
 static bool rows_map(CUtensorMap *map, const void *x, pa_dtype dtype, int num_tokens, int heads,
@@ -354,8 +355,6 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
-    if (cut.lines > 65535)
-        return PA_ERR_UNSUPPORTED;
     p.num_seqs = num_seqs;
     p.segment = cut.segment;
     p.lines = cut.lines;
