@@ -19,22 +19,28 @@ namespace lin {
 constexpr int kStepThreads = 128, kCols = 64; // of a CTA of the recurrent kernel
 constexpr int kHeadsAtOnce = 8; // query heads whose products share the state in registers
 
-// One CTA walks one sequence's tokens for 64 value channels of one kv head with that
-// part of the state in registers: a thread has 4 value channels (16 bytes of a state's
-// row) of every 8th key channel, so the state is read and written once, in pieces of 256
-// bytes, with all of a CTA's loads in flight, and a token's products cost one pass over
-// registers and a sum over the 8 row groups in shared memory.  Bound by HBM.  Five small
-// CTAs an SM keep reads and writes going side by side, and the states, which the next
-// step wants, go past the caches: 64 x 32 states of 128 x 128 take 41 us, 6.5 TB/s, 256 x
-// 8 with four query heads each 43 (with cached loads and stores 43 and 46, with whole
-// states by 256 threads 51 and 56, with four heads in one pass over the state 45 and 47,
-// with the stores before the products 45 and 48).
+// S = e^g S + k v^T and out = scale q S, token by token.  One CTA walks one sequence's
+// tokens for 64 value channels of one kv head with that part of the state in registers: a
+// thread has 4 value channels (16 bytes of a state's row) of an eighth of the key
+// channels, so the state is read and written once, in pieces of 256 bytes, with all of a
+// CTA's loads in flight, and a token's products cost one pass over registers and a sum
+// over the 8 row groups in shared memory.
+//
+// One token is bound by HBM.  Five small CTAs an SM keep reads and writes going side by
+// side, and the states, which the next step wants, go past the caches: 64 x 32 states of
+// 128 x 128 take 40.7 us, 6.6 TB/s, 256 x 8 with four query heads each 41.4, with eight 43
+// (with rows one by one, not in fours, from shared memory 41.3, 43.1 and 47; that form
+// with cached loads and stores 43 and 46 for the first two, with whole states by 256
+// threads 51 and 56, with four heads in one pass over the state 45 and 47).  More tokens
+// are bound by their chain of sums and barriers: 0.8 us a token alone on the card, 256 x 8
+// with four heads 10.4 (13.5 without the next token's loads under way).
 template <typename T, int D, bool kPrompt>
 __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearParams p)
 {
-    constexpr int kLanes = kCols / 4, kGroups = kStepThreads / kLanes, kRows = D / kGroups;
-    __shared__ float sk[D], sq[kHeadsAtOnce][D];
-    __shared__ float part[kGroups][kHeadsAtOnce][kCols];
+    constexpr int kLanes = kCols / 4, kGroups = kStepThreads / kLanes, kQuads = D / kGroups / 4;
+    constexpr int kPairs = kHeadsAtOnce * D / 2 / kStepThreads; // of a thread, of the queries
+    __shared__ __align__(16) float sk[D], sq[kHeadsAtOnce][D];
+    __shared__ __align__(16) float part[kGroups][kHeadsAtOnce][kCols];
     griddep_wait();
     const int tid = threadIdx.x, head = blockIdx.x / (D / kCols), s = blockIdx.y;
     const int col0 = blockIdx.x % (D / kCols) * kCols; // this CTA's value channels
@@ -53,60 +59,107 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearP
         return;
     if (tid == 0 && blockIdx.x == 0 && (src >= p.num_states || dst >= p.num_states))
         atomicOr(p.err, PA_DEVERR_STATE_);
-    const int64_t at = (int64_t)group * D + col0 + col, one = (int64_t)D * D;
-    float4 S[kRows];
+    // rows 4 group to 4 group + 3 of every 4 kGroups
+    const int64_t at = (int64_t)group * 4 * D + col0 + col, one = (int64_t)D * D;
+    float4 S[kQuads][4];
     if (src >= 0 && src < p.num_states) {
         const float *const from = p.states + ((int64_t)src * p.num_kv_heads + head) * one + at;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            S[i] = __ldcs(reinterpret_cast<const float4 *>(from + (int64_t)i * kGroups * D));
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = __ldcs(reinterpret_cast<const float4 *>(from + (int64_t)(4 * kGroups * i + r) * D));
     } else {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int per = p.num_heads / p.num_kv_heads;
+
+    // A token's inputs, or those of its next kHeadsAtOnce heads, are loaded while the
+    // ones before are worked on.
+    uint32_t k2 = 0, q2[kPairs];
+    uint2 v4 = {};
+    float decay = 0.f;
+    auto load = [&](int t, int g0) {
+        if (g0 == 0) {
+            decay = p.log_decay[t * p.decay_stride + head];
+            const T *const k = static_cast<const T *>(p.k) + t * p.k_stride + (int64_t)head * D;
+            const T *const v = static_cast<const T *>(p.v) + t * p.v_stride + (int64_t)head * D + col0;
+            if (tid < D / 2)
+                k2 = reinterpret_cast<const uint32_t *>(k)[tid];
+            v4 = *reinterpret_cast<const uint2 *>(v + col);
+        }
+        const T *const q = static_cast<const T *>(p.q) + t * p.q_stride + ((int64_t)head * per + g0) * D;
+        const int pairs = min(kHeadsAtOnce, per - g0) * (D / 2);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            if (tid + i * kStepThreads < pairs)
+                q2[i] = reinterpret_cast<const uint32_t *>(q)[tid + i * kStepThreads];
+    };
+    auto stage = [&](int g0) {
+        if (g0 == 0 && tid < D / 2)
+            reinterpret_cast<float2 *>(sk)[tid] = block::float2_of<T>(k2);
+        const int pairs = min(kHeadsAtOnce, per - g0) * (D / 2);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            if (tid + i * kStepThreads < pairs) {
+                const float2 x = block::float2_of<T>(q2[i]);
+                reinterpret_cast<float2 *>(sq)[tid + i * kStepThreads] = make_float2(x.x * p.scale, x.y * p.scale);
+            }
+    };
+    if (t0 < t1) {
+        load(t0, 0);
+        stage(0);
+        __syncthreads();
+    }
     for (int t = t0; t < t1; ++t) {
+        T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + (int64_t)head * per) * D + col0;
         // The decay less one: a decay near one, rounded to 24 bits, would be off by
         // the same 2^-25 in every step, and 256 steps of memory by 2^-17.
-        const float a = expm1f(p.log_decay[t * p.decay_stride + head]);
-        const T *const k = static_cast<const T *>(p.k) + t * p.k_stride + head * D;
-        const T *const v = static_cast<const T *>(p.v) + t * p.v_stride + head * D + col0;
-        const T *const q = static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)head * per * D;
-        T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + head * per) * D + col0;
-        const float2 v01 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col));
-        const float2 v23 = block::float2_of<T>(*reinterpret_cast<const uint32_t *>(v + col + 2));
+        const float a = expm1f(decay);
+        const float2 v01 = block::float2_of<T>(v4.x), v23 = block::float2_of<T>(v4.y);
         for (int g0 = 0; g0 < per; g0 += kHeadsAtOnce) {
             const int n = min(kHeadsAtOnce, per - g0);
-            if (g0 == 0)
-                for (int i = tid; i < D; i += kStepThreads)
-                    sk[i] = (float)k[i];
-            for (int i = tid; i < n * D; i += kStepThreads)
-                sq[i / D][i % D] = (float)q[g0 * D + i] * p.scale;
-            __syncthreads();
+            const bool last = g0 + kHeadsAtOnce >= per, more = !last || t + 1 < t1;
+            const int next = last ? 0 : g0 + kHeadsAtOnce;
+            if (more)
+                load(last ? t + 1 : t, next);
             if (g0 == 0) {
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const float kk = sk[group + i * kGroups];
-                    S[i].x = fmaf(kk, v01.x, fmaf(a, S[i].x, S[i].x));
-                    S[i].y = fmaf(kk, v01.y, fmaf(a, S[i].y, S[i].y));
-                    S[i].z = fmaf(kk, v23.x, fmaf(a, S[i].z, S[i].z));
-                    S[i].w = fmaf(kk, v23.y, fmaf(a, S[i].w, S[i].w));
+                for (int i = 0; i < kQuads; ++i) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&sk[4 * (kGroups * i + group)]);
+                    const float k4[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        S[i][r].x = fmaf(k4[r], v01.x, fmaf(a, S[i][r].x, S[i][r].x));
+                        S[i][r].y = fmaf(k4[r], v01.y, fmaf(a, S[i][r].y, S[i][r].y));
+                        S[i][r].z = fmaf(k4[r], v23.x, fmaf(a, S[i][r].z, S[i][r].z));
+                        S[i][r].w = fmaf(k4[r], v23.y, fmaf(a, S[i][r].w, S[i][r].w));
+                    }
                 }
             }
             for (int g = 0; g < n; ++g) {
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const float qq = sq[g][group + i * kGroups];
-                    o.x = fmaf(qq, S[i].x, o.x);
-                    o.y = fmaf(qq, S[i].y, o.y);
-                    o.z = fmaf(qq, S[i].z, o.z);
-                    o.w = fmaf(qq, S[i].w, o.w);
+                for (int i = 0; i < kQuads; ++i) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(&sq[g][4 * (kGroups * i + group)]);
+                    const float qr[4] = {qq.x, qq.y, qq.z, qq.w};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        o.x = fmaf(qr[r], S[i][r].x, o.x);
+                        o.y = fmaf(qr[r], S[i][r].y, o.y);
+                        o.z = fmaf(qr[r], S[i][r].z, o.z);
+                        o.w = fmaf(qr[r], S[i][r].w, o.w);
+                    }
                 }
                 *reinterpret_cast<float4 *>(&part[group][g][col]) = o;
             }
             __syncthreads();
+            if (more)
+                stage(next);
             for (int i = tid; i < n * kCols; i += kStepThreads) {
                 float o = 0.f;
 #pragma unroll
@@ -114,14 +167,17 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearP
                     o += part[j][i / kCols][i % kCols];
                 out[(g0 + i / kCols) * D + i % kCols] = (T)o;
             }
-            __syncthreads();
+            if (more)
+                __syncthreads();
         }
     }
     if (dst < p.num_states) {
         float *const to = p.states + ((int64_t)dst * p.num_kv_heads + head) * one + at;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            __stcs(reinterpret_cast<float4 *>(to + (int64_t)i * kGroups * D), S[i]);
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __stcs(reinterpret_cast<float4 *>(to + (int64_t)(4 * kGroups * i + r) * D), S[i][r]);
     }
 }
 
@@ -193,25 +249,101 @@ static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_siz
 // Prompts on the tensor cores
 // ---------------------------------------------------------------------------
 constexpr int kSms = 152;
-// The longest prompt, in tokens, that the recurrent kernel takes.
+// The longest prompt, in tokens, that the recurrent kernel takes.  A chunk costs the same
+// however few its tokens.  1, 4, 8, 16 and 32 tokens in us, and chunks: 1 sequence of 32
+// heads 8, 10, 12, 20, 35, chunks 16; 32 of 32 heads 29, 39, 55, 84, 152, chunks 84; 256
+// of 32 heads and 8 kv heads 49, 75, 117, 205, 385, chunks 231; with head_size 64 256 of 8
+// heads 18, 25, 35, 57, 104, chunks 117 to 121.
 constexpr int kShort = 16;
 
 // How prompts are cut.  A sequence and kv head is a chain of chunks that one CTA
-// walks.  Where the longest chain takes more than twice an SM's share of all work,
-// sequences are cut into segments (four for each SM, no shorter than four chunks)
-// whose states a first pass forms, at the price of reading K and V twice.
+// walks, an SM at a time.  Chains can be cut into segments whose states a first pass
+// forms, at the price of reading K and V twice.  Taken is the best of at most eight
+// cuts, the ones whose segments fill the SMs once, twice, ..., if it is an eighth
+// better than none, by these times in us (head_size 128; 64 is a tenth to a fifth
+// less on both sides): a chunk 2.3 for each query head and 2.4, or 3.9 with one query
+// head, in the first pass 2.5; a chain 8, a segment 12 in both passes; launches 4 and
+// 10.  Measured, without a cut and with the one taken: one prompt of 1024, 4096 and
+// 16384 tokens, 32 heads, 8 kv heads 102 and 35, 379 and 53, 1485 and 130; 32 kv heads
+// 43 and 38, 135 and 78, 506 and 228; 4 prompts of 4096 there, left alone, 141 and 204;
+// 512 tokens there 27 and 31, with 8 kv heads 55 and 34.
 struct Cut {
     int segment, lines;
 };
 
-static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_kv_heads)
+constexpr float kPassChunk = 2.5f, kChain = 8.f, kSegment = 12.f, kOnePass = 4.f, kTwoPasses = 10.f;
+
+struct Work {
+    float chunks, longest; // in chunks
+    int seqs, kv_heads;
+    // us of a chunk of `chunk` us each
+    float uncut(float chunk, float fixed) const
+    {
+        const float rounds = ceilf((float)seqs * kv_heads / kSms);
+        return std::max(longest * chunk + kChain * fixed,
+                        rounds * (chunks / seqs * chunk + kChain * fixed)) + kOnePass * fixed;
+    }
+    // chunks of a segment that fills the SMs `rounds` times; 0 if it does not cut
+    int segment(int rounds) const
+    {
+        const int each = kSms * rounds / kv_heads; // segments of a kv head
+        const int n = each ? (int)ceilf(chunks / each) : 0;
+        return n < longest ? n : 0;
+    }
+    bool better(int rounds, int n, float chunk, float fixed, float &best) const
+    {
+        const float us = rounds * ((chunk + kPassChunk * fixed) * n + kSegment * fixed) + kTwoPasses * fixed;
+        if (us >= best)
+            return false;
+        best = us;
+        return true;
+    }
+};
+constexpr int kRounds = 8;
+
+static Work work_of(int num_seqs, int num_tokens, int max_query_len, int num_kv_heads)
 {
-    const int64_t share = (int64_t)num_tokens * num_kv_heads / kSms;
-    if (max_query_len <= std::max<int64_t>(2 * share, 8 * kChunk))
-        return {INT32_MAX, num_seqs};
-    const int64_t segment = std::max<int64_t>(4, (share / 4 + kChunk - 1) / kChunk) * kChunk;
-    const int64_t lines = num_tokens / segment + num_seqs + 1;
-    return lines <= 65535 ? Cut{(int)segment, (int)lines} : Cut{INT32_MAX, num_seqs};
+    return {(float)num_tokens / kChunk, ceilf((float)std::min(num_tokens, max_query_len) / kChunk),
+            std::max(1, num_seqs), num_kv_heads};
+}
+
+static int64_t lines_of(int segment_chunks, int num_seqs, int num_tokens)
+{
+    return num_tokens / ((int64_t)segment_chunks * kChunk) + num_seqs + 1;
+}
+
+static float chunk_us(int heads_each) { return heads_each == 1 ? 3.9f : 2.3f * heads_each + 2.4f; }
+
+static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_heads, int num_kv_heads)
+{
+    const Work w = work_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    const float chunk = chunk_us(num_heads / num_kv_heads);
+    float best = 0.875f * w.uncut(chunk, 1.f);
+    Cut cut = {INT32_MAX, num_seqs};
+    for (int r = 1; r <= kRounds; ++r) {
+        const int n = w.segment(r);
+        if (n && lines_of(n, num_seqs, num_tokens) <= 65535 && w.better(r, n, chunk, 1.f, best))
+            cut = {n * kChunk, (int)lines_of(n, num_seqs, num_tokens)};
+    }
+    return cut;
+}
+
+// The most lines that cut_of can ask for with any number of query heads: a cut's time
+// is linear in a chunk's and the uncut time convex, so a cut that is no better with one
+// query head or with very many is none in between.
+static int64_t most_lines(int num_seqs, int num_tokens, int max_query_len, int num_kv_heads)
+{
+    const Work w = work_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    int64_t most = 0;
+    for (int r = 1; r <= kRounds; ++r) {
+        const int n = w.segment(r);
+        if (!n || lines_of(n, num_seqs, num_tokens) > 65535)
+            continue;
+        float one = 0.875f * w.uncut(chunk_us(1), 1.f), many = 0.875f * w.uncut(1.f, 0.f) * 1.0001f;
+        if (w.better(r, n, chunk_us(1), 1.f, one) || w.better(r, n, 1.f, 0.f, many))
+            most = std::max(most, lines_of(n, num_seqs, num_tokens));
+    }
+    return most;
 }
 
 static bool rows_map(CUtensorMap *map, const void *x, pa_dtype dtype, int num_tokens, int heads,
@@ -313,11 +445,11 @@ size_t pa_linear_prefill_workspace_size(int num_seqs, int num_tokens, int max_qu
 {
     if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || num_kv_heads <= 0 || head_size <= 0)
         return 0;
-    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
-    if (cut.segment == INT32_MAX)
+    const int64_t lines = most_lines(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    if (lines == 0)
         return 256;
     const size_t each = (size_t)num_kv_heads * 4 * ((size_t)head_size * head_size + 1);
-    return (each * (size_t)cut.lines + 255) / 256 * 256;
+    return (each * (size_t)lines + 255) / 256 * 256;
 }
 
 pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void *v,
@@ -354,7 +486,7 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
         e = launch_step<true>(p, num_seqs, head_size, dtype, s);
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
-    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
+    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads);
     p.num_seqs = num_seqs;
     p.segment = cut.segment;
     p.lines = cut.lines;

@@ -22,7 +22,7 @@ namespace seqs {
 constexpr int kThreads = 256;      // of the wide kernels
 constexpr int kChunk = 1024;       // table entries of a CTA
 constexpr int kRankThreads = 1024; // of a CTA of the ranking kernels
-constexpr int kCluster = 8;        // CTAs of a ranking kernel, at most
+constexpr int kCluster = 8;        // CTAs of a ranking kernel
 constexpr int kRows = 8;           // table rows of a thread of theirs: 65536 in all
 constexpr int kTile = 4 * kRankThreads; // counts that a CTA ranks at once
 constexpr int kUnit = 16384;       // bytes of a block that a CTA copies at once
@@ -42,8 +42,8 @@ struct Pool {
     int width;           // bytes of a load: 16, 4 or 1
 };
 
-template <int N> struct Pools {
-    Pool pool[N];
+struct Pools {
+    Pool pool[PA_MAX_POOLS];
     int count, units;    // units of a block, over all pools
 };
 
@@ -68,8 +68,7 @@ __device__ __forceinline__ void copy_bytes(uint8_t *dst, const uint8_t *src, int
     }
 }
 
-template <int N>
-__device__ __forceinline__ void copy_unit(const Pools<N> &ps, int u, int64_t src, int64_t dst)
+__device__ __forceinline__ void copy_unit(const Pools &ps, int u, int64_t src, int64_t dst)
 {
     int lo = 0, hi = ps.count - 1; // the last pool that begins at or before u
     while (lo < hi) {
@@ -156,8 +155,11 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p)
                 v[k] = src[base + tid + k * kThreads];
 #pragma unroll
         for (int k = 0; k < kChunk / kThreads; ++k)
-            if (base + tid + k * kThreads < end)
+            if (base + tid + k * kThreads < end) {
+                if (v[k] < 0 || v[k] >= p.num_blocks)
+                    atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
                 dst[base + tid + k * kThreads] = v[k];
+            }
     }
     if (r >= p.rows_in)
         return;
@@ -466,9 +468,8 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
 
 // The tables, the slots and the copies of extend: items of one list, CTA after
 // CTA.  Bound by the copies' bytes where there are any, else by latency.
-template <int N>
 __global__ void __launch_bounds__(kThreads) extend_apply_kernel(const ExtendParams p,
-                                                                const __grid_constant__ Pools<N> ps)
+                                                                const __grid_constant__ Pools ps)
 {
     griddep_wait();
     const int tid = threadIdx.x, tokens = p.head[0], bs = p.block_size;
@@ -583,9 +584,8 @@ __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const Compac
 }
 
 // The moves and the tables of compact; as extend_apply_kernel.
-template <int N>
 __global__ void __launch_bounds__(kThreads) compact_apply_kernel(const CompactParams p,
-                                                                 const __grid_constant__ Pools<N> ps)
+                                                                 const __grid_constant__ Pools ps)
 {
     griddep_wait();
     const int64_t copies = (int64_t)p.head[1] * ps.units;
@@ -636,37 +636,26 @@ static pa_status check_sizes(int rows, int num_blocks, int max_blocks, int block
     return PA_OK;
 }
 
-// Launch on one cluster of `ctas` CTAs, after the kernel before.
+// Launch on one cluster, after the kernel before.
 template <typename P>
-static cudaError_t launch_cluster(void (*kern)(const P), int ctas, cudaStream_t s, const P &p)
+static cudaError_t launch_cluster(void (*kern)(const P), cudaStream_t s, const P &p)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kRankThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = kCluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// CTAs of a ranking kernel: one for each two tiles, so that small pools pay for no
-// cluster.
-static int rank_ctas(int rows, int num_blocks)
-{
-    int n = 1;
-    while (n < kCluster && (num_blocks > 2 * kTile * n || rows > 2 * kRankThreads * n))
-        n *= 2;
-    return n;
-}
-
-static pa_status read_pools(Pools<PA_MAX_POOLS> *to, const pa_block_pool *from, int count,
-                            int num_blocks)
+static pa_status read_pools(Pools *to, const pa_block_pool *from, int count, int num_blocks)
 {
     if (count < 0 || (count > 0 && !from))
         return PA_ERR_INVALID_ARG;
@@ -696,26 +685,16 @@ static pa_status read_pools(Pools<PA_MAX_POOLS> *to, const pa_block_pool *from, 
     return PA_OK;
 }
 
-// Few pools travel in a small parameter block: a launch copies all of it.
-constexpr int kFewPools = 16;
-
 template <typename P>
-static cudaError_t launch_apply(void (*few)(const P, const Pools<kFewPools>),
-                                void (*many)(const P, const Pools<PA_MAX_POOLS>), const P &p,
-                                const Pools<PA_MAX_POOLS> &ps, int64_t items, cudaStream_t s)
+static cudaError_t launch_apply(void (*kern)(const P, const Pools), const P &p, const Pools &ps,
+                                int64_t items, cudaStream_t s)
 {
     cudaError_t e;
     const int sms = sm_count(&e);
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * 8)));
-    if (ps.count > kFewPools)
-        return launch_after_previous(many, grid, dim3(kThreads), 0, s, p, ps);
-    Pools<kFewPools> f;
-    std::copy(ps.pool, ps.pool + ps.count, f.pool);
-    f.count = ps.count;
-    f.units = ps.units;
-    return launch_after_previous(few, grid, dim3(kThreads), 0, s, p, f);
+    return launch_after_previous(kern, grid, dim3(kThreads), 0, s, p, ps);
 }
 
 } // namespace seqs
@@ -813,7 +792,7 @@ pa_status pa_extend_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_
         (ref_counts_out != ref_counts &&
          overlap(ref_counts_out, 4ll * num_blocks, ref_counts, 4ll * num_blocks)))
         return PA_ERR_INVALID_ARG;
-    Pools<PA_MAX_POOLS> ps;
+    Pools ps;
     st = read_pools(&ps, pools, num_pools, num_blocks);
     if (st != PA_OK)
         return st;
@@ -852,13 +831,12 @@ pa_status pa_extend_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_
     p.len_cap = max_blocks_per_seq * block_size;
     p.num_tokens = num_tokens;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_cluster(extend_rank_kernel, rank_ctas(num_seqs, num_blocks), s, p) != cudaSuccess)
+    if (launch_cluster(extend_rank_kernel, s, p) != cudaSuccess)
         return PA_ERR_CUDA;
     // as many items as there can be: every row may copy its last block
     const int64_t items = (int64_t)num_seqs * ((max_blocks_per_seq + kChunk - 1) / kChunk) +
                           (num_tokens + kThreads - 1) / kThreads + (int64_t)num_seqs * ps.units;
-    e = launch_apply(extend_apply_kernel<kFewPools>, extend_apply_kernel<PA_MAX_POOLS>, p, ps,
-                     items, s);
+    e = launch_apply(extend_apply_kernel, p, ps, items, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -882,7 +860,7 @@ pa_status pa_compact_blocks(int32_t *tables_out, int32_t *ref_counts_out, int32_
         overlap(new_ids, counts, ref_counts, counts) ||
         overlap(new_ids, counts, ref_counts_out, counts))
         return PA_ERR_INVALID_ARG;
-    Pools<PA_MAX_POOLS> ps;
+    Pools ps;
     st = read_pools(&ps, pools, num_pools, num_blocks);
     if (st != PA_OK)
         return st;
@@ -911,12 +889,11 @@ pa_status pa_compact_blocks(int32_t *tables_out, int32_t *ref_counts_out, int32_
     p.block_size = block_size;
     p.len_cap = max_blocks_per_seq * block_size;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_cluster(compact_rank_kernel, rank_ctas(0, num_blocks), s, p) != cudaSuccess)
+    if (launch_cluster(compact_rank_kernel, s, p) != cudaSuccess)
         return PA_ERR_CUDA;
     const int64_t items = (int64_t)num_seqs * ((max_blocks_per_seq + kChunk - 1) / kChunk) +
                           (int64_t)num_blocks * ps.units;
-    e = launch_apply(compact_apply_kernel<kFewPools>, compact_apply_kernel<PA_MAX_POOLS>, p, ps,
-                     items, s);
+    e = launch_apply(compact_apply_kernel, p, ps, items, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
