@@ -536,7 +536,8 @@ pa_status pa_copy_blocks(void *kv_cache, const int64_t *block_mapping, int num_p
  *   q            [num_tokens, num_heads, head_size], k and v [num_tokens,
  *                num_kv_heads, head_size], dtype; row t of each at its own token
  *                stride (elements, a multiple of 8, at least the row).
- *   out          [num_tokens, num_heads, head_size], dtype, contiguous.
+ *   out          [num_tokens, num_heads, head_size], dtype, contiguous; it must not
+ *                overlap an input.
  *   log_decay    float32: g of token t and kv head h at t * decay_stride + h;
  *                decay_stride 0: one for each head.  At most 0 (-inf is a decay
  *                of 0); growth may overflow.
@@ -555,9 +556,10 @@ pa_status pa_copy_blocks(void *kv_cache, const int64_t *block_mapping, int num_p
  *   workspace        pa_linear_prefill_workspace_size bytes, 256-byte aligned,
  *                    with the rules of pa_decode_splitk's
  * Its products run on the tensor cores with 16-bit operands.  Scores times decays
- * (P), decayed values and states go in as a rounded 16-bit part plus the rounded
- * remainder: 2^-17 of their size with bf16 and 2^-22 with fp16, so that the one
- * visible rounding is the output's own.
+ * (P) and states go in as a rounded 16-bit part plus the rounded remainder: 2^-17 of
+ * their size with bf16 and 2^-22 with fp16, so that the one visible rounding is the
+ * output's own.  Decayed values, which make the states, go in as two parts with fp16
+ * and three with bf16 (2^-24).
  */
 pa_status pa_linear_decode(void *out, const void *q, const void *k, const void *v,
                            const float *log_decay, int64_t decay_stride, float *states,

@@ -6,10 +6,10 @@
 // log decays up to its token i, and S the state before the chunk,
 //   o_i = e^(b_i) q_i S + sum_(j<=i) e^(b_i - b_j) (q_i . k_j) v_j
 //   S'  = e^(b_last) S + sum_j k_j (e^(b_last - b_j) v_j)^T
-// which is four products of 128 rows: Q K^T, P V, Q S and V'^T K.  Every exponent
-// is formed as a sum of the log decays between two tokens, never as a difference of
-// large sums: between blocks of 32 tokens as (rest of the column's block) + (blocks
-// between) + (the row's block up to it), each factor at most 1.
+// which is four products of 128 rows: Q K^T, P V, Q S and V'^T K.  An exponent between
+// blocks of 32 tokens is a sum of the log decays between two tokens (rest of the
+// column's block, blocks between, the row's block up to it), each factor at most 1 if
+// decays are; within a block it is a difference of two sums of at most 32.
 //
 // Precision.  P, S and V' are fp32 values that enter a product as a 16-bit part and
 // the rounded remainder (two MMAs that share the other operand).  One part alone
@@ -19,6 +19,13 @@
 // bits.  The state itself stays in fp32 registers and is only added to by fp32
 // additions that round to nearest.
 //
+// Bounds.  A chunk of 128 x 128 takes 3.9 us (8000 cycles) with one query head a kv head
+// and about 2.4 for each of more (5000), about twice its MMAs' time (64 and 40 of 64
+// cycles each).  With one head the chain V' -> delta -> state -> operand -> Q S sets the
+// pace, each step a wait for the one before, with more of them the rows' chain scores ->
+// P -> P V -> output.  16 prompts of 256 to 2048 tokens, 32 heads, take 207 us; one of
+// 131072, 64 heads and 8 kv heads, 1.41 ms, in which the MMAs run at 1.1 PFLOP/s.
+//
 // A CTA walks one segment of one sequence for one kv head with all of its query
 // heads.  Roles in a CTA of 640 threads:
 //   warps 0-7    a row of the chunk and half of its columns per thread: P from the
@@ -27,10 +34,10 @@
 //   warps 8-15   a value channel and half of the key channels (and tokens) per thread:
 //                V' from the V tile, and the state (in registers), which goes to
 //                shared memory as the operand of the next chunk's Q S
-//   warp 16      a chunk's decay sums, and its tiles by TMA: K (2 slots), the query
-//                heads' Q (2 slots), V (1 slot)
+//   warp 16      a chunk's decay sums, and its tiles by TMA: K (2 slots) and Q and V (2
+//                slots and 1, or with one query head 1 and 2)
 //   warp 17      the MMAs: per query head O = Q S, O += P V, the next head's scores;
-//                per chunk, after the first head's P V, delta = V'^T K
+//                per chunk delta = V'^T K, behind the second head's Q S (the only one's)
 //   warp 18      output tiles to global memory by TMA
 //   warp 19      looks through V tiles: rows behind the sequence and values that are not
 //                finite become zeros; with fp16 the channels' largest magnitudes
@@ -54,7 +61,6 @@ namespace pa {
 namespace lin {
 
 constexpr int kChunk = 128;        // tokens
-constexpr int kBlock = 32;         // tokens whose decays are summed as one
 constexpr int kTcThreads = 640;
 constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18, kLookWarp = 19;
 // Five warpgroups are launched with 96 registers a thread; the last one, whose warps
@@ -307,7 +313,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool tell = head == 0 && y == (int)gridDim.y - 1 && !kParts;
     if (p.segment == INT32_MAX) {
         // One segment each.  Of up to 32 sequences line y is the y-th longest, so that the
-        // long ones start first; with more of them their chains are many and even out.
+        // long ones start first (8 of 32 to 4000 tokens, 32 heads: 133 us, in their own order
+        // 188; 16 ascending ones 271 and 315; 24 in any order with 8 kv heads 373 and 369);
+        // with more of them their chains are many and even out.
         if (warp == 0) {
             int q0, len = -1, n = 0, s = y;
             if (p.num_seqs > 32) {
@@ -373,7 +381,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // With one query head a kv head (and without any, in the first pass) a chunk is short,
     // and its chain -- V', delta, state -- sets the pace: V is loaded a chunk ahead, into
     // what is the second Q slot otherwise, Q's slot is free after Q S, and the output
-    // goes over the K tile.
+    // goes over the K tile.  With more of them two Q slots let a head's scores be formed
+    // during the one before, and V has a chunk's time to arrive.
     const bool solo = kParts || per == 1;
     auto v_slot = [&](int c) { return solo ? c & 1 : 0; };
     auto v_phase = [&](int c) { return (uint32_t)(solo ? c >> 1 : c) & 1; };
@@ -425,12 +434,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     return false;
                 Decays &d = m->dec[b];
                 float upto[4], rest[4];
-                // in log2 units; below 2^-128 is 0, and a difference of two such sums stays
+                // in log2 units; below 2^-149 is 0, and a difference of two such sums stays
                 // a number
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     g[i] *= 1.4426950408889634f;
-                    g[i] = g[i] < -128.f ? -128.f : g[i];
+                    g[i] = g[i] < -150.f ? -150.f : g[i];
                 }
                 upto[0] = g[0];
 #pragma unroll
@@ -1079,8 +1088,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 back = power_of_two(exponent(ch));
             }
             // V', decayed to the chunk's end, from the last block on: of each block of 32
-            // tokens this warp has 16 channels.  Transposed 8x8 matrices give a lane two tokens of a channel, as the
-            // operand in tensor memory wants them.
+            // tokens this warp has 16 channels.  Transposed 8x8 matrices give a lane two
+            // tokens of a channel, as the operand in tensor memory wants them.
             const uint32_t tile = smem_addr(smem + v_offset(c) + (wg / 2) * kRegion) +
                                   (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 128 +
                                              ((((wg & 1) * 4 + half * 2 + (lane >> 3 & 1)) ^ (lane & 7)) * 16));

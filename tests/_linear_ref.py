@@ -44,8 +44,11 @@ def ref_linear(q, k, v, log_decay, states, src, dst, starts, scale):
 # off by (eps / 2)^2 of its size: 2^-16 with bf16, 2^-22 with fp16.  An output's sum
 # has at most two such values behind a term (a state that was made of decayed values,
 # then split itself).  In fp32: a decay's exponent is a sum of at most 7 levels, off by
-# 7 * 2^-24 * |x|, and |x| e^-|x| <= 0.37; exponentials 2^-22; a product's 8 steps of 16
-# terms that the matrix unit adds with truncation, 2^-23 each, twice: below 2^-18 in all.
+# 7 * 2^-24 * |x|, and |x| e^-|x| <= 0.37 (within a block of 32 tokens it is a difference
+# of two sums u from the block's first token, each off by 2^-24 |u| a level: with the
+# decays of `inputs` |u| is at most 23 and 6 at the mean, and the levels' errors have both
+# signs); exponentials 2^-22; a product's 8 steps of 16 terms that the matrix unit adds
+# with truncation, 2^-23 each, twice: below 2^-18 in all.
 SLACK = {torch.bfloat16: 2.0 ** -15 + 2.0 ** -18, torch.float16: 2.0 ** -21 + 2.0 ** -18}
 
 

@@ -334,3 +334,70 @@ def test_no_sequences_and_no_tokens(pa):
     y = inputs([], 2, 2, 64, "fp16", "head", seed=18, tail=4)
     out = prefill(pa, y)
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("run", [decode, prefill])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_a_decay_of_zero_forgets_large_states(pa, run, dtype):
+    """exp(-inf) is 0, not a small number: nothing of 1e35 is left.  (2^-8 of the sum of
+    absolute values is twice the outputs' rounding; the smallest 32-bit number times 1e35
+    would be 1e-4 at least, and times the sums of 64 channels more.)"""
+    lens = [1] * 3 if run is decode else [5, 1, 300]
+    x = inputs(lens, 4, 2, 64, dtype, "token", seed=21)
+    x["states"] *= 1e35 / 16
+    x["log_decay"][x["starts"][:-1].long()] = -math.inf
+    ref, states, mag, smag = ref_linear(*(x[k] for k in ("q", "k", "v", "log_decay", "states", "src",
+                                                         "dst", "starts", "scale")))
+    out = run(pa, x)
+    assert bool(((out.double() - ref).abs() <= 2.0 ** -8 * mag + 2.0 ** -24).all())
+    to = x["dst"].long()
+    assert bool(((x["states"].double() - states).abs() <= 2.0 ** -15 * smag)[to].all())
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_far_tokens(pa):
+    """Token rows, outputs and states beyond 2^32 bytes and 2^31 elements."""
+    t, h, hkv, d = 70_000, 256, 2, 128
+    # sequences of t - 280 (a padding row), 130, 9 and 141 tokens
+    g = torch.Generator().manual_seed(22)
+    q = torch.empty(t, h, d, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    k, v = (torch.randn(t, hkv, d, generator=g).half().cuda() for _ in range(2))
+    q[-280:] = torch.randn(280, h, d, generator=g).half().cuda()
+    out[-280:], out[:9] = 7.0, 7.0
+    decay = (-torch.rand(t, hkv, generator=g) / 16).cuda()
+    ns = (1 << 31) // (hkv * d * d) + 8
+    states = torch.empty(ns, hkv, d, d, device="cuda")
+    src = torch.tensor([3, ns - 1, -1, ns - 2], dtype=torch.int32, device="cuda")
+    dst = torch.tensor([-1, ns - 3, ns - 4, ns - 2], dtype=torch.int32, device="cuda")
+    states[-4:] = torch.randn(4, hkv, d, d, generator=g).cuda()
+    starts = torch.tensor([0, t - 280, t - 150, t - 141, t], dtype=torch.int32, device="cuda")
+    # states[-4:] as a pool of their own
+    ref, rs, mag, smag = ref_linear(q[-280:].cpu(), k[-280:].cpu(), v[-280:].cpu(), decay[-280:].cpu(),
+                                    states[-4:].cpu(), torch.tensor([3, -1, 2]), torch.tensor([1, 0, 2]),
+                                    starts[1:].cpu() - (t - 280), 0.1)
+    n = pa.pa_linear_prefill_workspace_size(4, t, t, hkv, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pa.pa_linear_prefill(out, q, k, v, decay, states, src, dst, starts, 0.1, t, ws)
+    assert bool((out[:9] == 7.0).all())
+    check_out(out[-280:].cpu(), ref, mag)
+    check_states(states[-4:].cpu(), rs, smag, out.dtype)
+    # one token of each sequence, of rows a long way apart
+    wide = torch.empty(130, 1 << 24, dtype=torch.float16, device="cuda")
+    row = 4 * d + 2 * hkv * d
+    wide[:, :row] = torch.randn(130, row, generator=g).half().cuda()
+    q, k, v = wide[:, :row].split([4 * d, hkv * d, hkv * d], dim=1)
+    q, k, v = q.view(130, 4, d), k.view(130, hkv, d), v.view(130, hkv, d)
+    src = torch.full((130,), -1, dtype=torch.int32, device="cuda")
+    dst, decay = src.clone(), decay[-130:].contiguous()
+    src[-2:], dst[-2:] = ns - 2, ns - 2
+    src[-2], dst[-2] = ns - 3, ns - 1
+    out = torch.full((130, 4, d), 7.0, dtype=torch.float16, device="cuda")
+    old = states[-4:].cpu()
+    ref, rs, mag, smag = ref_linear(q[-2:].cpu(), k[-2:].cpu(), v[-2:].cpu(), decay[-2:].cpu(), old,
+                                    torch.tensor([1, 2]), torch.tensor([3, 2]), torch.tensor([0, 1, 2]), 0.1)
+    pa.pa_linear_decode(out, q, k, v, decay, states, src, dst, 0.1)
+    assert bool((out[:-2] == 7.0).all())
+    check_out(out[-2:].cpu(), ref, mag)
+    check_states(states[-4:].cpu(), rs, smag, out.dtype)
+    assert pa.pa_device_errors(clear=True) == 0
