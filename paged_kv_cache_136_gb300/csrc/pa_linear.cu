@@ -248,7 +248,6 @@ static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_siz
 // ---------------------------------------------------------------------------
 // Prompts on the tensor cores
 // ---------------------------------------------------------------------------
-constexpr int kSms = 152;
 // The longest prompt, in tokens, that the recurrent kernel takes.  A chunk costs the same
 // however few its tokens.  1, 4, 8, 16 and 32 tokens in us, and chunks: 1 sequence of 32
 // heads 8, 10, 12, 20, 35, chunks 16; 32 of 32 heads 29, 39, 55, 84, 152, chunks 84; 256

@@ -14,9 +14,9 @@
 // Precision.  P, S and V' are fp32 values that enter a product as a 16-bit part and
 // the rounded remainder (two MMAs that share the other operand).  One part alone
 // would add the error of a second output rounding, and 2^-9 to the states.  fp16
-// operands are scaled by powers of two (P by row, V' by channel, S as a whole), so
-// that large scores or states do not leave fp16's range and small ones keep their
-// bits.  The state itself stays in fp32 registers and is only added to by fp32
+// operands are scaled by powers of two (P by row, V' by chunk, S as a whole), so that
+// large scores or states do not leave fp16's range and small ones keep their bits:
+// those down to 2^-17 of the largest all 22, smaller ones what lies above 2^-39 of it.  The state itself stays in fp32 registers and is only added to by fp32
 // additions that round to nearest.
 //
 // Bounds.  A chunk of 128 x 128 takes 3.9 us (8000 cycles) with one query head a kv head
@@ -40,7 +40,7 @@
 //                per chunk delta = V'^T K, behind the second head's Q S (the only one's)
 //   warp 18      output tiles to global memory by TMA
 //   warp 19      looks through V tiles: rows behind the sequence and values that are not
-//                finite become zeros; with fp16 the channels' largest magnitudes
+//                finite become zeros; with fp16 the largest magnitude
 // Two threads share a row or a channel because one warp a scheduler is not enough to
 // hide the latency of tensor memory and of fetching a role's instructions; the loops
 // over blocks are rolled for the latter's sake.
@@ -67,6 +67,7 @@ constexpr int kProducerWarp = 16, kMmaWarp = 17, kStoreWarp = 18, kLookWarp = 19
 // issue copies and MMAs, hands some to the two that hold states: 2 * 128 + 2 * 96 + 32.
 constexpr int kRegsLaunched = 96, kRegsFew = 32, kRegsMany = 128;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kSms = 152;
 // Named barriers: of all rows, of all channels, of the two warps that share 32 rows (4).
 constexpr int kRowsBarrier = 1, kChannelsBarrier = 2, kPairBarrier = 3;
 constexpr uint32_t kTmemO = 128, kTmemDelta = 256, kTmemV = 384;
@@ -97,19 +98,27 @@ struct alignas(16) Decays { // read four floats at a time
     float block[4];       // the blocks' sums
 };
 
+// What a CTA works on: a sequence (-1: nothing), one of its segments, its tokens, its
+// states.  Then the first token (-1: nothing), state and head of what will follow on some
+// SM when this is done.
+struct Unit {
+    int seq, segment, segments, first, tokens, src, dst;
+    int next_first, next_src, next_head;
+};
+
 struct Misc {
     uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];
     uint64_t dec_full[2], dec_empty[2];
     uint64_t s_full, p_full, o1_full, o_full, o_free, o_staged;
     uint64_t vok_full[2], st_full[2], ring_full[4], ring_empty[4], d_full, qs_done, drain;
     uint32_t hurt[2];        // whether a chunk had values that are not finite
+    int value_exponent[2];   // fp16: V' is divided by 2^this
     Decays dec[2];
     float state_scale[2];    // what the state's operand was divided by
     uint32_t tmem_base;
-    int unit[3];
+    Unit unit;
     uint8_t first[2][128];   // by value channel: the chunk's first token whose value is not
                              // finite, or 128
-    uint8_t exponent[2][128]; // fp16: by value channel, the chunk's largest exponent
     float warp_max[2][8];
 };
 
@@ -149,6 +158,19 @@ template <> __device__ __forceinline__ float value_of<__half>(uint16_t u)
 template <> __device__ __forceinline__ float value_of<__nv_bfloat16>(uint16_t u)
 {
     return __uint_as_float((uint32_t)u << 16);
+}
+
+template <typename T> struct Pair;
+template <> struct Pair<__half> { using type = __half2; };
+template <> struct Pair<__nv_bfloat16> { using type = __nv_bfloat162; };
+__device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t *>(&x); }
+
+// The larger magnitudes of two pairs; a NaN stays.
+template <typename T>
+__device__ __forceinline__ typename Pair<T>::type most_of_pairs(typename Pair<T>::type m, uint32_t x)
+{
+    return __hmax2_nan(m, __habs2(*reinterpret_cast<const typename Pair<T>::type *>(&x)));
 }
 
 // x less the two 16-bit values of `part`, by multiply-adds that take 16-bit factors: the
@@ -309,36 +331,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int head = blockIdx.x, y = blockIdx.y;
 
     griddep_wait();
-    // the last line is past every unit, so its search sees every sequence
-    const bool tell = head == 0 && y == (int)gridDim.y - 1 && !kParts;
-    if (p.segment == INT32_MAX) {
-        // One segment each.  Of up to 32 sequences line y is the y-th longest, so that the
-        // long ones start first (8 of 32 to 4000 tokens, 32 heads: 133 us, in their own order
-        // 188; 16 ascending ones 271 and 315; 24 in any order with 8 kv heads 373 and 369);
-        // with more of them their chains are many and even out.
-        if (warp == 0) {
-            int q0, len = -1, n = 0, s = y;
-            if (p.num_seqs > 32) {
-                n = segments_of(p, y, q0, len, head == 0 && lane == 0);
-            } else {
-                if (lane < p.num_seqs)
-                    n = segments_of(p, lane, q0, len, head == 0 && lane == y);
-                int rank = 0;
-                for (int i = 0; i < p.num_seqs; ++i) {
-                    const int other = __shfl_sync(~0u, len, i);
-                    rank += other > len || (other == len && i < lane);
-                }
-                s = __ffs(__ballot_sync(~0u, lane < p.num_seqs && rank == y)) - 1;
-                n = __shfl_sync(~0u, n, s);
-            }
-            if (lane == 0)
-                m->unit[0] = n ? s : -1, m->unit[1] = 0, m->unit[2] = n;
-        }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&m->tmem_base, kTmemCols);
+        tmem_relinquish();
     } else if (warp == 0) {
-        int s, j = 0, n = 0;
-        find_unit(p, y, lane, tell, s, j, n);
+        // the last line is past every unit, so its search sees every sequence
+        const bool tell = head == 0 && y == (int)gridDim.y - 1 && !kParts;
+        int s = y, j = 0, n = 0, q0 = 0, len = -1, src = -1, dst = -1;
+        const int64_t next = (int64_t)y * gridDim.x + head + kSms;
+        const int next_y = (int)(next / gridDim.x);
+        int next_first = -1, next_src = -1;
+        if (p.segment != INT32_MAX) {
+            find_unit(p, y, lane, tell, s, j, n);
+            if (s >= 0) {
+                q0 = p.query_start_loc[s], len = p.query_start_loc[s + 1] - q0;
+                src = p.src_states[s], dst = p.dst_states[s];
+            }
+        } else if (p.num_seqs > 32) {
+            // one segment each
+            src = p.src_states[y], dst = p.dst_states[y];
+            n = segments_of(p, y, q0, len, head == 0 && lane == 0);
+            if (next_y < p.num_seqs)
+                next_first = p.query_start_loc[next_y], next_src = p.src_states[next_y];
+        } else {
+            // Of up to 32 sequences line y is the y-th longest, so that the long ones start
+            // first (8 of 32 to 4000 tokens, 32 heads: 133 us, in their own order 188; 16
+            // ascending ones 271 and 315; 24 in any order with 8 kv heads 373 and 369); with
+            // more of them their chains are many and even out.
+            if (lane < p.num_seqs) {
+                src = p.src_states[lane], dst = p.dst_states[lane];
+                n = segments_of(p, lane, q0, len, head == 0 && lane == y);
+            }
+            int rank = 0;
+            for (int i = 0; i < p.num_seqs; ++i) {
+                const int other = __shfl_sync(~0u, len, i);
+                rank += other > len || (other == len && i < lane);
+            }
+            const int behind = __ffs(__ballot_sync(~0u, lane < p.num_seqs && rank == next_y)) - 1;
+            if (behind >= 0) {
+                const int live = __shfl_sync(~0u, n, behind), at = __shfl_sync(~0u, q0, behind);
+                next_first = live ? at : -1, next_src = __shfl_sync(~0u, src, behind);
+            }
+            s = __ffs(__ballot_sync(~0u, lane < p.num_seqs && rank == y)) - 1;
+            n = __shfl_sync(~0u, n, s), q0 = __shfl_sync(~0u, q0, s), len = __shfl_sync(~0u, len, s);
+            src = __shfl_sync(~0u, src, s), dst = __shfl_sync(~0u, dst, s);
+        }
         if (lane == 0)
-            m->unit[0] = s, m->unit[1] = j, m->unit[2] = n;
+            m->unit = {n ? s : -1, j, n, q0, len, src, dst, next_first, next_src, (int)(next % gridDim.x)};
     }
     if (tid == 32) {
         for (int i = 0; i < 2; ++i) {
@@ -368,14 +407,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(&m->drain, 1);
         fence_barrier_init();
     }
+    tc_fence_before_sync();
     __syncthreads();
-    const int s = m->unit[0], j = m->unit[1], nseg = m->unit[2];
-    if (s < 0 || (kParts && j == nseg - 1))
+    tc_fence_after_sync();
+    const uint32_t tmem = m->tmem_base;
+    const Unit unit = m->unit;
+    const int j = unit.segment, nseg = unit.segments, src = unit.src, dst = unit.dst;
+    if (unit.seq < 0 || (kParts && j == nseg - 1)) {
+        if (warp == kMmaWarp)
+            tmem_dealloc(tmem, kTmemCols);
         return;
-    const int q0 = p.query_start_loc[s], q1 = p.query_start_loc[s + 1];
-    const int t0 = q0 + (j ? j * p.segment : 0);
-    const int len = min(q1 - t0, p.segment), n = (len + kChunk - 1) / kChunk;
-    const int src = p.src_states[s], dst = p.dst_states[s];
+    }
+    const int t0 = unit.first + (j ? j * p.segment : 0);
+    const int len = min(unit.first + unit.tokens - t0, p.segment), n = (len + kChunk - 1) / kChunk;
     const int per = p.num_heads / p.num_kv_heads;
     const int total = kParts ? n : n * per; // (chunk, query head) pairs
     // With one query head a kv head (and without any, in the first pass) a chunk is short,
@@ -389,16 +433,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto v_offset = [&](int c) { return Gm::kOffV - v_slot(c) * TB; };
     auto q_slot = [&](int it) { return solo ? 0 : it & 1; };
     auto q_phase = [&](int it) { return (uint32_t)(solo ? it : it >> 1) & 1; };
+    const bool output_first = !kParts && solo && n == 1;
+    // where a pair's output is staged
+    auto out_offset = [&](int it) {
+        return (solo && !output_first ? Gm::kOffK : Gm::kOffQ) + (it & 1) * TB;
+    };
     if (tid == 0 && head == 0 && !kParts && (src >= p.num_states || dst >= p.num_states))
         atomicOr(p.err, PA_DEVERR_STATE_);
-    if (warp == kMmaWarp) {
-        tmem_alloc(&m->tmem_base, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = m->tmem_base;
 
     if (warp >= kProducerWarp) {
         registers_down<kRegsFew>();
@@ -522,6 +563,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (ok && more)
                     ok = load_k(c + 1) && load_q(c + 1, 0) && (solo || load_v(c + 1));
             }
+            // This chain's loads are under way: what will follow it starts with tiles and a
+            // state that are in L2.  (All SMs' first loads at once take HBM 4 us: 32 prompts
+            // of 100 tokens, 32 heads, 92 us without, 87 with.)
+            if (!kParts && ok && lane == 0 && unit.next_first >= 0 && unit.next_first < p.num_tokens) {
+                if (unit.next_src >= 0 && unit.next_src < p.num_states)
+                    l2_prefetch(p.states + ((int64_t)unit.next_src * p.num_kv_heads + unit.next_head) * D * D,
+                                D * D * 4);
+#pragma unroll
+                for (int hf = 0; hf < Gm::kHalves; ++hf) {
+                    tma_prefetch_3d(&k_map, hf * 64, unit.next_head, unit.next_first);
+                    tma_prefetch_3d(&v_map, hf * 64, unit.next_head, unit.next_first);
+                    tma_prefetch_3d(&q_map, hf * 64, unit.next_head * per, unit.next_first);
+                }
+            }
             if (!ok) {
                 // Given up: no tile may land in a later CTA's memory, so the last load on
                 // each barrier is awaited, within the waits' own limit.
@@ -589,7 +644,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 return true;
             };
-            // with several query heads V arrives late in the first one's time
+            // With several query heads V arrives late in the first one's time.  Nothing but
+            // its store waits for the state of an only chunk: its output goes first.
             const int delta_head = solo ? 0 : 1;
             bool ok = n == 0 || kParts || scores(0, 0, true);
             for (int it = 0, c = 0, h = 0; ok && it < total; ++it) {
@@ -624,7 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (kParts || h == delta_head)
+                if (kParts || (h == delta_head && !output_first))
                     ok = ok && delta(c);
                 if (!kParts) {
                     ok = ok && warp_wait(&m->p_full, (uint32_t)it & 1);
@@ -644,10 +700,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             umma_f16_tmem_a(tmem + kTmemO, pa + 16, vd, kIdescValue, 1u);
                         }
                         umma_commit(&m->o_full);
-                        if (last) // V' was made before delta
+                        if (last) // V' was made before delta (no V follows an only one)
                             umma_commit(&m->v_empty[v_slot(c)]);
                     }
                     __syncwarp();
+                    if (output_first)
+                        ok = delta(c);
                     if (it + 1 < total)
                         ok = scores(it + 1, next, last);
                 }
@@ -677,9 +735,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (len - c * kChunk >= kChunk) { // a tail's rows were written one by one
 #pragma unroll
                         for (int hf = 0; hf < Gm::kHalves; ++hf)
-                            tma_store_3d(&out_map,
-                                         smem + (solo ? Gm::kOffK : Gm::kOffQ) + (it & 1) * TB + hf * kRegion,
-                                         hf * 64, head * per + h, t0 + c * kChunk);
+                            tma_store_3d(&out_map, smem + out_offset(it) + hf * kRegion, hf * 64,
+                                         head * per + h, t0 + c * kChunk);
                         bulk_commit();
                         bulk_wait_read();
                     }
@@ -717,51 +774,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             make_uint4(0, 0, 0, 0);
                     }
                 __syncwarp();
-                // whether all is finite
-                uint32_t odd = 0;
-                if constexpr (kHalf) {
-                    // 16 channels by 16 tokens at a time, a channel's pairs in a lane; magnitudes
-                    // order as their bits
-#pragma unroll 1
-                    for (int g = 0; g < D / 16; ++g) {
-                        uint32_t most[2] = {0, 0};
-                        const uint32_t at = smem_addr(v + (g / 4) * kRegion) +
-                                            (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 128 +
-                                                       (((g % 4 * 2 + (lane >> 3 & 1)) ^ (lane & 7)) * 16));
+                // The largest magnitude, of both halves of four words; NaN stays.
+                typename Pair<T>::type most2[4] = {};
 #pragma unroll 4
-                        for (int k = 0; k < kChunk / 16; ++k) {
-                            uint32_t x[4];
-                            ldmatrix_x4_trans(x, at + (uint32_t)(k * 2048));
-                            most[0] = __vmaxu2(__vmaxu2(most[0], x[0] & 0x7FFF7FFFu), x[2] & 0x7FFF7FFFu);
-                            most[1] = __vmaxu2(__vmaxu2(most[1], x[1] & 0x7FFF7FFFu), x[3] & 0x7FFF7FFFu);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 1));
-                            most[i] = __vmaxu2(most[i], __shfl_xor_sync(~0u, most[i], 2));
-                            const uint32_t top = max(most[i] & 0xFFFFu, most[i] >> 16);
-                            odd |= (top + 0x0400u) << 16; // an exponent of ones carries to the top
-                            if ((lane & 3) == 0)
-                                m->exponent[b][g * 16 + i * 8 + (lane >> 2)] =
-                                    (uint8_t)(__float_as_uint(value_of<T>((uint16_t)top)) >> 23);
-                        }
-                    }
-                } else {
-#pragma unroll 4
-                    for (int i = 0; i < TB / 512; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(v + lane * 16 + i * 512);
-                        odd |= ((x.x & 0x7FFF7FFFu) + 0x00800080u) | ((x.y & 0x7FFF7FFFu) + 0x00800080u) |
-                               ((x.z & 0x7FFF7FFFu) + 0x00800080u) | ((x.w & 0x7FFF7FFFu) + 0x00800080u);
-                    }
+                for (int i = 0; i < TB / 512; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(v + lane * 16 + i * 512);
+                    most2[0] = most_of_pairs<T>(most2[0], x.x);
+                    most2[1] = most_of_pairs<T>(most2[1], x.y);
+                    most2[2] = most_of_pairs<T>(most2[2], x.z);
+                    most2[3] = most_of_pairs<T>(most2[3], x.w);
                 }
-                const bool hurt = __any_sync(~0u, (odd & 0x80008000u) != 0);
+                const float2 top = unpack2<T>(bits_of(__hmax2_nan(__hmax2_nan(most2[0], most2[1]),
+                                                                  __hmax2_nan(most2[2], most2[3]))));
+                const bool hurt = __any_sync(~0u, !(top.x < INFINITY && top.y < INFINITY));
+                float most = fmaxf(top.x, top.y);
                 if (hurt) {
                     // What is not finite is taken out of the tile: in P V it would reach the
                     // rows before it as 0 * NaN.  `first` is where a channel is lost from.
+                    most = 0.f;
 #pragma unroll 1
                     for (int ch = lane; ch < D; ch += 32) {
                         int first = 128;
-                        float most = 0.f;
 #pragma unroll 1
                         for (int t = kChunk - 1; t >= 0; --t) {
                             uint16_t *const at = reinterpret_cast<uint16_t *>(
@@ -776,11 +809,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         m->first[b][ch] = (uint8_t)first;
-                        m->exponent[b][ch] = (uint8_t)(__float_as_uint(most) >> 23);
                     }
                 }
-                if (lane == 0)
+                const unsigned largest = __reduce_max_sync(~0u, __float_as_uint(most));
+                if (lane == 0) {
                     m->hurt[b] = hurt;
+                    m->value_exponent[b] = range_exponent(__uint_as_float(largest));
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -929,8 +964,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             tc_fence_after_sync();
             const bool hurt = m->hurt[c & 1] != 0;
-            uint8_t *const tile = smem + (solo ? Gm::kOffK : Gm::kOffQ) + (it & 1) * TB +
-                                  (half * H / 64) * kRegion + row * 128;
+            uint8_t *const tile = smem + out_offset(it) + (half * H / 64) * kRegion + row * 128;
             T *const out = static_cast<T *>(p.out) + half * H +
                            ((int64_t)(t0 + c * kChunk + row) * p.num_heads + head * per + h) * D;
 #pragma unroll 1
@@ -1079,13 +1113,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok)
                 break;
             const bool hurt = mine && m->hurt[b] && m->first[b][ch] < 128;
-            float scale[2] = {1.f, 1.f}, back = 1.f; // of channels lane / 4 and 8 + lane / 4 of 16
-            if (kHalf && mine) {
-                auto exponent = [&](int i) { return max((int)m->exponent[b][i] - 127 - 13, -40); };
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    scale[i] = power_of_two(-exponent(wg * 32 + half * 16 + i * 8 + (lane >> 2)));
-                back = power_of_two(exponent(ch));
+            float scale = 1.f, back = 1.f;
+            if constexpr (kHalf) {
+                scale = power_of_two(-m->value_exponent[b]);
+                back = power_of_two(m->value_exponent[b]);
             }
             // V', decayed to the chunk's end, from the last block on: of each block of 32
             // tokens this warp has 16 channels.  Transposed 8x8 matrices give a lane two
@@ -1121,7 +1152,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             *reinterpret_cast<const float2 *>(&d.rest[k * 32 + (z >> 1) * 8 + (lane & 3) * 2]), f2);
                         float2 v = __fmul2_rn(unpack2<T>(x[z >> 2][z & 3]), w);
                         if constexpr (kHalf)
-                            v = __fmul2_rn(v, make_float2(scale[z & 1], scale[z & 1]));
+                            v = __fmul2_rn(v, make_float2(scale, scale));
                         uint32_t y[kSplit];
                         split<T, kSplit>(v, y);
 #pragma unroll
