@@ -1,9 +1,10 @@
 /*
  * pa_block_calls.c -- the binding of the block-scaled and block-sparse calls, of
  * linear attention and of the sequence calls (CPython C API): checks of torch
- * tensors' types, shapes and devices, and the calls of include/pa.h, in one step.  A decode step makes several of these
- * calls a layer; through ctypes the checks and the marshalling of about 20
- * arguments took longer than the launch (8 against 4 us a call).
+ * tensors' types, shapes and devices, and the calls of include/pa.h, in one step.
+ * A decode step makes several of these calls a layer; through ctypes the checks and
+ * the marshalling of about 20 arguments took longer than the launch (8 against 4 us
+ * a call).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -935,9 +936,9 @@ PyMODINIT_FUNC PyInit_pa_block_calls(void)
     struct {
         PyObject **to;
         const char *name;
-    } types[] = {{&t_i32, "int32"}, {&t_i64, "int64"},
+    } types[] = {{&t_i32, "int32"},   {&t_i64, "int64"},
                  {&t_f32, "float32"}, {&t_u8, "uint8"},
-                 {&t_i8, "int8"},   {&t_f16, "float16"}, {&t_bf16, "bfloat16"}},
+                 {&t_i8, "int8"},     {&t_f16, "float16"}, {&t_bf16, "bfloat16"}},
       names[] = {{&n_shape, "shape"},         {&n_dtype, "dtype"},
                  {&n_stride, "stride"},       {&n_is_contiguous, "is_contiguous"},
                  {&n_data_ptr, "data_ptr"},   {&n_get_device, "get_device"},

@@ -264,7 +264,7 @@ constexpr int kShort = 16;
 // head, in the first pass 2.5; a chain 8, a segment 12 in both passes; launches 4 and
 // 10.  Measured, without a cut and with the one taken: one prompt of 1024, 4096 and
 // 16384 tokens, 32 heads, 8 kv heads 102 and 35, 379 and 53, 1485 and 130; 32 kv heads
-// 43 and 38, 135 and 78, 506 and 228; 4 prompts of 4096 there, left alone, 141 and 204;
+// 43 and 38, 135 and 78, 506 and 238; 4 prompts of 4096 there, left alone, 141 and 204;
 // 512 tokens there 27 and 31, with 8 kv heads 55 and 34.
 struct Cut {
     int segment, lines;
@@ -275,7 +275,8 @@ constexpr float kPassChunk = 2.5f, kChain = 8.f, kSegment = 12.f, kOnePass = 4.f
 struct Work {
     float chunks, longest; // in chunks
     int seqs, kv_heads;
-    // us of a chunk of `chunk` us each
+    // us without a cut, at `chunk` us a chunk; `fixed` 0 leaves out all that does not grow
+    // with that
     float uncut(float chunk, float fixed) const
     {
         const float rounds = ceilf((float)seqs * kv_heads / kSms);
@@ -343,6 +344,13 @@ static int64_t most_lines(int num_seqs, int num_tokens, int max_query_len, int n
             most = std::max(most, lines_of(n, num_seqs, num_tokens));
     }
     return most;
+}
+
+// Bytes for the states and decays of `lines` segments.
+static size_t workspace_of(int64_t lines, int num_kv_heads, int head_size)
+{
+    const size_t each = (size_t)num_kv_heads * 4 * ((size_t)head_size * head_size + 1);
+    return lines ? (each * (size_t)lines + 255) / 256 * 256 : 256;
 }
 
 static bool rows_map(CUtensorMap *map, const void *x, pa_dtype dtype, int num_tokens, int heads,
@@ -444,11 +452,8 @@ size_t pa_linear_prefill_workspace_size(int num_seqs, int num_tokens, int max_qu
 {
     if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || num_kv_heads <= 0 || head_size <= 0)
         return 0;
-    const int64_t lines = most_lines(num_seqs, num_tokens, max_query_len, num_kv_heads);
-    if (lines == 0)
-        return 256;
-    const size_t each = (size_t)num_kv_heads * 4 * ((size_t)head_size * head_size + 1);
-    return (each * (size_t)lines + 255) / 256 * 256;
+    return workspace_of(most_lines(num_seqs, num_tokens, max_query_len, num_kv_heads), num_kv_heads,
+                        head_size);
 }
 
 pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void *v,
@@ -485,7 +490,10 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
         e = launch_step<true>(p, num_seqs, head_size, dtype, s);
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
-    const Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads);
+    Cut cut = cut_of(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads);
+    // the size asked for covers every cut; were the last bit of a float to say otherwise, none
+    if (cut.segment != INT32_MAX && workspace_bytes < workspace_of(cut.lines, num_kv_heads, head_size))
+        cut = {INT32_MAX, num_seqs};
     p.num_seqs = num_seqs;
     p.segment = cut.segment;
     p.lines = cut.lines;

@@ -23,8 +23,10 @@
 // and about 2.4 for each of more (5000), about twice its MMAs' time (64 and 40 of 64
 // cycles each).  With one head the chain V' -> delta -> state -> operand -> Q S sets the
 // pace, each step a wait for the one before, with more of them the rows' chain scores ->
-// P -> P V -> output.  16 prompts of 256 to 2048 tokens, 32 heads, take 207 us; one of
-// 131072, 64 heads and 8 kv heads, 1.41 ms, in which the MMAs run at 1.1 PFLOP/s.
+// P -> P V -> output.  16 prompts of 256 to 2048 tokens, 32 heads, take 180 us in fp16;
+// one of 131072, 64 heads and 8 kv heads, in bf16 1.37 ms, in which the MMAs run at 1.1
+// PFLOP/s.  A chain's start (an SM's turnover, its first tiles and state, a first look at
+// V) and its state's store take 8 us besides.
 //
 // A CTA walks one segment of one sequence for one kv head with all of its query
 // heads.  Roles in a CTA of 640 threads:
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // This chain's loads are under way: what will follow it starts with tiles and a
             // state that are in L2.  (All SMs' first loads at once take HBM 4 us: 32 prompts
-            // of 100 tokens, 32 heads, 92 us without, 87 with.)
+            // of 100 tokens, 32 heads, 90 us without, 82 with.)
             if (!kParts && ok && lane == 0 && unit.next_first >= 0 && unit.next_first < p.num_tokens) {
                 if (unit.next_src >= 0 && unit.next_src < p.num_states)
                     l2_prefetch(p.states + ((int64_t)unit.next_src * p.num_kv_heads + unit.next_head) * D * D,
