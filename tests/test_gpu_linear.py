@@ -1,6 +1,7 @@
 """Linear attention with a decay for each head on the GPU, against the 64-bit
 recurrence of tests/_linear_ref.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -401,3 +402,118 @@ def test_far_tokens(pa):
     check_out(out[-2:].cpu(), ref, mag)
     check_states(states[-4:].cpu(), rs, smag, out.dtype)
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (9, 1), (34, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_few_tokens(pa, heads, kv_heads, d, dtype):
+    """Speculated tokens, at most 16 a sequence, with more heads a group than one pass
+    over the state takes; a padding row and a sequence past its bound among them."""
+    x = inputs([16, 3, 0, 9, 1, 2, 15], heads, kv_heads, d, dtype, "token", seed=31, fresh=(3,),
+               fused=True, tail=2)
+    x["dst"][5] = -1
+    check(pa, x, prefill)
+    y = inputs([4, 16, 2], heads, kv_heads, d, dtype, "head", seed=32)
+    before, out = y["states"].clone(), torch.full_like(y["q"], 7.0)
+    prefill(pa, y, out=out, most=15)
+    assert pa.pa_device_errors(clear=True) == pa.DEVERR_SEQ_LEN
+    assert bool((out[4:20] == 7.0).all()) and not bool((out[:4] == 7.0).all())
+    assert torch.equal(y["states"][int(y["dst"][1])], before[int(y["dst"][1])])
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(4, 4), (6, 2)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_many_sequences(pa, heads, kv_heads, dtype):
+    """More chains than SMs, in the order of lengths (up to 32 sequences) and in their own,
+    with padding rows and empty sequences, whose tiles are asked for ahead as well."""
+    for b, seed in ((32, 33), (70, 34)):
+        lens = [(37 * i * i + 11 * i) % 290 for i in range(b)]
+        lens[5] = lens[b - 1] = 0
+        x = inputs(lens, heads, kv_heads, 64, dtype, "token", seed=seed, fresh=range(0, b, 4))
+        x["dst"][7] = x["dst"][b - 3] = -1
+        check(pa, x, prefill)
+
+
+def test_graphs_share_a_workspace(pa):
+    """Two captured calls with cut prompts on one workspace, replayed in turn: the same bits
+    as eager calls on a workspace of their own."""
+    xs = [inputs(lens, 8, 2, 128, "bf16", "token", seed=35 + i) for i, lens in enumerate(([2500], [900, 1800]))]
+    ws = max((workspace(pa, x) for x in xs), key=len)
+    assert len(ws) > 256
+    outs, wants, graphs = [], [], []
+    for x in xs:
+        most = longest(x)
+        eager = {**x, "states": x["states"].clone()}
+        wants.append((prefill(pa, eager), eager["states"]))
+        x["before"] = x["states"].clone()
+        outs.append(torch.full_like(x["q"], 7.0))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            prefill(pa, x, out=outs[-1], most=most, ws=ws)
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            prefill(pa, x, out=outs[-1], most=most, ws=ws)
+    for i in (0, 1, 1, 0):
+        xs[i]["states"].copy_(xs[i]["before"])
+        outs[i].fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(outs[i], wants[i][0]) and torch.equal(xs[i]["states"], wants[i][1])
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_host_threads(pa):
+    """Four threads, a stream and a workspace each: the bits of one thread alone."""
+    def inputs_of(i):
+        return (inputs([300 + i, 40], 4, 2, 64, "fp16", "token", seed=40 + i),
+                inputs([1] * 5, 4, 2, 64, "fp16", "token", seed=50 + i))
+
+    wants = []
+    for i in range(4):
+        x, y = inputs_of(i)
+        wants.append((prefill(pa, x), x["states"], decode(pa, y), y["states"]))
+    work = [inputs_of(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def run(i):
+        try:
+            x, y = work[i]
+            first = [t["states"].clone() for t in (x, y)]
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    for t, s in zip((x, y), first):
+                        t["states"].copy_(s)
+                    a, b = prefill(pa, x), decode(pa, y)
+                stream.synchronize()
+            got[i] = (a, x["states"], b, y["states"])
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for g, w in zip(got, wants):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("lens", [[300], [1200]], ids=str)
+def test_channels_of_different_sizes(pa, lens, dtype):
+    """Value channels 2^14 apart keep the precision of their own size: a chunk's values and
+    a state are scaled as a whole in fp16, and parts of 22 bits reach 2^-39 of the largest,
+    2^-25 of the small ones."""
+    x = inputs(lens, 4, 2, 128, dtype, "token", seed=60)
+    x["v"][..., ::3] *= 2.0 ** -8
+    x["v"][..., 1::3] *= 2.0 ** 6
+    x["states"][..., ::3] *= 2.0 ** -8
+    x["states"][..., 1::3] *= 2.0 ** 6
+    check(pa, x, prefill)
