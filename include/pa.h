@@ -554,7 +554,11 @@ pa_status pa_copy_blocks(void *kv_cache, const int64_t *block_mapping, int num_p
  *   max_query_len    an upper bound of every q_len; a sequence that breaks these
  *                    rules is skipped and flagged (PA_DEVERR_SEQ_LEN).
  *   workspace        pa_linear_prefill_workspace_size bytes, 256-byte aligned,
- *                    with the rules of pa_decode_splitk's
+ *                    with the rules of pa_decode_splitk's.  Few long sequences need
+ *                    more than many short ones: the size is that of this call's
+ *                    numbers, and for no call with as many sequences more than
+ *                    (1216 + (num_seqs + 1) * num_kv_heads) states and 4 bytes for
+ *                    each, rounded up to 256.
  * Its products run on the tensor cores with 16-bit operands.  Scores times decays
  * (P) and states go in as a rounded 16-bit part plus the rounded remainder: 2^-17 of
  * their size with bf16 and 2^-22 with fp16 (there of those within 2^17 of the

@@ -142,6 +142,11 @@ def test_workspace_sizes(pa):
     assert size(1, 131072, 131072, 8, 128) > 64 * 8 * 128 * 128 * 4
     assert size(-1, 10, 10, 8, 128) == 0 and size(1, 10, 10, 0, 128) == 0
     assert size(1, -1, 10, 8, 128) == 0 and size(1, 10, -1, 8, 128) == 0
+    for b, t, most in ((1, 131072, 131072), (1, 129, 129), (7, 30000, 9000), (300, 500000, 300000),
+                       (2, 1 << 30, 1 << 30), (1, 2 ** 31 - 1, 2 ** 31 - 1)):
+        for hkv in (1, 2, 5, 8, 32, 200, 1216, 1217):
+            states = 1216 + (b + 1) * hkv
+            assert 0 < size(b, t, most, hkv, 64) <= states * (64 * 64 * 4 + 4) + 255
     size = pa.pa_sequences_workspace_size
     assert size(0, 1) > 0 and size(100, 5000) >= 4 * (3 * 5000 + 6 * 100)
     assert size(-1, 10) == 0 and size(1, 0) == 0 and size(65536, 10) == 0
