@@ -250,27 +250,28 @@ static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_siz
 // ---------------------------------------------------------------------------
 // The longest prompt, in tokens, that the recurrent kernel takes.  A chunk costs the same
 // however few its tokens.  1, 4, 8, 16 and 32 tokens in us, and chunks: 1 sequence of 32
-// heads 8, 10, 12, 20, 35, chunks 16; 32 of 32 heads 29, 39, 55, 84, 152, chunks 84; 256
-// of 32 heads and 8 kv heads 49, 75, 117, 205, 385, chunks 231; with head_size 64 256 of 8
-// heads 18, 25, 35, 57, 104, chunks 117 to 121.
+// heads 8, 10, 13, 20, 35, chunks 14; 32 of 32 heads 29, 39, 55, 84, 152, chunks 78; 256 of
+// 32 heads and 8 kv heads 49, 75, 115, 205, 385, chunks 225; with head_size 64 256 of 8
+// heads 18, 25, 35, 57, 104, chunks 108.
 constexpr int kShort = 16;
 
 // How prompts are cut.  A sequence and kv head is a chain of chunks that one CTA
 // walks, an SM at a time.  Chains can be cut into segments whose states a first pass
 // forms, at the price of reading K and V twice.  Taken is the best of at most eight
-// cuts, the ones whose segments fill the SMs once, twice, ..., if it is an eighth
+// cuts, the ones whose segments fill the SMs once, twice, ..., if it is a ninth
 // better than none, by these times in us (head_size 128; 64 is a tenth to a fifth
 // less on both sides): a chunk 2.3 for each query head and 2.4, or 3.9 with one query
 // head, in the first pass 2.5; a chain 8, a segment 12 in both passes; launches 4 and
-// 10.  Measured, without a cut and with the one taken: one prompt of 1024, 4096 and
-// 16384 tokens, 32 heads, 8 kv heads 102 and 35, 379 and 53, 1485 and 130; 32 kv heads
-// 43 and 38, 135 and 78, 506 and 238; 4 prompts of 4096 there, left alone, 141 and 204;
-// 512 tokens there 27 and 31, with 8 kv heads 55 and 34.
+// 10.  Measured, without a cut and with one: one prompt of 1024, 4096 and 16384 tokens, 32
+// heads, 8 kv heads 100 and 36, 371 and 53, 1455 and 131; 32 kv heads 43 and 39, 137 and
+// 80, 510 and 241; one of 8192 among 32 of 1024, 8 kv heads, 752 and 344.  Left alone are 4 prompts of 4096 tokens there (141, cut 259),
+// one of 512 (27 and 28) and 24 of 32 to 4000 tokens, 8 kv heads (372 and 443).
 struct Cut {
     int segment, lines;
 };
 
-constexpr float kPassChunk = 2.5f, kChain = 8.f, kSegment = 12.f, kOnePass = 4.f, kTwoPasses = 10.f;
+constexpr float kPassChunk = 2.5f, kChain = 8.f, kSegment = 12.f, kOnePass = 4.f, kTwoPasses = 10.f,
+                kWorth = 0.89f;
 
 struct Work {
     float chunks, longest; // in chunks
@@ -290,13 +291,22 @@ struct Work {
         const int n = each ? (int)ceilf(chunks / each) : 0;
         return n < longest ? n : 0;
     }
-    bool better(int rounds, int n, float chunk, float fixed, float &best) const
+    // us of whole rounds of such segments: a bound that even lengths come near to
+    float rounds_of(int rounds, int n, float chunk, float fixed) const
     {
-        const float us = rounds * ((chunk + kPassChunk * fixed) * n + kSegment * fixed) + kTwoPasses * fixed;
-        if (us >= best)
-            return false;
-        best = us;
-        return true;
+        return rounds * ((chunk + kPassChunk * fixed) * n + kSegment * fixed) + kTwoPasses * fixed;
+    }
+    // us of an SM's share and half of a segment, since what is left of uneven lengths ends
+    // unevenly; if the others are shorter than a segment at the mean, the longest alone is
+    // taken to be cut
+    float uneven(int n, float chunk) const
+    {
+        const bool one = seqs == 1 || (chunks - longest) / (seqs - 1) <= n;
+        const float passed = one ? std::min(longest, chunks) : chunks;
+        const float chains = one ? ceilf(longest / n) * kSegment + (seqs - 1) * kChain
+                                 : (chunks / n + 0.5f * seqs) * kSegment;
+        return (chunks * chunk + passed * kPassChunk + chains) * kv_heads / kSms +
+               0.5f * (1.f - 1.f / seqs) * (n * (chunk + kPassChunk) + kSegment) + kTwoPasses;
     }
 };
 constexpr int kRounds = 8;
@@ -318,19 +328,24 @@ static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_heads
 {
     const Work w = work_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
     const float chunk = chunk_us(num_heads / num_kv_heads);
-    float best = 0.875f * w.uncut(chunk, 1.f);
+    float best = kWorth * w.uncut(chunk, 1.f);
     Cut cut = {INT32_MAX, num_seqs};
     for (int r = 1; r <= kRounds; ++r) {
         const int n = w.segment(r);
-        if (n && lines_of(n, num_seqs, num_tokens) <= 65535 && w.better(r, n, chunk, 1.f, best))
+        if (!n || lines_of(n, num_seqs, num_tokens) > 65535)
+            continue;
+        const float us = std::max(w.rounds_of(r, n, chunk, 1.f), w.uneven(n, chunk));
+        if (us < best) {
+            best = us;
             cut = {n * kChunk, (int)lines_of(n, num_seqs, num_tokens)};
+        }
     }
     return cut;
 }
 
-// The most lines that cut_of can ask for with any number of query heads: a cut's time
-// is linear in a chunk's and the uncut time convex, so a cut that is no better with one
-// query head or with very many is none in between.
+// The most lines that cut_of can ask for with any number of query heads: a cut takes
+// rounds_of at least, which is linear in a chunk's time, and the uncut time is convex, so
+// a cut that is no better with one query head or with very many is none in between.
 static int64_t most_lines(int num_seqs, int num_tokens, int max_query_len, int num_kv_heads)
 {
     const Work w = work_of(num_seqs, num_tokens, max_query_len, num_kv_heads);
@@ -339,8 +354,8 @@ static int64_t most_lines(int num_seqs, int num_tokens, int max_query_len, int n
         const int n = w.segment(r);
         if (!n || lines_of(n, num_seqs, num_tokens) > 65535)
             continue;
-        float one = 0.875f * w.uncut(chunk_us(1), 1.f), many = 0.875f * w.uncut(1.f, 0.f) * 1.0001f;
-        if (w.better(r, n, chunk_us(1), 1.f, one) || w.better(r, n, 1.f, 0.f, many))
+        if (w.rounds_of(r, n, chunk_us(1), 1.f) < kWorth * w.uncut(chunk_us(1), 1.f) ||
+            w.rounds_of(r, n, 1.f, 0.f) < kWorth * w.uncut(1.f, 0.f) * 1.0001f)
             most = std::max(most, lines_of(n, num_seqs, num_tokens));
     }
     return most;
