@@ -264,8 +264,9 @@ constexpr int kShort = 16;
 // head, in the first pass 2.5; a chain 8, a segment 12 in both passes; launches 4 and
 // 10.  Measured, without a cut and with one: one prompt of 1024, 4096 and 16384 tokens, 32
 // heads, 8 kv heads 100 and 36, 371 and 53, 1455 and 131; 32 kv heads 43 and 39, 137 and
-// 80, 510 and 241; one of 8192 among 32 of 1024, 8 kv heads, 752 and 344.  Left alone are 4 prompts of 4096 tokens there (141, cut 259),
-// one of 512 (27 and 28) and 24 of 32 to 4000 tokens, 8 kv heads (372 and 443).
+// 80, 510 and 241; one of 8192 among 32 of 1024, 8 kv heads, 752 and 344.  Left alone are,
+// with 32 kv heads, 4 prompts of 4096 tokens (141, cut 259) and one of 512 (27 and 31), and
+// with 8, 24 of 32 to 4000 tokens (372 and 443).
 struct Cut {
     int segment, lines;
 };
