@@ -300,6 +300,10 @@ __device__ __forceinline__ void find_unit(const LinearParams &p, int y, int lane
             s = base + l;
             n = __shfl_sync(~0u, mine, l);
             j = y - before - (__shfl_sync(~0u, x, l) - n);
+            // Sequences that overlap can be more than the lines there are: one that does
+            // not fit is skipped as a whole, here and in the join.
+            if (y - j + n > p.lines)
+                s = -1;
             return;
         }
         before += __shfl_sync(~0u, x, 31);
@@ -308,7 +312,11 @@ __device__ __forceinline__ void find_unit(const LinearParams &p, int y, int lane
 
 // kParts: the first pass over sequences of several segments.  It forms the state
 // that each segment but the last one leaves, the first from the sequence's own
-// state, the others from zero, and the segments' decays.
+// state, the others from zero, and the segments' decays.  The last segment's line,
+// which has no such state, takes a copy of the sequence's own: the second pass starts
+// the first segment from there.  So that pass reads no state of a cut sequence, and
+// its last segment can write the state at any time, src_states[s] = dst_states[s] or
+// not.
 template <typename T, int D, bool kParts>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -416,6 +424,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const Unit unit = m->unit;
     const int j = unit.segment, nseg = unit.segments, src = unit.src, dst = unit.dst;
     if (unit.seq < 0 || (kParts && j == nseg - 1)) {
+        if (kParts && unit.seq >= 0 && nseg > 1) {
+            const int64_t one = (int64_t)D * D;
+            float4 *const to = reinterpret_cast<float4 *>(p.parts + ((int64_t)y * p.num_kv_heads + head) * one);
+            const float4 *const from =
+                src >= 0 && src < p.num_states
+                    ? reinterpret_cast<const float4 *>(p.states + ((int64_t)src * p.num_kv_heads + head) * one)
+                    : nullptr;
+            for (int i = tid; i < D * D / 4; i += kTcThreads)
+                to[i] = from ? from[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         if (warp == kMmaWarp)
             tmem_dealloc(tmem, kTmemCols);
         return;
@@ -1026,8 +1044,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float S[H]; // key channels from half * H on
         {
             const float *from = nullptr;
-            if (j > 0 && !kParts)
-                from = p.parts + ((int64_t)(y - 1) * p.num_kv_heads + head) * one + at0;
+            if (!kParts && nseg > 1) // behind the segment before, or the sequence's own
+                from = p.parts + ((int64_t)(j ? y - 1 : y + nseg - 1) * p.num_kv_heads + head) * one + at0;
             else if (j == 0 && src >= 0 && src < p.num_states)
                 from = p.states + ((int64_t)src * p.num_kv_heads + head) * one + at0;
 #pragma unroll
@@ -1260,8 +1278,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p)
 #pragma unroll
         for (int o = 16; o; o /= 2)
             before += __shfl_xor_sync(~0u, before, o);
-        // sequences that overlap can be more than the lines there are
-        if (tid == 0)
+        if (tid == 0) // skipped as in find_unit
             first = before, count = before + n <= p.lines ? n : 0;
     }
     __syncthreads();
@@ -1272,7 +1289,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p)
                  blockIdx.x * 256 + tid;
     const float *decay = p.part_decay + (int64_t)first * p.num_kv_heads + head;
     float4 S = *at;
-    // the last segment has no part
+    // the last segment's line has the sequence's own state
     constexpr int kAhead = 8;
     for (int j = 1; j < count - 1; j += kAhead) {
         float4 x[kAhead];
