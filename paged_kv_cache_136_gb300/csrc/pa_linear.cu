@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_block.cuh"
@@ -117,9 +118,13 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearP
     }
     for (int t = t0; t < t1; ++t) {
         T *const out = static_cast<T *>(p.out) + ((int64_t)t * p.num_heads + (int64_t)head * per) * D + col0;
-        // The decay less one: a decay near one, rounded to 24 bits, would be off by
-        // the same 2^-25 in every step, and 256 steps of memory by 2^-17.
-        const float a = expm1f(decay);
+        // S e^g, by e^g less one where that is at least a half: a decay near one, rounded
+        // to 24 bits, would be off by the same 2^-25 in every step, and 256 steps of memory
+        // by 2^-17.  A smaller one is formed as it is: S + (e^g - 1) S is off by 2^-25 of
+        // the old state, which is 2^-25 e^(-g) of the new one.  Either way a step's states
+        // are within 2^-22 of their size.
+        const bool strong = decay < -0.6931472f;
+        const float a = strong ? expf(decay) : expm1f(decay);
         const float2 v01 = block::float2_of<T>(v4.x), v23 = block::float2_of<T>(v4.y);
         for (int g0 = 0; g0 < per; g0 += kHeadsAtOnce) {
             const int n = min(kHeadsAtOnce, per - g0);
@@ -128,18 +133,25 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearP
             if (more)
                 load(last ? t + 1 : t, next);
             if (g0 == 0) {
+                auto step = [&](auto is_strong) {
 #pragma unroll
-                for (int i = 0; i < kQuads; ++i) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&sk[4 * (kGroups * i + group)]);
-                    const float k4[4] = {kk.x, kk.y, kk.z, kk.w};
+                    for (int i = 0; i < kQuads; ++i) {
+                        const float4 kk = *reinterpret_cast<const float4 *>(&sk[4 * (kGroups * i + group)]);
+                        const float k4[4] = {kk.x, kk.y, kk.z, kk.w};
+                        auto decayed = [&](float x) { return is_strong ? a * x : fmaf(a, x, x); };
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        S[i][r].x = fmaf(k4[r], v01.x, fmaf(a, S[i][r].x, S[i][r].x));
-                        S[i][r].y = fmaf(k4[r], v01.y, fmaf(a, S[i][r].y, S[i][r].y));
-                        S[i][r].z = fmaf(k4[r], v23.x, fmaf(a, S[i][r].z, S[i][r].z));
-                        S[i][r].w = fmaf(k4[r], v23.y, fmaf(a, S[i][r].w, S[i][r].w));
+                        for (int r = 0; r < 4; ++r) {
+                            S[i][r].x = fmaf(k4[r], v01.x, decayed(S[i][r].x));
+                            S[i][r].y = fmaf(k4[r], v01.y, decayed(S[i][r].y));
+                            S[i][r].z = fmaf(k4[r], v23.x, decayed(S[i][r].z));
+                            S[i][r].w = fmaf(k4[r], v23.y, decayed(S[i][r].w));
+                        }
                     }
-                }
+                };
+                if (strong)
+                    step(std::true_type());
+                else
+                    step(std::false_type());
             }
             for (int g = 0; g < n; ++g) {
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
