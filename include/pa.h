@@ -562,8 +562,11 @@ pa_status pa_copy_blocks(void *kv_cache, const int64_t *block_mapping, int num_p
  * Its products run on the tensor cores with 16-bit operands.  Scores times decays
  * (P) and states go in as a rounded 16-bit part plus the rounded remainder: 2^-17 of
  * their size with bf16 and 2^-22 with fp16 (there of those within 2^17 of the
- * largest), so that the one visible rounding is the output's own.  Decayed values, which make the states, go in as two parts with fp16
- * and three with bf16 (2^-24).
+ * largest), so that the one visible rounding is the output's own.  Decayed values,
+ * which make the states, go in as two parts with fp16 and three with bf16 (2^-24).
+ * A decay over several tokens of a chunk of 128 is exp of the fp32 sum of log_decay
+ * over those tokens alone, which is off by at most 2^-19 of itself however strong the
+ * others are; over more, it is that of the chunks' decays.
  */
 pa_status pa_linear_decode(void *out, const void *q, const void *k, const void *v,
                            const float *log_decay, int64_t decay_stride, float *states,

@@ -6,18 +6,20 @@
 // log decays up to its token i, and S the state before the chunk,
 //   o_i = e^(b_i) q_i S + sum_(j<=i) e^(b_i - b_j) (q_i . k_j) v_j
 //   S'  = e^(b_last) S + sum_j k_j (e^(b_last - b_j) v_j)^T
-// which is four products of 128 rows: Q K^T, P V, Q S and V'^T K.  An exponent between
-// blocks of 32 tokens is a sum of the log decays between two tokens (rest of the
+// which is four products of 128 rows: Q K^T, P V, Q S and V'^T K.  An exponent is
+// always a sum of the log decays between two tokens (between blocks of 32: rest of the
 // column's block, blocks between, the row's block up to it), each factor at most 1 if
-// decays are; within a block it is a difference of two sums of at most 32.
+// decays are.  A difference of two sums from a common start would be off by 2^-24 of
+// the larger one: weights by 2e-4 where half of a block's tokens forget.
 //
 // Precision.  P, S and V' are fp32 values that enter a product as a 16-bit part and
 // the rounded remainder (two MMAs that share the other operand).  One part alone
 // would add the error of a second output rounding, and 2^-9 to the states.  fp16
 // operands are scaled by powers of two (P by row, V' by chunk, S as a whole), so that
 // large scores or states do not leave fp16's range and small ones keep their bits:
-// those down to 2^-17 of the largest all 22, smaller ones what lies above 2^-39 of it.  The state itself stays in fp32 registers and is only added to by fp32
-// additions that round to nearest.
+// those down to 2^-17 of the largest all 22, smaller ones what lies above 2^-39 of it.
+// The state itself stays in fp32 registers and is only added to by fp32 additions that
+// round to nearest.
 //
 // Bounds.  A chunk of 128 x 128 takes 3.9 us (8000 cycles) with one query head a kv head
 // and about 2.4 for each of more (5000), about twice its MMAs' time (64 and 40 of 64
@@ -95,7 +97,7 @@ struct Geo {
 
 // A chunk's decays, in log2 units where they are sums.
 struct alignas(16) Decays { // read four floats at a time
-    float upto[kChunk];   // sum from the block's first token up to this one
+    float each[kChunk];   // the token's own
     float rest[kChunk];   // 2^(sum behind this one to the block's end)
     float block[4];       // the blocks' sums
 };
@@ -494,42 +496,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (c >= 2 && !warp_wait(&m->dec_empty[b], (uint32_t)((c >> 1) - 1) & 1))
                     return false;
                 Decays &d = m->dec[b];
-                float upto[4], rest[4];
-                // in log2 units; below 2^-149 is 0, and a difference of two such sums stays
-                // a number
+                float rest[4], sum = 0.f;
+                // in log2 units; below 2^-149 is 0, and so many of them add up to a number
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     g[i] *= 1.4426950408889634f;
                     g[i] = g[i] < -150.f ? -150.f : g[i];
+                    sum += g[i];
                 }
-                upto[0] = g[0];
-#pragma unroll
-                for (int i = 1; i < 4; ++i)
-                    upto[i] = upto[i - 1] + g[i];
                 rest[3] = 0.f;
 #pragma unroll
                 for (int i = 2; i >= 0; --i)
                     rest[i] = rest[i + 1] + g[i + 1];
-                float up = upto[3], down = upto[3]; // over the 8 lanes of a block
+                float down = sum; // over the 8 lanes of a block
 #pragma unroll
                 for (int o = 1; o < 8; o *= 2) {
-                    const float a = __shfl_up_sync(~0u, up, o, 8);
                     const float z = __shfl_down_sync(~0u, down, o, 8);
-                    if ((lane & 7) >= o)
-                        up += a;
                     if ((lane & 7) + o < 8)
                         down += z;
                 }
-                float before = __shfl_up_sync(~0u, up, 1, 8), behind = __shfl_down_sync(~0u, down, 1, 8);
-                before = lane & 7 ? before : 0.f;
+                float behind = __shfl_down_sync(~0u, down, 1, 8);
                 behind = (lane & 7) < 7 ? behind : 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    d.upto[lane * 4 + i] = before + upto[i];
+                    d.each[lane * 4 + i] = g[i];
                     d.rest[lane * 4 + i] = exp2f(behind + rest[i]);
                 }
-                if ((lane & 7) == 7)
-                    d.block[lane >> 3] = up;
+                if ((lane & 7) == 0)
+                    d.block[lane >> 3] = down;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&m->dec_full[b]);
@@ -854,22 +848,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // triangle allows
         const int block[2] = {half, 3 - half};
         bool ok = true;
-        float upto = 0.f, inter = 0.f, f[2] = {0.f, 0.f};
+        float inter = 0.f, f[2] = {0.f, 0.f};
+        float after[4] = {}; // sums behind each 8 tokens of the row's block, up to the row
         for (int it = 0; !kParts && it < total; ++it) {
             const int c = it / per, h = it - c * per;
             const Decays &d = m->dec[c & 1];
             const int live = min(kChunk, len - c * kChunk);
-            if (warp == 0)
-                ok = warp_wait(&m->s_full, (uint32_t)it & 1);
-            else if (h == 0 && warp == 1)
+            if (h == 0) { // there before the scores
                 ok = warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1);
-            if (!(ok = together<256>(kRowsBarrier, ok)))
-                break;
-            if (h == 0) {
                 // decays from the end of a column block to this row, and from the
                 // chunk's beginning
-                upto = d.upto[row];
-                float sum = upto;
+                float sum = 0.f; // from the block's first token up to this row
+#pragma unroll
+                for (int k = 3; k >= 0; --k) {
+                    float of8 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k * 8 + i <= lane)
+                            of8 += d.each[blk * 32 + k * 8 + i];
+                    after[k] = sum;
+                    sum += of8;
+                }
                 f[0] = f[1] = 0.f;
 #pragma unroll
                 for (int k = 3; k >= 0; --k)
@@ -882,6 +881,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 inter = exp2f(sum) * p.scale;
             }
+            if (warp == 0)
+                ok = ok && warp_wait(&m->s_full, (uint32_t)it & 1);
+            if (!(ok = together<256>(kRowsBarrier, ok)))
+                break;
             tc_fence_after_sync();
             float down = 1.f, up = 1.f; // 2^-E, 2^E
             if constexpr (kHalf) {
@@ -935,13 +938,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     } else {
                         const float2 fb2 = make_float2(p.scale * down, p.scale * down);
-                        const float2 up2 = make_float2(upto, upto), less = make_float2(-1.f, -1.f);
+                        // from this row back, 8 columns at a time: the sum of what lies
+                        // behind each (one chain of 32 costs 2.5 % with 8 query heads)
+                        float sum = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 l = __ffma2_rn(
-                                *reinterpret_cast<const float2 *>(&d.upto[b * 32 + i * 2]), less, up2);
-                            const float2 x = __fmul2_rn(
-                                pair_of(sv + i * 2), __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), fb2));
+                        for (int i = 15; i >= 0; --i) {
+                            if (i % 4 == 3)
+                                sum = after[i / 4];
+                            const float2 g = *reinterpret_cast<const float2 *>(&d.each[b * 32 + i * 2]);
+                            float2 w;
+                            w.y = ex2(sum);
+                            if (2 * i < lane)
+                                sum += g.y;
+                            w.x = ex2(sum);
+                            if (2 * i <= lane)
+                                sum += g.x;
+                            const float2 x = __fmul2_rn(pair_of(sv + i * 2), __fmul2_rn(w, fb2));
                             put(i, make_float2(2 * i <= lane ? x.x : 0.f, 2 * i < lane ? x.y : 0.f));
                         }
                     }

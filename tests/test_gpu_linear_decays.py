@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from tests._linear_ref import check_out, inputs, ref_linear
+from tests._linear_ref import check_out, check_states, inputs, ref_linear
 from tests.test_gpu_linear import decode, pa, prefill  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +38,34 @@ def test_strong_decays(pa, run, lens, new, d):
     check_out(out, ref, mag)
     assert pa.pa_device_errors(clear=True) == 0
     assert math.isfinite(float(out.float().sum()))
+
+
+@pytest.mark.parametrize("every", [2, 3, 4, 8])
+@pytest.mark.parametrize("strong", [-20.0, -1e4, -math.inf])
+@pytest.mark.parametrize("heads", [1, 3])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_ordinary_tokens_between_strong_decays(pa, every, strong, heads, dtype):
+    """The weight of a token for one that follows is that of the decays between them,
+    however strong the ones before.
+
+    All scores are equal and values are 1 or -1, so that many outputs are small differences
+    of terms that are not, and only those terms' errors show.  The tolerance is that of
+    tests/_linear_ref.py; its exponents' part, for sums of up to 31 terms that are off by
+    2^-24 of the sum x each, with |x| e^-|x| <= 0.37, is 31 * 0.37 * 2^-24 < 2^-20, and the
+    other parts are below 2^-19 + 2^-21."""
+    d = 64
+    x = inputs([300, 129, 40], 2 * heads, 2, d, dtype, "token", seed=81, fresh=(0,))
+    g = x["log_decay"]
+    g.uniform_(-0.02, 0.0, generator=torch.Generator("cuda").manual_seed(every))
+    g[every // 2::every, 0] = strong
+    g[torch.rand(len(g), generator=torch.Generator().manual_seed(every)).cuda() < 1 / every, 1] = strong
+    x["q"].fill_(1.0)
+    x["k"].fill_(1.0)
+    x["v"].copy_(x["v"].sign())
+    x["states"].sign_()
+    ref, states, mag, smag = ref_linear(*(x[k] for k in ("q", "k", "v", "log_decay", "states", "src",
+                                                         "dst", "starts", "scale")))
+    out = prefill(pa, x)
+    check_out(out, ref, mag)
+    check_states(x["states"], states, smag, out.dtype)
+    assert pa.pa_device_errors(clear=True) == 0
