@@ -284,7 +284,7 @@ struct Cut {
 };
 
 constexpr float kPassChunk = 2.5f, kChain = 8.f, kSegment = 12.f, kOnePass = 4.f, kTwoPasses = 10.f,
-                kWorth = 0.89f;
+                kWorth = 0.89f, kReturn = 2.5f, kLook = 0.55f;
 
 struct Work {
     float chunks, longest; // in chunks
@@ -294,8 +294,14 @@ struct Work {
     float uncut(float chunk, float fixed) const
     {
         const float rounds = ceilf((float)seqs * kv_heads / kSms);
-        return std::max(longest * chunk + kChain * fixed,
-                        rounds * (chunks / seqs * chunk + kChain * fixed)) + kOnePass * fixed;
+        const float one = longest * chunk + kChain * fixed,
+                    all = rounds * (chunks / seqs * chunk + kChain * fixed);
+        // Up to 32 sequences the longest starts first.  Of more it starts anywhere in the
+        // others' time; this is the mean, of terms linear in `chunk`, so convex in it.
+        const float us = seqs <= 32 ? std::max(one, all)
+                         : one < all ? all + 0.5f * one * one / all
+                                     : one + 0.5f * all;
+        return us + kOnePass * fixed;
     }
     // chunks of a segment that fills the SMs `rounds` times; 0 if it does not cut
     int segment(int rounds) const
@@ -320,6 +326,13 @@ struct Work {
                                  : (chunks / n + 0.5f * seqs) * kSegment;
         return (chunks * chunk + passed * kPassChunk + chains) * kv_heads / kSms +
                0.5f * (1.f - 1.f / seqs) * (n * (chunk + kPassChunk) + kSegment) + kTwoPasses;
+    }
+    // us of what grows with the sequences besides: CTAs of the first pass that have nothing
+    // to do, and every CTA's search, in both passes, past half of the sequences at the mean
+    float search(int64_t lines) const
+    {
+        const float looks = 0.5f * (float)((seqs - 1) / 32);
+        return (seqs * kReturn + lines * 2 * looks * kLook) * kv_heads / kSms;
     }
 };
 constexpr int kRounds = 8;
@@ -347,7 +360,8 @@ static Cut cut_of(int num_seqs, int num_tokens, int max_query_len, int num_heads
         const int n = w.segment(r);
         if (!n || lines_of(n, num_seqs, num_tokens) > 65535)
             continue;
-        const float us = std::max(w.rounds_of(r, n, chunk, 1.f), w.uneven(n, chunk));
+        const float us = std::max(w.rounds_of(r, n, chunk, 1.f), w.uneven(n, chunk)) +
+                         w.search(lines_of(n, num_seqs, num_tokens));
         if (us < best) {
             best = us;
             cut = {n * kChunk, (int)lines_of(n, num_seqs, num_tokens)};
