@@ -631,7 +631,9 @@ typedef struct pa_block_pool {
  *   num_new        int32 [num_seqs]; a negative one, or one past the table's end,
  *                  counts as 0, flagged (PA_DEVERR_SEQ_LEN)
  *   slot_mapping   int64 [num_tokens]: the new tokens' slots, row after row without
- *                  gaps, for pa_reshape_and_cache; -1 behind the last
+ *                  gaps, for pa_reshape_and_cache; -1 behind the last, and for
+ *                  tokens that would go on in a block outside the pool or of count
+ *                  0 (flagged, PA_DEVERR_BLOCK_ID)
  *   info           int32 [2]: blocks that the call needs, and free blocks less
  *                  those.  Where that is negative, or slot_mapping is too short,
  *                  nothing is taken: tables, lengths and counts stay as they were,

@@ -327,15 +327,16 @@ struct ExtendParams {
     // workspace: per block
     int32_t *writers, *latest, *free_ids;
     // per row: old length, new tokens, first rank of its blocks, first token, and
-    // its old last block if that is copied, else -1; the rows that copy
+    // its old last block if that is copied, else kKept or kLost; the rows that copy
     int32_t *row_len, *row_new, *row_begin, *row_token, *row_copy, *copy_rows;
     Told *told;          // of each CTA
     int32_t *head;       // tokens, rows that copy
     int rows, num_blocks, max_blocks, block_size, len_cap, num_tokens;
 };
 
+constexpr int kKept = -1, kLost = -2;
 struct Row {
-    int len, fresh, last; // last: the block that new tokens go on in, or -1
+    int len, fresh, last; // last: the block that new tokens go on in, or kKept
 };
 
 __device__ __forceinline__ Row read_row(const ExtendParams &p, int r)
@@ -347,7 +348,7 @@ __device__ __forceinline__ Row read_row(const ExtendParams &p, int r)
         atomicOr(p.err, PA_DEVERR_SEQ_LEN_);
         x.fresh = 0;
     }
-    x.last = -1;
+    x.last = kKept;
     if (x.fresh > 0 && x.len % p.block_size) {
         const int b = p.tables[(int64_t)r * p.max_blocks + x.len / p.block_size];
         if (b >= 0 && b < p.num_blocks)
@@ -379,13 +380,14 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
     const int b0 = min(p.num_blocks, rank * part), b1 = min(p.num_blocks, b0 + part);
 
     // A thread's rows stay in registers over the barriers: the last block only where it
-    // is shared, and its count.
+    // is shared, and its count.  One that is free may be another row's in a moment: no
+    // token goes on there.
     Row row[kRows];
     int held[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         const int r = r0 + tid + k * kRankThreads;
-        row[k] = {0, 0, -1};
+        row[k] = {0, 0, kKept};
         held[k] = 0;
         if (r >= r1)
             continue;
@@ -395,7 +397,9 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
             if (held[k] > 1)
                 p.writers[row[k].last] = 0, p.latest[row[k].last] = -1;
             else
-                row[k].last = -1;
+                row[k].last = held[k] == 1 ? kKept : kLost;
+            if (row[k].last == kLost)
+                atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
         }
     }
     const int free_here = sum_of(my_free(p.refs, b0, b1), counts);
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
         Row &x = row[k];
         const int r = r0 + tid + k * kRankThreads;
         if (x.last >= 0 && __ldcg(p.writers + x.last) == held[k] && __ldcg(p.latest + x.last) == r)
-            x.last = -1;
+            x.last = kKept;
         // need: blocks below kCopyBit, rows that copy above
         int64_t v[2] = {blocks_of(x.len + x.fresh, p.block_size) - blocks_of(x.len, p.block_size), x.fresh};
         if (x.last >= 0)
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kRankThreads) extend_rank_kernel(const ExtendP
         const int64_t need = need_before + begin[k];
         p.row_len[r] = x.len;
         p.row_new[r] = ok ? x.fresh : 0;
-        p.row_copy[r] = copies ? x.last : -1;
+        p.row_copy[r] = copies || x.last < 0 ? x.last : kKept;
         p.row_begin[r] = (int)(need & low);
         p.row_token[r] = ok ? (int)(new_before + token[k]) : 0;
         p.lens_out[r] = x.len + (ok ? x.fresh : 0);
@@ -526,7 +530,8 @@ __global__ void __launch_bounds__(kThreads) extend_apply_kernel(const ExtendPara
             const int kept = blocks_of(len, bs) - (p.row_copy[lo] >= 0);
             const int block = j < kept ? p.tables[(int64_t)lo * p.max_blocks + j]
                                        : p.free_ids[p.row_begin[lo] + j - kept];
-            if (block >= 0 && block < p.num_blocks)
+            const bool lost = j < kept && p.row_copy[lo] == kLost;
+            if (block >= 0 && block < p.num_blocks && !lost)
                 slot = (int64_t)block * bs + pos % bs;
         }
         p.slots[t] = slot;

@@ -342,3 +342,17 @@ def test_two_streams(pa):
     for d, b, n, g in zip(devs, books, news, got):
         assert g == b.extend(n, sum(n))
         d.same(b)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_extend_in_a_free_block(pa, in_place):
+    """A last block of count 0 is handed to whoever needs one: no token of the row that
+    still names it goes there."""
+    book = Book([[0, -7, -7], [1, -7, -7], [-7, -7, -7]], [10, 10, 0], [0, 1, 0, 0, 0], 16)
+    dev = Dev(pa, book)
+    slots, info = dev.extend([8, 2, 3], 13, in_place)
+    assert info == [2, 2]
+    # row 0's second block and row 2's first are the lowest free ones, 0 and 2
+    assert slots == [-1] * 6 + [0, 1, 26, 27, 32, 33, 34]
+    assert dev.refs.tolist() == [1, 1, 1, 0, 0] and dev.lens.tolist() == [18, 12, 3]
+    assert pa.pa_device_errors(clear=True) == pa.DEVERR_BLOCK_ID
