@@ -506,10 +506,15 @@ __global__ void __launch_bounds__(kThreads) extend_apply_kernel(const ExtendPara
             const int32_t *const got = p.free_ids + p.row_begin[r] - kept;
             const int64_t row = (int64_t)r * p.max_blocks;
             for (int j = base + tid; j < end; j += kThreads)
-                if (j >= kept)
+                if (j >= kept) {
                     p.tables_out[row + j] = got[j];
-                else if (p.tables_out != p.tables)
-                    p.tables_out[row + j] = p.tables[row + j];
+                } else {
+                    const int b = p.tables[row + j];
+                    if (b < 0 || b >= p.num_blocks)
+                        atomicOr(p.err, PA_DEVERR_BLOCK_ID_);
+                    if (p.tables_out != p.tables)
+                        p.tables_out[row + j] = b;
+                }
             continue;
         }
         const int64_t t64 = (item - copies - entries) * kThreads + tid;

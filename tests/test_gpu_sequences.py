@@ -345,6 +345,24 @@ def test_two_streams(pa):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bad", [-3, 40, 1 << 30])
+def test_extend_flags_ids_in_any_entry(pa, bad, in_place):
+    """An id outside the pool anywhere in a row, whether the row grows or not; entries
+    behind a row's last are not looked at."""
+    book = Book([[3, 5, 7, -7], [9, 11, bad, bad], [2, bad, bad, bad]], [40, 20, 0],
+                [int(b in (3, 5, 7, 9, 11)) for b in range(40)], 16)
+    for row, new in ((0, [1, 0, 0]), (0, [0, 0, 0]), (1, [0, 1, 3])):
+        dev = Dev(pa, book)
+        dev.extend(new, 4, in_place)
+        assert pa.pa_device_errors(clear=True) == 0
+        dev = Dev(pa, book)
+        dev.tables[row, 0] = bad
+        dev.extend(new, 4, in_place)
+        assert dev.tables[row, 0].item() == bad
+        assert pa.pa_device_errors(clear=True) == pa.DEVERR_BLOCK_ID
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_extend_in_a_free_block(pa, in_place):
     """A last block of count 0 is handed to whoever needs one: no token of the row that
     still names it goes there."""
