@@ -596,12 +596,12 @@ pa_status pa_linear_prefill(void *out, const void *q, const void *k, const void 
  * written.  block_size is any positive number: a pool of one state for each
  * sequence (pa_linear_*) is one whose block_size no sequence outgrows.  Results
  * are whole numbers and do not depend on the order in which anything runs.  Each
- * metadata output may be the input itself where nothing else is said, and must
- * not overlap it otherwise: separate ones leave the inputs to the step that still
- * runs.  At most 65535 rows; max_blocks_per_seq * block_size < 2^31.  A seq_len
- * outside [0, max_blocks_per_seq * block_size] is clamped and flagged
- * (PA_DEVERR_SEQ_LEN), a block id outside the pool has no count and no bytes and
- * is flagged (PA_DEVERR_BLOCK_ID).
+ * metadata output may be its input itself where nothing else is said: separate ones
+ * leave the inputs to the step that still runs.  Outputs and workspace must overlap
+ * no other metadata of the call (PA_ERR_INVALID_ARG) and no pool.  At most 65535 rows;
+ * max_blocks_per_seq * block_size < 2^31.  A seq_len outside [0, max_blocks_per_seq *
+ * block_size] is clamped and flagged (PA_DEVERR_SEQ_LEN), a block id outside the pool
+ * has no count and no bytes and is flagged (PA_DEVERR_BLOCK_ID).
  *
  * Extend and compact also move blocks' bytes, in every pool that is indexed by
  * these block ids (layers' caches, scales, bounds, states), given as a HOST array:

@@ -642,10 +642,29 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(const CompactPa
 // ---------------------------------------------------------------------------
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-static bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+// An array of a call; of an output, the input that it may be.
+struct Span {
+    const void *at;
+    int64_t bytes;
+    const void *self;
+};
+
+// Whether an output lies on another output, or on an input that it may not be.
+template <int N, int M> static bool overlap(const Span (&out)[N], const Span (&in)[M])
 {
-    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-    return x < y + b_bytes && y < x + a_bytes;
+    auto meet = [](const Span &a, const Span &b) {
+        const char *x = static_cast<const char *>(a.at), *y = static_cast<const char *>(b.at);
+        return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (int i = 0; i < N; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (meet(out[i], out[k]))
+                return true;
+        for (const Span &x : in)
+            if (!(x.at == out[i].at && x.at == out[i].self) && meet(out[i], x))
+                return true;
+    }
+    return false;
 }
 
 // Rows and blocks of the tables and counts.
@@ -745,11 +764,14 @@ pa_status pa_fork_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_t 
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(tables_out, 4) ||
         !aligned(seq_lens_out, 4) || !aligned(parents, 4))
         return PA_ERR_INVALID_ARG;
-    const int64_t wide = (int64_t)max_blocks_per_seq * 4, counts = (int64_t)num_blocks * 4;
+    const int64_t wide = 4ll * max_blocks_per_seq, counts = 4ll * num_blocks;
     // rows trade places, so that they cannot be written where others are read
-    if (overlap(tables_out, num_seqs_out * wide, block_tables, num_seqs * wide) ||
-        overlap(seq_lens_out, num_seqs_out * 4ll, seq_lens, num_seqs * 4ll) ||
-        (ref_counts != ref_counts_out && overlap(ref_counts, counts, ref_counts_out, counts)))
+    const Span out[] = {{tables_out, num_seqs_out * wide, nullptr},
+                        {seq_lens_out, num_seqs_out * 4ll, nullptr},
+                        {ref_counts_out, counts, ref_counts}};
+    const Span in[] = {{block_tables, num_seqs * wide}, {seq_lens, num_seqs * 4ll}, {ref_counts, counts},
+                       {parents, num_seqs_out * 4ll}};
+    if (overlap(out, in))
         return PA_ERR_INVALID_ARG;
     cudaError_t e;
     ForkParams p = {};
@@ -809,18 +831,20 @@ pa_status pa_extend_sequences(int32_t *tables_out, int32_t *seq_lens_out, int32_
         !aligned(slot_mapping, 8) || !aligned(info, 4) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4) || !aligned(ref_counts, 4) || !aligned(num_new, 4))
         return PA_ERR_INVALID_ARG;
-    const int64_t wide = 4ll * num_seqs * max_blocks_per_seq;
-    if ((tables_out != block_tables && overlap(tables_out, wide, block_tables, wide)) ||
-        (seq_lens_out != seq_lens && overlap(seq_lens_out, 4ll * num_seqs, seq_lens, 4ll * num_seqs)) ||
-        (ref_counts_out != ref_counts &&
-         overlap(ref_counts_out, 4ll * num_blocks, ref_counts, 4ll * num_blocks)))
+    const int64_t wide = 4ll * num_seqs * max_blocks_per_seq, rows = 4ll * num_seqs,
+                  counts = 4ll * num_blocks;
+    const int64_t needed = (int64_t)pa_sequences_workspace_size(num_seqs, num_blocks);
+    const Span out[] = {{tables_out, wide, block_tables}, {seq_lens_out, rows, seq_lens},
+                        {ref_counts_out, counts, ref_counts}, {slot_mapping, 8ll * num_tokens, nullptr},
+                        {info, 8, nullptr}, {workspace, needed, nullptr}};
+    const Span in[] = {{block_tables, wide}, {seq_lens, rows}, {ref_counts, counts}, {num_new, rows}};
+    if (overlap(out, in))
         return PA_ERR_INVALID_ARG;
     Pools ps;
     st = read_pools(&ps, pools, num_pools, num_blocks);
     if (st != PA_OK)
         return st;
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < pa_sequences_workspace_size(num_seqs, num_blocks))
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)needed)
         return PA_ERR_WORKSPACE;
     cudaError_t e;
     ExtendParams p = {};
@@ -878,17 +902,17 @@ pa_status pa_compact_blocks(int32_t *tables_out, int32_t *ref_counts_out, int32_
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(ref_counts, 4))
         return PA_ERR_INVALID_ARG;
     const int64_t wide = 4ll * num_seqs * max_blocks_per_seq, counts = 4ll * num_blocks;
-    if ((tables_out != block_tables && overlap(tables_out, wide, block_tables, wide)) ||
-        (ref_counts_out != ref_counts && overlap(ref_counts_out, counts, ref_counts, counts)) ||
-        overlap(new_ids, counts, ref_counts, counts) ||
-        overlap(new_ids, counts, ref_counts_out, counts))
+    const int64_t needed = (int64_t)pa_sequences_workspace_size(num_seqs, num_blocks);
+    const Span out[] = {{tables_out, wide, block_tables}, {ref_counts_out, counts, ref_counts},
+                        {new_ids, counts, nullptr}, {info, 8, nullptr}, {workspace, needed, nullptr}};
+    const Span in[] = {{block_tables, wide}, {seq_lens, 4ll * num_seqs}, {ref_counts, counts}};
+    if (overlap(out, in))
         return PA_ERR_INVALID_ARG;
     Pools ps;
     st = read_pools(&ps, pools, num_pools, num_blocks);
     if (st != PA_OK)
         return st;
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < pa_sequences_workspace_size(num_seqs, num_blocks))
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)needed)
         return PA_ERR_WORKSPACE;
     cudaError_t e;
     CompactParams p = {};

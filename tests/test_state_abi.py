@@ -131,6 +131,39 @@ def test_compact_refusals(pa, kw, status):
     assert _caller(pa, "pa_compact_blocks", COMPACT)(**kw) == status
 
 
+# Sizes of the arrays of FORK, EXTEND and COMPACT as they stand above, in bytes.
+SPANS = {"tables": 160, "lens": 16, "refs": 400, "tables_out": 160, "lens_out": 16, "refs_out": 400,
+         "parents": 16, "new": 16, "slots": 72, "info": 8, "ids": 400}
+MAY_BE = {"tables_out": "tables", "lens_out": "lens", "refs_out": "refs"}
+
+
+@pytest.mark.parametrize("name,spec,outs,ins", [
+    ("pa_fork_sequences", FORK, ["tables_out", "lens_out", "refs_out"],
+     ["tables", "lens", "refs", "parents"]),
+    ("pa_extend_sequences", EXTEND, ["tables_out", "lens_out", "refs_out", "slots", "info"],
+     ["tables", "lens", "refs", "new"]),
+    ("pa_compact_blocks", COMPACT, ["tables_out", "refs_out", "ids", "info"],
+     ["tables", "lens", "refs"])])
+def test_outputs_on_other_arrays(pa, name, spec, outs, ins):
+    """An output that lies on any other array, by its first bytes or its last, is refused,
+    but for the input that it may be."""
+    call = _caller(pa, name, spec)
+    at = {n: v for n, _, v in spec}
+    both = [(o, x) for o in outs for x in ins + outs if x != o] + \
+        ([(o, "ws") for o in outs] + [("ws", x) for x in ins] if "ws" in at else [])
+    for out, other in both:
+        if out == "ws":
+            assert call(ws=at[other]) == INVALID, (out, other)
+            continue
+        least = 256 if other == "ws" else SPANS[other]
+        for place in (at[other] + least - 8, at[other] - SPANS[out] + 8, at[other]):
+            if place == at[other] and MAY_BE.get(out) == other and name != "pa_fork_sequences":
+                continue
+            if place == at[other] and (out, other) == ("refs_out", "refs"):
+                continue
+            assert call(**{out: place}) == INVALID, (out, other, place - at[other])
+
+
 def test_nothing_to_do_is_ok(pa):
     assert _caller(pa, "pa_linear_decode", DECODE)(B=0) == 0
     assert _caller(pa, "pa_linear_prefill", PREFILL)(B=0) == 0
