@@ -777,13 +777,15 @@ static int read_block_pools(PyObject *pools, int64_t num_blocks, int device, pa_
 {
     static const char *const wanted =
         "pools must be a list of contiguous CUDA tensors [planes, num_blocks, ...]";
-    PyObject *list = PySequence_Fast(pools, wanted);
+    /* a tuple of its own: what the tensors' methods run, and other threads meanwhile, may
+     * change a list */
+    PyObject *list = PySequence_Tuple(pools);
     if (!list)
         return -1;
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
+    const Py_ssize_t n = PyTuple_GET_SIZE(list);
     int st = n <= PA_MAX_POOLS ? 0 : bad("too many pools for one call");
     for (Py_ssize_t i = 0; i < n && !st; ++i) {
-        PyObject *const t = PySequence_Fast_GET_ITEM(list, i);
+        PyObject *const t = PyTuple_GET_ITEM(list, i);
         int64_t s[2];
         const int dims = shape_of(t, s, 2);
         const int c = dims < 0 ? -1 : contiguous(t);

@@ -332,6 +332,31 @@ def test_binding_checks_pools(pa, pool):
         calls.bind(pa.PAError, pa._current_device, pa._raw_current_stream)
 
 
+def test_a_list_of_pools_that_changes_meanwhile(pa):
+    """The pools are those that the list held when the call was made."""
+    calls = pa._block_calls
+    calls.bind(pa.PAError, lambda: 0, lambda device: 0)
+    try:
+        a = _args()
+        for f in vars(a):
+            setattr(a, f, _Elsewhere(getattr(a, f), 0))
+        seen = []
+
+        class Pool(_Elsewhere):
+            def get_device(self):
+                seen.append(len(pools))
+                pools.clear()
+                return 0
+
+        pools = [Pool(torch.zeros(2, 6, 16), 0) for _ in range(5)]
+        with pytest.raises(pa.PAError) as e:  # the workspace is too small: no launch
+            pa.pa_compact_blocks(a.tout, a.rout, a.ids, a.info, a.tables, a.lens, a.refs, pools, 16, a.ws)
+        assert e.value.status in (INVALID, WORKSPACE)
+        assert seen == [5, 0, 0, 0, 0]
+    finally:
+        calls.bind(pa.PAError, pa._current_device, pa._raw_current_stream)
+
+
 def test_a_failed_call_raises_its_status(pa):
     """The C call's own refusal comes out as PAError (no launch: the workspace is too
     small)."""
