@@ -858,16 +858,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = warp_wait(&m->dec_full[c & 1], (uint32_t)(c >> 1) & 1);
                 // decays from the end of a column block to this row, and from the
                 // chunk's beginning
-                float sum = 0.f; // from the block's first token up to this row
+                float sum = d.each[row]; // of the row's 8 tokens, up to it
 #pragma unroll
-                for (int k = 3; k >= 0; --k) {
-                    float of8 = 0.f;
+                for (int o = 1; o < 8; o *= 2) {
+                    const float x = __shfl_up_sync(~0u, sum, o, 8);
+                    sum += (lane & 7) >= o ? x : 0.f;
+                }
+                const float own = sum;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (k * 8 + i <= lane)
-                            of8 += d.each[blk * 32 + k * 8 + i];
-                    after[k] = sum;
-                    sum += of8;
+                for (int k = 2; k >= 0; --k) { // and of those before, in its block
+                    const float of8 = __shfl_sync(~0u, own, k * 8 + 7);
+                    after[k] = k < lane / 8 ? sum : 0.f;
+                    sum += k < lane / 8 ? of8 : 0.f;
                 }
                 f[0] = f[1] = 0.f;
 #pragma unroll
@@ -939,7 +941,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     } else {
                         const float2 fb2 = make_float2(p.scale * down, p.scale * down);
                         // from this row back, 8 columns at a time: the sum of what lies
-                        // behind each (one chain of 32 costs 2.5 % with 8 query heads)
+                        // behind each (16 prompts of 32 heads in fp16 178 us; one chain of
+                        // 32 182; differences of sums from the block's start 179)
                         float sum = 0.f;
 #pragma unroll
                         for (int i = 15; i >= 0; --i) {
@@ -948,11 +951,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const float2 g = *reinterpret_cast<const float2 *>(&d.each[b * 32 + i * 2]);
                             float2 w;
                             w.y = ex2(sum);
-                            if (2 * i < lane)
-                                sum += g.y;
+                            sum += 2 * i < lane ? g.y : 0.f;
                             w.x = ex2(sum);
-                            if (2 * i <= lane)
-                                sum += g.x;
+                            sum += 2 * i <= lane ? g.x : 0.f;
                             const float2 x = __fmul2_rn(pair_of(sv + i * 2), __fmul2_rn(w, fb2));
                             put(i, make_float2(2 * i <= lane ? x.x : 0.f, 2 * i < lane ? x.y : 0.f));
                         }
