@@ -496,9 +496,10 @@ def pa_decode_splitk_fp8(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
 
 
 # The block-scaled and block-sparse calls, linear attention and the sequence
-# calls.  Their checks and marshalling are native (csrc/pa_block_calls.c): a decode step makes several of these calls per
-# layer, and each costs the host little more than its launch.  The binding is
-# loaded when the first of them is made, so that the other calls do not need it.
+# calls.  Their checks and marshalling are native (csrc/pa_block_calls.c): a
+# decode step makes several of these calls per layer, and each costs the host
+# little more than its launch.  The binding is loaded when the first of them is
+# made, so that the other calls do not need it.
 def _load_block_calls():
     path = os.path.join(os.path.dirname(_LIB_PATH),
                         "pa_block_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
@@ -674,9 +675,10 @@ def pa_extend_sequences(tables_out: torch.Tensor, seq_lens_out: torch.Tensor,
     """Room for ``num_new[s]`` more tokens in every row: the lowest free blocks in
     the order of rows, copies of last blocks that are shared (in every tensor of
     ``pools``, each [planes, num_blocks, ...]), and the new tokens' slots (int64,
-    row after row without gaps, -1 behind the last).  ``info`` (int32 [2]) receives the blocks needed and the
-    free blocks less those; if that is negative, or slot_mapping too short,
-    nothing is taken.  Each output may be its input.  ``workspace`` holds
+    row after row without gaps, -1 behind the last).  ``info`` (int32 [2])
+    receives the blocks needed and the free blocks less those; if that is
+    negative, or slot_mapping too short, nothing is taken.  Each output may be
+    its input, and overlaps nothing else.  ``workspace`` holds
     pa_sequences_workspace_size bytes."""
     _block_calls.extend_sequences(tables_out, seq_lens_out, ref_counts_out, slot_mapping, info,
                                   block_tables, seq_lens, ref_counts, num_new, workspace, pools,

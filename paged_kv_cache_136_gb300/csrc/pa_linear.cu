@@ -29,12 +29,13 @@ constexpr int kHeadsAtOnce = 8; // query heads whose products share the state in
 //
 // One token is bound by HBM.  Five small CTAs an SM keep reads and writes going side by
 // side, and the states, which the next step wants, go past the caches: 64 x 32 states of
-// 128 x 128 take 40.7 us, 6.6 TB/s, 256 x 8 with four query heads each 41.4, with eight 43
-// (with rows one by one, not in fours, from shared memory 41.3, 43.1 and 47; that form
-// with cached loads and stores 43 and 46 for the first two, with whole states by 256
-// threads 51 and 56, with four heads in one pass over the state 45 and 47).  More tokens
-// are bound by their chain of sums and barriers: 0.8 us a token alone on the card, 256 x 8
-// with four heads 10.4 (13.5 without the next token's loads under way).
+// 128 x 128 take 40.6 us, 6.6 TB/s, 256 x 8 with four query heads each 41.5 (43 where the
+// states' order is random), with eight 43.3 (with rows one by one, not in fours, from
+// shared memory 41.3, 43.1 and 47; that form with cached loads and stores 43 and 46 for
+// the first two, with whole states by 256 threads 51 and 56, with four heads in one pass
+// over the state 45 and 47).  More tokens are bound by their chain of sums and barriers:
+// 0.6 us a token alone on the card, 256 x 8 with four heads 10 (13.5 without the next
+// token's loads under way).
 template <typename T, int D, bool kPrompt>
 __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearParams p)
 {
@@ -262,9 +263,11 @@ static cudaError_t launch_step(const LinearParams &p, int num_seqs, int head_siz
 // ---------------------------------------------------------------------------
 // The longest prompt, in tokens, that the recurrent kernel takes.  A chunk costs the same
 // however few its tokens.  1, 4, 8, 16 and 32 tokens in us, and chunks: 1 sequence of 32
-// heads 8, 10, 13, 20, 35, chunks 14; 32 of 32 heads 29, 39, 55, 84, 152, chunks 78; 256 of
-// 32 heads and 8 kv heads 49, 75, 115, 205, 385, chunks 225; with head_size 64 256 of 8
-// heads 18, 25, 35, 57, 104, chunks 108.
+// heads 8, 10, 14, 22, 37, chunks 15; 32 of 32 heads 28, 39, 55, 86, 158, chunks 78; 256 of
+// 32 heads and 8 kv heads 49, 76, 117, 207, 391, chunks 229; with head_size 64 256 of 8
+// heads 18, 25, 37, 57, 104, chunks 106.  One number for all sizes: it is that of many
+// grouped sequences; for 32 sequences of 32 heads 13 would be right, for a single one 8,
+// with head_size 64 32.
 constexpr int kShort = 16;
 
 // How prompts are cut.  A sequence and kv head is a chain of chunks that one CTA
@@ -275,10 +278,11 @@ constexpr int kShort = 16;
 // less on both sides): a chunk 2.3 for each query head and 2.4, or 3.9 with one query
 // head, in the first pass 2.5; a chain 8, a segment 12 in both passes; launches 4 and
 // 10.  Measured, without a cut and with one: one prompt of 1024, 4096 and 16384 tokens, 32
-// heads, 8 kv heads 100 and 36, 371 and 53, 1455 and 131; 32 kv heads 43 and 39, 137 and
-// 80, 510 and 241; one of 8192 among 32 of 1024, 8 kv heads, 752 and 344.  Left alone are,
-// with 32 kv heads, 4 prompts of 4096 tokens (141, cut 259) and one of 512 (27 and 31), and
-// with 8, 24 of 32 to 4000 tokens (372 and 443).
+// heads, 8 kv heads 102 and 36, 379 and 54, 1488 and 131; 32 kv heads 43 and 39, 137 and
+// 79, 512 and 239; one of 8192 among 32 of 1024, 8 kv heads, 762 and 347, among 511 of 64
+// 1236 and 909.  Left alone are, with 32 kv heads, 4 prompts of 4096 tokens (141, cut 259)
+// and, less rightly, one of 8192 among 16 of 512 (270 and 244); with 8, 16 of 4096 (395 and
+// 487) and one of 65536 among 4095 of 64 (9800 and 19300).
 struct Cut {
     int segment, lines;
 };

@@ -25,7 +25,7 @@
 // and about 2.4 for each of more (5000), about twice its MMAs' time (64 and 40 of 64
 // cycles each).  With one head the chain V' -> delta -> state -> operand -> Q S sets the
 // pace, each step a wait for the one before, with more of them the rows' chain scores ->
-// P -> P V -> output.  16 prompts of 256 to 2048 tokens, 32 heads, take 180 us in fp16;
+// P -> P V -> output.  16 prompts of 256 to 2048 tokens, 32 heads, take 178 us in fp16;
 // one of 131072, 64 heads and 8 kv heads, in bf16 1.37 ms, in which the MMAs run at 1.1
 // PFLOP/s.  A chain's start (an SM's turnover, its first tiles and state, a first look at
 // V) and its state's store take 8 us besides.
@@ -368,8 +368,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else {
             // Of up to 32 sequences line y is the y-th longest, so that the long ones start
             // first (8 of 32 to 4000 tokens, 32 heads: 133 us, in their own order 188; 16
-            // ascending ones 271 and 315; 24 in any order with 8 kv heads 373 and 369); with
-            // more of them their chains are many and even out.
+            // ascending ones 272 and 315; 24 in any order with 8 kv heads 373 and 371).  More
+            // keep their own order: 33 to 60 with 2 or 4 kv heads take the same in any, within
+            // 1 %; 40 with 8 heads and 8 kv heads 180 descending, 235 ascending, 250 mixed.
             if (lane < p.num_seqs) {
                 src = p.src_states[lane], dst = p.dst_states[lane];
                 n = segments_of(p, lane, q0, len, head == 0 && lane == y);
